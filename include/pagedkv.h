@@ -23,6 +23,15 @@
  *                         a chunk of one) attend causally over the paged cache
  *                         ("vLLM" page, prefill vs decoding; FAQ, chunked
  *                         prefill).
+ *   pa_build_tables       block tables, slot mapping and positions of a step,
+ *                         built on the GPU from the requests' lengths and a
+ *                         free list (tiemojia.cn vLLM V1 walkthrough, KV
+ *                         Manager and Model Runner: block table + slot_mapping).
+ *   pa_rope_reshape_and_cache  rotary positions on q and k (one or several
+ *                         position axes), fused with the cache write.
+ *   pa_extend             pa_prefill's attention over every cache: 8-bit
+ *                         caches, windows and ring tables, small blocks, any
+ *                         group up to 16, few rows over long contexts.
  *   pa_swap_blocks        whole-block moves between the GPU cache and a pinned
  *                         CPU cache ("vLLM" page, section "CacheEngine":
  *                         swap_in = CPU->GPU, swap_out = GPU->CPU; section
@@ -108,6 +117,8 @@ typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_INT8_F16 = 2, PA_INT8_BF16 =
 #define PA_DEVERR_PREFIX 0x10u   /* pa_decode_shared_prefix: a member's block ids differ from its group's
                                     inside the shared prefix (its rows are zeroed), or the group
                                     starts are out of order (sharing is then ignored) */
+#define PA_DEVERR_OUT_OF_BLOCKS 0x20u /* pa_build_tables: the free list has too few blocks (the step is empty) */
+#define PA_DEVERR_POSITION 0x40u /* pa_rope_reshape_and_cache: a position outside [0, max_position) */
 
 /* Geometry of a cache pool.  head_size in {64, 128}; block_size in {1, 2, 4, 8, 16, 32}
  * (block_size 1 is token-granular paging);
@@ -161,6 +172,91 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
                                const void* key, int64_t key_token_stride, const void* value,
                                int64_t value_token_stride, const int64_t* slot_mapping,
                                int32_t num_tokens, uint32_t* dev_err, void* stream);
+
+/* Rotary positions on q and k, fused with the cache write: what a layer does
+ * between its projections and attention.  The pages' store_kvcache (nano-vLLM
+ * article, section 5.2.3) stores keys that are rotated already; this call takes
+ * them as the projection leaves them and writes each vector once.
+ * Pair i (0 <= i < rotary_dim / 2) of a head vector x is (x[i], x[i +
+ * rotary_dim / 2]), or (x[2i], x[2i + 1]) when interleaved is non-zero; with
+ * a = pair_axis[i], p = positions[a * positions_axis_stride + token], c =
+ * cos_sin[p * rotary_dim + i] and s = cos_sin[p * rotary_dim + rotary_dim / 2 + i]
+ *   y1 = x1 * c - x2 * s,   y2 = x2 * c + x1 * s,
+ * each product and sum rounded to fp32 (never contracted), so results are a pure
+ * function of the input bits; dims from rotary_dim on pass unchanged.  q's
+ * results are rounded to q_out's type; k's are rounded to the cache's 16-bit
+ * type, or quantised from fp32 (one rounding) for an 8-bit cache; v is stored
+ * as pa_reshape_and_cache stores it.
+ *   q_out, q     device [num_tokens, num_q_heads, head_size], 16-bit; token
+ *                strides in elements (multiples of 8), 16-byte aligned.  q_out
+ *                may be q itself (with the same stride), and may otherwise not
+ *                overlap it.  num_q_heads 0: no queries, both may be NULL.
+ *   kv_cache, desc, layer, key, value, strides, slot_mapping: as
+ *                pa_reshape_and_cache; a token with slot -1 is not stored, its
+ *                query is still rotated.
+ *   positions    device int32, num_axes rows positions_axis_stride elements
+ *                apart (0: every axis has the same positions).  A token with a
+ *                position outside [0, max_position) sets PA_DEVERR_POSITION, is
+ *                not stored, and gets a zero q_out row.
+ *   cos_sin      device fp32 [max_position, rotary_dim]: a position's
+ *                rotary_dim / 2 cosines, then its sines (computed in fp64: the
+ *                angles of far positions need it); 4-byte aligned.
+ *   rotary_dim   a multiple of 16 in [16, head_size].
+ *   num_axes     1 .. 4 (time, height, width, ...).
+ *   pair_axis    HOST uint8 [rotary_dim / 2], each < num_axes, read before the
+ *                call returns; NULL: axis 0 for every pair.
+ * num_tokens == 0 launches nothing. */
+pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, const void* q, int64_t q_token_stride,
+                                    int32_t num_q_heads, void* kv_cache, const pa_cache_desc* desc, int32_t layer,
+                                    const void* key, int64_t key_token_stride, const void* value,
+                                    int64_t value_token_stride, const int64_t* slot_mapping, const int32_t* positions,
+                                    int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
+                                    int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
+                                    int32_t interleaved, int32_t num_tokens, uint32_t* dev_err, void* stream);
+
+/* Block tables, slot mapping and positions of one step, built on the GPU from
+ * the requests' lengths: the KV manager's and model runner's bookkeeping
+ * (tiemojia.cn vLLM V1 walkthrough, sections 3.3-3.4) for a step whose lengths
+ * are only known on the device.  Request s holds cached_lens[s] tokens and gets
+ * new_lens[s] more.  With ctx = cached + new, and R = ring_blocks (0: no ring):
+ *   context_lens[s] = ctx;  query_start_loc = the prefix sums of new_lens;
+ *   new blocks: the request held min(ceil(cached / bs), R) and needs
+ *     min(ceil(ctx / bs), R); the k-th block handed out in the call (requests in
+ *     order, each one's blocks in logical order) is
+ *     free_blocks[*num_free - 1 - k], written to the request's table row;
+ *   *num_free_out = *num_free - blocks handed out;
+ *   token i = query_start_loc[s] + j sits at positions[i] = cached + j; its slot
+ *     is block_tables[s][b % R] * bs + position % bs with b = position / bs
+ *     (b itself without a ring).  With a ring, tokens whose block a later token
+ *     of the same step takes over (b <= (ctx - 1) / bs - R) get slot -1.
+ *   Behind the last token, up to max_tokens: slot -1, position 0 (padding of a
+ *     captured graph; pa_reshape_and_cache skips them).
+ * Other table entries are left as they were.  cached_lens may be context_lens,
+ * and num_free may be num_free_out (an update in place).  No reference counts:
+ * rows own their blocks.  A row's blocks are given back by copying its first
+ * entries behind the free list and raising *num_free.
+ *   desc            only num_blocks and block_size are used (and checked).
+ *   block_tables    device int32 [num_seqs, block_table_stride], updated.
+ *   free_blocks     device int32 [num_blocks]; the first *num_free are free.
+ *   query_start_loc device int32 [num_seqs + 1]; context_lens device int32
+ *                   [num_seqs]; slot_mapping device int64 [max_tokens];
+ *                   positions device int32 [max_tokens], may be NULL.
+ * A step that cannot be built is empty: query_start_loc and context_lens 0, all
+ * slots -1, all positions 0, tables unchanged, *num_free_out = *num_free, and
+ *   PA_DEVERR_OUT_OF_BLOCKS  too few free blocks, or *num_free not in
+ *                            [0, num_blocks];
+ *   PA_DEVERR_CONTEXT        a negative length, a context longer than its row
+ *                            (without a ring) or than 2^31 - 1, or more than
+ *                            max_tokens new tokens.
+ * A block id outside [0, num_blocks) (of the free list, or of the entry that
+ * a token falls in) sets PA_DEVERR_BLOCK_ID and gives its tokens slot -1.
+ * num_seqs 0 .. PA_BUILD_TABLES_MAX_SEQS (more: PA_ERR_UNSUPPORTED). */
+#define PA_BUILD_TABLES_MAX_SEQS 16384
+pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64_t* slot_mapping, int32_t* positions,
+                          int32_t* block_tables, int32_t block_table_stride, const int32_t* free_blocks,
+                          const int32_t* num_free, int32_t* num_free_out, const pa_cache_desc* desc,
+                          const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens,
+                          int32_t ring_blocks, uint32_t* dev_err, void* stream);
 
 /* Workspace bytes pa_decode needs for these shapes (0 when no sequence can span
  * more than one partition, or desc is NULL; SIZE_MAX when the size does not fit
@@ -250,6 +346,51 @@ pa_status pa_prefill(void* out, const void* q, int64_t q_token_stride, const voi
                      int32_t block_table_stride, const int32_t* context_lens,
                      const int32_t* query_start_loc, int32_t num_seqs, int32_t num_q_heads,
                      int32_t max_query_len, float scale, uint32_t* dev_err, void* stream);
+
+/* Workspace bytes pa_extend needs for these shapes (0: nothing to do, or desc
+ * NULL; SIZE_MAX where it does not fit in half the address space).  Follows the
+ * SM count of the current device. */
+size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                 int32_t num_q_heads, int32_t max_query_len);
+
+/* pa_prefill's attention over every cache this library has: several new tokens
+ * per sequence (a whole prompt, a chunk of one, a few drafted tokens to check)
+ * attend causally over the paged cache, with an optional sliding window and
+ * ring tables as in pa_decode_window.  With ctx = context_lens[s] and q_len new
+ * tokens, query j sits at position p = ctx - q_len + j and attends
+ *   [max(0, p - window + 1, ((ctx-1)/bs - ring_blocks + 1) * bs), p]
+ * (the window term only with window > 0, the ring term only with
+ * ring_blocks > 0; the ring holds what the whole step leaves in it, so it must
+ * have ceil((window + q_len - 1) / bs) + 1 blocks for every window to be exact).
+ * A query with nothing to attend gets a zero row.  Softmax statistics and
+ * outputs accumulate in fp32; weights enter the second product as 16-bit
+ * values.  Contexts are split over SMs where a step has few rows, and the parts
+ * merged by log-sum-exp; results do not depend on timing.
+ *   out             device [num_tokens, num_q_heads, head_size], contiguous.
+ *   q               device [num_tokens, num_q_heads, head_size]; token stride
+ *                   q_token_stride elements (multiple of 8); 16-byte aligned.
+ *   query_start_loc device int32 [num_seqs + 1], non-decreasing from 0; rows
+ *                   from query_start_loc[num_seqs] on are neither read nor
+ *                   written.
+ *   num_tokens      rows of q and out.  A sequence whose queries are not inside
+ *                   [0, num_tokens), or whose start is above its end, is
+ *                   skipped with PA_DEVERR_CONTEXT.
+ *   max_query_len   an upper bound of every q_len (sizes the workspace); a
+ *                   longer sequence gets zero rows and PA_DEVERR_CONTEXT.
+ *   workspace       device, 16-byte aligned, >= pa_extend_workspace_bytes(...);
+ *                   needs no initialisation, and is free again once the call's
+ *                   work on the stream is done.
+ *   dev_err         optional; also PA_DEVERR_CONTEXT for q_len > ctx or (without
+ *                   a ring) ctx beyond the table row (zero rows), and
+ *                   PA_DEVERR_BLOCK_ID for a bad block id: every row that
+ *                   attends the block is zero, and rows computed beside it may be.
+ * Supported: every cache of pa_decode (16-bit with head_size 64 or 128, 8-bit
+ * with 128; block_size 1 .. 32), 1 to 16 query heads per kv head. */
+pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc,
+                    int32_t layer, const int32_t* block_tables, int32_t block_table_stride,
+                    const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                    int32_t num_tokens, int32_t num_q_heads, int32_t max_query_len, float scale, int32_t window,
+                    int32_t ring_blocks, void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream);
 
 /* Paged decode where groups of sequences share the first tokens of their
  * context physically: beams of one prompt, or parallel samples, whose prompt

@@ -22,13 +22,15 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE_TOO
 PA_ALLOC_OK, PA_ALLOC_LATER, PA_ALLOC_NEVER = range(3)
 PA_F16, PA_BF16, PA_INT8_F16, PA_INT8_BF16 = 0, 1, 2, 3
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_CONTEXT, DEVERR_TIMEOUT, DEVERR_PREFIX = 1, 2, 4, 8, 16
+DEVERR_OUT_OF_BLOCKS, DEVERR_POSITION = 32, 64
 DTYPE_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
 EXPORTED = [
     "pa_cache_bytes", "pa_cache_element_offset", "pa_cache_scale_offset", "pa_reshape_and_cache", "pa_decode_workspace_bytes",
     "pa_decode_partition_size", "pa_decode", "pa_decode_window", "pa_decode_window_span", "pa_prefill",
     "pa_decode_static_workspace", "pa_decode_shared_prefix", "pa_decode_shared_prefix_partition_size",
-    "pa_decode_shared_prefix_workspace_bytes", "pa_copy_blocks", "pa_swap_blocks", "pa_read_device_errors",
+    "pa_decode_shared_prefix_workspace_bytes", "pa_rope_reshape_and_cache", "pa_build_tables", "pa_extend",
+    "pa_extend_workspace_bytes", "pa_copy_blocks", "pa_swap_blocks", "pa_read_device_errors",
     "pa_status_string", "pa_last_error_message",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_can_allocate", "pa_bm_allocate", "pa_bm_append_slot", "pa_bm_fork",
     "pa_bm_free", "pa_bm_block_table", "pa_bm_swap_out", "pa_bm_swap_in", "pa_bm_num_free_blocks",
@@ -114,6 +116,16 @@ def load():
     lib.pa_decode_shared_prefix_partition_size.restype = i32
     lib.pa_decode_shared_prefix_workspace_bytes.argtypes = [D, i32, i32, i32, i32, i32]
     lib.pa_decode_shared_prefix_workspace_bytes.restype = sz
+    lib.pa_rope_reshape_and_cache.argtypes = [P, i64, P, i64, i32, P, D, i32, P, i64, P, i64, P, P, i64, P, i32, i32,
+                                              P, i32, i32, i32, P, P]
+    lib.pa_rope_reshape_and_cache.restype = ctypes.c_int
+    lib.pa_build_tables.argtypes = [P, P, P, P, P, i32, P, P, P, D, P, P, i32, i32, i32, P, P]
+    lib.pa_build_tables.restype = ctypes.c_int
+    lib.pa_extend.argtypes = [P, P, i64, P, D, i32, P, i32, P, P, i32, i32, i32, i32, ctypes.c_float, i32, i32, P, sz,
+                              P, P]
+    lib.pa_extend.restype = ctypes.c_int
+    lib.pa_extend_workspace_bytes.argtypes = [D, i32, i32, i32, i32]
+    lib.pa_extend_workspace_bytes.restype = sz
     lib.pa_copy_blocks.argtypes = [P, D, P, i32, P]
     lib.pa_copy_blocks.restype = ctypes.c_int
     lib.pa_swap_blocks.argtypes = [P, D, P, D, i32, P, i32, P]
@@ -284,6 +296,132 @@ def prefill(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Ca
     _check(load().pa_prefill(_ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), ctypes.byref(desc.c()), layer,
                              _ptr(block_tables), block_tables.stride(0), _ptr(context_lens), _ptr(query_start_loc),
                              S, Hq, max_query_len, scale, _ptr(dev_err), _stream(stream)))
+
+
+def _tensors(dtype, **tensors):
+    """Marshalling passes raw pointers on, so a tensor of another type is refused here."""
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be {dtype}, not {t.dtype}")
+
+
+def _rows(**tensors):
+    """[tokens, heads, dims] tensors: heads and dims contiguous (the token stride is free)."""
+    for name, t in tensors.items():
+        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be [tokens, heads, dims] with heads and dims "
+                                                   f"contiguous, not {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _dense(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _same(name, got, want):
+    if got != want:
+        raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} is {got}, expected {want}")
+
+
+def rope_table(max_position: int, inv_freq: torch.Tensor, device="cuda") -> torch.Tensor:
+    """The cos_sin table of rope_reshape_and_cache: fp32 [max_position, 2 * len(inv_freq)], the cosines
+    of position * inv_freq (angles in fp64), then the sines."""
+    f = inv_freq.to(device=device, dtype=torch.float64)
+    ang = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32)
+
+
+def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, kv_cache: torch.Tensor,
+                           desc: CacheDesc, key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor,
+                           positions: torch.Tensor, cos_sin: torch.Tensor, pair_axis=None, interleaved: bool = False,
+                           layer: int = 0, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """pa_rope_reshape_and_cache: q/q_out [N, Hq, D] (or None), key/value [N, Hkv, D], positions int32 [N] or
+    [axes, N], cos_sin fp32 [max_position, rotary_dim]; pair_axis uint8 per rotary pair on the host (None: all
+    on axis 0)."""
+    n, hkv = key.shape[0], desc.num_kv_heads
+    _rows(key=key, value=value)
+    _same("key's shape", tuple(key.shape), (n, hkv, desc.head_size))
+    _same("value's shape", tuple(value.shape), (n, hkv, desc.head_size))
+    _tensors(desc.dtype, key=key, value=value, q=q, q_out=q_out)
+    _tensors(torch.int64, slot_mapping=slot_mapping)
+    _tensors(torch.int32, positions=positions)
+    _tensors(torch.float32, cos_sin=cos_sin)
+    _dense(slot_mapping=slot_mapping, cos_sin=cos_sin)
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.shape[-1] != n or slot_mapping.numel() != n or (n > 1 and positions.stride(-1) != 1):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "positions and slot_mapping must have one dense entry per token")
+    hq = 0 if q is None else q.shape[1]
+    if q is not None:
+        _rows(q=q, q_out=q_out)
+        _same("q's shape", tuple(q.shape), (n, hq, desc.head_size))
+        _same("q_out's shape", tuple(q_out.shape), (n, hq, desc.head_size))
+    pa = None
+    if pair_axis is not None:
+        pa = pair_axis if isinstance(pair_axis, np.ndarray) and pair_axis.dtype == np.uint8 and \
+            pair_axis.flags.c_contiguous else np.ascontiguousarray(np.asarray(pair_axis, dtype=np.uint8))
+        _same("pair_axis' length", pa.size, cos_sin.shape[1] // 2)
+    _check(load().pa_rope_reshape_and_cache(
+        _ptr(q_out), 0 if q is None else q_out.stride(0), _ptr(q), 0 if q is None else q.stride(0), hq,
+        _ptr(kv_cache), ctypes.byref(desc.c()), layer, _ptr(key), key.stride(0), _ptr(value), value.stride(0),
+        _ptr(slot_mapping), _ptr(positions), positions.stride(0) if axes > 1 else 0, _ptr(cos_sin), cos_sin.shape[0],
+        cos_sin.shape[1], None if pa is None else pa.ctypes.data, axes, int(interleaved), n, _ptr(dev_err),
+        _stream(stream)))
+
+
+def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot_mapping: torch.Tensor,
+                 positions: torch.Tensor | None, block_tables: torch.Tensor, free_blocks: torch.Tensor,
+                 num_free: torch.Tensor, num_free_out: torch.Tensor, desc: CacheDesc, cached_lens: torch.Tensor,
+                 new_lens: torch.Tensor, ring_blocks: int = 0, dev_err: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """pa_build_tables: query_start_loc [S + 1], context_lens [S], slot_mapping int64 [max_tokens] and positions
+    [max_tokens] (or None) are written, block_tables [S, W] and num_free_out [1] updated, from cached_lens [S],
+    new_lens [S] and the free list free_blocks [num_blocks], num_free [1] (int32 all but slot_mapping)."""
+    S = cached_lens.shape[0]
+    _tensors(torch.int32, query_start_loc=query_start_loc, context_lens=context_lens, positions=positions,
+             block_tables=block_tables, free_blocks=free_blocks, num_free=num_free, num_free_out=num_free_out,
+             cached_lens=cached_lens, new_lens=new_lens)
+    _tensors(torch.int64, slot_mapping=slot_mapping)
+    _dense(query_start_loc=query_start_loc, context_lens=context_lens, positions=positions, free_blocks=free_blocks,
+           cached_lens=cached_lens, new_lens=new_lens, slot_mapping=slot_mapping)
+    if (query_start_loc.numel() < S + 1 or context_lens.numel() < S or new_lens.numel() != S
+            or block_tables.shape[0] < S or free_blocks.numel() < desc.num_blocks or num_free.numel() < 1
+            or num_free_out.numel() < 1
+            or (positions is not None and positions.numel() < slot_mapping.numel())
+            or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1)):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "an array of build_tables is too short, or table rows are not dense")
+    _check(load().pa_build_tables(
+        _ptr(query_start_loc), _ptr(context_lens), _ptr(slot_mapping), _ptr(positions), _ptr(block_tables),
+        block_tables.stride(0) if S > 1 else max(block_tables.shape[1], 1), _ptr(free_blocks), _ptr(num_free),
+        _ptr(num_free_out), ctypes.byref(desc.c()), _ptr(cached_lens), _ptr(new_lens), S, slot_mapping.numel(),
+        ring_blocks, _ptr(dev_err), _stream(stream)))
+
+
+def extend_workspace_bytes(desc: CacheDesc, num_seqs: int, num_tokens: int, num_q_heads: int,
+                           max_query_len: int) -> int:
+    return load().pa_extend_workspace_bytes(ctypes.byref(desc.c()), num_seqs, num_tokens, num_q_heads, max_query_len)
+
+
+def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: CacheDesc, block_tables: torch.Tensor,
+           context_lens: torch.Tensor, query_start_loc: torch.Tensor, max_query_len: int, scale: float,
+           workspace: torch.Tensor | None, window: int = 0, ring_blocks: int = 0, layer: int = 0,
+           dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """pa_extend: out/q [T, Hq, D] packed by query_start_loc (int32 [S + 1]); causal over each sequence's cache
+    (its last q_len positions are the queries), with an optional window and ring tables."""
+    S, T, Hq = context_lens.shape[0], q.shape[0], q.shape[1]
+    _rows(q=q)
+    _dense(out=out, context_lens=context_lens, query_start_loc=query_start_loc)
+    _tensors(desc.dtype, out=out, q=q)
+    _tensors(torch.int32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
+    _same("out's shape", tuple(out.shape), (T, Hq, desc.head_size))
+    if query_start_loc.numel() < S + 1 or block_tables.shape[0] < S or \
+            (block_tables.shape[1] > 1 and block_tables.stride(1) != 1):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "query_start_loc or block_tables is too short, or rows are not dense")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().pa_extend(_ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), ctypes.byref(desc.c()), layer,
+                            _ptr(block_tables), block_tables.stride(0) if S > 1 else max(block_tables.shape[1], 1),
+                            _ptr(context_lens), _ptr(query_start_loc), S, T, Hq, max_query_len, scale, window,
+                            ring_blocks, _ptr(workspace), ws_bytes, _ptr(dev_err), _stream(stream)))
 
 
 def decode_window_span(max_context_len: int, block_size: int, window: int, ring_blocks: int = 0) -> int:

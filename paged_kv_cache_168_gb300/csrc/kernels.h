@@ -143,6 +143,84 @@ constexpr int kTcSpMaxSeqs = 160;
 cudaError_t launch_decode_tc_sp(const DecodeParams& p, int dtype, int group, int num_sms, cudaStream_t stream);
 cudaError_t launch_merge_sp(const DecodeParams& p, int dtype, int head_size, cudaStream_t stream);
 
+// Rotary positions on q and k, and the cache write (16-bit and 8-bit caches).
+constexpr int kMaxPairs = 64;     // rotary_dim / 2 at head_size 128
+struct RopeParams {
+  void* q_out;
+  int64_t q_out_stride;           // elements
+  const void* q;
+  int64_t q_stride;
+  int32_t num_q_heads;
+  uint8_t* cache;                 // this layer's pool
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_size;
+  const void* key;
+  int64_t key_stride;
+  const void* value;
+  int64_t value_stride;
+  const int64_t* slot_mapping;
+  const int32_t* positions;
+  int64_t axis_stride;
+  int32_t num_axes;
+  const float* cos_sin;
+  int32_t max_position;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t num_tokens;
+  uint32_t* dev_err;
+  uint8_t pair_axis[kMaxPairs];
+};
+cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, cudaStream_t stream);
+
+// Block tables, slot mapping and positions from request lengths.
+struct TablesParams {
+  int32_t* query_start_loc;
+  int32_t* context_lens;
+  int64_t* slot_mapping;
+  int32_t* positions;             // may be null
+  int32_t* block_tables;
+  int32_t bt_stride;
+  const int32_t* free_blocks;
+  const int32_t* num_free;
+  int32_t* num_free_out;
+  int32_t num_blocks;
+  int32_t block_size;
+  const int32_t* cached_lens;
+  const int32_t* new_lens;
+  int32_t num_seqs;
+  int32_t max_tokens;
+  int32_t ring_blocks;
+  uint32_t* dev_err;
+};
+cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream);
+
+// Attention of a chunk of new tokens per sequence over any cache.
+struct ExtendParams {
+  void* out;                      // [num_tokens, Hq, D] act dtype, contiguous
+  const void* q;
+  int64_t q_token_stride;         // elements
+  const uint8_t* cache;           // this layer's pool
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t num_q_heads;
+  int32_t group;                  // query heads per kv head, 1 .. 16
+  const int32_t* block_tables;
+  int32_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t max_query_len;
+  int32_t window;
+  int32_t ring_blocks;
+  float scale_log2;
+  uint32_t* dev_err;
+};
+cudaError_t launch_extend(const ExtendParams& p, int act_dtype, int head_size, bool i8, cudaStream_t stream);
+
 // Paged decode over an 8-bit cache on CUDA cores: head_size 128, group 1/2/4/8;
 // q / out in act_dtype.  Launches the decode kernel and the merge.
 cudaError_t launch_decode_i8(const DecodeParams& p, int act_dtype, int group, cudaStream_t stream);

@@ -316,6 +316,133 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "reshape_and_cache launch");
 }
 
+pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, const void* q, int64_t q_token_stride,
+                                    int32_t num_q_heads, void* kv_cache, const pa_cache_desc* desc, int32_t layer,
+                                    const void* key, int64_t key_token_stride, const void* value,
+                                    int64_t value_token_stride, const int64_t* slot_mapping, const int32_t* positions,
+                                    int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
+                                    int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
+                                    int32_t interleaved, int32_t num_tokens, uint32_t* dev_err, void* stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_q_heads < 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
+  if (rotary_dim < 16 || rotary_dim > desc->head_size || rotary_dim % 16)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d must be a multiple of 16 in [16, head_size %d]", rotary_dim,
+                desc->head_size);
+  if (num_axes < 1 || num_axes > 4) return fail(PA_ERR_INVALID_ARG, "num_axes %d not in [1, 4]", num_axes);
+  if (max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position %d", max_position);
+  if (pair_axis)
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      if (pair_axis[i] >= num_axes)
+        return fail(PA_ERR_INVALID_ARG, "pair_axis[%d] = %d with num_axes %d", i, pair_axis[i], num_axes);
+  if (num_tokens == 0) return PA_OK;
+  if (!kv_cache || !key || !value || !slot_mapping || !positions || !cos_sin)
+    return fail(PA_ERR_INVALID_ARG, "kv_cache, key, value, slot_mapping, positions and cos_sin must be non-NULL");
+  if (!aligned16(kv_cache) || !aligned16(key) || !aligned16(value))
+    return fail(PA_ERR_INVALID_ARG, "kv_cache, key and value must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7) || (reinterpret_cast<uintptr_t>(positions) & 3) ||
+      (reinterpret_cast<uintptr_t>(cos_sin) & 3))
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned, positions and cos_sin 4-byte aligned");
+  if (positions_axis_stride < 0 || (num_axes > 1 && positions_axis_stride > 0 && positions_axis_stride < num_tokens))
+    return fail(PA_ERR_INVALID_ARG, "positions_axis_stride %lld must be 0 or >= num_tokens",
+                (long long)positions_axis_stride);
+  const int64_t row = (int64_t)desc->num_kv_heads * desc->head_size;
+  if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 || value_token_stride % 8)
+    return fail(PA_ERR_INVALID_ARG, "token strides must be >= num_kv_heads*head_size and multiples of 8");
+  if (num_q_heads > 0) {
+    const int64_t qrow = (int64_t)num_q_heads * desc->head_size;
+    if (!q || !q_out || !aligned16(q) || !aligned16(q_out))
+      return fail(PA_ERR_INVALID_ARG, "q and q_out must be non-NULL and 16-byte aligned");
+    if (q_token_stride < qrow || q_out_token_stride < qrow || q_token_stride % 8 || q_out_token_stride % 8)
+      return fail(PA_ERR_INVALID_ARG, "q strides must be >= num_q_heads*head_size and multiples of 8");
+    // a row is read and written by one block, so rows may share memory only with themselves
+    const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
+    const uintptr_t na = (uintptr_t)((num_tokens - 1) * q_token_stride + qrow) * 2;
+    const uintptr_t nb = (uintptr_t)((num_tokens - 1) * q_out_token_stride + qrow) * 2;
+    if (!(a == b && q_token_stride == q_out_token_stride) && a < b + nb && b < a + na)
+      return fail(PA_ERR_INVALID_ARG, "q_out must be q itself (with the same stride) or not overlap it");
+  }
+  pkv::RopeParams p{};
+  p.q_out = q_out;
+  p.q_out_stride = q_out_token_stride;
+  p.q = q;
+  p.q_stride = q_token_stride;
+  p.num_q_heads = num_q_heads;
+  p.cache = static_cast<uint8_t*>(kv_cache) + layer * layer_stride(desc);
+  p.num_blocks = desc->num_blocks;
+  p.block_size = desc->block_size;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.head_size = desc->head_size;
+  p.key = key;
+  p.key_stride = key_token_stride;
+  p.value = value;
+  p.value_stride = value_token_stride;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.axis_stride = positions_axis_stride;
+  p.num_axes = num_axes;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.num_tokens = num_tokens;
+  p.dev_err = dev_err;
+  if (pair_axis) memcpy(p.pair_axis, pair_axis, rotary_dim / 2);
+  cudaError_t e = pkv::launch_rope_cache(p, act_dtype(desc), is_i8(desc), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope_reshape_and_cache launch");
+}
+
+pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64_t* slot_mapping, int32_t* positions,
+                          int32_t* block_tables, int32_t block_table_stride, const int32_t* free_blocks,
+                          const int32_t* num_free, int32_t* num_free_out, const pa_cache_desc* desc,
+                          const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens,
+                          int32_t ring_blocks, uint32_t* dev_err, void* stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
+  if (num_seqs > PA_BUILD_TABLES_MAX_SEQS)
+    return fail(PA_ERR_UNSUPPORTED, "num_seqs %d (supported: up to %d)", num_seqs, PA_BUILD_TABLES_MAX_SEQS);
+  if (max_tokens < 0) return fail(PA_ERR_INVALID_ARG, "max_tokens %d < 0", max_tokens);
+  if (!query_start_loc || !num_free || !num_free_out || !free_blocks)
+    return fail(PA_ERR_INVALID_ARG, "query_start_loc, free_blocks, num_free and num_free_out must be non-NULL");
+  if (num_seqs > 0 && (!context_lens || !block_tables || !cached_lens || !new_lens))
+    return fail(PA_ERR_INVALID_ARG, "context_lens, block_tables, cached_lens and new_lens must be non-NULL");
+  if (max_tokens > 0 && !slot_mapping) return fail(PA_ERR_INVALID_ARG, "slot_mapping must be non-NULL");
+  const void* ints[] = {query_start_loc, context_lens, positions, block_tables, free_blocks,
+                        num_free,        num_free_out, cached_lens, new_lens};
+  for (const void* a : ints)
+    if (reinterpret_cast<uintptr_t>(a) & 3) return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slot_mapping) & 7)
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
+  if (num_seqs > 0 && block_table_stride <= 0)
+    return fail(PA_ERR_INVALID_ARG, "block_table_stride %d", block_table_stride);
+  if (ring_blocks < 0 || (num_seqs > 0 && ring_blocks > block_table_stride))
+    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, block_table_stride %d]", ring_blocks,
+                block_table_stride);
+  pkv::TablesParams p{};
+  p.query_start_loc = query_start_loc;
+  p.context_lens = context_lens;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.block_tables = block_tables;
+  p.bt_stride = block_table_stride;
+  p.free_blocks = free_blocks;
+  p.num_free = num_free;
+  p.num_free_out = num_free_out;
+  p.num_blocks = desc->num_blocks;
+  p.block_size = desc->block_size;
+  p.cached_lens = cached_lens;
+  p.new_lens = new_lens;
+  p.num_seqs = num_seqs;
+  p.max_tokens = max_tokens;
+  p.ring_blocks = ring_blocks;
+  p.dev_err = dev_err;
+  cudaError_t e = pkv::launch_build_tables(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "build_tables launch");
+}
+
 int32_t pa_decode_partition_size(const pa_cache_desc* desc, int32_t num_seqs, int32_t max_context_len,
                                  int32_t partition_size) {
   if (partition_size > 0) return partition_size;
@@ -597,6 +724,78 @@ pa_status pa_prefill(void* out, const void* q, int64_t q_token_stride, const voi
   p.dev_err = dev_err;
   cudaError_t e = pkv::launch_prefill_tc(p, desc->dtype, desc->head_size, group, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "prefill launch");
+}
+
+size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                 int32_t num_q_heads, int32_t max_query_len) {
+  (void)desc; (void)num_seqs; (void)num_tokens; (void)num_q_heads; (void)max_query_len;
+  return 0;
+}
+
+pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc,
+                    int32_t layer, const int32_t* block_tables, int32_t block_table_stride,
+                    const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                    int32_t num_tokens, int32_t num_q_heads, int32_t max_query_len, float scale, int32_t window,
+                    int32_t ring_blocks, void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
+  if (num_seqs < 0 || num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_seqs %d not in [0, 65535]", num_seqs);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "max_query_len %d < 0", max_query_len);
+  if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d",
+                num_q_heads, desc->num_kv_heads);
+  const int group = num_q_heads / desc->num_kv_heads;
+  if (group > 16) return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d (supported: 1 to 16)", group);
+  if (desc->num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads > 65535");
+  if (window < 0) return fail(PA_ERR_INVALID_ARG, "window %d < 0", window);
+  if (!(scale > 0.f) || scale != scale) return fail(PA_ERR_INVALID_ARG, "scale must be a positive number");
+  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+  if (!out || !q || !kv_cache || !block_tables || !context_lens || !query_start_loc)
+    return fail(PA_ERR_INVALID_ARG,
+                "out, q, kv_cache, block_tables, context_lens and query_start_loc must be non-NULL");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache))
+    return fail(PA_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_tables) & 3) || (reinterpret_cast<uintptr_t>(context_lens) & 3) ||
+      (reinterpret_cast<uintptr_t>(query_start_loc) & 3))
+    return fail(PA_ERR_INVALID_ARG, "block_tables, context_lens and query_start_loc must be 4-byte aligned");
+  if (q_token_stride < (int64_t)num_q_heads * desc->head_size || q_token_stride % 8)
+    return fail(PA_ERR_INVALID_ARG, "q_token_stride must be >= num_q_heads*head_size and a multiple of 8");
+  if (block_table_stride <= 0) return fail(PA_ERR_INVALID_ARG, "block_table_stride %d", block_table_stride);
+  if (ring_blocks < 0 || ring_blocks > block_table_stride)
+    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, block_table_stride %d]", ring_blocks,
+                block_table_stride);
+  const size_t need = pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  if (need && (!workspace || !aligned16(workspace)))
+    return fail(PA_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
+
+  pkv::ExtendParams p{};
+  p.out = out;
+  p.q = q;
+  p.q_token_stride = q_token_stride;
+  p.cache = static_cast<const uint8_t*>(kv_cache) + layer * layer_stride(desc);
+  p.num_blocks = desc->num_blocks;
+  p.block_size = desc->block_size;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.group = group;
+  p.block_tables = block_tables;
+  p.bt_stride = block_table_stride;
+  p.context_lens = context_lens;
+  p.query_start_loc = query_start_loc;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.max_query_len = max_query_len;
+  p.window = window;
+  p.ring_blocks = ring_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.dev_err = dev_err;
+  cudaError_t e = pkv::launch_extend(p, act_dtype(desc), desc->head_size, is_i8(desc),
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "extend launch");
 }
 
 pa_status pa_copy_blocks(void* kv_cache, const pa_cache_desc* desc, const int64_t* pairs, int32_t num_pairs,

@@ -1,0 +1,252 @@
+"""pa_extend against attention in 64 bits, within bounds derived in step_ref.extend."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_168_gb300 as pkv
+import step_ref
+from gpu_helpers import dev_to_u16, ensure_built, u16_to_dev
+from paged_helpers import bits_to_f64
+from step_ref import Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_device):
+    ensure_built()
+
+
+def pool_to_dev(cache):
+    return torch.from_numpy(cache.pool.copy()).cuda() if cache.kv8 else u16_to_dev(cache.pool, cache.dtype)
+
+
+def run(case, scale, window=0, tables=None, ctx=None, qsl=None, max_q=None, err=None, out=None, q=None, ws=None, pool=None):
+    c = case.cache
+    desc = pkv.CacheDesc(c.nb, c.bs, c.Hkv, c.D, step_ref.torch_dtype(c.dtype), kv_int8=c.kv8)
+    q = u16_to_dev(case.q_bits, c.dtype) if q is None else q
+    out = torch.full((case.T, case.Hq, c.D), float("nan"), dtype=q.dtype, device="cuda") if out is None else out
+    max_q = int(case.q_lens.max()) if max_q is None else max_q
+    if ws is None:
+        # poisoned: results must not depend on what a workspace held
+        ws = torch.full((pkv.extend_workspace_bytes(desc, len(case.ctx), case.T, case.Hq, max_q),), 0xff, dtype=torch.uint8, device="cuda")
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    pkv.extend(out, q, pool_to_dev(c) if pool is None else pool, desc, dev(case.tables if tables is None else tables), dev(case.ctx if ctx is None else ctx),
+               dev(case.qsl if qsl is None else qsl), max_q, scale, ws, window=window, ring_blocks=case.ring, dev_err=err)
+    return out
+
+
+def assert_close(got, want, what=""):
+    out, tol = want
+    g = bits_to_f64(dev_to_u16(got), {torch.float16: "f16", torch.bfloat16: "bf16"}[got.dtype])[:len(out)]
+    bad = ~(np.abs(g - out) <= tol)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(bad, np.nan_to_num(np.abs(g - out) / tol, nan=np.inf), 0)), out.shape)
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.size} out of bound; worst at {i}: {g[i]!r}, {out[i]!r} +- {tol[i]!r}")
+
+
+def check(case, scale=None, window=0, rows=None, **kw):
+    scale = 1 / math.sqrt(case.cache.D) if scale is None else scale
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(case, scale, window, err=err, **kw)
+    assert pkv.read_device_errors(err) == 0
+    n = int(case.qsl[-1])
+    out, tol = case.expected(scale, window)
+    assert_close(got[:n], (out[:n], tol[:n]))
+    return got
+
+
+#        q_lens, ctx: single tokens, tile borders, no new tokens, long prefixes
+MIX = ([1, 5, 127, 128, 129, 17, 64, 0, 1, 40, 3], [1, 5, 127, 128, 129, 400, 320, 50, 1000, 40, 257])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D,kv8", [(64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 7, 8, 12, 16])
+def test_groups(G, D, kv8, dtype):
+    rng = np.random.default_rng(900 + G * 10 + D)
+    check(Chunk(rng, *MIX, Hq=2 * G, Hkv=2, D=D, bs=16, dtype=dtype, kv8=kv8))
+
+
+@pytest.mark.parametrize("bs", [1, 2, 4, 8, 16, 32])
+@pytest.mark.parametrize("D,kv8", [(64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("window,ring", [(0, 0), (50, 0), (1, 0), (200, -1), (40, 2)])
+def test_blocks_windows_and_rings(bs, D, kv8, window, ring):
+    """ring -1: just long enough for exact windows; 2: so short that early queries find nothing held."""
+    rng = np.random.default_rng(bs + window)
+    q_lens, ctx = [60, 1, 33, 0, 130], [60, 500, 333, 70, 400]
+    if ring < 0:
+        ring = -(-(window + 130 - 1) // bs) + 1
+    case = Chunk(rng, q_lens, ctx, Hq=6, Hkv=2, D=D, bs=bs, dtype="f16", kv8=kv8, ring=ring)
+    check(case, window=window)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("q_len", [1, 4, 31, 32, 33, 70])
+def test_few_rows_over_long_contexts(q_len, dtype, kv8):
+    """Work split over the context and merged."""
+    rng = np.random.default_rng(q_len)
+    check(Chunk(rng, [q_len, 1, q_len], [4000, 9001, q_len], Hq=8, Hkv=2, D=128, bs=16, dtype=dtype, kv8=kv8))
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_scores(dtype, kv8):
+    """Scores tens of units apart: the running maximum rises from tile to tile."""
+    rng = np.random.default_rng(3)
+    check(Chunk(rng, [300, 1], [700, 1500], Hq=4, Hkv=1, D=128, bs=16, dtype=dtype, kv8=kv8), scale=1.0)
+
+
+def test_tiny_scale_and_constant_keys():
+    rng = np.random.default_rng(4)
+    check(Chunk(rng, [9, 200], [400, 200], Hq=4, Hkv=2, D=64, bs=8, dtype="bf16"), scale=1e-6)
+    check(Chunk(rng, [9, 200], [400, 200], Hq=4, Hkv=2, D=128, bs=8, dtype="f16", scale_k=0.0))
+    check(Chunk(rng, [9, 200], [400, 200], Hq=4, Hkv=2, D=128, bs=8, dtype="f16", kv8=True, scale_k=0.0))
+
+
+def test_many_short_sequences():
+    rng = np.random.default_rng(5)
+    n = 700
+    q = rng.integers(0, 4, n)
+    check(Chunk(rng, q, q + rng.integers(0, 30, n), Hq=2, Hkv=1, D=64, bs=16, dtype="f16"))
+
+
+def test_rows_behind_the_last_sequence_stay():
+    rng = np.random.default_rng(6)
+    case = Chunk(rng, [5, 140], [50, 140], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16", extra_rows=70)
+    got = check(case)
+    assert bool(torch.isnan(got[145:]).all())
+
+
+def test_strided_queries():
+    rng = np.random.default_rng(7)
+    case = Chunk(rng, [5, 140], [50, 140], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16")
+    wide = torch.full((case.T, 4 * 128 + 264), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, :512] = u16_to_dev(case.q_bits, "bf16").view(case.T, -1)
+    check(case, q=wide[:, :512].unflatten(1, (4, 128)))
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_bad_sequences_are_zero_and_the_others_right(kv8):
+    rng = np.random.default_rng(8)
+    case = Chunk(rng, [10, 6, 3, 300, 1], [50, 4, 60, 300, 2000], Hq=4, Hkv=2, D=128, bs=16, dtype="f16", kv8=kv8)
+    ctx, tables = case.ctx.copy(), case.tables.copy()
+    tables[2, 3] = case.cache.nb + 7
+    tables[4, 90] = -1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(case, 0.1, tables=tables, ctx=ctx, err=err)
+    assert pkv.read_device_errors(err) == pkv.DEVERR_CONTEXT | pkv.DEVERR_BLOCK_ID
+    a = case.qsl
+    case.ctx[1] = 6                                                  # (the reference cannot state q_len > ctx)
+    tables[1, 0] = 0
+    case.q_lens[[1, 2, 4]] = 0
+    for s in (1, 2, 4):
+        assert bool((got[a[s]:a[s + 1]] == 0).all()), s
+    for s in (0, 3):
+        sub = step_ref.extend(case.q[a[s]:a[s + 1]], case.cache, case.tables[s:s + 1], case.ctx[s:s + 1], [0, a[s + 1] - a[s]], 0.1)
+        assert_close(got[a[s]:a[s + 1]], sub, f"sequence {s}")
+
+
+def test_bad_starts_and_long_chunks():
+    rng = np.random.default_rng(9)
+    case = Chunk(rng, [10, 6, 30], [50, 40, 60], Hq=4, Hkv=2, D=128, bs=16, dtype="f16")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(case, 0.1, max_q=10, err=err)                          # the third sequence is longer than that
+    assert pkv.read_device_errors(err) == pkv.DEVERR_CONTEXT
+    assert bool((got[16:46] == 0).all())
+    out, tol = case.expected(0.1)
+    assert_close(got[:16], (out[:16], tol[:16]))
+    for qsl in ([0, 10, 16, 47], [0, 10, 4, 46], [-1, 10, 16, 46], [0, 2**31 - 1, 16, 46]):
+        err.zero_()
+        out_t = torch.full((case.T, 4, 128), 7.0, dtype=torch.float16, device="cuda")
+        run(case, 0.1, qsl=np.asarray(qsl, np.int32), err=err, out=out_t)
+        assert pkv.read_device_errors(err) & pkv.DEVERR_CONTEXT
+    ctx = case.ctx.copy()
+    ctx[0] = case.tables.shape[1] * 16 + 1                           # past its row
+    err.zero_()
+    got = run(case, 0.1, ctx=ctx, err=err)
+    assert pkv.read_device_errors(err) == pkv.DEVERR_CONTEXT
+    assert bool((got[:10] == 0).all())
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_replays_and_streams(kv8):
+    """Two captured calls with a workspace each, replayed on two streams at once, and an eager call beside them."""
+    rng = np.random.default_rng(10)
+    cases = [Chunk(rng, [4, 200, 1], [3000, 300, 900], Hq=8, Hkv=2, D=128, bs=16, dtype="bf16", kv8=kv8) for _ in range(2)]
+    graphs, outs, streams, keep = [], [], [], []
+    for case in cases:
+        s = torch.cuda.Stream()
+        c = case.cache
+        desc = pkv.CacheDesc(c.nb, c.bs, c.Hkv, c.D, torch.bfloat16, kv_int8=c.kv8)
+        ws = torch.empty(pkv.extend_workspace_bytes(desc, 3, case.T, 8, 200), dtype=torch.uint8, device="cuda")
+        t = [u16_to_dev(case.q_bits, "bf16"), pool_to_dev(c)] + [torch.from_numpy(x).cuda() for x in (case.tables, case.ctx, case.qsl)]
+        out = torch.zeros((case.T, 8, 128), dtype=torch.bfloat16, device="cuda")
+        call = lambda: pkv.extend(out, t[0], t[1], desc, t[2], t[3], t[4], 200, 0.1, ws)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            call()
+            s.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                call()
+        graphs.append(g)
+        outs.append(out)
+        streams.append(s)
+        keep.append((t, ws))
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    eager = run(cases[0], 0.1)
+    torch.cuda.synchronize()
+    for case, o in zip(cases, outs):
+        assert_close(o, case.expected(0.1))
+    assert bool((eager == outs[0]).all())                            # results do not depend on timing
+
+
+def test_repeated_calls_give_the_same_bits():
+    rng = np.random.default_rng(11)
+    case = Chunk(rng, [3, 260, 17], [5000, 900, 4100], Hq=8, Hkv=2, D=128, bs=8, dtype="bf16")
+    first = run(case, 0.09)
+    for _ in range(20):
+        assert bool((run(case, 0.09) == first).all())
+
+
+def test_long_cache_offsets():
+    """Blocks whose byte offset passes 2^32 (a pool of 5 GB)."""
+    rng = np.random.default_rng(12)
+    case = Chunk(rng, [40], [100], Hq=16, Hkv=8, D=128, bs=16, dtype="bf16")
+    c = case.cache
+    nb = 5 * 2**30 // (8 * 2 * 16 * 128 * 2)
+    pool = torch.full((nb * 8 * 2 * 16 * 128,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    n = c.pool.size
+    pool[-n:] = u16_to_dev(c.pool, "bf16")
+    tables = np.where(case.tables >= 0, case.tables + nb - c.nb, -1).astype(np.int32)
+    desc = pkv.CacheDesc(nb, 16, 8, 128, torch.bfloat16)
+    q = u16_to_dev(case.q_bits, "bf16")
+    out = torch.empty_like(q)
+    ws = torch.empty(pkv.extend_workspace_bytes(desc, 1, 40, 16, 40), dtype=torch.uint8, device="cuda")
+    pkv.extend(out, q, pool, desc, *[torch.from_numpy(x).cuda() for x in (tables, case.ctx, case.qsl)], 40, 0.1, ws)
+    assert_close(out, case.expected(0.1))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_agrees_with_prefill(dtype):
+    """The same chunk through pa_prefill: both within their bounds of the same value."""
+    rng = np.random.default_rng(13)
+    case = Chunk(rng, [100, 300], [400, 300], Hq=8, Hkv=2, D=128, bs=16, dtype=dtype)
+    c = case.cache
+    got = check(case)
+    desc = pkv.CacheDesc(c.nb, 16, 2, 128, step_ref.torch_dtype(dtype))
+    q = u16_to_dev(case.q_bits, dtype)
+    out = torch.empty_like(q)
+    pkv.prefill(out, q, pool_to_dev(c), desc, *[torch.from_numpy(x).cuda() for x in (case.tables, case.ctx, case.qsl)], 300, 1 / math.sqrt(128))
+    _, tol = case.expected(1 / math.sqrt(128))
+    assert bool(((got.double() - out.double()).abs().cpu().numpy() <= 2 * tol).all())
