@@ -185,8 +185,11 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
  * each product and sum rounded to fp32 (never contracted), so results are a pure
  * function of the input bits; dims from rotary_dim on pass unchanged.  q's
  * results are rounded to q_out's type; k's are rounded to the cache's 16-bit
- * type, or quantised from fp32 (one rounding) for an 8-bit cache; v is stored
- * as pa_reshape_and_cache stores it.
+ * type; v is stored bit for bit.  An 8-bit cache stores codes and scales of k's
+ * fp32 results and of v, by the scheme above with its divisions taken as
+ * products: r = 127 * (1 / max|x|), codes round-half-even(x * r) clipped, scale
+ * max|x| * (1 / 127), each step rounded to fp32 (one division per vector; a scale
+ * may differ from pa_reshape_and_cache's of the same vector in its last bit).
  *   q_out, q     device [num_tokens, num_q_heads, head_size], 16-bit; token
  *                strides in elements (multiples of 8), 16-byte aligned.  q_out
  *                may be q itself (with the same stride), and may otherwise not
@@ -347,9 +350,10 @@ pa_status pa_prefill(void* out, const void* q, int64_t q_token_stride, const voi
                      const int32_t* query_start_loc, int32_t num_seqs, int32_t num_q_heads,
                      int32_t max_query_len, float scale, uint32_t* dev_err, void* stream);
 
-/* Workspace bytes pa_extend needs for these shapes (0: nothing to do, or desc
- * NULL; SIZE_MAX where it does not fit in half the address space).  Follows the
- * SM count of the current device. */
+/* Workspace bytes pa_extend needs for these shapes (0: nothing to do, desc NULL,
+ * or shapes it refuses).  Follows the SM count of the current device, not the
+ * context lengths: a list of work items, and room for the partial results of the
+ * parts that contexts are split into where there are few rows. */
 size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
                                  int32_t num_q_heads, int32_t max_query_len);
 

@@ -1,0 +1,1334 @@
+// extend_tc.cu -- attention of a chunk of new tokens per sequence over any paged
+// cache, on the tensor cores (tcgen05 + TMEM).
+//
+// Sequence s owns the packed query tokens query_start_loc[s] .. [s + 1]; query j
+// of its q_len sits at position ctx - q_len + j and attends the positions from
+// its window's (or ring's) start up to its own.  Three launches:
+//
+//   plan_kernel    one CTA: from the lengths, the list of work items in the
+//                  workspace.  An item is up to two query tiles of 128 rows (row
+//                  = position * group + head) of one sequence, over its context
+//                  or a part of it; contexts are cut only where the whole call
+//                  has too few items for the SMs.
+//   extend_kernel  one persistent CTA per SM draws (item, kv head) pairs from a
+//                  counter, a sequence's heads and tiles next to each other so
+//                  that its K and V are read from L2 while they are hot.
+//   finish_kernel  merges parts by log-sum-exp, zeroes the rows of items with a
+//                  bad block id, and recomputes on CUDA cores the items whose
+//                  partly masked tiles hold a non-finite V (0 * NaN = NaN in the
+//                  second product, so those tiles cannot go through it).
+//
+// extend_kernel, per 128-token KV tile c and query tile t (0 or 1):
+//     S_t  = Q_t K_c^T     (M = 128 rows, N = 128 tokens, K = D)  -> TMEM (fp32)
+//     O_t += P_t V_c       (M = 128 rows, N = D, K = 128 tokens)  -> TMEM (fp32)
+// P_t is written by the softmax threads over the S_t columns they have read and
+// is the A operand straight from TMEM.  The two query tiles share every K and V
+// tile and take turns: while one's softmax runs, the other's products do.  An
+// item with at most 128 rows lets both share its one query tile instead: tile t
+// takes every other KV tile, and the two results are merged in the epilogue.
+// Roles (one warp each but for the softmax):
+//   warps 0-3, 4-7  softmax of query tile 0 and 1: thread = TMEM lane = row.
+//                   Base-2 online softmax; the running maximum is raised only
+//                   when a tile's exceeds it by more than 8 (a factor 256), and
+//                   only then is O rescaled in TMEM.  Statistics are fp32;
+//                   weights are rounded to the cache's 16-bit type (fp16 for an
+//                   8-bit cache), the sum takes them unrounded.
+//   warp 8          one lane issues the products, whichever is ready: per query
+//                   tile QK(c), PV(c), QK(c'), ... strictly in turn.
+//   warp 9          draws items, publishes them in a ring, and copies K tiles
+//                   (8-token groups, one bulk copy each) into a 2-stage ring.
+//   warp 10         copies V tiles into a 2-stage ring.
+//   warp 11         gathers Q rows into the swizzled K-major operand.
+//   warps 12-15     (caches whose chunks are not operands: 8-bit codes, blocks
+//                   of fewer than 8 tokens) fill the K and V stages in place of
+//                   the copies: codes become exact 16-bit integers, and the
+//                   scales are applied in the softmax: K's to the scores, V's
+//                   by adding log2(scale) to the exponent, so that weights stay
+//                   at most 2^8 whatever the scales are.
+// Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, and the CTA drains its
+// own copies and products before releasing TMEM.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kRows = 128;                 // MMA M: rows of one query tile
+constexpr int kKv = 128;                   // tokens of a KV tile
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kRescaleThreshold = 8.f;   // base-2 units
+constexpr int kMinPartTiles = 2;           // shortest part of a split context
+constexpr int kPartsPerSm = 4;             // parts wanted per SM where contexts are split
+
+// Flags of a query tile and kv head.
+constexpr uint32_t kBadBlock = 1, kNonFinite = 2, kTimedOut = 4;
+
+// ------------------------------------------------------------------ workspace
+struct Header {
+  int32_t next;                            // (item, head) pairs handed out
+  int32_t total;                           // items * kv heads
+  int32_t num_split;                       // query tiles whose contexts are split
+  int32_t any_flag;
+};
+
+// One work item, for every kv head.
+struct __align__(16) Item {
+  int32_t seq, base, count;                // its sequence, the sequence's first item and number of items
+  int32_t row0, pos0, npos;                // first token row, position and number of positions
+  int32_t tile0, ntiles;                   // KV tiles [tile0, tile0 + ntiles) of this part
+  int32_t first;                           // first position any of its queries attends
+  int32_t held;                            // first position a ring still holds
+  int32_t part_row;                        // first row of its partial results for kv head 0, or -1
+  int32_t head_rows;                       // partial rows between kv heads
+  int32_t flag;                            // the item whose flags it raises: its query tile's first
+  int32_t parts;                           // of its query tile's context
+  int32_t pad[2];
+};
+
+// What the planner decides for a sequence.
+struct __align__(16) SeqPlan {
+  int32_t base, parts, part_row, pad;
+};
+
+struct Space {
+  Header* head;
+  SeqPlan* seqs;                           // [num_seqs]
+  Item* items;                             // [max_items]
+  int32_t* splits;                         // [max_items] first items of the split query tiles
+  uint32_t* flags;                         // [max_items * kv heads]
+  float* o;                                // [max_rows][D]
+  float* ml;                               // [max_rows][2]
+  int32_t max_items;
+  int32_t tile_rows;                       // most rows an item can have
+  int64_t max_rows;
+};
+
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace of these shapes, laid out from `base`; its size in *bytes.
+Space lay_out(uint8_t* base, int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len,
+              int head_size, int sms, size_t* bytes) {
+  const int pair = 2 * (kRows / group);                       // positions of two query tiles
+  const int64_t parts = (int64_t)kPartsPerSm * sms;
+  Space w{};
+  w.tile_rows = (max_query_len < pair ? max_query_len : pair) * group;
+  w.max_items = (int32_t)((int64_t)num_tokens / pair + num_seqs + parts);
+  w.max_rows = 2 * parts * w.tile_rows;                       // see plan_kernel
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at = align_up(at + n);
+    return base + here;
+  };
+  w.head = reinterpret_cast<Header*>(take(sizeof(Header)));
+  w.seqs = reinterpret_cast<SeqPlan*>(take((size_t)num_seqs * sizeof(SeqPlan)));
+  w.items = reinterpret_cast<Item*>(take((size_t)w.max_items * sizeof(Item)));
+  w.splits = reinterpret_cast<int32_t*>(take((size_t)w.max_items * 4));
+  w.flags = reinterpret_cast<uint32_t*>(take((size_t)w.max_items * num_kv_heads * 4));
+  w.o = reinterpret_cast<float*>(take((size_t)w.max_rows * head_size * 4));
+  w.ml = reinterpret_cast<float*>(take((size_t)w.max_rows * 8));
+  *bytes = at;
+  return w;
+}
+
+// ------------------------------------------------------------------ planner
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanCache = 8192;           // sequences whose first items are searched in shared memory
+
+struct Seq {
+  int start, q_len, ctx, held;
+  bool listed, zero;                       // has items; only zero rows
+};
+
+__device__ __forceinline__ Seq read_seq(const ExtendParams& p, int s, uint32_t& err) {
+  Seq q;
+  q.start = p.query_start_loc[s];
+  const int64_t end = p.query_start_loc[s + 1];
+  q.ctx = p.context_lens[s];
+  q.held = 0;
+  q.zero = false;
+  q.listed = q.start >= 0 && end > q.start && end <= p.num_tokens;
+  q.q_len = q.listed ? (int)(end - q.start) : 0;
+  if (!q.listed) {
+    if (end != q.start || q.start < 0 || end > p.num_tokens) err |= PA_DEVERR_CONTEXT;
+    return q;
+  }
+  if (q.q_len > p.max_query_len || q.q_len > q.ctx ||
+      (p.ring_blocks == 0 && (int64_t)q.ctx > (int64_t)p.bt_stride * p.block_size)) {
+    q.zero = true;
+    err |= PA_DEVERR_CONTEXT;
+    return q;
+  }
+  if (p.ring_blocks > 0) {
+    const int64_t h = ((int64_t)((q.ctx - 1) / p.block_size) - p.ring_blocks + 1) * p.block_size;
+    q.held = h > 0 ? (int)h : 0;
+  }
+  return q;
+}
+
+// First position that the query at position pos attends.
+__device__ __forceinline__ int attend_from(int pos, int window, int held) {
+  const int w = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
+  return max(w, held);
+}
+
+// KV tiles [tile0, tile0 + n) that the queries at pos0 .. pos0 + npos - 1 attend.
+__device__ __forceinline__ int tile_range(const ExtendParams& p, const Seq& q, int pos0, int npos, int& tile0) {
+  const int first = attend_from(pos0, p.window, q.held), last = pos0 + npos - 1;
+  tile0 = first / kKv;
+  return q.zero || first > last ? 0 : last / kKv - tile0 + 1;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Exclusive prefix of v over the CTA, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t in = warp_scan(v, lane);
+  __syncthreads();
+  if (lane == 31) tmp[warp] = in;
+  __syncthreads();
+  const int64_t w = warp_scan(tmp[lane], lane);
+  total = __shfl_sync(kFull, w, 31);
+  const int64_t before = __shfl_sync(kFull, w, (warp + 31) & 31);
+  return in - v + (warp ? before : 0);
+}
+
+// One CTA; thread t owns the sequences [t * per, (t + 1) * per) and then takes
+// items in turn.  The part length follows the whole call's work: `longest` KV
+// tiles, so that all heads' work makes kPartsPerSm parts per SM; a sequence is
+// cut into equal parts when its last (longest) query tile exceeds that.  Cut
+// tiles and parts are then at most kPartsPerSm * sms each (a cut tile has more
+// than `longest` tiles of the work), so their partial rows fit 2 * kPartsPerSm *
+// sms tiles; sequences whose rows would not (the estimate of the work is
+// rounded) stay whole.
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_constant__ ExtendParams p,
+                                                              const __grid_constant__ Space ws, int sms) {
+  __shared__ int64_t tmp[32];
+  __shared__ int32_t bases[kPlanCache];
+  __shared__ uint32_t errs;
+  __shared__ int nsplit;
+  const int S = p.num_seqs, G = p.group, pair = 2 * (kRows / G), tid = threadIdx.x, hkv = p.num_kv_heads;
+  if (tid == 0) errs = nsplit = 0;
+  const int per = (S + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  // KV tiles of a sequence's last query tile
+  auto last_range = [&](const Seq& q, int nt) {
+    int t0;
+    const int q0 = (nt - 1) * pair;
+    return tile_range(p, q, q.ctx - q.q_len + q0, q.q_len - q0, t0);
+  };
+
+  uint32_t err = 0, none = 0;
+  int64_t work = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = read_seq(p, s, err);
+    if (!q.listed || q.zero) continue;
+    const int nt = (q.q_len + pair - 1) / pair;
+    int t0;
+    const int n0 = tile_range(p, q, q.ctx - q.q_len, min(pair, q.q_len), t0);
+    work += ((int64_t)n0 + last_range(q, nt)) * nt / 2;
+  }
+  int64_t total;
+  block_scan(work, tmp, total);
+  const int64_t want = (int64_t)kPartsPerSm * sms;
+  const int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
+
+  // parts wanted and their partial rows
+  auto parts_of = [&](const Seq& q, int nt, int64_t& rows) {
+    const int64_t parts = q.zero ? 1 : max((int64_t)1, (last_range(q, nt) + longest - 1) / longest);
+    rows = parts > 1 ? parts * nt * hkv * (int64_t)(min(pair, q.q_len) * G) : 0;
+    return parts;
+  };
+  int64_t rows = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = read_seq(p, s, none);
+    int64_t r = 0;
+    if (q.listed) parts_of(q, (q.q_len + pair - 1) / pair, r);
+    rows += r;
+  }
+  int64_t row = block_scan(rows, tmp, total);
+  int64_t items = 0;
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = read_seq(p, s, none);
+    SeqPlan sp{0, 0, -1, 0};
+    if (q.listed) {
+      const int nt = (q.q_len + pair - 1) / pair;
+      int64_t r;
+      int64_t parts = parts_of(q, nt, r);
+      if (parts > 1 && row + r > ws.max_rows) parts = 1;
+      if (parts > 1) sp.part_row = (int)row;
+      row += r;
+      sp.parts = (int)parts;
+      items += parts * nt;
+    }
+    ws.seqs[s] = sp;
+  }
+  int64_t n_items;
+  int64_t item = block_scan(items, tmp, n_items);
+  for (int s = s0; s < s1; ++s) {
+    const Seq q = read_seq(p, s, none);
+    const int base = (int)min(item, (int64_t)ws.max_items);
+    ws.seqs[s].base = base;
+    if (s < kPlanCache) bases[s] = base;
+    if (q.listed) item += (int64_t)ws.seqs[s].parts * ((q.q_len + pair - 1) / pair);
+  }
+  if (n_items > ws.max_items) err |= PA_DEVERR_CONTEXT;       // sequences overlap: the last ones are left out
+  if (err) atomicOr(&errs, err);
+  __syncthreads();
+
+  const int listed = (int)min(n_items, (int64_t)ws.max_items);
+  for (int i = tid; i < listed; i += kPlanThreads) {
+    int lo = 0, hi = S;                                       // the last sequence with base <= i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((mid < kPlanCache ? bases[mid] : ws.seqs[mid].base) <= i) lo = mid; else hi = mid;
+    }
+    const SeqPlan sp = ws.seqs[lo];
+    const Seq q = read_seq(p, lo, none);
+    const int nt = (q.q_len + pair - 1) / pair;
+    const int k = (i - sp.base) / sp.parts, part = (i - sp.base) % sp.parts;
+    const int q0 = (nt - 1 - k) * pair;                       // the longest contexts first
+    Item it;
+    it.seq = lo;
+    it.base = sp.base;
+    it.count = min(nt * sp.parts, listed - sp.base);
+    it.row0 = q.start + q0;
+    it.pos0 = q.ctx - q.q_len + q0;
+    it.npos = min(pair, q.q_len - q0);
+    int t0;
+    const int n = tile_range(p, q, it.pos0, it.npos, t0);
+    const int plen = (n + sp.parts - 1) / sp.parts;
+    it.tile0 = t0 + part * plen;
+    it.ntiles = max(0, min(plen, n - part * plen));
+    it.first = attend_from(it.pos0, p.window, q.held);
+    it.held = q.held;
+    const int tile_rows = min(pair, q.q_len) * G;
+    it.part_row = sp.part_row < 0 ? -1 : sp.part_row + (k * hkv * sp.parts + part) * tile_rows;
+    it.head_rows = sp.parts * tile_rows;
+    it.flag = sp.base + k * sp.parts;
+    it.parts = sp.parts;
+    it.pad[0] = tile_rows;
+    it.pad[1] = 0;
+    ws.items[i] = it;
+    if (sp.part_row >= 0 && part == 0) ws.splits[atomicAdd(&nsplit, 1)] = i;
+  }
+  for (int i = tid; i < listed * hkv; i += kPlanThreads) ws.flags[i] = 0;
+  __syncthreads();
+  if (tid == 0) {
+    ws.head->next = 0;
+    ws.head->total = listed * hkv;
+    ws.head->num_split = nsplit;
+    ws.head->any_flag = 0;
+    if (errs) report(p.dev_err, errs);
+  }
+}
+
+// ------------------------------------------------------------------ the attention kernel
+// How the K and V stages are filled.
+enum Fill { kBulk, kGather, kCodes };
+
+constexpr int kRing = 4;                   // items between the drawing warp and the others
+// Tiles' scales (8-bit caches).  They have no barrier of their own for reuse: when
+// tile c's are written, tiles up to c - 2 have gone through their first product,
+// and a softmax warpgroup can then be at most six tiles behind (items of one
+// tile each, all for query tile 0: their epilogues meet).
+constexpr int kScaleRing = 8;
+
+// An item as the roles see it.
+struct Work {
+  int kvh;                                 // -1: no more
+  int seq, row0, pos0, npos;
+  int tile0, n[2];                         // first KV tile; KV tiles of query tile t (alt: its every other one)
+  int alt;                                 // both take query tile 0's rows
+  int first, held, kv_end;                 // attended positions lie in [first, kv_end)
+  int edge_lo, edge_hi;                    // KV tiles (counted from tile0) below / from which on some pair is masked
+  int c0;                                  // ring number of the first KV tile
+  int qload[2];                            // load number of Q tile t, if it has one
+  int part_row, flag;
+};
+
+template <int D, Fill F>
+struct Cfg {
+  static constexpr int kTileBytes = kKv * D * 2;              // K (or V) of one KV tile
+  static constexpr int kGroupBytes = 8 * D * 2;               // 8 tokens of it
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr bool kConvert = F != kBulk;
+  static constexpr int kThreads = kConvert ? 512 : 384;
+  // registers: the softmax warpgroups hold a row's 128 scores (sums equal the launch's)
+  static constexpr int kRegsSoftmax = kConvert ? 184 : 208;
+  static constexpr int kRegsRest = kConvert ? 56 : 88;
+  static constexpr int kRegsConvert = 88;
+  static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
+                2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
+  static constexpr size_t kSmem = 1024 + 2 * kQBytes + 4 * kTileBytes;
+};
+
+struct Shared {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2];
+  // PV of tile number n of query tile t completes pv_done[t][n & 1]: a waiter is never two phases behind
+  uint64_t pv_done[2][2];
+  uint64_t item_full[kRing], item_empty[kRing];
+  uint64_t xbar;                           // the two softmax warpgroups (items that share a query tile)
+  uint64_t sc_full[kScaleRing];
+  uint64_t mma_drain;
+  Work work[kRing];
+  volatile int bad[kRing];                 // a block id out of range was met
+  float red[2][kRows][2];                  // the other warpgroup's (maximum, sum)
+  uint32_t tmem_base;
+  volatile int abort_flag;
+};
+struct __align__(16) Scales {
+  float k[kScaleRing][kKv], lv[kScaleRing][kKv], iv[kScaleRing][kKv];
+};
+
+// Bound of every wait: about a second, far above any wait of a healthy call.
+constexpr uint32_t kPolls = 1u << 20;
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 32 TMEM lanes x 64 columns; the wait is part of the statement.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;             // 0: the destination is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Offset of the 16-byte piece (8 dims) of row r in a 128B-swizzled K-major operand of 128 rows.
+__device__ __forceinline__ uint32_t q_offset(int r, int piece) {
+  return (uint32_t)((piece >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
+}
+// The same piece of token r in a K or V stage (8-token groups, a group's 64-dim atoms together).
+template <int D>
+__device__ __forceinline__ uint32_t kv_offset(int r, int piece) {
+  return (uint32_t)((r >> 3) * (8 * D * 2) + (piece >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
+}
+
+// Whether any 16-bit value of w (two of them) is an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ bool non_finite2(uint32_t w) {
+  constexpr uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// Table entry and validity of the block that holds position pos.
+__device__ __forceinline__ int block_of(const ExtendParams& p, const int32_t* row, int blk) {
+  return row[p.ring_blocks > 0 ? blk % p.ring_blocks : blk];
+}
+
+template <typename T, int D, Fill F>
+__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
+                                                                       const __grid_constant__ Space ws) {
+  using C = Cfg<D, F>;
+  constexpr bool kI8 = F == kCodes;
+  constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
+  using PT = typename std::conditional<kI8, __half, T>::type;      // type of the weights and of V's operand
+  __shared__ Shared sh;
+  __shared__ typename std::conditional<kI8, Scales, int>::type scales;
+  extern __shared__ __align__(1024) uint8_t dyn_raw[];
+  const uint32_t raw_s = smem_u32(dyn_raw);
+  uint8_t* qbuf = dyn_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
+  uint8_t* kbuf = qbuf + 2 * C::kQBytes;
+  uint8_t* vbuf = kbuf + 2 * C::kTileBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.group, ptile = kRows / G;                        // positions of one query tile
+  const int bs = p.block_size;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.k_full[i], C::kConvert ? 4 : 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], C::kConvert ? 4 : 1);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.pv_done[i][0], 1);
+      mbar_init(&sh.pv_done[i][1], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.item_full[i], 1);
+      // 8 softmax warps, the issuer once per query tile, the Q warp, and the V warp or 4 converter warps
+      mbar_init(&sh.item_empty[i], C::kConvert ? 15 : 12);
+    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sh.sc_full[i], 4);
+    mbar_init(&sh.xbar, 8);
+    mbar_init(&sh.mma_drain, 1);
+    sh.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tc::tmem_alloc(&sh.tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;                              // S_t at 128 t, O_t at 256 + 128 t
+
+  // a role gave up: tell the others
+  auto give_up = [&]() {
+    report(p.dev_err, PA_DEVERR_TIMEOUT);
+    sh.abort_flag = 1;
+  };
+  // waits of whole warps; false (in every lane): it ran out, or another role gave up
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(kFull, bar_wait(bar, parity) && !sh.abort_flag);
+  };
+  // the next item of the ring
+  auto next_item = [&](int i, Work& w) -> bool {
+    if (!wait(&sh.item_full[i % kRing], (i / kRing) & 1)) return false;
+    w = sh.work[i % kRing];
+    return true;
+  };
+  auto done_item = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.item_empty[i % kRing]);
+  };
+  // KV tiles of an item
+  auto tiles_of = [](const Work& w) { return w.alt ? w.n[0] + w.n[1] : max(w.n[0], w.n[1]); };
+
+  if (warp >= 8 && warp < 12) {
+    set_regs_dec<C::kRegsRest>();
+    if (warp == 9) {
+      // ================================================================= items, and K copies
+      int32_t w_next = 0;
+      int total = ws.head->total;
+      if (lane == 0) w_next = atomicAdd(&ws.head->next, 1);
+      w_next = __shfl_sync(kFull, w_next, 0);
+      int c = 0, q0 = 0, q1 = 0;
+      bool ok = true;
+      int issued = 0;
+      for (int i = 0; ok; ++i) {
+        Work w;
+        w.kvh = -1;
+        if (w_next < total) {
+          // heads outside, items inside: a sequence's (head, tile) pairs are numbered head by head
+          const Item a = ws.items[w_next / p.num_kv_heads];
+          const int local = w_next - a.base * p.num_kv_heads;
+          const int h = local / a.count, k = a.base + local % a.count;
+          const Item it = ws.items[k];
+          w.kvh = h;
+          w.seq = it.seq;
+          w.row0 = it.row0;
+          w.pos0 = it.pos0;
+          w.npos = it.npos;
+          w.tile0 = it.tile0;
+          w.alt = it.npos <= ptile;
+          w.first = it.first;
+          w.held = it.held;
+          w.kv_end = it.pos0 + it.npos;
+          if (w.alt) {
+            w.n[0] = (it.ntiles + 1) / 2;
+            w.n[1] = it.ntiles / 2;
+          } else {
+            // tile 0's last position may need one KV tile less
+            w.n[0] = max(0, min(it.ntiles, (it.pos0 + ptile - 1) / kKv + 1 - it.tile0));
+            w.n[1] = it.ntiles;
+          }
+          const int last_first = attend_from(w.kv_end - 1, p.window, it.held);
+          w.edge_lo = (last_first + kKv - 1) / kKv - it.tile0;
+          w.edge_hi = (it.pos0 + 1) / kKv - it.tile0;
+          w.c0 = c;
+          w.qload[0] = q0;
+          w.qload[1] = q1;
+          if (w.n[0] > 0) ++q0;
+          if (!w.alt && w.n[1] > 0) ++q1;
+          w.part_row = it.part_row < 0 ? -1 : it.part_row + h * it.head_rows;
+          w.flag = it.flag * p.num_kv_heads + h;
+        }
+        const int slot = i % kRing;
+        if (i >= kRing && !wait(&sh.item_empty[slot], ((i / kRing) - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          sh.work[slot] = w;
+          sh.bad[slot] = 0;
+          mbar_arrive(&sh.item_full[slot]);
+        }
+        __syncwarp();
+        if (w.kvh < 0) break;
+        if (lane == 0) w_next = atomicAdd(&ws.head->next, 1);
+        const int n = tiles_of(w);
+        if constexpr (!C::kConvert) {
+          const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+          const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;   // blocks [fb, nblk) are read
+          for (int j = 0; j < n; ++j, ++c) {
+            const int st = c & 1;
+            // lane l < 16 copies the tile's 8-token group l
+            const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
+            const bool take = lane < 16 && blk >= fb && blk < nblk;
+            int id = take ? block_of(p, row, blk) : 0;
+            if (take && (unsigned)id >= (unsigned)p.num_blocks) {
+              id = 0;
+              sh.bad[slot] = 1;
+            }
+            if (c >= 2 && !wait(&sh.k_empty[st], ((c >> 1) - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            const unsigned m = __ballot_sync(kFull, take);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st], (uint32_t)__popc(m) * C::kGroupBytes);
+            __syncwarp();
+            if (take) {
+              const int g = (lane & 15) & (bs / 8 - 1);             // group within the block
+              bulk_g2s(kbuf + st * C::kTileBytes + (lane & 15) * C::kGroupBytes,
+                       p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes),
+                       C::kGroupBytes, &sh.k_full[st]);
+            }
+            issued = c + 1;
+          }
+        } else {
+          c += n;
+        }
+        w_next = __shfl_sync(kFull, w_next, 0);
+      }
+      if (!ok && lane == 0) give_up();
+      // never leave copies in flight, whether or not another role gave up
+      if (lane == 0)
+        for (int j = max(0, issued - 2); j < issued; ++j)
+          if (!bar_wait(&sh.k_full[j & 1], (j >> 1) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+      __syncwarp();
+    } else if (warp == 10) {
+      // ================================================================= V copies
+      if constexpr (!C::kConvert) {
+        int c = 0, issued = 0;
+        bool ok = true;
+        for (int i = 0; ok; ++i) {
+          Work w;
+          if (!next_item(i, w)) {
+            ok = false;
+            break;
+          }
+          if (w.kvh < 0) break;
+          const int n = tiles_of(w);
+          const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+          const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;
+          for (int j = 0; j < n; ++j, ++c) {
+            const int st = c & 1;
+            const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
+            const bool take = lane < 16 && blk >= fb && blk < nblk;
+            int id = take ? block_of(p, row, blk) : 0;
+            if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;      // reported by the K copies
+            if (c >= 2 && !wait(&sh.v_empty[st], ((c >> 1) - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            const unsigned m = __ballot_sync(kFull, take);
+            if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[st], (uint32_t)__popc(m) * C::kGroupBytes);
+            __syncwarp();
+            if (take) {
+              const int g = (lane & 15) & (bs / 8 - 1);
+              bulk_g2s(vbuf + st * C::kTileBytes + (lane & 15) * C::kGroupBytes,
+                       p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes) +
+                           C::kGroupBytes,
+                       C::kGroupBytes, &sh.v_full[st]);
+            }
+            issued = c + 1;
+          }
+          if (ok) done_item(i);
+        }
+        if (!ok && lane == 0) give_up();
+        if (lane == 0)
+          for (int j = max(0, issued - 2); j < issued; ++j)
+            if (!bar_wait(&sh.v_full[j & 1], (j >> 1) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+        __syncwarp();
+      }
+    } else if (warp == 11) {
+      // ================================================================= Q rows
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        Work w;
+        if (!next_item(i, w)) {
+          ok = false;
+          break;
+        }
+        if (w.kvh < 0) break;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (w.n[t] == 0 || (w.alt && t == 1)) continue;
+          const int load = w.qload[t];
+          if (load > 0 && !wait(&sh.q_empty[t], (load - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          const int rows = (w.alt ? w.npos : min(ptile, w.npos - t * ptile)) * G;
+          const T* q = static_cast<const T*>(p.q) + (int64_t)(w.row0 + t * ptile) * p.q_token_stride +
+                       (int64_t)w.kvh * G * D;
+          const uint32_t dst = smem_u32(qbuf + t * C::kQBytes);
+          for (int k = lane; k < kRows * (D / 8); k += 32) {
+            const int r = k / (D / 8), piece = k % (D / 8);
+            const bool take = r < rows;
+            const int rr = take ? r : 0;
+            cp_async16(dst + q_offset(r, piece), q + (int64_t)(rr / G) * p.q_token_stride + (rr % G) * D + piece * 8, take);
+          }
+          cp_async_wait();
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full[t]);
+        }
+        if (ok) done_item(i);
+      }
+      if (!ok && lane == 0) give_up();
+      __syncwarp();
+    } else if (lane == 0) {
+      // ================================================================= warp 8: products
+      const uint32_t id_qk = tc::idesc_f16(kRows, kKv, kBF16, false, false);
+      const uint32_t id_pv = tc::idesc_f16(kRows, D, kBF16 && !kI8, false, true);
+      const uint32_t qa = smem_u32(qbuf), ka = smem_u32(kbuf), va = smem_u32(vbuf);
+      // Barriers that either query tile may look at are observed in order, each phase once.
+      int k_seen = 0, v_seen = 0, q_seen[2] = {0, 0};
+      auto k_ready = [&](int c) {
+        while (k_seen <= c && mbar_test_wait(&sh.k_full[k_seen & 1], (k_seen >> 1) & 1)) ++k_seen;
+        return c < k_seen;
+      };
+      auto v_ready = [&](int c) {
+        while (v_seen <= c && mbar_test_wait(&sh.v_full[v_seen & 1], (v_seen >> 1) & 1)) ++v_seen;
+        return c < v_seen;
+      };
+      auto q_ready = [&](int t, int load) {
+        while (q_seen[t] <= load && mbar_test_wait(&sh.q_full[t], q_seen[t] & 1)) ++q_seen[t];
+        return load < q_seen[t];
+      };
+      int k_use[2] = {0, 0}, v_use[2] = {0, 0}, q_alt = 0;           // users so far of a stage / of a shared Q
+      int item[2] = {0, 0}, j[2] = {0, 0}, num[2] = {0, 0};          // item, tile in it, tiles in all
+      int state[2] = {0, 0};                                         // 0: needs an item, 1: QK next, 2: PV next, 3: end
+      Work w[2];
+      uint32_t idle = 0;
+      bool ok = true;
+      while (state[0] != 3 || state[1] != 3) {
+        bool moved = false;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (state[t] == 0) {
+            const int slot = item[t] % kRing;
+            if (!mbar_test_wait(&sh.item_full[slot], (item[t] / kRing) & 1)) continue;
+            w[t] = sh.work[slot];
+            j[t] = 0;
+            moved = true;
+            if (w[t].kvh < 0) {
+              state[t] = 3;
+            } else if (w[t].n[t] == 0) {
+              mbar_arrive(&sh.item_empty[slot]);
+              ++item[t];
+            } else {
+              state[t] = 1;
+            }
+          }
+          const Work& x = w[t];
+          const int jt = x.alt ? 2 * j[t] + t : j[t];                // KV tile of the item
+          const int c = x.c0 + jt, st = c & 1;
+          const int users = x.alt ? 1 : (jt < x.n[0]) + (jt < x.n[1]);
+          if (state[t] == 1) {
+            const int qt = x.alt ? 0 : t;
+            const bool edge = jt < x.edge_lo || jt >= x.edge_hi;     // its softmax looks at V
+            if (k_ready(c) && q_ready(qt, x.qload[qt]) && (!edge || v_ready(c))) {
+              tc::fence_after_sync();
+              const uint64_t qd = tc::smem_desc(qa + qt * C::kQBytes, 16, 1024, tc::kSwizzle128B);
+              const uint64_t kd = tc::smem_desc(ka + st * C::kTileBytes, 16, C::kGroupBytes, tc::kSwizzle128B);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                            kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
+              tc::commit(&sh.s_full[t]);
+              if (++k_use[st] == users) {
+                k_use[st] = 0;
+                tc::commit(&sh.k_empty[st]);
+              }
+              if (j[t] == x.n[t] - 1) {
+                if (!x.alt) {
+                  tc::commit(&sh.q_empty[t]);
+                } else if (++q_alt == (x.n[0] > 0) + (x.n[1] > 0)) {
+                  q_alt = 0;
+                  tc::commit(&sh.q_empty[0]);
+                }
+              }
+              state[t] = 2;
+              moved = true;
+            }
+          } else if (state[t] == 2) {
+            if (mbar_test_wait(&sh.p_full[t], num[t] & 1) && v_ready(c)) {
+              tc::fence_after_sync();
+              const uint64_t vd = tc::smem_desc(va + st * C::kTileBytes, 1024, C::kGroupBytes, tc::kSwizzle128B);
+              const int valid = min(kKv, x.kv_end - (x.tile0 + jt) * kKv), steps = (valid + 15) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < kKv / 16; ++kk)
+                if (kk < steps)
+                  tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + kk * 8,
+                                 vd + (uint64_t)((kk * 2 * C::kGroupBytes) >> 4), id_pv, (j[t] > 0 || kk > 0) ? 1u : 0u);
+              tc::commit(&sh.pv_done[t][num[t] & 1]);
+              if (++v_use[st] == users) {
+                v_use[st] = 0;
+                tc::commit(&sh.v_empty[st]);
+              }
+              ++num[t];
+              state[t] = 1;
+              if (++j[t] == x.n[t]) {
+                mbar_arrive(&sh.item_empty[item[t] % kRing]);
+                ++item[t];
+                state[t] = 0;
+              }
+              moved = true;
+            }
+          }
+        }
+        if (moved) {
+          idle = 0;
+        } else if (++idle > 8 * kPolls || sh.abort_flag) {
+          ok = false;
+          break;
+        }
+      }
+      if (!ok) give_up();
+      // every product this lane issued completes before TMEM can be freed
+      tc::commit(&sh.mma_drain);
+      if (!bar_wait(&sh.mma_drain, 0)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    // =================================================================== converters (warps 12-15)
+    if constexpr (C::kConvert) {
+      set_regs_dec<C::kRegsConvert>();
+      const int ct = threadIdx.x - 384;                              // 0 .. 127
+      int c = 0;
+      bool ok = true;
+      constexpr int kPer = F == kCodes ? 8 : D / 8;                  // 16-byte source pieces of one vector
+      constexpr int kLoads = kKv * kPer / 128;                       // of one thread, K or V
+      for (int i = 0; ok; ++i) {
+        Work w;
+        if (!next_item(i, w)) {
+          ok = false;
+          break;
+        }
+        if (w.kvh < 0) break;
+        const int n = tiles_of(w);
+        const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+        const Layout L{bs, D, p.num_kv_heads};
+        const I8Layout L8{bs, p.num_kv_heads};
+        for (int j = 0; j < n && ok; ++j, ++c) {
+          const int st = c & 1, t0 = (w.tile0 + j) * kKv;
+          // token u of the tile is read if its block holds an attended position
+          auto find = [&](int u, int& b) -> bool {
+            const int pos = t0 + u;
+            b = 0;
+            if (pos / bs < w.first / bs || pos >= w.kv_end) return false;
+            b = block_of(p, row, pos / bs);
+            if ((unsigned)b < (unsigned)p.num_blocks) return true;
+            sh.bad[i % kRing] = 1;
+            return false;
+          };
+          uint4 x[2][kLoads];
+          float sc[2] = {0.f, 0.f};
+          auto load = [&](int part) {
+#pragma unroll
+            for (int e = 0; e < kLoads; ++e) {
+              const int u = (ct + e * 128) / kPer, piece = (ct + e * 128) % kPer;
+              int b;
+              const bool have = find(u, b);
+              const int t = (t0 + u) & (bs - 1);
+              x[part][e] = !have ? make_uint4(0, 0, 0, 0)
+                           : kI8 ? *reinterpret_cast<const uint4*>(p.cache + L8.code(b, w.kvh, part, t, piece * 16))
+                                 : *reinterpret_cast<const uint4*>(p.cache + 2 * L.offset(b, w.kvh, part, t, piece * 8));
+            }
+          };
+          load(0);
+          if constexpr (kI8) {
+            load(1);                                                 // (16-bit rows: after K's have gone, registers)
+            int b;
+            if (find(ct, b)) {
+              const int t = (t0 + ct) & (bs - 1);
+              sc[0] = *reinterpret_cast<const float*>(p.cache + L8.scale(b, w.kvh, 0, t));
+              sc[1] = *reinterpret_cast<const float*>(p.cache + L8.scale(b, w.kvh, 1, t));
+            }
+          }
+          if (c >= 2 && !wait(&sh.k_empty[st], ((c >> 1) - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          if constexpr (kI8) {
+            const int r = c % kScaleRing;
+            // zero vectors have scale 0 and zero codes: any positive scale stands for them
+            const float sv = sc[1] == 0.f ? 1.f : fmaxf(sc[1], 1.2e-38f);
+            scales.k[r][ct] = sc[0] * p.scale_log2;
+            scales.lv[r][ct] = log2f(sv);
+            scales.iv[r][ct] = 1.f / sv;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.sc_full[r]);
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            if (part == 1) {
+              if constexpr (!kI8) load(1);
+              if (c >= 2 && !wait(&sh.v_empty[st], ((c >> 1) - 1) & 1)) {
+                ok = false;
+                break;
+              }
+            }
+            uint8_t* dst = (part ? vbuf : kbuf) + st * C::kTileBytes;
+#pragma unroll
+            for (int e = 0; e < kLoads; ++e) {
+              const int u = (ct + e * 128) / kPer, piece = (ct + e * 128) % kPer;
+              if constexpr (!kI8) {
+                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, piece)) = x[part][e];
+              } else {
+                const uint32_t in[4] = {x[part][e].x, x[part][e].y, x[part][e].z, x[part][e].w};
+                uint32_t y[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (part == 1 || !kBF16) {
+                    // fp16 1024 + (code + 128), less 1152: exact
+                    const uint32_t b = in[k] ^ 0x80808080u;
+                    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));
+                    const uint32_t a0 = __byte_perm(b, 0x64646464u, 0x4140), a1 = __byte_perm(b, 0x64646464u, 0x4342);
+                    const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), off);
+                    const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), off);
+                    y[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
+                    y[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                  } else {
+                    // bf16 128 + (low 7 bits), less 128 (code >= 0) or 256: exact
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                      const uint32_t b = __byte_perm(in[k], 0, hf ? 0x4342 : 0x4140);
+                      const uint32_t a = 0x43004300u | (b & 0x007f007fu), s = 0x43004300u | (b & 0x00800080u);
+                      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                                       *reinterpret_cast<const __nv_bfloat162*>(&s));
+                      y[2 * k + hf] = *reinterpret_cast<const uint32_t*>(&r);
+                    }
+                  }
+                }
+                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(part ? &sh.v_full[st] : &sh.k_full[st]);
+          }
+        }
+        if (ok) done_item(i);
+      }
+      if (!ok && lane == 0) give_up();
+      __syncwarp();
+    }
+  } else {
+    // =================================================================== softmax warpgroups (warps 0-7)
+    set_regs_inc<C::kRegsSoftmax>();
+    const int t = warp >> 2;                                         // query tile
+    const int row = threadIdx.x & 127;                               // TMEM lane
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + quarter + t * kKv, o_addr = tmem + quarter + 256 + t * 128;
+    const int ipos = row / G, head = row - ipos * G;
+    int num = 0, nx = 0;                                             // KV tiles, exchanges so far
+    bool ok = true;
+    // an exchange of the two warpgroups: everything before it is seen after it
+    auto meet = [&]() {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.xbar);
+      if (!wait(&sh.xbar, nx & 1)) ok = false;
+      ++nx;
+      tc::fence_after_sync();
+    };
+    for (int i = 0; ok; ++i) {
+      Work w;
+      if (!next_item(i, w)) {
+        ok = false;
+        break;
+      }
+      if (w.kvh < 0) break;
+      const int my0 = w.alt ? 0 : t * ptile;                         // my tile's first position in the item
+      const int npos = w.alt ? w.npos : min(ptile, w.npos - my0);
+      const bool row_ok = ipos < npos;
+      const int pos = w.pos0 + my0 + ipos;
+      const int from = attend_from(pos, p.window, w.held);
+      const int n = w.n[t];
+      float m = -INFINITY, l = 0.f;
+      bool odd_v = false;                                            // a non-finite V in a partly masked tile
+      for (int j = 0; j < n; ++j, ++num) {
+        const int jt = w.alt ? 2 * j + t : j, c = w.c0 + jt, st = c & 1;
+        const int t0 = (w.tile0 + jt) * kKv;
+        if (!wait(&sh.s_full[t], num & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        float x[kKv];
+        tmem_ld64(s_addr, x);
+        tmem_ld64(s_addr + 64, x + 64);
+        const bool edge = jt < w.edge_lo || jt >= w.edge_hi;
+        if constexpr (kI8) {
+          if (!wait(&sh.sc_full[c % kScaleRing], (c / kScaleRing) & 1)) {
+            ok = false;
+            break;
+          }
+          const float4* sk = reinterpret_cast<const float4*>(scales.k[c % kScaleRing]);
+          const float4* lv = reinterpret_cast<const float4*>(scales.lv[c % kScaleRing]);
+#pragma unroll
+          for (int e = 0; e < kKv / 4; ++e) {
+            const float4 a = sk[e], b = lv[e];
+            x[4 * e] = fmaf(x[4 * e], a.x, b.x);
+            x[4 * e + 1] = fmaf(x[4 * e + 1], a.y, b.y);
+            x[4 * e + 2] = fmaf(x[4 * e + 2], a.z, b.z);
+            x[4 * e + 3] = fmaf(x[4 * e + 3], a.w, b.w);
+          }
+        }
+        if (edge) {
+          const int lo = from - t0, hi = row_ok ? pos + 1 - t0 : 0;  // attended columns [lo, hi)
+#pragma unroll
+          for (int e = 0; e < kKv; ++e) x[e] = (e >= lo && e < hi) ? x[e] : -INFINITY;
+          if constexpr (!kI8) {
+            // thread = token here: V rows that no block filled become zero, and
+            // non-finite ones are noted (V has landed: the issuer waited for it)
+            if (!wait(&sh.v_full[st], (c >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            uint8_t* v = vbuf + st * C::kTileBytes;
+            if (t0 + row >= w.kv_end || t0 + row < w.first) {
+#pragma unroll
+              for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
+            } else {
+#pragma unroll
+              for (int e = 0; e < D / 8; ++e) {
+                const uint4 y = *reinterpret_cast<const uint4*>(v + kv_offset<D>(row, e));
+                odd_v |= non_finite2<T>(y.x) || non_finite2<T>(y.y) || non_finite2<T>(y.z) || non_finite2<T>(y.w);
+              }
+            }
+            tc::fence_proxy_async_smem();
+          }
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kKv; ++e) mt = fmaxf(mt, x[e]);
+        const float unit = kI8 ? 1.f : p.scale_log2;                 // x is in base-2 units already (8-bit)
+        mt *= unit;
+        const float m_new = fmaxf(m, mt);
+        const bool need = m != -INFINITY && m_new > m + kRescaleThreshold;
+        if (m == -INFINITY) m = m_new;
+        if (__any_sync(kFull, need)) {
+          // O holds exactly the tiles before this one once the last PV has completed
+          if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const float alpha = need ? exp2f(m - m_new) : 1.f;
+          if (need) {
+            l *= alpha;
+            m = m_new;
+          }
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            float o[16];
+            tc::tmem_ld16(o_addr + e * 16, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= alpha;
+            tc::tmem_st16(o_addr + e * 16, o);
+          }
+        }
+        // weights 2^(x - m), the sum of the unrounded ones in fp32
+        const float nm = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+        for (int e = 0; e < kKv / 32; ++e) {
+          uint32_t y[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int col = e * 32 + 2 * k;
+            const float a = ex2_approx(kI8 ? x[col] + nm : fmaf(x[col], unit, nm));
+            const float b = ex2_approx(kI8 ? x[col + 1] + nm : fmaf(x[col + 1], unit, nm));
+            if constexpr (kI8) {
+              const float2 iv = *reinterpret_cast<const float2*>(&scales.iv[c % kScaleRing][col]);
+              l = fmaf(a, iv.x, l);
+              l = fmaf(b, iv.y, l);
+            } else {
+              l += a + b;
+            }
+            y[k] = Elem<PT>::pack2(a, b);
+          }
+          tc::tmem_st16u(s_addr + e * 16, y);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+      if (ok && n > 0 && !wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
+      if (!ok) break;
+      tc::fence_after_sync();
+      if (lane == 0 && sh.bad[i % kRing]) {
+        atomicOr(&ws.flags[w.flag], kBadBlock);
+        atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
+        report(p.dev_err, PA_DEVERR_BLOCK_ID);
+      }
+      if (!kI8 && __any_sync(kFull, odd_v) && lane == 0) {
+        atomicOr(&ws.flags[w.flag], kNonFinite);
+        atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
+      }
+      // ---- results: columns [c0, c0 + nc) of my row
+      float f[2] = {1.f, 1.f};
+      int col0 = 0, ncol = D;
+      bool have0 = n > 0, have1 = false;
+      uint32_t o0 = o_addr, o1 = o_addr;
+      if (w.alt) {
+        sh.red[t][row][0] = m;
+        sh.red[t][row][1] = l;
+        meet();
+        if (!ok) break;
+        const float mo = sh.red[t ^ 1][row][0], lo = sh.red[t ^ 1][row][1];
+        const float mm = fmaxf(m, mo);
+        const float fm = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mm);
+        const float fo = mo == -INFINITY ? (lo == 0.f ? 0.f : 1.f) : exp2f(mo - mm);
+        // in the order of the tiles, whichever half this is
+        l = t == 0 ? l * fm + lo * fo : lo * fo + l * fm;
+        m = mm;
+        f[0] = t == 0 ? fm : fo;
+        f[1] = t == 0 ? fo : fm;
+        have0 = w.n[0] > 0;
+        have1 = w.n[1] > 0;
+        o0 = tmem + quarter + 256;
+        o1 = o0 + 128;
+        ncol = D / 2;
+        col0 = t * ncol;
+      }
+      const bool part = w.part_row >= 0;
+      const float scale = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      const int rr = (my0 + ipos) * G + head;                        // row within the item
+      T* orow = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0 + ipos) * p.num_q_heads + w.kvh * G + head) * D;
+      float* prow = ws.o + (int64_t)(w.part_row + rr) * D;
+      for (int e = col0; e < col0 + ncol; e += 16) {
+        float o[16];
+        if (have0) {
+          tc::tmem_ld16(o0 + e, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = 0.f;
+        }
+        if (w.alt) {
+          float b[16];
+          if (have1) {
+            tc::tmem_ld16(o1 + e, b);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) b[k] = 0.f;
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = o[k] * f[0] + b[k] * f[1];
+        }
+        if (row_ok && !part) {
+          uint32_t y[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = Elem<T>::pack2(o[2 * k] * scale, o[2 * k + 1] * scale);
+          *reinterpret_cast<uint4*>(orow + e) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(orow + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+        } else if (row_ok) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<float4*>(prow + e + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      if (row_ok && part && col0 == 0)
+        *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(w.part_row + rr)) = make_float2(m, l);
+      // both halves have read both accumulators before either is overwritten
+      if (w.alt) meet(); else tc::fence_before_sync();
+      if (!ok) break;
+      done_item(i);
+    }
+    if (!ok && lane == 0) give_up();
+    __syncwarp();
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ finish
+// Attention of one row on CUDA cores by one warp, for tiles that the tensor
+// cores cannot take: positions [from, pos], fp32 online softmax.
+template <typename T, int D>
+__device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh, int r, int lane) {
+  constexpr int kDims = D / 32;
+  const int bs = p.block_size, j = r / p.group, h = kvh * p.group + r % p.group;
+  const int pos = it.pos0 + j, from = attend_from(pos, p.window, it.held);
+  const T* q = static_cast<const T*>(p.q) + (int64_t)(it.row0 + j) * p.q_token_stride + (int64_t)h * D + lane * kDims;
+  float x[kDims], o[kDims], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) {
+    x[d] = (float)q[d] * p.scale_log2;
+    o[d] = 0.f;
+  }
+  const Layout L{bs, D, p.num_kv_heads};
+  const int32_t* row = p.block_tables + (int64_t)it.seq * p.bt_stride;
+  for (int t = from; t <= pos; ++t) {
+    const int b = block_of(p, row, t / bs);
+    if ((unsigned)b >= (unsigned)p.num_blocks) continue;             // its tile is flagged as bad
+    const T* cache = reinterpret_cast<const T*>(p.cache);
+    float z = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) z = fmaf(x[d], (float)cache[L.offset(b, kvh, 0, t & (bs - 1), lane * kDims + d)], z);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(kFull, z, i);
+    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = exp2f(z - mn);
+    l = l * a + e;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) o[d] = o[d] * a + e * (float)cache[L.offset(b, kvh, 1, t & (bs - 1), lane * kDims + d)];
+    m = mn;
+  }
+  T* out = static_cast<T*>(p.out) + ((int64_t)(it.row0 + j) * p.num_q_heads + h) * D + lane * kDims;
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) out[d] = Elem<T>::from_float(l == 0.f ? 0.f : o[d] / l);
+}
+
+// Warps take rows of split query tiles: out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, in the order of the
+// parts; then, where any flag was raised, the rows of flagged items.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ExtendParams p,
+                                                     const __grid_constant__ Space ws) {
+  constexpr int kDims = D / 32;
+  const int lane = threadIdx.x & 31, hkv = p.num_kv_heads, G = p.group;
+  const int64_t w0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5, nw = ((int64_t)gridDim.x * blockDim.x) >> 5;
+  const Header hd = *ws.head;
+  for (int64_t u = w0; u < (int64_t)hd.num_split * hkv * ws.tile_rows; u += nw) {
+    const int r = (int)(u % ws.tile_rows), h = (int)(u / ws.tile_rows % hkv);
+    const int item = ws.splits[u / ws.tile_rows / hkv];
+    const Item& it = ws.items[item];
+    if (r >= it.npos * G || (hd.any_flag && ws.flags[item * hkv + h])) continue;
+    const int64_t first = it.part_row + (int64_t)h * it.head_rows + r;
+    const int rows = it.pad[0];                                      // partial rows of one part
+    float M = -INFINITY;
+    for (int k = lane; k < it.parts; k += 32) M = fmaxf(M, ws.ml[2 * (first + (int64_t)k * rows)]);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, i));
+    float l = 0.f, o[kDims] = {};
+    for (int k = 0; k < it.parts; ++k) {
+      const int64_t at = first + (int64_t)k * rows;
+      const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
+      if (ml.y == 0.f) continue;                                     // nothing attended in this part
+      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);     // (-inf with a sum: NaN scores)
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[d] = fmaf(ws.o[at * D + lane * kDims + d], f, o[d]);
+    }
+    T* out = static_cast<T*>(p.out) +
+             ((int64_t)(it.row0 + r / G) * p.num_q_heads + h * G + r % G) * D + lane * kDims;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) out[d] = Elem<T>::from_float(l == 0.f ? 0.f : o[d] / l);
+  }
+  if (!hd.any_flag) return;
+  for (int u = 0; u < hd.total; ++u) {
+    const int item = u / hkv, h = u % hkv;
+    const uint32_t f = ws.flags[u];
+    if (!f) continue;
+    const Item& it = ws.items[item];
+    for (int64_t r = w0; r < it.npos * G; r += nw) {
+      if (f & (kBadBlock | kTimedOut)) {
+        T* out = static_cast<T*>(p.out) +
+                 ((int64_t)(it.row0 + r / G) * p.num_q_heads + h * G + r % G) * D + lane * kDims;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) out[d] = Elem<T>::from_float(0.f);
+      } else {
+        row_on_cuda_cores<T, D>(p, it, h, (int)r, lane);
+      }
+    }
+  }
+}
+
+template <typename T, int D, Fill F>
+cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
+  using C = Cfg<D, F>;
+  cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F>>(C::kSmem);
+  if (e != cudaSuccess) return e;
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, ws, sms);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  extend_kernel<T, D, F><<<sms, C::kThreads, C::kSmem, stream>>>(p, ws);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  finish_kernel<T, D><<<2 * sms, 256, 0, stream>>>(p, ws);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const ExtendParams& p, const Space& ws, int sms, int head_size, bool i8, cudaStream_t stream) {
+  if (i8) return launch_fill<T, 128, kCodes>(p, ws, sms, stream);
+  const bool bulk = p.block_size >= 8;                               // whole 8-token groups
+  if (head_size == 128)
+    return bulk ? launch_fill<T, 128, kBulk>(p, ws, sms, stream) : launch_fill<T, 128, kGather>(p, ws, sms, stream);
+  return bulk ? launch_fill<T, 64, kBulk>(p, ws, sms, stream) : launch_fill<T, 64, kGather>(p, ws, sms, stream);
+}
+
+}  // namespace
+
+size_t extend_workspace(int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len, int head_size,
+                        int sms) {
+  size_t bytes;
+  lay_out(nullptr, num_seqs, num_tokens, num_kv_heads, group, max_query_len, head_size, sms, &bytes);
+  return bytes;
+}
+
+cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                          cudaStream_t stream) {
+  size_t bytes;
+  const Space ws = lay_out(static_cast<uint8_t*>(workspace), p.num_seqs, p.num_tokens, p.num_kv_heads, p.group,
+                           p.max_query_len, head_size, sms, &bytes);
+  return act_dtype == PA_F16 ? launch_typed<__half>(p, ws, sms, head_size, i8, stream)
+                             : launch_typed<__nv_bfloat16>(p, ws, sms, head_size, i8, stream);
+}
+
+}  // namespace pkv

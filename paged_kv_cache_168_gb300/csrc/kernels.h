@@ -219,7 +219,11 @@ struct ExtendParams {
   float scale_log2;
   uint32_t* dev_err;
 };
-cudaError_t launch_extend(const ExtendParams& p, int act_dtype, int head_size, bool i8, cudaStream_t stream);
+// Workspace bytes, and the launches (planner, attention, finish) on a device of `sms` SMs.
+size_t extend_workspace(int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len, int head_size,
+                        int sms);
+cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                          cudaStream_t stream);
 
 // Paged decode over an 8-bit cache on CUDA cores: head_size 128, group 1/2/4/8;
 // q / out in act_dtype.  Launches the decode kernel and the merge.

@@ -728,8 +728,12 @@ pa_status pa_prefill(void* out, const void* q, int64_t q_token_stride, const voi
 
 size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
                                  int32_t num_q_heads, int32_t max_query_len) {
-  (void)desc; (void)num_seqs; (void)num_tokens; (void)num_q_heads; (void)max_query_len;
-  return 0;
+  if (!desc || num_seqs <= 0 || num_tokens <= 0 || max_query_len <= 0 || num_q_heads <= 0) return 0;
+  if (check_desc(desc) != PA_OK || num_q_heads % desc->num_kv_heads) return 0;
+  const int group = num_q_heads / desc->num_kv_heads;
+  if (group > 16) return 0;
+  return pkv::extend_workspace(num_seqs, num_tokens, desc->num_kv_heads, group, max_query_len, desc->head_size,
+                               device_sm_count());
 }
 
 pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc,
@@ -793,7 +797,7 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
   p.ring_blocks = ring_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.dev_err = dev_err;
-  cudaError_t e = pkv::launch_extend(p, act_dtype(desc), desc->head_size, is_i8(desc),
+  cudaError_t e = pkv::launch_extend(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size, is_i8(desc),
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "extend launch");
 }

@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const __grid_const
         uint32_t code[4] = {0, 0, 0, 0};
         float scale = 0.f;
         if (amax > 0.f) {
-          const float inv = __fdiv_rn(127.f, amax);
+          const float inv = __fmul_rn(127.f, __fdiv_rn(1.f, amax));
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             code[e >> 2] |= (uint32_t)(min(127, max(-127, __float2int_rn(__fmul_rn(x[e], inv)))) & 0xff) << (8 * (e & 3));
-          scale = __fdiv_rn(amax, 127.f);
+          scale = __fmul_rn(amax, 1.f / 127.f);
         }
         *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, a * 8)) = make_uint2(code[0], code[1]);
         *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, b * 8)) = make_uint2(code[2], code[3]);

@@ -143,12 +143,14 @@ def rotate64(x, angles, rot, pairs):
 
 
 def quantise(x):
-    """Codes and scale [.., 1] of float32 vectors [.., 128]: symmetric, binary32 throughout."""
+    """Codes and scale [.., 1] of float32 vectors [.., 128]: symmetric, binary32 throughout, products with
+    reciprocals (127 * (1 / amax), amax * (1 / 127))."""
+    one, n = np.float32(1), np.float32(127)
     amax = np.abs(x).max(-1, keepdims=True).astype(np.float32)
     with np.errstate(divide="ignore", invalid="ignore"):
-        inv = np.where(amax > 0, np.float32(127) / amax, np.float32(0)).astype(np.float32)
+        inv = np.where(amax > 0, n * (one / amax), np.float32(0)).astype(np.float32)
         codes = np.clip(np.rint((x * inv).astype(np.float32)), -127, 127).astype(np.int8)
-        return codes, (amax / np.float32(127)).astype(np.float32)
+        return codes, (amax * (one / n)).astype(np.float32)
 
 
 def store8(cache, codes, scales, part, slots):

@@ -1,0 +1,375 @@
+"""A CPU model of the chunk-attention kernel's barrier protocol (csrc/extend_tc.cu): its roles as coroutines
+under random schedules, barriers with the hardware's parity semantics, and tags in place of data.  It checks
+that every role finds the data it expects, that no buffer is overwritten while it is read, and that no
+schedule deadlocks.  Mistakes planted in the model are caught."""
+import random
+
+import pytest
+
+RING, SCALES = 4, 8
+
+
+class Bar:
+    def __init__(self, count):
+        self.count, self.pending, self.phase = count, count, 0
+
+    def arrive(self):
+        self.pending -= 1
+        assert self.pending >= 0
+        if self.pending == 0:
+            self.pending, self.phase = self.count, self.phase + 1
+
+    def test(self, parity):                    # the phase of that parity has completed, as far as the parity tells
+        return (self.phase & 1) != parity
+
+
+class Model:
+    """items: (alt, n0, n1, edge tiles) as the drawing warp publishes them."""
+
+    def __init__(self, items, convert, plant=""):
+        self.items, self.convert, self.plant = items, convert, plant
+        fill = 4 if convert else 1
+        self.k_full, self.v_full = [[Bar(fill) for _ in range(2)] for _ in range(2)]
+        self.k_empty, self.v_empty, self.q_full, self.q_empty, self.s_full, self.p_full = \
+            [[Bar(4 if i == 5 else 1) for _ in range(2)] for i in range(6)]
+        self.pv_done = [[Bar(1) for _ in range(2)] for _ in range(2)]
+        self.item_full = [Bar(1) for _ in range(RING)]
+        self.item_empty = [Bar(15 if convert else 12) for _ in range(RING)]
+        self.sc_full = [Bar(4) for _ in range(SCALES)]
+        self.xbar = Bar(8)
+        self.work = [None] * RING
+        self.k, self.v, self.q = [None] * 2, [None] * 2, [None] * 2
+        self.sc = [[None] * 4 for _ in range(SCALES)]
+        self.s = [[None] * 4 for _ in range(2)]          # S / P per query tile and warp
+        self.o = [None] * 2
+        self.reading = {}                                # (kind, index) -> readers
+        self.tensor = []                                 # issued products and commits, executed in order
+        self.out = []
+
+    def wait(self, bar, parity):
+        while not bar.test(parity):
+            yield
+
+    def tiles(self, w):
+        return w["n"][0] + w["n"][1] if w["alt"] else max(w["n"])
+
+    def draw(self):
+        c = q0 = q1 = 0
+        for i, it in enumerate(self.items + [None]):
+            slot = i % RING
+            if i >= RING:
+                yield from self.wait(self.item_empty[slot], (i // RING - 1) & 1)
+            if it is None:
+                self.work[slot] = None
+                self.item_full[slot].arrive()
+                return
+            alt, n0, n1, edges = it
+            w = dict(i=i, alt=alt, n=(n0, n1), c0=c, qload=(q0, q1), edges=edges)
+            q0 += n0 > 0
+            q1 += (not alt) and n1 > 0
+            self.work[slot] = w
+            self.item_full[slot].arrive()
+            n = self.tiles(w)
+            if self.convert:
+                c += n
+                continue
+            for j in range(n):
+                st = c & 1
+                if c >= 2:
+                    yield from self.wait(self.k_empty[st], (c // 2 - 1) & 1)
+                yield
+                self.fill(self.k, "k", st, c)
+                self.k_full[st].arrive()
+                c += 1
+
+    def fill(self, buf, kind, st, c):
+        assert not self.reading.get((kind, st)), f"{kind} stage {st} overwritten while read"
+        buf[st] = c
+
+    def consume(self, arrive=1):
+        """Items in order, for one warp (generator of work; the caller sends done)."""
+
+    def next_item(self, i):
+        yield from self.wait(self.item_full[i % RING], (i // RING) & 1)
+        return self.work[i % RING]
+
+    def v_copies(self):
+        c = i = 0
+        while True:
+            w = yield from self.next_item(i)
+            if w is None:
+                return
+            assert w["i"] == i
+            for j in range(self.tiles(w)):
+                st = c & 1
+                if c >= 2:
+                    yield from self.wait(self.v_empty[st], (c // 2 - 1) & 1)
+                yield
+                self.fill(self.v, "v", st, c)
+                self.v_full[st].arrive()
+                c += 1
+            self.item_empty[i % RING].arrive()
+            i += 1
+
+    def converter(self, me):
+        c = i = 0
+        while True:
+            w = yield from self.next_item(i)
+            if w is None:
+                return
+            for j in range(self.tiles(w)):
+                st = c & 1
+                if c >= 2:
+                    yield from self.wait(self.k_empty[st], (c // 2 - 1) & 1)
+                yield
+                n = 4 if self.plant == "short scale ring" else SCALES
+                assert not self.reading.get(("sc", c % n)), "scales overwritten while read"
+                self.sc[c % n][me] = c
+                self.sc_full[c % n].arrive()
+                yield
+                self.fill(self.k, "k", st, c)
+                self.k_full[st].arrive()
+                if c >= 2:
+                    yield from self.wait(self.v_empty[st], (c // 2 - 1) & 1)
+                yield
+                self.fill(self.v, "v", st, c)
+                self.v_full[st].arrive()
+                c += 1
+            self.item_empty[i % RING].arrive()
+            i += 1
+
+    def q_rows(self):
+        i = 0
+        while True:
+            w = yield from self.next_item(i)
+            if w is None:
+                return
+            for t in range(2):
+                if w["n"][t] == 0 or (w["alt"] and t == 1):
+                    continue
+                load = w["qload"][t]
+                if load > 0:
+                    yield from self.wait(self.q_empty[t], (load - 1) & 1)
+                yield
+                self.fill(self.q, "q", t, i)
+                self.q_full[t].arrive()
+            self.item_empty[i % RING].arrive()
+            i += 1
+
+    def products(self):
+        seen = {"k": 0, "v": 0, "q0": 0, "q1": 0}
+
+        def ready(key, bars, x, per):
+            if self.plant == "unordered":
+                return bars[x % per if per > 1 else 0].test((x // per) & 1)
+            while seen[key] <= x and bars[seen[key] % per].test((seen[key] // per) & 1):
+                seen[key] += 1
+            return x < seen[key]
+
+        use = {"k": [0, 0], "v": [0, 0]}
+        q_alt = 0
+        state, item, j, num, w = [0, 0], [0, 0], [0, 0], [0, 0], [None, None]
+        while state != [3, 3]:
+            yield
+            for t in range(2):
+                if state[t] == 0:
+                    slot = item[t] % RING
+                    if not self.item_full[slot].test((item[t] // RING) & 1):
+                        continue
+                    w[t], j[t] = self.work[slot], 0
+                    if w[t] is None:
+                        state[t] = 3
+                    else:
+                        assert w[t]["i"] == item[t]
+                        if w[t]["n"][t] == 0:
+                            self.item_empty[slot].arrive()
+                            item[t] += 1
+                        else:
+                            state[t] = 1
+                    continue
+                if state[t] == 3:
+                    continue
+                x = w[t]
+                jt = 2 * j[t] + t if x["alt"] else j[t]
+                c = x["c0"] + jt
+                st = c & 1
+                users = 1 if x["alt"] else (jt < x["n"][0]) + (jt < x["n"][1])
+                if state[t] == 1:
+                    qt = 0 if x["alt"] else t
+                    edge = jt in x["edges"]
+                    if ready("k", self.k_full, c, 2) and ready("q%d" % qt, [self.q_full[qt]], x["qload"][qt], 1) and \
+                            (not edge or ready("v", self.v_full, c, 2)):
+                        self.tensor.append(("qk", t, qt, st, c, item[t]))
+                        self.tensor.append(("commit", self.s_full[t]))
+                        use["k"][st] += 1
+                        if use["k"][st] == users:
+                            use["k"][st] = 0
+                            self.tensor.append(("commit", self.k_empty[st]))
+                        if j[t] == x["n"][t] - 1:
+                            if not x["alt"]:
+                                self.tensor.append(("commit", self.q_empty[t]))
+                            else:
+                                q_alt += 1
+                                if q_alt == (x["n"][0] > 0) + (x["n"][1] > 0):
+                                    q_alt = 0
+                                    self.tensor.append(("commit", self.q_empty[0]))
+                        state[t] = 2
+                elif self.p_full[t].test(num[t] & 1) and ready("v", self.v_full, c, 2):
+                    self.tensor.append(("pv", t, st, c, j[t] == 0))
+                    self.tensor.append(("commit", self.pv_done[t][num[t] & 1]))
+                    use["v"][st] += 1
+                    if use["v"][st] == users:
+                        use["v"][st] = 0
+                        self.tensor.append(("commit", self.v_empty[st]))
+                    num[t] += 1
+                    j[t] += 1
+                    state[t] = 1
+                    if j[t] == x["n"][t]:
+                        self.item_empty[item[t] % RING].arrive()
+                        item[t] += 1
+                        state[t] = 0
+
+    def tensor_core(self):
+        while True:
+            if not self.tensor:
+                yield "idle"
+                continue
+            op = self.tensor[0]
+            if op[0] == "commit":
+                op[1].arrive()
+            elif op[0] == "qk":
+                _, t, qt, st, c, item = op
+                for key in (("k", st), ("q", qt)):
+                    self.reading[key] = self.reading.get(key, 0) + 1
+                yield
+                assert self.k[st] == c and self.q[qt] == item, (self.k, self.q, op)
+                for key in (("k", st), ("q", qt)):
+                    self.reading[key] -= 1
+                self.s[t] = [("s", c)] * 4
+            else:
+                _, t, st, c, first = op
+                self.reading[("v", st)] = self.reading.get(("v", st), 0) + 1
+                yield
+                assert self.v[st] == c and all(x == ("p", c) for x in self.s[t]), (self.v, self.s, op)
+                self.reading[("v", st)] -= 1
+                assert not self.reading.get(("o", t)), "accumulator overwritten while read"
+                self.o[t] = [c] if first else self.o[t] + [c]
+            self.tensor.pop(0)
+            yield
+
+    def softmax(self, t, me, rng):
+        num = nx = i = 0
+        while True:
+            w = yield from self.next_item(i)
+            if w is None:
+                return
+            assert w["i"] == i
+            mine = []
+            for j in range(w["n"][t]):
+                jt = 2 * j + t if w["alt"] else j
+                c = w["c0"] + jt
+                st = c & 1
+                yield from self.wait(self.s_full[t], num & 1)
+                assert self.s[t][me] == ("s", c)
+                if self.convert:
+                    n = 4 if self.plant == "short scale ring" else SCALES
+                    yield from self.wait(self.sc_full[c % n], (c // n) & 1)
+                    self.reading[("sc", c % n)] = self.reading.get(("sc", c % n), 0) + 1
+                    assert self.sc[c % n] == [c] * 4
+                    for _ in range(rng.choice([0, 1, 30])):
+                        yield
+                    assert self.sc[c % n] == [c] * 4
+                    self.reading[("sc", c % n)] -= 1
+                if jt in w["edges"] and not self.convert:
+                    yield from self.wait(self.v_full[st], (c // 2) & 1)
+                    self.reading[("v", st)] = self.reading.get(("v", st), 0) + 1
+                    yield
+                    assert self.v[st] == c
+                    self.reading[("v", st)] -= 1
+                if j > 0 and rng.random() < 0.3:         # the rescale
+                    yield from self.wait(self.pv_done[t][(num - 1) & 1], ((num - 1) // 2) & 1)
+                    assert self.o[t][-1] == c - (2 if w["alt"] else 1)
+                for _ in range(rng.choice([0, 2, 9])):
+                    yield
+                self.s[t] = self.s[t][:me] + [("p", c)] + self.s[t][me + 1:]
+                self.p_full[t].arrive()
+                mine.append(c)
+                num += 1
+            if w["n"][t]:
+                yield from self.wait(self.pv_done[t][(num - 1) & 1], ((num - 1) // 2) & 1)
+                assert self.o[t] == mine
+            if w["alt"]:
+                self.xbar.arrive()
+                yield from self.wait(self.xbar, nx & 1)
+                nx += 1
+                for u in range(2):
+                    if w["n"][u]:
+                        self.reading[("o", u)] = self.reading.get(("o", u), 0) + 1
+                yield
+                for u in range(2):
+                    if w["n"][u]:
+                        assert self.o[u] == [w["c0"] + 2 * k + u for k in range(w["n"][u])]
+                        self.reading[("o", u)] -= 1
+                if self.plant != "no second meeting":
+                    self.xbar.arrive()
+                    yield from self.wait(self.xbar, nx & 1)
+                    nx += 1
+            if me == 0:
+                self.out.append((i, t))
+            self.item_empty[i % RING].arrive()
+            i += 1
+
+    def run(self, seed):
+        rng = random.Random(seed)
+        roles = [self.draw(), self.q_rows(), self.products()]
+        roles += [self.converter(m) for m in range(4)] if self.convert else [self.v_copies()]
+        roles += [self.softmax(t, m, rng) for t in range(2) for m in range(4)]
+        core = self.tensor_core()
+        slow = [rng.choice([1, 1, 1, 4, 60]) for _ in roles]
+        live = list(range(len(roles)))
+        for step in range(400000):
+            if not live:
+                break
+            r = rng.randrange(len(roles) + 2)
+            if r >= len(roles):
+                next(core)
+            elif r in live and rng.randrange(slow[r]) == 0:
+                try:
+                    next(roles[r])
+                except StopIteration:
+                    live.remove(r)
+        assert not live, "deadlock"
+        assert sorted(self.out) == [(i, t) for i in range(len(self.items)) for t in range(2)]
+
+
+def items_of(rng, count):
+    items = []
+    for _ in range(count):
+        if rng.random() < 0.5:
+            n = rng.choice([0, 1, 1, 1, 2, 3, 5])
+            items.append((True, (n + 1) // 2, n // 2, set(rng.sample(range(n), min(n, rng.randint(0, 2))))))
+        else:
+            n = rng.choice([1, 1, 2, 3])
+            n0 = n - rng.randint(0, 1)
+            items.append((False, n0, n, set(rng.sample(range(n), rng.randint(0, min(n, 2))))))
+    return items
+
+
+@pytest.mark.parametrize("convert", [False, True])
+def test_random_schedules(convert):
+    for seed in range(60):
+        rng = random.Random(seed)
+        Model(items_of(rng, rng.randint(1, 12)), convert).run(seed)
+
+
+@pytest.mark.parametrize("plant,convert", [("unordered", True), ("no second meeting", False), ("short scale ring", True)])
+def test_planted_mistakes_are_caught(plant, convert):
+    caught = 0
+    for seed in range(20):
+        rng = random.Random(seed)
+        try:
+            Model(items_of(rng, 20), convert, plant).run(seed)
+        except AssertionError:
+            caught += 1
+            break
+    assert caught

@@ -250,3 +250,36 @@ def test_agrees_with_prefill(dtype):
     pkv.prefill(out, q, pool_to_dev(c), desc, *[torch.from_numpy(x).cuda() for x in (case.tables, case.ctx, case.qsl)], 300, 1 / math.sqrt(128))
     _, tol = case.expected(1 / math.sqrt(128))
     assert bool(((got.double() - out.double()).abs().cpu().numpy() <= 2 * tol).all())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bs", [4, 16])
+@pytest.mark.parametrize("q_lens,ctx,window", [([40, 3], [300, 50], 0), ([90, 1], [4000, 20], 0), ([40, 200], [900, 1200], 100)])
+def test_infinities_and_nan_in_masked_places(q_lens, ctx, window, bs, dtype):
+    """K and V of single tokens hold infinities and NaN: queries that do not attend those tokens are untouched,
+    the others get what the formula gives."""
+    rng = np.random.default_rng(bs + window)
+    case = Chunk(rng, q_lens, ctx, Hq=6, Hkv=2, D=128, bs=bs, dtype=dtype)
+    inf, nan, minf = (0x7F80, 0x7FC0, 0xFF80) if dtype == "bf16" else (0x7C00, 0x7E00, 0xFC00)
+    c = case.cache
+
+    def plant(s, pos, part, head, dims, bits):
+        block, t = int(case.tables[s, pos // bs]), pos % bs
+        base = (block * c.Hkv + head) * step_ref.chunk_elements(bs, c.D)
+        c.pool[base + step_ref.offsets16(bs, c.D, [t], part)[0][dims]] = bits
+
+    first = ctx[0] - q_lens[0]
+    plant(0, first + 21, 1, 0, [3, 70], inf)                         # V that the last queries attend
+    plant(0, first + 33, 1, 0, [3], minf)
+    plant(0, first + 35, 0, 1, [5], nan)                             # K
+    if window:
+        plant(0, first - window + 10, 1, 1, [9], nan)                # leaves the window of the later queries
+        plant(0, first - window - 1, 1, 0, [1], nan)                 # attended by nobody
+    out, tol = case.expected(0.09, window)
+    got = bits_to_f64(dev_to_u16(run(case, 0.09, window)), dtype)
+    fine = np.isfinite(out)
+    assert fine.sum() < fine.size and fine.mean() > 0.5
+    assert (np.abs(got - out) <= tol)[fine].all()
+    assert (np.isnan(got) == np.isnan(out)).all()
+    big = np.isinf(out)
+    assert (got[big] == out[big]).all()
