@@ -700,12 +700,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           break;
         }
         if (w.kvh < 0) break;
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (w.n[t] == 0 || (w.alt && t == 1)) continue;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || w.n[t] == 0 || (w.alt && t == 1)) continue;
           const int load = w.qload[t];
           if (load > 0 && !wait(&sh.q_empty[t], (load - 1) & 1)) {
             ok = false;
-            break;
+            continue;
           }
           const int rows = (w.alt ? w.npos : min(ptile, w.npos - t * ptile)) * G;
           const T* q = static_cast<const T*>(p.q) + (int64_t)(w.row0 + t * ptile) * p.q_token_stride +
@@ -731,8 +732,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const uint32_t id_qk = tc::idesc_f16(kRows, kKv, kBF16, false, false);
       const uint32_t id_pv = tc::idesc_f16(kRows, D, kBF16 && !kI8, false, true);
       const uint32_t qa = smem_u32(qbuf), ka = smem_u32(kbuf), va = smem_u32(vbuf);
-      // Barriers that either query tile may look at are observed in order, each phase once.
-      int k_seen = 0, v_seen = 0, q_seen[2] = {0, 0};
+      // Barriers that either query tile may look at are observed in order, each phase
+      // once: the parity of a barrier two phases behind would say it is complete.
+      // (No array here is indexed by a variable: local memory is an L2 trip away
+      // beside this much shared memory, and this lane feeds the tensor cores.)
+      int k_seen = 0, v_seen = 0, q_seen0 = 0, q_seen1 = 0;
       auto k_ready = [&](int c) {
         while (k_seen <= c && mbar_test_wait(&sh.k_full[k_seen & 1], (k_seen >> 1) & 1)) ++k_seen;
         return c < k_seen;
@@ -741,93 +745,108 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         while (v_seen <= c && mbar_test_wait(&sh.v_full[v_seen & 1], (v_seen >> 1) & 1)) ++v_seen;
         return c < v_seen;
       };
-      auto q_ready = [&](int t, int load) {
-        while (q_seen[t] <= load && mbar_test_wait(&sh.q_full[t], q_seen[t] & 1)) ++q_seen[t];
-        return load < q_seen[t];
+      auto q_ready = [&](uint64_t* bar, int& seen, int load) {
+        while (seen <= load && mbar_test_wait(bar, seen & 1)) ++seen;
+        return load < seen;
       };
-      int k_use[2] = {0, 0}, v_use[2] = {0, 0}, q_alt = 0;           // users so far of a stage / of a shared Q
-      int item[2] = {0, 0}, j[2] = {0, 0}, num[2] = {0, 0};          // item, tile in it, tiles in all
-      int state[2] = {0, 0};                                         // 0: needs an item, 1: QK next, 2: PV next, 3: end
-      Work w[2];
+      // users so far of the two stages (a byte each), and of a shared query tile
+      uint32_t k_use = 0, v_use = 0;
+      int q_alt = 0;
+      auto last_user = [](uint32_t& use, int st, int users) {
+        const uint32_t n = ((use >> (8 * st)) & 0xffu) + 1;
+        use = (use & ~(0xffu << (8 * st))) | ((n == (uint32_t)users ? 0u : n) << (8 * st));
+        return n == (uint32_t)users;
+      };
+      struct Side {
+        int state = 0;                     // 0: needs an item, 1: QK next, 2: PV next, 3: end
+        int item = 0, j = 0, num = 0;      // item, tile in it, tiles in all
+        int n, other, alt, tile0, c0, kv_end, edge_lo, edge_hi, qload;
+      };
+      // one step of query tile t, if something is ready
+      auto step = [&](auto which, Side& x) -> bool {
+        constexpr int t = decltype(which)::value;
+        if (x.state == 3) return false;
+        if (x.state == 0) {
+          const int slot = x.item % kRing;
+          if (!mbar_test_wait(&sh.item_full[slot], (x.item / kRing) & 1)) return false;
+          const Work& w = sh.work[slot];
+          if (w.kvh < 0) {
+            x.state = 3;
+            return true;
+          }
+          x.n = w.n[t];
+          if (x.n == 0) {
+            mbar_arrive(&sh.item_empty[slot]);
+            ++x.item;
+            return true;
+          }
+          x.other = w.n[1 - t];
+          x.alt = w.alt;
+          x.tile0 = w.tile0;
+          x.c0 = w.c0;
+          x.kv_end = w.kv_end;
+          x.edge_lo = w.edge_lo;
+          x.edge_hi = w.edge_hi;
+          x.qload = w.alt ? w.qload[0] : w.qload[t];
+          x.j = 0;
+          x.state = 1;
+        }
+        const int jt = x.alt ? 2 * x.j + t : x.j;                    // KV tile of the item
+        const int c = x.c0 + jt, st = c & 1;
+        const int users = x.alt || jt >= x.other ? 1 : 2;
+        if (x.state == 1) {
+          const bool edge = jt < x.edge_lo || jt >= x.edge_hi;       // its softmax looks at V
+          if (!k_ready(c)) return false;
+          if (t == 0 || x.alt ? !q_ready(&sh.q_full[0], q_seen0, x.qload) : !q_ready(&sh.q_full[1], q_seen1, x.qload))
+            return false;
+          if (edge && !v_ready(c)) return false;
+          tc::fence_after_sync();
+          const uint64_t qd = tc::smem_desc(qa + (t == 0 || x.alt ? 0 : C::kQBytes), 16, 1024, tc::kSwizzle128B);
+          const uint64_t kd = tc::smem_desc(ka + st * C::kTileBytes, 16, C::kGroupBytes, tc::kSwizzle128B);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                        kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
+          tc::commit(&sh.s_full[t]);
+          if (last_user(k_use, st, users)) tc::commit(&sh.k_empty[st]);
+          if (x.j == x.n - 1) {
+            if (!x.alt) {
+              tc::commit(&sh.q_empty[t]);
+            } else if (++q_alt == 1 + (x.other > 0)) {
+              q_alt = 0;
+              tc::commit(&sh.q_empty[0]);
+            }
+          }
+          x.state = 2;
+          return true;
+        }
+        if (!mbar_test_wait(&sh.p_full[t], x.num & 1) || !v_ready(c)) return false;
+        tc::fence_after_sync();
+        const uint64_t vd = tc::smem_desc(va + st * C::kTileBytes, 1024, C::kGroupBytes, tc::kSwizzle128B);
+        const int valid = min(kKv, x.kv_end - (x.tile0 + jt) * kKv), steps = (valid + 15) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < kKv / 16; ++kk)
+          if (kk < steps)
+            tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + kk * 8,
+                           vd + (uint64_t)((kk * 2 * C::kGroupBytes) >> 4), id_pv, (x.j > 0 || kk > 0) ? 1u : 0u);
+        tc::commit(&sh.pv_done[t][x.num & 1]);
+        if (last_user(v_use, st, users)) tc::commit(&sh.v_empty[st]);
+        ++x.num;
+        x.state = 1;
+        if (++x.j == x.n) {
+          mbar_arrive(&sh.item_empty[x.item % kRing]);
+          ++x.item;
+          x.state = 0;
+        }
+        return true;
+      };
+      Side a, b;
       uint32_t idle = 0;
       bool ok = true;
-      while (state[0] != 3 || state[1] != 3) {
-        bool moved = false;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (state[t] == 0) {
-            const int slot = item[t] % kRing;
-            if (!mbar_test_wait(&sh.item_full[slot], (item[t] / kRing) & 1)) continue;
-            w[t] = sh.work[slot];
-            j[t] = 0;
-            moved = true;
-            if (w[t].kvh < 0) {
-              state[t] = 3;
-            } else if (w[t].n[t] == 0) {
-              mbar_arrive(&sh.item_empty[slot]);
-              ++item[t];
-            } else {
-              state[t] = 1;
-            }
-          }
-          const Work& x = w[t];
-          const int jt = x.alt ? 2 * j[t] + t : j[t];                // KV tile of the item
-          const int c = x.c0 + jt, st = c & 1;
-          const int users = x.alt ? 1 : (jt < x.n[0]) + (jt < x.n[1]);
-          if (state[t] == 1) {
-            const int qt = x.alt ? 0 : t;
-            const bool edge = jt < x.edge_lo || jt >= x.edge_hi;     // its softmax looks at V
-            if (k_ready(c) && q_ready(qt, x.qload[qt]) && (!edge || v_ready(c))) {
-              tc::fence_after_sync();
-              const uint64_t qd = tc::smem_desc(qa + qt * C::kQBytes, 16, 1024, tc::kSwizzle128B);
-              const uint64_t kd = tc::smem_desc(ka + st * C::kTileBytes, 16, C::kGroupBytes, tc::kSwizzle128B);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                            kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
-              tc::commit(&sh.s_full[t]);
-              if (++k_use[st] == users) {
-                k_use[st] = 0;
-                tc::commit(&sh.k_empty[st]);
-              }
-              if (j[t] == x.n[t] - 1) {
-                if (!x.alt) {
-                  tc::commit(&sh.q_empty[t]);
-                } else if (++q_alt == (x.n[0] > 0) + (x.n[1] > 0)) {
-                  q_alt = 0;
-                  tc::commit(&sh.q_empty[0]);
-                }
-              }
-              state[t] = 2;
-              moved = true;
-            }
-          } else if (state[t] == 2) {
-            if (mbar_test_wait(&sh.p_full[t], num[t] & 1) && v_ready(c)) {
-              tc::fence_after_sync();
-              const uint64_t vd = tc::smem_desc(va + st * C::kTileBytes, 1024, C::kGroupBytes, tc::kSwizzle128B);
-              const int valid = min(kKv, x.kv_end - (x.tile0 + jt) * kKv), steps = (valid + 15) >> 4;
-#pragma unroll
-              for (int kk = 0; kk < kKv / 16; ++kk)
-                if (kk < steps)
-                  tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + kk * 8,
-                                 vd + (uint64_t)((kk * 2 * C::kGroupBytes) >> 4), id_pv, (j[t] > 0 || kk > 0) ? 1u : 0u);
-              tc::commit(&sh.pv_done[t][num[t] & 1]);
-              if (++v_use[st] == users) {
-                v_use[st] = 0;
-                tc::commit(&sh.v_empty[st]);
-              }
-              ++num[t];
-              state[t] = 1;
-              if (++j[t] == x.n[t]) {
-                mbar_arrive(&sh.item_empty[item[t] % kRing]);
-                ++item[t];
-                state[t] = 0;
-              }
-              moved = true;
-            }
-          }
-        }
-        if (moved) {
+      while (a.state != 3 || b.state != 3) {
+        const bool moved_a = step(std::integral_constant<int, 0>{}, a);
+        const bool moved_b = step(std::integral_constant<int, 1>{}, b);
+        if (moved_a || moved_b) {
           idle = 0;
         } else if (++idle > 8 * kPolls || sh.abort_flag) {
           ok = false;
@@ -996,7 +1015,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const bool row_ok = ipos < npos;
       const int pos = w.pos0 + my0 + ipos;
       const int from = attend_from(pos, p.window, w.held);
-      const int n = w.n[t];
+      const int n = t == 0 ? w.n[0] : w.n[1];
       float m = -INFINITY, l = 0.f;
       bool odd_v = false;                                            // a non-finite V in a partly masked tile
       for (int j = 0; j < n; ++j, ++num) {
@@ -1052,9 +1071,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             tc::fence_proxy_async_smem();
           }
         }
-        float mt = -INFINITY;
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
 #pragma unroll
-        for (int e = 0; e < kKv; ++e) mt = fmaxf(mt, x[e]);
+        for (int e = 0; e < kKv; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
+        float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const float unit = kI8 ? 1.f : p.scale_log2;                 // x is in base-2 units already (8-bit)
         mt *= unit;
         const float m_new = fmaxf(m, mt);
@@ -1083,6 +1105,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
         // weights 2^(x - m), the sum of the unrounded ones in fp32
         const float nm = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < kKv / 32; ++e) {
           uint32_t y[16];
@@ -1093,15 +1116,17 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             const float b = ex2_approx(kI8 ? x[col + 1] + nm : fmaf(x[col + 1], unit, nm));
             if constexpr (kI8) {
               const float2 iv = *reinterpret_cast<const float2*>(&scales.iv[c % kScaleRing][col]);
-              l = fmaf(a, iv.x, l);
-              l = fmaf(b, iv.y, l);
+              sum[2 * (k & 1)] = fmaf(a, iv.x, sum[2 * (k & 1)]);
+              sum[2 * (k & 1) + 1] = fmaf(b, iv.y, sum[2 * (k & 1) + 1]);
             } else {
-              l += a + b;
+              sum[2 * (k & 1)] += a;
+              sum[2 * (k & 1) + 1] += b;
             }
             y[k] = Elem<PT>::pack2(a, b);
           }
           tc::tmem_st16u(s_addr + e * 16, y);
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
