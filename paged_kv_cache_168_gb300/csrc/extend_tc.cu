@@ -33,8 +33,8 @@
 //                   only then is O rescaled in TMEM.  Statistics are fp32;
 //                   weights are rounded to the cache's 16-bit type (fp16 for an
 //                   8-bit cache), the sum takes them unrounded.
-//   warp 8          one lane issues the products, whichever is ready: per query
-//                   tile QK(c), PV(c), QK(c'), ... strictly in turn.
+//   warp 8          issues the products, in a fixed order that alternates between
+//                   the query tiles.
 //   warp 9          draws items, publishes them in a ring, and copies K tiles
 //                   (8-token groups, one bulk copy each) into a 2-stage ring.
 //   warp 10         copies V tiles into a 2-stage ring.
@@ -368,9 +368,9 @@ struct Cfg {
   static constexpr bool kConvert = F != kBulk;
   static constexpr int kThreads = kConvert ? 512 : 384;
   // registers: the softmax warpgroups hold a row's 128 scores (sums equal the launch's)
-  static constexpr int kRegsSoftmax = kConvert ? 184 : 208;
-  static constexpr int kRegsRest = kConvert ? 56 : 88;
-  static constexpr int kRegsConvert = 88;
+  static constexpr int kRegsSoftmax = kConvert ? 176 : 200;
+  static constexpr int kRegsRest = kConvert ? 80 : 104;
+  static constexpr int kRegsConvert = 80;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
   static constexpr size_t kSmem = 1024 + 2 * kQBytes + 4 * kTileBytes;
@@ -379,7 +379,7 @@ struct Cfg {
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2];
+  uint64_t s_full[2], p_half[2], p_full[2];
   // PV of tile number n of query tile t completes pv_done[t][n & 1]: a waiter is never two phases behind
   uint64_t pv_done[2][2];
   uint64_t item_full[kRing], item_empty[kRing];
@@ -408,6 +408,26 @@ __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2f(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // 32 TMEM lanes x 64 columns; the wait is part of the statement.
@@ -458,11 +478,11 @@ __device__ __forceinline__ uint32_t kv_offset(int r, int piece) {
   return (uint32_t)((r >> 3) * (8 * D * 2) + (piece >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
 }
 
-// Whether any 16-bit value of w (two of them) is an infinity or NaN.
+// Bits 15 and 31 are set where the lower / upper 16-bit value of w is an infinity or NaN (exponent all ones).
 template <typename T>
-__device__ __forceinline__ bool non_finite2(uint32_t w) {
-  constexpr uint32_t e = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
-  return (w & e) == e || ((w >> 16) & e) == e;
+__device__ __forceinline__ uint32_t exponents(uint32_t w) {
+  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+  return (w & (bf ? 0x7f807f80u : 0x7c007c00u)) + (bf ? 0x00800080u : 0x04000400u);
 }
 
 // Table entry and validity of the block that holds position pos.
@@ -497,14 +517,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_half[i], 4);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i][0], 1);
       mbar_init(&sh.pv_done[i][1], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      // 8 softmax warps, the issuer once per query tile, the Q warp, and the V warp or 4 converter warps
-      mbar_init(&sh.item_empty[i], C::kConvert ? 15 : 12);
+      // 8 softmax warps, the issuing warp, the Q warp, and the V warp or 4 converter warps
+      mbar_init(&sh.item_empty[i], C::kConvert ? 14 : 11);
     }
     for (int i = 0; i < kScaleRing; ++i) mbar_init(&sh.sc_full[i], 4);
     mbar_init(&sh.xbar, 8);
@@ -712,11 +733,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const T* q = static_cast<const T*>(p.q) + (int64_t)(w.row0 + t * ptile) * p.q_token_stride +
                        (int64_t)w.kvh * G * D;
           const uint32_t dst = smem_u32(qbuf + t * C::kQBytes);
-          for (int k = lane; k < kRows * (D / 8); k += 32) {
-            const int r = k / (D / 8), piece = k % (D / 8);
-            const bool take = r < rows;
-            const int rr = take ? r : 0;
-            cp_async16(dst + q_offset(r, piece), q + (int64_t)(rr / G) * p.q_token_stride + (rr % G) * D + piece * 8, take);
+          constexpr int kStep = 32 / (D / 8);                        // rows a round of the warp takes
+          const int piece = lane % (D / 8);
+          int r = lane / (D / 8), h = r % G;
+          const T* src = q + (int64_t)(r / G) * p.q_token_stride + h * D + piece * 8;
+#pragma unroll 8
+          for (int k = 0; k < kRows / kStep; ++k) {
+            cp_async16(dst + q_offset(r, piece), r < rows ? src : q, r < rows);
+            r += kStep;
+            h += kStep;
+            src += kStep * D;
+            while (h >= G) {                                         // the next token
+              h -= G;
+              src += p.q_token_stride - G * D;
+            }
           }
           cp_async_wait();
           tc::fence_proxy_async_smem();
@@ -727,136 +757,143 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       }
       if (!ok && lane == 0) give_up();
       __syncwarp();
-    } else if (lane == 0) {
+    } else {
       // ================================================================= warp 8: products
+      // The whole warp runs the schedule, so that operands stay in uniform registers;
+      // one elected lane issues.  Order: items in turn, and per item, KV tile by KV
+      // tile, for query tile t = 0, 1: PV_t of its tile before, then QK_t of this one.
+      // While one query tile's weights are being made, the other's products run.
       const uint32_t id_qk = tc::idesc_f16(kRows, kKv, kBF16, false, false);
       const uint32_t id_pv = tc::idesc_f16(kRows, D, kBF16 && !kI8, false, true);
-      const uint32_t qa = smem_u32(qbuf), ka = smem_u32(kbuf), va = smem_u32(vbuf);
-      // Barriers that either query tile may look at are observed in order, each phase
-      // once: the parity of a barrier two phases behind would say it is complete.
-      // (No array here is indexed by a variable: local memory is an L2 trip away
-      // beside this much shared memory, and this lane feeds the tensor cores.)
-      int k_seen = 0, v_seen = 0, q_seen0 = 0, q_seen1 = 0;
-      auto k_ready = [&](int c) {
-        while (k_seen <= c && mbar_test_wait(&sh.k_full[k_seen & 1], (k_seen >> 1) & 1)) ++k_seen;
-        return c < k_seen;
-      };
-      auto v_ready = [&](int c) {
-        while (v_seen <= c && mbar_test_wait(&sh.v_full[v_seen & 1], (v_seen >> 1) & 1)) ++v_seen;
-        return c < v_seen;
-      };
-      auto q_ready = [&](uint64_t* bar, int& seen, int load) {
-        while (seen <= load && mbar_test_wait(bar, seen & 1)) ++seen;
-        return load < seen;
-      };
-      // users so far of the two stages (a byte each), and of a shared query tile
-      uint32_t k_use = 0, v_use = 0;
-      int q_alt = 0;
-      auto last_user = [](uint32_t& use, int st, int users) {
-        const uint32_t n = ((use >> (8 * st)) & 0xffu) + 1;
-        use = (use & ~(0xffu << (8 * st))) | ((n == (uint32_t)users ? 0u : n) << (8 * st));
-        return n == (uint32_t)users;
-      };
-      struct Side {
-        int state = 0;                     // 0: needs an item, 1: QK next, 2: PV next, 3: end
-        int item = 0, j = 0, num = 0;      // item, tile in it, tiles in all
-        int n, other, alt, tile0, c0, kv_end, edge_lo, edge_hi, qload;
-      };
-      // one step of query tile t, if something is ready
-      auto step = [&](auto which, Side& x) -> bool {
-        constexpr int t = decltype(which)::value;
-        if (x.state == 3) return false;
-        if (x.state == 0) {
-          const int slot = x.item % kRing;
-          if (!mbar_test_wait(&sh.item_full[slot], (x.item / kRing) & 1)) return false;
-          const Work& w = sh.work[slot];
-          if (w.kvh < 0) {
-            x.state = 3;
-            return true;
+      const uint64_t qd0 = tc::smem_desc(smem_u32(qbuf), 16, 1024, tc::kSwizzle128B);
+      const uint64_t kd0 = tc::smem_desc(smem_u32(kbuf), 16, C::kGroupBytes, tc::kSwizzle128B);
+      const uint64_t vd0 = tc::smem_desc(smem_u32(vbuf), 1024, C::kGroupBytes, tc::kSwizzle128B);
+      bool ok = true;
+      auto spin = [&](uint64_t* bar, uint32_t parity) {
+        if (!ok) return;
+        for (uint32_t i = 0; i < 8 * kPolls; ++i) {
+          if (__all_sync(kFull, mbar_test_wait(bar, parity))) {
+            tc::fence_after_sync();
+            return;
           }
-          x.n = w.n[t];
-          if (x.n == 0) {
-            mbar_arrive(&sh.item_empty[slot]);
-            ++x.item;
-            return true;
-          }
-          x.other = w.n[1 - t];
-          x.alt = w.alt;
-          x.tile0 = w.tile0;
-          x.c0 = w.c0;
-          x.kv_end = w.kv_end;
-          x.edge_lo = w.edge_lo;
-          x.edge_hi = w.edge_hi;
-          x.qload = w.alt ? w.qload[0] : w.qload[t];
-          x.j = 0;
-          x.state = 1;
+          if ((i & 255) == 255 && __any_sync(kFull, sh.abort_flag)) break;
         }
-        const int jt = x.alt ? 2 * x.j + t : x.j;                    // KV tile of the item
-        const int c = x.c0 + jt, st = c & 1;
-        const int users = x.alt || jt >= x.other ? 1 : 2;
-        if (x.state == 1) {
-          const bool edge = jt < x.edge_lo || jt >= x.edge_hi;       // its softmax looks at V
-          if (!k_ready(c)) return false;
-          if (t == 0 || x.alt ? !q_ready(&sh.q_full[0], q_seen0, x.qload) : !q_ready(&sh.q_full[1], q_seen1, x.qload))
-            return false;
-          if (edge && !v_ready(c)) return false;
-          tc::fence_after_sync();
-          const uint64_t qd = tc::smem_desc(qa + (t == 0 || x.alt ? 0 : C::kQBytes), 16, 1024, tc::kSwizzle128B);
-          const uint64_t kd = tc::smem_desc(ka + st * C::kTileBytes, 16, C::kGroupBytes, tc::kSwizzle128B);
+        ok = false;
+      };
+      // Every barrier's phases are waited for in order, each once: the parity of one
+      // two phases behind would say it is complete.
+      int k_seen = 0, v_seen = 0, q_seen0 = 0, q_seen1 = 0;
+      auto k_wait = [&](int c) {
+        for (; k_seen <= c; ++k_seen) spin(&sh.k_full[k_seen & 1], (k_seen >> 1) & 1);
+      };
+      auto v_wait = [&](int c) {
+        for (; v_seen <= c; ++v_seen) spin(&sh.v_full[v_seen & 1], (v_seen >> 1) & 1);
+      };
+      // the product that each query tile still owes: its KV tile's ring number, steps of 16 tokens, flags
+      struct Owed {
+        int c = -1, steps = 0, first = 0, last_user = 0, num = 0;
+      };
+      Owed owed0, owed1;
+      auto pv = [&](auto which, Owed& x) {
+        constexpr int t = decltype(which)::value;
+        if (x.c < 0) return;
+        const int st = x.c & 1;
+        const uint64_t vd = vd0 + (uint64_t)((st * C::kTileBytes) >> 4);
+        v_wait(x.c);
+        // the first half of the tokens as soon as their weights are there
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
-                        kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
-          tc::commit(&sh.s_full[t]);
-          if (last_user(k_use, st, users)) tc::commit(&sh.k_empty[st]);
-          if (x.j == x.n - 1) {
-            if (!x.alt) {
-              tc::commit(&sh.q_empty[t]);
-            } else if (++q_alt == 1 + (x.other > 0)) {
-              q_alt = 0;
-              tc::commit(&sh.q_empty[0]);
+        for (int h = 0; h < 2; ++h) {
+          spin(h ? &sh.p_full[t] : &sh.p_half[t], x.num & 1);
+          if (ok && tc::elect()) {
+#pragma unroll
+            for (int kk = 0; kk < kKv / 32; ++kk) {
+              const int k = kk + h * (kKv / 32);
+              if (k < x.steps)
+                tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8,
+                               vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4), id_pv, k > 0 ? 1u : (uint32_t)!x.first);
+            }
+            if (h == 1) {
+              tc::commit(&sh.pv_done[t][x.num & 1]);
+              if (x.last_user) tc::commit(&sh.v_empty[st]);
             }
           }
-          x.state = 2;
-          return true;
+          __syncwarp();
         }
-        if (!mbar_test_wait(&sh.p_full[t], x.num & 1) || !v_ready(c)) return false;
-        tc::fence_after_sync();
-        const uint64_t vd = tc::smem_desc(va + st * C::kTileBytes, 1024, C::kGroupBytes, tc::kSwizzle128B);
-        const int valid = min(kKv, x.kv_end - (x.tile0 + jt) * kKv), steps = (valid + 15) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < kKv / 16; ++kk)
-          if (kk < steps)
-            tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + kk * 8,
-                           vd + (uint64_t)((kk * 2 * C::kGroupBytes) >> 4), id_pv, (x.j > 0 || kk > 0) ? 1u : 0u);
-        tc::commit(&sh.pv_done[t][x.num & 1]);
-        if (last_user(v_use, st, users)) tc::commit(&sh.v_empty[st]);
         ++x.num;
-        x.state = 1;
-        if (++x.j == x.n) {
-          mbar_arrive(&sh.item_empty[x.item % kRing]);
-          ++x.item;
-          x.state = 0;
-        }
-        return true;
+        x.c = -1;
       };
-      Side a, b;
-      uint32_t idle = 0;
-      bool ok = true;
-      while (a.state != 3 || b.state != 3) {
-        const bool moved_a = step(std::integral_constant<int, 0>{}, a);
-        const bool moved_b = step(std::integral_constant<int, 1>{}, b);
-        if (moved_a || moved_b) {
-          idle = 0;
-        } else if (++idle > 8 * kPolls || sh.abort_flag) {
-          ok = false;
+      for (int i = 0; ok; ++i) {
+        const int slot = i % kRing;
+        if (!__all_sync(kFull, mbar_test_wait(&sh.item_full[slot], (i / kRing) & 1))) {
+          // nothing to go on with yet: what is owed first
+          pv(std::integral_constant<int, 0>{}, owed0);
+          pv(std::integral_constant<int, 1>{}, owed1);
+          spin(&sh.item_full[slot], (i / kRing) & 1);
+        }
+        if (!ok) break;
+        const Work& w = sh.work[slot];
+        auto uni = [&](int v) { return __shfl_sync(kFull, v, 0); };
+        if (uni(w.kvh) < 0) {
+          pv(std::integral_constant<int, 0>{}, owed0);
+          pv(std::integral_constant<int, 1>{}, owed1);
           break;
         }
+        const int n0 = uni(w.n[0]), n1 = uni(w.n[1]), alt = uni(w.alt), c0 = uni(w.c0);
+        const int tok = uni(w.kv_end) - uni(w.tile0) * kKv;          // tokens from the first KV tile on
+        const int edge_lo = uni(w.edge_lo), edge_hi = uni(w.edge_hi);
+        const int load0 = uni(w.qload[0]), load1 = uni(w.qload[1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
+        auto turn = [&](auto which, Owed& x, int j, int n, int other) {
+          constexpr int t = decltype(which)::value;
+          pv(which, x);
+          if (j >= n) return;
+          const int jt = alt ? 2 * j + t : j, c = c0 + jt, st = c & 1;
+          const bool q0 = t == 0 || alt;                             // which query tile's rows
+          k_wait(c);
+          if (q0) {
+            for (; q_seen0 <= load0; ++q_seen0) spin(&sh.q_full[0], q_seen0 & 1);
+          } else {
+            for (; q_seen1 <= load1; ++q_seen1) spin(&sh.q_full[1], q_seen1 & 1);
+          }
+          if (jt < edge_lo || jt >= edge_hi) v_wait(c);              // its softmax looks at V
+          const uint64_t qd = qd0 + (uint64_t)((q0 ? 0 : C::kQBytes) >> 4);
+          const uint64_t kd = kd0 + (uint64_t)((st * C::kTileBytes) >> 4);
+          // the last of the (one or two) query tiles that use this K and V; of those that use this Q
+          const bool last_k = alt || t == 1 || jt >= other;
+          const bool last_q = j == n - 1 && (!alt || (t == 0 ? other < n : other <= n));
+          if (ok && tc::elect()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
+                          kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
+            tc::commit(&sh.s_full[t]);
+            if (last_k) tc::commit(&sh.k_empty[st]);
+            if (last_q) tc::commit(q0 ? &sh.q_empty[0] : &sh.q_empty[1]);
+          }
+          __syncwarp();
+          x.c = c;
+          x.steps = min(kKv / 16, (tok - jt * kKv + 15) >> 4);
+          x.first = j == 0;
+          x.last_user = last_k;
+        };
+        // its rows may still be on their way: then the other tile's product goes first
+        pv(std::integral_constant<int, 0>{}, owed0);
+        if (n0 > 0 && q_seen0 <= load0 && !__all_sync(kFull, mbar_test_wait(&sh.q_full[0], q_seen0 & 1)))
+          pv(std::integral_constant<int, 1>{}, owed1);
+        const int rounds = max(n0, n1);
+        for (int j = 0; j < rounds && ok; ++j) {
+          turn(std::integral_constant<int, 0>{}, owed0, j, n0, n1);
+          turn(std::integral_constant<int, 1>{}, owed1, j, n1, n0);
+        }
       }
-      if (!ok) give_up();
-      // every product this lane issued completes before TMEM can be freed
-      tc::commit(&sh.mma_drain);
-      if (!bar_wait(&sh.mma_drain, 0)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+      if (!ok && lane == 0) give_up();
+      // every product issued completes before TMEM can be freed
+      if (tc::elect()) {
+        tc::commit(&sh.mma_drain);
+      }
+      __syncwarp();
+      if (!__all_sync(kFull, bar_wait(&sh.mma_drain, 0)) && lane == 0) report(p.dev_err, PA_DEVERR_TIMEOUT);
     }
     __syncwarp();
   } else if (warp >= 12) {
@@ -1040,16 +1077,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
           for (int e = 0; e < kKv / 4; ++e) {
             const float4 a = sk[e], b = lv[e];
-            x[4 * e] = fmaf(x[4 * e], a.x, b.x);
-            x[4 * e + 1] = fmaf(x[4 * e + 1], a.y, b.y);
-            x[4 * e + 2] = fmaf(x[4 * e + 2], a.z, b.z);
-            x[4 * e + 3] = fmaf(x[4 * e + 3], a.w, b.w);
+            unpack2f(fma2f(pack2f(x[4 * e], x[4 * e + 1]), pack2f(a.x, a.y), pack2f(b.x, b.y)), x[4 * e], x[4 * e + 1]);
+            unpack2f(fma2f(pack2f(x[4 * e + 2], x[4 * e + 3]), pack2f(a.z, a.w), pack2f(b.z, b.w)), x[4 * e + 2],
+                     x[4 * e + 3]);
           }
         }
         if (edge) {
           const int lo = from - t0, hi = row_ok ? pos + 1 - t0 : 0;  // attended columns [lo, hi)
 #pragma unroll
-          for (int e = 0; e < kKv; ++e) x[e] = (e >= lo && e < hi) ? x[e] : -INFINITY;
+          for (int e = 0; e < kKv / 32; ++e) {
+            const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
+            const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+          }
           if constexpr (!kI8) {
             // thread = token here: V rows that no block filled become zero, and
             // non-finite ones are noted (V has landed: the issuer waited for it)
@@ -1058,16 +1099,19 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               break;
             }
             uint8_t* v = vbuf + st * C::kTileBytes;
-            if (t0 + row >= w.kv_end || t0 + row < w.first) {
-#pragma unroll
-              for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
-            } else {
-#pragma unroll
-              for (int e = 0; e < D / 8; ++e) {
-                const uint4 y = *reinterpret_cast<const uint4*>(v + kv_offset<D>(row, e));
-                odd_v |= non_finite2<T>(y.x) || non_finite2<T>(y.y) || non_finite2<T>(y.z) || non_finite2<T>(y.w);
+            const bool none = t0 + row >= w.kv_end || t0 + row < w.first;
+            uint32_t seen = 0;
+#pragma unroll 2
+            for (int e = 0; e < D / 8; ++e) {
+              uint4* at = reinterpret_cast<uint4*>(v + kv_offset<D>(row, e));
+              if (none) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 y = *at;
+                seen |= exponents<T>(y.x) | exponents<T>(y.y) | exponents<T>(y.z) | exponents<T>(y.w);
               }
             }
+            odd_v |= (seen & 0x80008000u) != 0;
             tc::fence_proxy_async_smem();
           }
         }
@@ -1105,28 +1149,39 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
         // weights 2^(x - m), the sum of the unrounded ones in fp32
         const float nm = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t unit2 = pack2f(unit, unit), nm2 = pack2f(nm, nm);
+        uint64_t sum[2] = {0, 0};
 #pragma unroll
         for (int e = 0; e < kKv / 32; ++e) {
           uint32_t y[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int col = e * 32 + 2 * k;
-            const float a = ex2_approx(kI8 ? x[col] + nm : fmaf(x[col], unit, nm));
-            const float b = ex2_approx(kI8 ? x[col + 1] + nm : fmaf(x[col + 1], unit, nm));
-            if constexpr (kI8) {
-              const float2 iv = *reinterpret_cast<const float2*>(&scales.iv[c % kScaleRing][col]);
-              sum[2 * (k & 1)] = fmaf(a, iv.x, sum[2 * (k & 1)]);
-              sum[2 * (k & 1) + 1] = fmaf(b, iv.y, sum[2 * (k & 1) + 1]);
-            } else {
-              sum[2 * (k & 1)] += a;
-              sum[2 * (k & 1) + 1] += b;
-            }
+            const uint64_t xx = pack2f(x[col], x[col + 1]);
+            float a, b;
+            unpack2f(kI8 ? add2f(xx, nm2) : fma2f(xx, unit2, nm2), a, b);
+            a = ex2_approx(a);
+            b = ex2_approx(b);
+            const uint64_t ab = pack2f(a, b);
+            if constexpr (kI8)
+              sum[k & 1] = fma2f(ab, *reinterpret_cast<const uint64_t*>(&scales.iv[c % kScaleRing][col]), sum[k & 1]);
+            else
+              sum[k & 1] = add2f(ab, sum[k & 1]);
             y[k] = Elem<PT>::pack2(a, b);
           }
           tc::tmem_st16u(s_addr + e * 16, y);
+          if (e == kKv / 64 - 1) {
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_half[t]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        {
+          float a, b;
+          unpack2f(add2f(sum[0], sum[1]), a, b);
+          l += a + b;
+        }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
