@@ -15,8 +15,8 @@
 //                  that its K and V are read from L2 while they are hot.
 //   finish_kernel  merges parts by log-sum-exp, zeroes the rows of items with a
 //                  bad block id, and recomputes on CUDA cores the items whose
-//                  partly masked tiles hold a non-finite V (0 * NaN = NaN in the
-//                  second product, so those tiles cannot go through it).
+//                  results are not finite: an infinite or NaN V reaches rows that
+//                  do not attend it through the second product (0 * NaN = NaN).
 //
 // extend_kernel, per 128-token KV tile c and query tile t (0 or 1):
 //     S_t  = Q_t K_c^T     (M = 128 rows, N = 128 tokens, K = D)  -> TMEM (fp32)
@@ -478,11 +478,10 @@ __device__ __forceinline__ uint32_t kv_offset(int r, int piece) {
   return (uint32_t)((r >> 3) * (8 * D * 2) + (piece >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
 }
 
-// Bits 15 and 31 are set where the lower / upper 16-bit value of w is an infinity or NaN (exponent all ones).
-template <typename T>
-__device__ __forceinline__ uint32_t exponents(uint32_t w) {
-  constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-  return (w & (bf ? 0x7f807f80u : 0x7c007c00u)) + (bf ? 0x00800080u : 0x04000400u);
+// Whether KV tile jt of the item holds places without a token of the context.
+__device__ __forceinline__ bool ragged(const Work& w, int jt) {
+  const int t0 = (w.tile0 + jt) * kKv;
+  return t0 < w.first || t0 + kKv > w.kv_end;
 }
 
 // Table entry and validity of the block that holds position pos.
@@ -840,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
         const int n0 = uni(w.n[0]), n1 = uni(w.n[1]), alt = uni(w.alt), c0 = uni(w.c0);
         const int tok = uni(w.kv_end) - uni(w.tile0) * kKv;          // tokens from the first KV tile on
-        const int edge_lo = uni(w.edge_lo), edge_hi = uni(w.edge_hi);
+        const int skip = uni(w.first) - uni(w.tile0) * kKv;          // of them, before the first attended one
         const int load0 = uni(w.qload[0]), load1 = uni(w.qload[1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
@@ -856,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           } else {
             for (; q_seen1 <= load1; ++q_seen1) spin(&sh.q_full[1], q_seen1 & 1);
           }
-          if (jt < edge_lo || jt >= edge_hi) v_wait(c);              // its softmax looks at V
+          if (!kI8 && (jt * kKv < skip || (jt + 1) * kKv > tok)) v_wait(c);   // ragged: its softmax writes V
           const uint64_t qd = qd0 + (uint64_t)((q0 ? 0 : C::kQBytes) >> 4);
           const uint64_t kd = kd0 + (uint64_t)((st * C::kTileBytes) >> 4);
           // the last of the (one or two) query tiles that use this K and V; of those that use this Q
@@ -1054,7 +1053,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int from = attend_from(pos, p.window, w.held);
       const int n = t == 0 ? w.n[0] : w.n[1];
       float m = -INFINITY, l = 0.f;
-      bool odd_v = false;                                            // a non-finite V in a partly masked tile
       for (int j = 0; j < n; ++j, ++num) {
         const int jt = w.alt ? 2 * j + t : j, c = w.c0 + jt, st = c & 1;
         const int t0 = (w.tile0 + jt) * kKv;
@@ -1088,31 +1086,26 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           for (int e = 0; e < kKv / 32; ++e) {
             const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
             const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+            if (__any_sync(kFull, on != kFull)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+              for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+            }
           }
           if constexpr (!kI8) {
-            // thread = token here: V rows that no block filled become zero, and
-            // non-finite ones are noted (V has landed: the issuer waited for it)
-            if (!wait(&sh.v_full[st], (c >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            uint8_t* v = vbuf + st * C::kTileBytes;
-            const bool none = t0 + row >= w.kv_end || t0 + row < w.first;
-            uint32_t seen = 0;
-#pragma unroll 2
-            for (int e = 0; e < D / 8; ++e) {
-              uint4* at = reinterpret_cast<uint4*>(v + kv_offset<D>(row, e));
-              if (none) {
-                *at = make_uint4(0, 0, 0, 0);
-              } else {
-                const uint4 y = *at;
-                seen |= exponents<T>(y.x) | exponents<T>(y.y) | exponents<T>(y.z) | exponents<T>(y.w);
+            if (ragged(w, jt)) {
+              // thread = token here: V rows that hold no token of the context become
+              // zero (V has landed: the issuer waited for it)
+              if (!wait(&sh.v_full[st], (c >> 1) & 1)) {
+                ok = false;
+                break;
               }
+              if (t0 + row >= w.kv_end || t0 + row < w.first) {
+                uint8_t* v = vbuf + st * C::kTileBytes;
+#pragma unroll 2
+                for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
+              }
+              tc::fence_proxy_async_smem();
             }
-            odd_v |= (seen & 0x80008000u) != 0;
-            tc::fence_proxy_async_smem();
           }
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
@@ -1195,10 +1188,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
         report(p.dev_err, PA_DEVERR_BLOCK_ID);
       }
-      if (!kI8 && __any_sync(kFull, odd_v) && lane == 0) {
-        atomicOr(&ws.flags[w.flag], kNonFinite);
-        atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
-      }
       // ---- results: columns [c0, c0 + nc) of my row
       float f[2] = {1.f, 1.f};
       int col0 = 0, ncol = D;
@@ -1230,6 +1219,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int rr = (my0 + ipos) * G + head;                        // row within the item
       T* orow = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0 + ipos) * p.num_q_heads + w.kvh * G + head) * D;
       float* prow = ws.o + (int64_t)(w.part_row + rr) * D;
+      float odd = 0.f;
       for (int e = col0; e < col0 + ncol; e += 16) {
         float o[16];
         if (have0) {
@@ -1249,6 +1239,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
           for (int k = 0; k < 16; ++k) o[k] = o[k] * f[0] + b[k] * f[1];
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) odd = fmaf(o[k], 0.f, odd);     // NaN once any value is not finite
         if (row_ok && !part) {
           uint32_t y[8];
 #pragma unroll
@@ -1263,6 +1255,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       }
       if (row_ok && part && col0 == 0)
         *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(w.part_row + rr)) = make_float2(m, l);
+      // A V that is not finite reaches rows that do not attend it (0 * NaN = NaN):
+      // finish_kernel redoes the item.  (8-bit codes are finite, and a masked
+      // token's weight is 0 whatever its scale.)
+      if (!kI8 && __any_sync(kFull, row_ok && !(odd == 0.f)) && lane == 0) {
+        atomicOr(&ws.flags[w.flag], kNonFinite);
+        atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
+      }
       // both halves have read both accumulators before either is overwritten
       if (w.alt) meet(); else tc::fence_before_sync();
       if (!ok) break;
