@@ -36,8 +36,8 @@
 //   warp 8          issues the products, in a fixed order that alternates between
 //                   the query tiles.
 //   warp 9          draws items, publishes them in a ring, and copies K tiles
-//                   (8-token groups, one bulk copy each) into a 2-stage ring.
-//   warp 10         copies V tiles into a 2-stage ring.
+//                   (8-token groups, one bulk copy each) into the ring of K and V.
+//   warp 10         copies V tiles.
 //   warp 11         gathers Q rows into the swizzled K-major operand.
 //   warps 12-15     (caches whose chunks are not operands: 8-bit codes, blocks
 //                   of fewer than 8 tokens) fill the K and V stages in place of
@@ -373,13 +373,18 @@ struct Cfg {
   static constexpr int kRegsConvert = 80;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
-  static constexpr size_t kSmem = 1024 + 2 * kQBytes + 4 * kTileBytes;
+  // K and V tiles take turns in one ring: K of tile c is fill 2c, V fill 2c + 1, fill
+  // n sits in buffer n % kBufs.  Five buffers of 32 KiB beside the query tiles are
+  // all that fits (K and V in rings of two each waited ~1200 of 4500 clocks a tile
+  // for copies).
+  static constexpr int kBufs = kConvert ? 4 : 5;
+  static constexpr size_t kRingBytes = (size_t)kBufs * kTileBytes;
 };
 
-struct Shared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+struct __align__(16) Shared {
+  uint64_t full[5], empty[5];              // the buffers of K and V tiles
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_half[2], p_full[2];
+  uint64_t s_full[2], p_full[2];
   // PV of tile number n of query tile t completes pv_done[t][n & 1]: a waiter is never two phases behind
   uint64_t pv_done[2][2];
   uint64_t item_full[kRing], item_empty[kRing];
@@ -391,6 +396,8 @@ struct Shared {
   float red[2][kRows][2];                  // the other warpgroup's (maximum, sum)
   uint32_t tmem_base;
   volatile int abort_flag;
+  int last_fill[5];                        // the last copies into each buffer, -1: none
+  int pad[2];
 };
 struct __align__(16) Scales {
   float k[kScaleRing][kKv], lv[kScaleRing][kKv], iv[kScaleRing][kKv];
@@ -496,30 +503,33 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   constexpr bool kI8 = F == kCodes;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   using PT = typename std::conditional<kI8, __half, T>::type;      // type of the weights and of V's operand
-  __shared__ Shared sh;
-  __shared__ typename std::conditional<kI8, Scales, int>::type scales;
-  extern __shared__ __align__(1024) uint8_t dyn_raw[];
-  const uint32_t raw_s = smem_u32(dyn_raw);
-  uint8_t* qbuf = dyn_raw + (((raw_s + 1023u) & ~1023u) - raw_s);
-  uint8_t* kbuf = qbuf + 2 * C::kQBytes;
-  uint8_t* vbuf = kbuf + 2 * C::kTileBytes;
+  // (no static shared memory: the operands start 1024-byte aligned without padding)
+  extern __shared__ __align__(1024) uint8_t qbuf[];
+  uint8_t* ring = qbuf + 2 * C::kQBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(ring + C::kRingBytes);
+  Scales& scales = *reinterpret_cast<Scales*>(&sh + 1);            // 8-bit caches alone
+  constexpr int NB = C::kBufs;
+  if (smem_u32(qbuf) & 1023u) {                                    // never, as laid out
+    if (threadIdx.x == 0) report(p.dev_err, PA_DEVERR_TIMEOUT);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, ptile = kRows / G;                        // positions of one query tile
   const int bs = p.block_size;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.k_full[i], C::kConvert ? 4 : 1);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_full[i], C::kConvert ? 4 : 1);
-      mbar_init(&sh.v_empty[i], 1);
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_half[i], 4);
       mbar_init(&sh.p_full[i], 4);
       mbar_init(&sh.pv_done[i][0], 1);
       mbar_init(&sh.pv_done[i][1], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&sh.full[i], C::kConvert ? 4 : 1);
+      mbar_init(&sh.empty[i], 1);
+      sh.last_fill[i] = -1;
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.item_full[i], 1);
@@ -560,6 +570,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.item_empty[i % kRing]);
   };
+  // fill n's buffer: free to be filled / filled
+  auto wait_empty = [&](int n) -> bool { return n < NB || wait(&sh.empty[n % NB], (n / NB - 1) & 1); };
+  auto buffer = [&](int n) { return ring + (n % NB) * C::kTileBytes; };
   // KV tiles of an item
   auto tiles_of = [](const Work& w) { return w.alt ? w.n[0] + w.n[1] : max(w.n[0], w.n[1]); };
 
@@ -573,7 +586,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       w_next = __shfl_sync(kFull, w_next, 0);
       int c = 0, q0 = 0, q1 = 0;
       bool ok = true;
-      int issued = 0;
       for (int i = 0; ok; ++i) {
         Work w;
         w.kvh = -1;
@@ -630,7 +642,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;   // blocks [fb, nblk) are read
           for (int j = 0; j < n; ++j, ++c) {
-            const int st = c & 1;
             // lane l < 16 copies the tile's 8-token group l
             const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
             const bool take = lane < 16 && blk >= fb && blk < nblk;
@@ -639,20 +650,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               id = 0;
               sh.bad[slot] = 1;
             }
-            if (c >= 2 && !wait(&sh.k_empty[st], ((c >> 1) - 1) & 1)) {
+            if (!wait_empty(2 * c)) {
               ok = false;
               break;
             }
             const unsigned m = __ballot_sync(kFull, take);
-            if (lane == 0) mbar_arrive_expect_tx(&sh.k_full[st], (uint32_t)__popc(m) * C::kGroupBytes);
+            if (lane == 0) sh.last_fill[2 * c % NB] = 2 * c;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[2 * c % NB], (uint32_t)__popc(m) * C::kGroupBytes);
             __syncwarp();
             if (take) {
               const int g = (lane & 15) & (bs / 8 - 1);             // group within the block
-              bulk_g2s(kbuf + st * C::kTileBytes + (lane & 15) * C::kGroupBytes,
+              bulk_g2s(buffer(2 * c) + (lane & 15) * C::kGroupBytes,
                        p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes),
-                       C::kGroupBytes, &sh.k_full[st]);
+                       C::kGroupBytes, &sh.full[2 * c % NB]);
             }
-            issued = c + 1;
           }
         } else {
           c += n;
@@ -660,15 +671,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         w_next = __shfl_sync(kFull, w_next, 0);
       }
       if (!ok && lane == 0) give_up();
-      // never leave copies in flight, whether or not another role gave up
-      if (lane == 0)
-        for (int j = max(0, issued - 2); j < issued; ++j)
-          if (!bar_wait(&sh.k_full[j & 1], (j >> 1) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
       __syncwarp();
     } else if (warp == 10) {
       // ================================================================= V copies
       if constexpr (!C::kConvert) {
-        int c = 0, issued = 0;
+        int c = 0;
         bool ok = true;
         for (int i = 0; ok; ++i) {
           Work w;
@@ -681,33 +688,29 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;
           for (int j = 0; j < n; ++j, ++c) {
-            const int st = c & 1;
             const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
             const bool take = lane < 16 && blk >= fb && blk < nblk;
             int id = take ? block_of(p, row, blk) : 0;
             if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;      // reported by the K copies
-            if (c >= 2 && !wait(&sh.v_empty[st], ((c >> 1) - 1) & 1)) {
+            if (!wait_empty(2 * c + 1)) {
               ok = false;
               break;
             }
             const unsigned m = __ballot_sync(kFull, take);
-            if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[st], (uint32_t)__popc(m) * C::kGroupBytes);
+            if (lane == 0) sh.last_fill[(2 * c + 1) % NB] = 2 * c + 1;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.full[(2 * c + 1) % NB], (uint32_t)__popc(m) * C::kGroupBytes);
             __syncwarp();
             if (take) {
               const int g = (lane & 15) & (bs / 8 - 1);
-              bulk_g2s(vbuf + st * C::kTileBytes + (lane & 15) * C::kGroupBytes,
+              bulk_g2s(buffer(2 * c + 1) + (lane & 15) * C::kGroupBytes,
                        p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes) +
                            C::kGroupBytes,
-                       C::kGroupBytes, &sh.v_full[st]);
+                       C::kGroupBytes, &sh.full[(2 * c + 1) % NB]);
             }
-            issued = c + 1;
           }
           if (ok) done_item(i);
         }
         if (!ok && lane == 0) give_up();
-        if (lane == 0)
-          for (int j = max(0, issued - 2); j < issued; ++j)
-            if (!bar_wait(&sh.v_full[j & 1], (j >> 1) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
         __syncwarp();
       }
     } else if (warp == 11) {
@@ -765,8 +768,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const uint32_t id_qk = tc::idesc_f16(kRows, kKv, kBF16, false, false);
       const uint32_t id_pv = tc::idesc_f16(kRows, D, kBF16 && !kI8, false, true);
       const uint64_t qd0 = tc::smem_desc(smem_u32(qbuf), 16, 1024, tc::kSwizzle128B);
-      const uint64_t kd0 = tc::smem_desc(smem_u32(kbuf), 16, C::kGroupBytes, tc::kSwizzle128B);
-      const uint64_t vd0 = tc::smem_desc(smem_u32(vbuf), 1024, C::kGroupBytes, tc::kSwizzle128B);
+      const uint64_t kd0 = tc::smem_desc(smem_u32(ring), 16, C::kGroupBytes, tc::kSwizzle128B);
+      const uint64_t vd0 = tc::smem_desc(smem_u32(ring), 1024, C::kGroupBytes, tc::kSwizzle128B);
       bool ok = true;
       auto spin = [&](uint64_t* bar, uint32_t parity) {
         if (!ok) return;
@@ -779,14 +782,25 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
         ok = false;
       };
-      // Every barrier's phases are waited for in order, each once: the parity of one
-      // two phases behind would say it is complete.
+      // Fills of K and of V are waited for in order, each phase once: the parity of a
+      // barrier two phases behind would say it is complete.  A fill is looked at one
+      // step before it is needed (look), so that the answer comes while products are
+      // issued: shared memory is slow to answer while they read it.
       int k_seen = 0, v_seen = 0, q_seen0 = 0, q_seen1 = 0;
+      bool k_there = false, v_there = false;
+      auto k_look = [&]() { k_there = mbar_test_wait(&sh.full[2 * k_seen % NB], (2 * k_seen / NB) & 1); };
+      auto v_look = [&]() { v_there = mbar_test_wait(&sh.full[(2 * v_seen + 1) % NB], ((2 * v_seen + 1) / NB) & 1); };
       auto k_wait = [&](int c) {
-        for (; k_seen <= c; ++k_seen) spin(&sh.k_full[k_seen & 1], (k_seen >> 1) & 1);
+        for (; k_seen <= c; ++k_seen) {
+          if (!__all_sync(kFull, k_there)) spin(&sh.full[2 * k_seen % NB], (2 * k_seen / NB) & 1);
+          k_there = false;
+        }
       };
       auto v_wait = [&](int c) {
-        for (; v_seen <= c; ++v_seen) spin(&sh.v_full[v_seen & 1], (v_seen >> 1) & 1);
+        for (; v_seen <= c; ++v_seen) {
+          if (!__all_sync(kFull, v_there)) spin(&sh.full[(2 * v_seen + 1) % NB], ((2 * v_seen + 1) / NB) & 1);
+          v_there = false;
+        }
       };
       // the product that each query tile still owes: its KV tile's ring number, steps of 16 tokens, flags
       struct Owed {
@@ -796,28 +810,21 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       auto pv = [&](auto which, Owed& x) {
         constexpr int t = decltype(which)::value;
         if (x.c < 0) return;
-        const int st = x.c & 1;
+        const int st = (2 * x.c + 1) % NB;
         const uint64_t vd = vd0 + (uint64_t)((st * C::kTileBytes) >> 4);
         v_wait(x.c);
-        // the first half of the tokens as soon as their weights are there
+        spin(&sh.p_full[t], x.num & 1);
+        k_look();
+        if (ok && tc::elect()) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          spin(h ? &sh.p_full[t] : &sh.p_half[t], x.num & 1);
-          if (ok && tc::elect()) {
-#pragma unroll
-            for (int kk = 0; kk < kKv / 32; ++kk) {
-              const int k = kk + h * (kKv / 32);
-              if (k < x.steps)
-                tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8,
-                               vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4), id_pv, k > 0 ? 1u : (uint32_t)!x.first);
-            }
-            if (h == 1) {
-              tc::commit(&sh.pv_done[t][x.num & 1]);
-              if (x.last_user) tc::commit(&sh.v_empty[st]);
-            }
-          }
-          __syncwarp();
+          for (int k = 0; k < kKv / 16; ++k)
+            if (k < x.steps)
+              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8,
+                             vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4), id_pv, k > 0 ? 1u : (uint32_t)!x.first);
+          tc::commit(&sh.pv_done[t][x.num & 1]);
+          if (x.last_user) tc::commit(&sh.empty[st]);
         }
+        __syncwarp();
         ++x.num;
         x.c = -1;
       };
@@ -847,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           constexpr int t = decltype(which)::value;
           pv(which, x);
           if (j >= n) return;
-          const int jt = alt ? 2 * j + t : j, c = c0 + jt, st = c & 1;
+          const int jt = alt ? 2 * j + t : j, c = c0 + jt, st = 2 * c % NB;
           const bool q0 = t == 0 || alt;                             // which query tile's rows
           k_wait(c);
           if (q0) {
@@ -861,13 +868,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           // the last of the (one or two) query tiles that use this K and V; of those that use this Q
           const bool last_k = alt || t == 1 || jt >= other;
           const bool last_q = j == n - 1 && (!alt || (t == 0 ? other < n : other <= n));
+          v_look();
           if (ok && tc::elect()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                           kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
             tc::commit(&sh.s_full[t]);
-            if (last_k) tc::commit(&sh.k_empty[st]);
+            if (last_k) tc::commit(&sh.empty[st]);
             if (last_q) tc::commit(q0 ? &sh.q_empty[0] : &sh.q_empty[1]);
           }
           __syncwarp();
@@ -916,7 +924,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         const Layout L{bs, D, p.num_kv_heads};
         const I8Layout L8{bs, p.num_kv_heads};
         for (int j = 0; j < n && ok; ++j, ++c) {
-          const int st = c & 1, t0 = (w.tile0 + j) * kKv;
+          const int t0 = (w.tile0 + j) * kKv;
           // token u of the tile is read if its block holds an attended position
           auto find = [&](int u, int& b) -> bool {
             const int pos = t0 + u;
@@ -951,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               sc[1] = *reinterpret_cast<const float*>(p.cache + L8.scale(b, w.kvh, 1, t));
             }
           }
-          if (c >= 2 && !wait(&sh.k_empty[st], ((c >> 1) - 1) & 1)) {
+          if (!wait_empty(2 * c)) {
             ok = false;
             break;
           }
@@ -969,12 +977,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           for (int part = 0; part < 2; ++part) {
             if (part == 1) {
               if constexpr (!kI8) load(1);
-              if (c >= 2 && !wait(&sh.v_empty[st], ((c >> 1) - 1) & 1)) {
+              if (!wait_empty(2 * c + 1)) {
                 ok = false;
                 break;
               }
             }
-            uint8_t* dst = (part ? vbuf : kbuf) + st * C::kTileBytes;
+            uint8_t* dst = buffer(2 * c + part);
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
               const int u = (ct + e * 128) / kPer, piece = (ct + e * 128) % kPer;
@@ -1012,7 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(part ? &sh.v_full[st] : &sh.k_full[st]);
+            if (lane == 0) mbar_arrive(&sh.full[(2 * c + part) % NB]);
           }
         }
         if (ok) done_item(i);
@@ -1054,7 +1062,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int n = t == 0 ? w.n[0] : w.n[1];
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++num) {
-        const int jt = w.alt ? 2 * j + t : j, c = w.c0 + jt, st = c & 1;
+        const int jt = w.alt ? 2 * j + t : j, c = w.c0 + jt;
         const int t0 = (w.tile0 + jt) * kKv;
         if (!wait(&sh.s_full[t], num & 1)) {
           ok = false;
@@ -1095,12 +1103,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             if (ragged(w, jt)) {
               // thread = token here: V rows that hold no token of the context become
               // zero (V has landed: the issuer waited for it)
-              if (!wait(&sh.v_full[st], (c >> 1) & 1)) {
+              if (!wait(&sh.full[(2 * c + 1) % NB], ((2 * c + 1) / NB) & 1)) {
                 ok = false;
                 break;
               }
               if (t0 + row >= w.kv_end || t0 + row < w.first) {
-                uint8_t* v = vbuf + st * C::kTileBytes;
+                uint8_t* v = buffer(2 * c + 1);
 #pragma unroll 2
                 for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
               }
@@ -1163,12 +1171,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             y[k] = Elem<PT>::pack2(a, b);
           }
           tc::tmem_st16u(s_addr + e * 16, y);
-          if (e == kKv / 64 - 1) {
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_half[t]);
-          }
         }
         {
           float a, b;
@@ -1273,6 +1275,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 
   tc::fence_before_sync();
   __syncthreads();
+  // Never leave copies in flight: all have been waited for by the products, unless a role gave up.
+  if (!C::kConvert && threadIdx.x == 0 && sh.abort_flag)
+    for (int i = 0; i < NB; ++i) {
+      const int n = sh.last_fill[i];
+      if (n >= 0 && !bar_wait(&sh.full[i], (n / NB) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+    }
   if (warp == 8) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
@@ -1373,11 +1381,13 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
 template <typename T, int D, Fill F>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
   using C = Cfg<D, F>;
-  cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F>>(C::kSmem);
+  constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) : 0);
+  static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
+  cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F>>(smem);
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, ws, sms);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  extend_kernel<T, D, F><<<sms, C::kThreads, C::kSmem, stream>>>(p, ws);
+  extend_kernel<T, D, F><<<sms, C::kThreads, smem, stream>>>(p, ws);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   finish_kernel<T, D><<<2 * sms, 256, 0, stream>>>(p, ws);
   return cudaGetLastError();

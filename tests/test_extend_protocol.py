@@ -29,16 +29,17 @@ class Model:
     def __init__(self, items, convert, plant=""):
         self.items, self.convert, self.plant = items, convert, plant
         fill = 4 if convert else 1
-        self.k_full, self.v_full = [[Bar(fill) for _ in range(2)] for _ in range(2)]
-        self.k_empty, self.v_empty, self.q_full, self.q_empty, self.s_full, self.p_half, self.p_full = \
-            [[Bar(4 if i >= 5 else 1) for _ in range(2)] for i in range(7)]
+        self.nb = nb = 4 if convert else 5
+        self.full, self.empty = [Bar(fill) for _ in range(nb)], [Bar(1) for _ in range(nb)]
+        self.q_full, self.q_empty, self.s_full, self.p_half, self.p_full = \
+            [[Bar(4 if i >= 3 else 1) for _ in range(2)] for i in range(5)]
         self.pv_done = [[Bar(1) for _ in range(2)] for _ in range(2)]
         self.item_full = [Bar(1) for _ in range(RING)]
         self.item_empty = [Bar(14 if convert else 11) for _ in range(RING)]
         self.sc_full = [Bar(4) for _ in range(SCALES)]
         self.xbar = Bar(8)
         self.work = [None] * RING
-        self.k, self.v, self.q = [None] * 2, [None] * 2, [None] * 2
+        self.kv, self.q = [None] * nb, [None] * 2
         self.sc = [[None] * 4 for _ in range(SCALES)]
         self.s = [[None] * 4 for _ in range(2)]          # S / P per query tile and warp
         self.o = [None] * 2
@@ -74,20 +75,19 @@ class Model:
                 c += n
                 continue
             for j in range(n):
-                st = c & 1
-                if c >= 2:
-                    yield from self.wait(self.k_empty[st], (c // 2 - 1) & 1)
+                yield from self.wait_empty(2 * c)
                 yield
-                self.fill(self.k, "k", st, c)
-                self.k_full[st].arrive()
+                self.fill(self.kv, "kv", 2 * c % self.nb, 2 * c)
+                self.full[2 * c % self.nb].arrive()
                 c += 1
 
     def fill(self, buf, kind, st, c):
         assert not self.reading.get((kind, st)), f"{kind} stage {st} overwritten while read"
         buf[st] = c
 
-    def consume(self, arrive=1):
-        """Items in order, for one warp (generator of work; the caller sends done)."""
+    def wait_empty(self, n):
+        if n >= self.nb:
+            yield from self.wait(self.empty[n % self.nb], (n // self.nb - 1) & 1)
 
     def next_item(self, i):
         yield from self.wait(self.item_full[i % RING], (i // RING) & 1)
@@ -101,12 +101,10 @@ class Model:
                 return
             assert w["i"] == i
             for j in range(self.tiles(w)):
-                st = c & 1
-                if c >= 2:
-                    yield from self.wait(self.v_empty[st], (c // 2 - 1) & 1)
+                yield from self.wait_empty(2 * c + 1)
                 yield
-                self.fill(self.v, "v", st, c)
-                self.v_full[st].arrive()
+                self.fill(self.kv, "kv", (2 * c + 1) % self.nb, 2 * c + 1)
+                self.full[(2 * c + 1) % self.nb].arrive()
                 c += 1
             self.item_empty[i % RING].arrive()
             i += 1
@@ -118,22 +116,18 @@ class Model:
             if w is None:
                 return
             for j in range(self.tiles(w)):
-                st = c & 1
-                if c >= 2:
-                    yield from self.wait(self.k_empty[st], (c // 2 - 1) & 1)
+                yield from self.wait_empty(2 * c)
                 yield
                 n = SCALES
                 assert not self.reading.get(("sc", c % n)), "scales overwritten while read"
                 self.sc[c % n][me] = c
                 self.sc_full[c % n].arrive()
-                yield
-                self.fill(self.k, "k", st, c)
-                self.k_full[st].arrive()
-                if c >= 2:
-                    yield from self.wait(self.v_empty[st], (c // 2 - 1) & 1)
-                yield
-                self.fill(self.v, "v", st, c)
-                self.v_full[st].arrive()
+                for part in (0, 1):
+                    if part:
+                        yield from self.wait_empty(2 * c + 1)
+                    yield
+                    self.fill(self.kv, "kv", (2 * c + part) % self.nb, 2 * c + part)
+                    self.full[(2 * c + part) % self.nb].arrive()
                 c += 1
             self.item_empty[i % RING].arrive()
             i += 1
@@ -159,10 +153,16 @@ class Model:
     def products(self):
         seen = {"k": 0, "v": 0, 0: 0, 1: 0}
 
-        def in_order(key, bars, x, per):
-            while seen[key] <= x:
-                yield from self.wait(bars[seen[key] % per], (seen[key] // per) & 1)
+        def filled(key, c):
+            while seen[key] <= c:
+                n = 2 * seen[key] + (key == "v")
+                yield from self.wait(self.full[n % self.nb], (n // self.nb) & 1)
                 seen[key] += 1
+
+        def rows(t, load):
+            while seen[t] <= load:
+                yield from self.wait(self.q_full[t], seen[t] & 1)
+                seen[t] += 1
 
         owed, num = [None, None], [0, 0]
 
@@ -170,14 +170,14 @@ class Model:
             if owed[t] is None:
                 return
             c, first, last = owed[t]
-            yield from in_order("v", self.v_full, c, 2)
+            yield from filled("v", c)
             yield from self.wait(self.p_half[t], num[t] & 1)
-            self.tensor.append(("pv", t, c & 1, c, first, 0))
+            self.tensor.append(("pv", t, (2 * c + 1) % self.nb, c, first, 0))
             yield from self.wait(self.p_full[t], num[t] & 1)
-            self.tensor.append(("pv", t, c & 1, c, first, 1))
+            self.tensor.append(("pv", t, (2 * c + 1) % self.nb, c, first, 1))
             self.tensor.append(("commit", self.pv_done[t][num[t] & 1]))
             if last:
-                self.tensor.append(("commit", self.v_empty[c & 1]))
+                self.tensor.append(("commit", self.empty[(2 * c + 1) % self.nb]))
             num[t] += 1
             owed[t] = None
 
@@ -209,16 +209,16 @@ class Model:
                     jt = 2 * j + t if alt else j
                     c = w["c0"] + jt
                     qt = 0 if alt else t
-                    yield from in_order("k", self.k_full, c, 2)
-                    yield from in_order(qt, [self.q_full[qt]], w["qload"][qt], 1)
+                    yield from filled("k", c)
+                    yield from rows(qt, w["qload"][qt])
                     if jt in w["edges"]:
-                        yield from in_order("v", self.v_full, c, 2)
+                        yield from filled("v", c)
                     last_k = alt or t == 1 or jt >= other or self.plant == "the first user releases"
                     last_q = j == n[t] - 1 and (not alt or (other < n[t] if t == 0 else other <= n[t]))
-                    self.tensor.append(("qk", t, qt, c & 1, c, i))
+                    self.tensor.append(("qk", t, qt, 2 * c % self.nb, c, i))
                     self.tensor.append(("commit", self.s_full[t]))
                     if last_k:
-                        self.tensor.append(("commit", self.k_empty[c & 1]))
+                        self.tensor.append(("commit", self.empty[2 * c % self.nb]))
                     if last_q:
                         self.tensor.append(("commit", self.q_empty[qt]))
                     owed[t] = (c, j == 0, last_k)
@@ -234,19 +234,19 @@ class Model:
                 op[1].arrive()
             elif op[0] == "qk":
                 _, t, qt, st, c, item = op
-                for key in (("k", st), ("q", qt)):
+                for key in (("kv", st), ("q", qt)):
                     self.reading[key] = self.reading.get(key, 0) + 1
                 yield
-                assert self.k[st] == c and self.q[qt] == item, (self.k, self.q, op)
-                for key in (("k", st), ("q", qt)):
+                assert self.kv[st] == 2 * c and self.q[qt] == item, (self.kv, self.q, op)
+                for key in (("kv", st), ("q", qt)):
                     self.reading[key] -= 1
                 self.s[t] = [("s", c)] * 4
             else:
                 _, t, st, c, first, half = op
-                self.reading[("v", st)] = self.reading.get(("v", st), 0) + 1
+                self.reading[("kv", st)] = self.reading.get(("kv", st), 0) + 1
                 yield
-                assert self.v[st] == c and all(x in ((("h", c), ("p", c)) if half == 0 else (("p", c),)) for x in self.s[t]), op
-                self.reading[("v", st)] -= 1
+                assert self.kv[st] == 2 * c + 1 and all(x in ((("h", c), ("p", c)) if half == 0 else (("p", c),)) for x in self.s[t]), op
+                self.reading[("kv", st)] -= 1
                 assert not self.reading.get(("o", t)), "accumulator overwritten while read"
                 if half:
                     self.o[t] = [c] if first else self.o[t] + [c]
@@ -264,7 +264,7 @@ class Model:
             for j in range(w["n"][t]):
                 jt = 2 * j + t if w["alt"] else j
                 c = w["c0"] + jt
-                st = c & 1
+                st = (2 * c + 1) % self.nb
                 yield from self.wait(self.s_full[t], num & 1)
                 assert self.s[t][me] == ("s", c)
                 if self.convert:
@@ -277,11 +277,11 @@ class Model:
                     assert self.sc[c % n] == [c] * 4
                     self.reading[("sc", c % n)] -= 1
                 if jt in w["edges"] and not self.convert:
-                    yield from self.wait(self.v_full[st], (c // 2) & 1)
-                    self.reading[("v", st)] = self.reading.get(("v", st), 0) + 1
+                    yield from self.wait(self.full[st], ((2 * c + 1) // self.nb) & 1)
+                    self.reading[("kv", st)] = self.reading.get(("kv", st), 0) + 1
                     yield
-                    assert self.v[st] == c
-                    self.reading[("v", st)] -= 1
+                    assert self.kv[st] == 2 * c + 1
+                    self.reading[("kv", st)] -= 1
                 if j > 0 and rng.random() < 0.3:         # the rescale
                     yield from self.wait(self.pv_done[t][(num - 1) & 1], ((num - 1) // 2) & 1)
                     assert self.o[t][-1] == c - (2 if w["alt"] else 1)
