@@ -771,129 +771,144 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const uint64_t kd0 = tc::smem_desc(smem_u32(ring), 16, C::kGroupBytes, tc::kSwizzle128B);
       const uint64_t vd0 = tc::smem_desc(smem_u32(ring), 1024, C::kGroupBytes, tc::kSwizzle128B);
       bool ok = true;
-      auto spin = [&](uint64_t* bar, uint32_t parity) {
-        if (!ok) return;
-        for (uint32_t i = 0; i < 8 * kPolls; ++i) {
-          if (__all_sync(kFull, mbar_test_wait(bar, parity))) {
-            tc::fence_after_sync();
-            return;
+      // Every instruction between two batches of products is felt: the tensor cores
+      // queue only about four of them ahead (256 clocks).
+      auto spin = [&](uint64_t* bar, uint32_t parity, bool there) {
+        if (!__all_sync(kFull, there)) {
+          for (uint32_t i = 0; ok && !__all_sync(kFull, mbar_test_wait(bar, parity)); ++i)
+            if ((i & 255) == 255 && (i > 8 * kPolls || __any_sync(kFull, sh.abort_flag))) ok = false;
+        }
+        tc::fence_after_sync();
+      };
+      // The ring's buffer and phase of the next K fill; its V fill is the one after.
+      // Fills are used, and so waited for, in order, each at least once: no phase of a
+      // barrier is skipped, so its parity never stands for one two phases back.
+      struct Fills {
+        int kb = 0;
+        uint32_t kp = 0;
+        __device__ int vb() const { return kb == NB - 1 ? 0 : kb + 1; }
+        __device__ uint32_t vp() const { return kb == NB - 1 ? kp ^ 1u : kp; }
+        __device__ void next() {
+          kb += 2;
+          if (kb >= NB) {
+            kb -= NB;
+            kp ^= 1u;
           }
-          if ((i & 255) == 255 && __any_sync(kFull, sh.abort_flag)) break;
-        }
-        ok = false;
-      };
-      // Fills of K and of V are waited for in order, each phase once: the parity of a
-      // barrier two phases behind would say it is complete.  A fill is looked at one
-      // step before it is needed (look), so that the answer comes while products are
-      // issued: shared memory is slow to answer while they read it.
-      int k_seen = 0, v_seen = 0, q_seen0 = 0, q_seen1 = 0;
-      bool k_there = false, v_there = false;
-      auto k_look = [&]() { k_there = mbar_test_wait(&sh.full[2 * k_seen % NB], (2 * k_seen / NB) & 1); };
-      auto v_look = [&]() { v_there = mbar_test_wait(&sh.full[(2 * v_seen + 1) % NB], ((2 * v_seen + 1) / NB) & 1); };
-      auto k_wait = [&](int c) {
-        for (; k_seen <= c; ++k_seen) {
-          if (!__all_sync(kFull, k_there)) spin(&sh.full[2 * k_seen % NB], (2 * k_seen / NB) & 1);
-          k_there = false;
         }
       };
-      auto v_wait = [&](int c) {
-        for (; v_seen <= c; ++v_seen) {
-          if (!__all_sync(kFull, v_there)) spin(&sh.full[(2 * v_seen + 1) % NB], ((2 * v_seen + 1) / NB) & 1);
-          v_there = false;
-        }
-      };
-      // the product that each query tile still owes: its KV tile's ring number, steps of 16 tokens, flags
+      // the product that each query tile still owes
       struct Owed {
-        int c = -1, steps = 0, first = 0, last_user = 0, num = 0;
+        int buf = -1, steps = 0;           // V's buffer; steps of 16 tokens
+        uint32_t phase = 0, num = 0;       // V's phase; KV tiles of this query tile so far
+        bool first = false, wait_v = false, last_user = false;
       };
       Owed owed0, owed1;
+      Fills fill;
+      bool k_there = false;
       auto pv = [&](auto which, Owed& x) {
         constexpr int t = decltype(which)::value;
-        if (x.c < 0) return;
-        const int st = (2 * x.c + 1) % NB;
-        const uint64_t vd = vd0 + (uint64_t)((st * C::kTileBytes) >> 4);
-        v_wait(x.c);
-        spin(&sh.p_full[t], x.num & 1);
-        k_look();
+        if (x.buf < 0) return;
+        const bool p_there = mbar_test_wait(&sh.p_full[t], x.num & 1);
+        if (x.wait_v) spin(&sh.full[x.buf], x.phase, mbar_test_wait(&sh.full[x.buf], x.phase));
+        spin(&sh.p_full[t], x.num & 1, p_there);
+        // the next K is looked at now: shared memory is slow to answer while products read it
+        k_there = mbar_test_wait(&sh.full[fill.kb], fill.kp);
+        const uint64_t vd = vd0 + (uint64_t)((x.buf * C::kTileBytes) >> 4);
         if (ok && tc::elect()) {
+          tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv, vd, id_pv, (uint32_t)!x.first);
+          if (x.steps == kKv / 16) {
 #pragma unroll
-          for (int k = 0; k < kKv / 16; ++k)
-            if (k < x.steps)
-              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8,
-                             vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4), id_pv, k > 0 ? 1u : (uint32_t)!x.first);
+            for (int k = 1; k < kKv / 16; ++k)
+              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8, vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
+                             id_pv, 1u);
+          } else {
+            for (int k = 1; k < x.steps; ++k)
+              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8, vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
+                             id_pv, 1u);
+          }
           tc::commit(&sh.pv_done[t][x.num & 1]);
-          if (x.last_user) tc::commit(&sh.empty[st]);
+          if (x.last_user) tc::commit(&sh.empty[x.buf]);
         }
         __syncwarp();
         ++x.num;
-        x.c = -1;
+        x.buf = -1;
       };
+      auto flush = [&]() {
+        pv(std::integral_constant<int, 0>{}, owed0);
+        pv(std::integral_constant<int, 1>{}, owed1);
+      };
+      uint32_t q_num0 = 0, q_num1 = 0;                               // loads of each query tile so far
+      auto uni = [&](int v) { return __shfl_sync(kFull, v, 0); };
       for (int i = 0; ok; ++i) {
         const int slot = i % kRing;
-        if (!__all_sync(kFull, mbar_test_wait(&sh.item_full[slot], (i / kRing) & 1))) {
-          // nothing to go on with yet: what is owed first
-          pv(std::integral_constant<int, 0>{}, owed0);
-          pv(std::integral_constant<int, 1>{}, owed1);
-          spin(&sh.item_full[slot], (i / kRing) & 1);
-        }
+        uint64_t* bar = &sh.item_full[slot];
+        const uint32_t par = (i / kRing) & 1;
+        if (!__all_sync(kFull, mbar_test_wait(bar, par))) flush();   // nothing to go on with: what is owed first
+        spin(bar, par, false);
         if (!ok) break;
         const Work& w = sh.work[slot];
-        auto uni = [&](int v) { return __shfl_sync(kFull, v, 0); };
-        if (uni(w.kvh) < 0) {
-          pv(std::integral_constant<int, 0>{}, owed0);
-          pv(std::integral_constant<int, 1>{}, owed1);
-          break;
-        }
-        const int n0 = uni(w.n[0]), n1 = uni(w.n[1]), alt = uni(w.alt), c0 = uni(w.c0);
+        if (uni(w.kvh) < 0) break;
+        const int n0 = uni(w.n[0]), n1 = uni(w.n[1]);
+        const bool alt = uni(w.alt) != 0;
         const int tok = uni(w.kv_end) - uni(w.tile0) * kKv;          // tokens from the first KV tile on
         const int skip = uni(w.first) - uni(w.tile0) * kKv;          // of them, before the first attended one
-        const int load0 = uni(w.qload[0]), load1 = uni(w.qload[1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.item_empty[slot]);
+        const int rounds = max(n0, n1);
+        if (rounds == 0) continue;
+        // its rows may still be on their way: then what is owed goes first
+        const bool load0 = n0 > 0, load1 = !alt && n1 > 0;
+        pv(std::integral_constant<int, 0>{}, owed0);
+        if (load0) {
+          const bool there = mbar_test_wait(&sh.q_full[0], q_num0 & 1);
+          if (!__all_sync(kFull, there)) pv(std::integral_constant<int, 1>{}, owed1);
+          spin(&sh.q_full[0], q_num0 & 1, there);
+          ++q_num0;
+        }
         auto turn = [&](auto which, Owed& x, int j, int n, int other) {
           constexpr int t = decltype(which)::value;
           pv(which, x);
           if (j >= n) return;
-          const int jt = alt ? 2 * j + t : j, c = c0 + jt, st = 2 * c % NB;
-          const bool q0 = t == 0 || alt;                             // which query tile's rows
-          k_wait(c);
-          if (q0) {
-            for (; q_seen0 <= load0; ++q_seen0) spin(&sh.q_full[0], q_seen0 & 1);
-          } else {
-            for (; q_seen1 <= load1; ++q_seen1) spin(&sh.q_full[1], q_seen1 & 1);
+          const int jt = alt ? 2 * j + t : j;                        // KV tile of the item
+          // the last of the (one or two) query tiles that use this K and V
+          const bool both = !alt && j < other, last_k = !both || t == 1;
+          const int kb = fill.kb, vb = fill.vb();
+          const uint32_t vp = fill.vp();
+          if (!both || t == 0) spin(&sh.full[kb], fill.kp, k_there);
+          k_there = false;
+          if (t == 1 && load1 && j == 0) {
+            spin(&sh.q_full[1], q_num1 & 1, false);
+            ++q_num1;
           }
-          if (!kI8 && (jt * kKv < skip || (jt + 1) * kKv > tok)) v_wait(c);   // ragged: its softmax writes V
-          const uint64_t qd = qd0 + (uint64_t)((q0 ? 0 : C::kQBytes) >> 4);
-          const uint64_t kd = kd0 + (uint64_t)((st * C::kTileBytes) >> 4);
-          // the last of the (one or two) query tiles that use this K and V; of those that use this Q
-          const bool last_k = alt || t == 1 || jt >= other;
+          const int after = tok - jt * kKv;                          // tokens from this KV tile on
+          if (!kI8 && (jt * kKv < skip || after < kKv)) spin(&sh.full[vb], vp, false);   // its softmax writes V
+          const uint64_t qd = qd0 + (uint64_t)((t == 0 || alt ? 0 : C::kQBytes) >> 4);
+          const uint64_t kd = kd0 + (uint64_t)((kb * C::kTileBytes) >> 4);
           const bool last_q = j == n - 1 && (!alt || (t == 0 ? other < n : other <= n));
-          v_look();
           if (ok && tc::elect()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               tc::mma_f16(tmem + t * kKv, qd + (uint64_t)(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4),
                           kd + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id_qk, kk > 0);
             tc::commit(&sh.s_full[t]);
-            if (last_k) tc::commit(&sh.empty[st]);
-            if (last_q) tc::commit(q0 ? &sh.q_empty[0] : &sh.q_empty[1]);
+            if (last_k) tc::commit(&sh.empty[kb]);
+            if (last_q) tc::commit(&sh.q_empty[alt ? 0 : t]);
           }
           __syncwarp();
-          x.c = c;
-          x.steps = min(kKv / 16, (tok - jt * kKv + 15) >> 4);
+          x.buf = vb;
+          x.phase = vp;
+          x.steps = after >= kKv ? kKv / 16 : (after + 15) >> 4;
           x.first = j == 0;
+          x.wait_v = !both || t == 0;
           x.last_user = last_k;
+          if (last_k) fill.next();
         };
-        // its rows may still be on their way: then the other tile's product goes first
-        pv(std::integral_constant<int, 0>{}, owed0);
-        if (n0 > 0 && q_seen0 <= load0 && !__all_sync(kFull, mbar_test_wait(&sh.q_full[0], q_seen0 & 1)))
-          pv(std::integral_constant<int, 1>{}, owed1);
-        const int rounds = max(n0, n1);
         for (int j = 0; j < rounds && ok; ++j) {
           turn(std::integral_constant<int, 0>{}, owed0, j, n0, n1);
           turn(std::integral_constant<int, 1>{}, owed1, j, n1, n0);
         }
       }
+      flush();
       if (!ok && lane == 0) give_up();
       // every product issued completes before TMEM can be freed
       if (tc::elect()) {
