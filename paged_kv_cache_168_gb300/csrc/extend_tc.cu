@@ -38,7 +38,8 @@
 //   warp 9          draws items, publishes them in a ring, and copies K tiles
 //                   (8-token groups, one bulk copy each) into the ring of K and V.
 //   warp 10         copies V tiles.
-//   warp 11         gathers Q rows into the swizzled K-major operand.
+//   warp 11         copies Q rows (positions x heads of the kv head) into the
+//                   swizzled K-major operand.
 //   warps 12-15     (caches whose chunks are not operands: 8-bit codes, blocks
 //                   of fewer than 8 tokens) fill the K and V stages in place of
 //                   the copies: codes become exact 16-bit integers, and the
@@ -47,8 +48,10 @@
 //                   at most 2^8 whatever the scales are.
 // Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, and the CTA drains its
 // own copies and products before releasing TMEM.
+#include <cuda.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -396,8 +399,8 @@ struct __align__(16) Shared {
   float red[2][kRows][2];                  // the other warpgroup's (maximum, sum)
   uint32_t tmem_base;
   volatile int abort_flag;
-  int last_fill[5];                        // the last copies into each buffer, -1: none
-  int pad[2];
+  int last_fill[5], last_q[2];             // the last copies into each buffer, -1: none
+  int pad[3];
 };
 struct __align__(16) Scales {
   float k[kScaleRing][kKv], lv[kScaleRing][kKv], iv[kScaleRing][kKv];
@@ -469,17 +472,23 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  const int n = take ? 16 : 0;             // 0: the destination is zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// Tensor copies global -> shared, completing their bytes on `bar`.
+__device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void tma_load4(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
 
-// Offset of the 16-byte piece (8 dims) of row r in a 128B-swizzled K-major operand of 128 rows.
-__device__ __forceinline__ uint32_t q_offset(int r, int piece) {
-  return (uint32_t)((piece >> 3) * (kRows * 128) + (r >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
-}
-// The same piece of token r in a K or V stage (8-token groups, a group's 64-dim atoms together).
+// Offset of the 16-byte piece (8 dims) of token r in a K or V stage (8-token groups, a group's 64-dim atoms together).
 template <int D>
 __device__ __forceinline__ uint32_t kv_offset(int r, int piece) {
   return (uint32_t)((r >> 3) * (8 * D * 2) + (piece >> 3) * 1024 + (r & 7) * 128 + (((piece & 7) ^ (r & 7)) << 4));
@@ -498,7 +507,9 @@ __device__ __forceinline__ int block_of(const ExtendParams& p, const int32_t* ro
 
 template <typename T, int D, Fill F>
 __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
-                                                                       const __grid_constant__ Space ws) {
+                                                                       const __grid_constant__ Space ws,
+                                                                       const __grid_constant__ CUtensorMap q_map,
+                                                                       const __grid_constant__ CUtensorMap kv_map) {
   using C = Cfg<D, F>;
   constexpr bool kI8 = F == kCodes;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
@@ -531,6 +542,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       mbar_init(&sh.empty[i], 1);
       sh.last_fill[i] = -1;
     }
+    sh.last_q[0] = sh.last_q[1] = -1;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.item_full[i], 1);
       // 8 softmax warps, the issuing warp, the Q warp, and the V warp or 4 converter warps
@@ -573,6 +585,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   // fill n's buffer: free to be filled / filled
   auto wait_empty = [&](int n) -> bool { return n < NB || wait(&sh.empty[n % NB], (n / NB - 1) & 1); };
   auto buffer = [&](int n) { return ring + (n % NB) * C::kTileBytes; };
+  // fill n: the K (part 0) or V (part 1) vectors of the blocks `id` of the lanes that take one, one copy a block
+  auto copy_blocks = [&](int n, int part, int id, int kvh, bool take) {
+    const uint32_t bytes = bs / 8 * C::kGroupBytes;
+    const unsigned m = __ballot_sync(kFull, take);
+    uint64_t* bar = &sh.full[n % NB];
+    if (lane == 0) {
+      sh.last_fill[n % NB] = n;
+      mbar_arrive_expect_tx(bar, (uint32_t)__popc(m) * bytes);
+    }
+    __syncwarp();
+    if (take)
+      tma_load4(buffer(n) + lane * bytes, &kv_map, 0, 0, part, (id * p.num_kv_heads + kvh) * (bs / 8), bar);
+    __syncwarp();
+  };
   // KV tiles of an item
   auto tiles_of = [](const Work& w) { return w.alt ? w.n[0] + w.n[1] : max(w.n[0], w.n[1]); };
 
@@ -642,9 +668,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;   // blocks [fb, nblk) are read
           for (int j = 0; j < n; ++j, ++c) {
-            // lane l < 16 copies the tile's 8-token group l
-            const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
-            const bool take = lane < 16 && blk >= fb && blk < nblk;
+            // lane l copies the tile's block l
+            const int blk = (w.tile0 + j) * (kKv / bs) + lane;
+            const bool take = lane < kKv / bs && blk >= fb && blk < nblk;
             int id = take ? block_of(p, row, blk) : 0;
             if (take && (unsigned)id >= (unsigned)p.num_blocks) {
               id = 0;
@@ -654,16 +680,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               ok = false;
               break;
             }
-            const unsigned m = __ballot_sync(kFull, take);
-            if (lane == 0) sh.last_fill[2 * c % NB] = 2 * c;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[2 * c % NB], (uint32_t)__popc(m) * C::kGroupBytes);
-            __syncwarp();
-            if (take) {
-              const int g = (lane & 15) & (bs / 8 - 1);             // group within the block
-              bulk_g2s(buffer(2 * c) + (lane & 15) * C::kGroupBytes,
-                       p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes),
-                       C::kGroupBytes, &sh.full[2 * c % NB]);
-            }
+            copy_blocks(2 * c, 0, id, w.kvh, take);
           }
         } else {
           c += n;
@@ -688,25 +705,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;
           for (int j = 0; j < n; ++j, ++c) {
-            const int blk = ((w.tile0 + j) * kKv + (lane & 15) * 8) / bs;
-            const bool take = lane < 16 && blk >= fb && blk < nblk;
+            const int blk = (w.tile0 + j) * (kKv / bs) + lane;
+            const bool take = lane < kKv / bs && blk >= fb && blk < nblk;
             int id = take ? block_of(p, row, blk) : 0;
             if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;      // reported by the K copies
             if (!wait_empty(2 * c + 1)) {
               ok = false;
               break;
             }
-            const unsigned m = __ballot_sync(kFull, take);
-            if (lane == 0) sh.last_fill[(2 * c + 1) % NB] = 2 * c + 1;
-            if (lane == 0) mbar_arrive_expect_tx(&sh.full[(2 * c + 1) % NB], (uint32_t)__popc(m) * C::kGroupBytes);
-            __syncwarp();
-            if (take) {
-              const int g = (lane & 15) & (bs / 8 - 1);
-              bulk_g2s(buffer(2 * c + 1) + (lane & 15) * C::kGroupBytes,
-                       p.cache + (((int64_t)id * p.num_kv_heads + w.kvh) * (bs / 8) + g) * (2 * C::kGroupBytes) +
-                           C::kGroupBytes,
-                       C::kGroupBytes, &sh.full[(2 * c + 1) % NB]);
-            }
+            copy_blocks(2 * c + 1, 1, id, w.kvh, take);
           }
           if (ok) done_item(i);
         }
@@ -731,29 +738,17 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             ok = false;
             continue;
           }
-          const int rows = (w.alt ? w.npos : min(ptile, w.npos - t * ptile)) * G;
-          const T* q = static_cast<const T*>(p.q) + (int64_t)(w.row0 + t * ptile) * p.q_token_stride +
-                       (int64_t)w.kvh * G * D;
-          const uint32_t dst = smem_u32(qbuf + t * C::kQBytes);
-          constexpr int kStep = 32 / (D / 8);                        // rows a round of the warp takes
-          const int piece = lane % (D / 8);
-          int r = lane / (D / 8), h = r % G;
-          const T* src = q + (int64_t)(r / G) * p.q_token_stride + h * D + piece * 8;
-#pragma unroll 8
-          for (int k = 0; k < kRows / kStep; ++k) {
-            cp_async16(dst + q_offset(r, piece), r < rows ? src : q, r < rows);
-            r += kStep;
-            h += kStep;
-            src += kStep * D;
-            while (h >= G) {                                         // the next token
-              h -= G;
-              src += p.q_token_stride - G * D;
-            }
+          // ptile positions x group heads, 64 dims a copy; rows past the sequence's are
+          // the next sequence's (or zero behind the last token), and are not used
+          if (lane == 0) {
+            sh.last_q[t] = load;
+            mbar_arrive_expect_tx(&sh.q_full[t], (uint32_t)(ptile * G * D * 2));
+#pragma unroll
+            for (int a = 0; a < D / 64; ++a)
+              tma_load3(qbuf + t * C::kQBytes + a * (kRows * 128), &q_map, a * 64, w.kvh * G, w.row0 + t * ptile,
+                        &sh.q_full[t]);
           }
-          cp_async_wait();
-          tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full[t]);
         }
         if (ok) done_item(i);
       }
@@ -1140,7 +1135,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         const float unit = kI8 ? 1.f : p.scale_log2;                 // x is in base-2 units already (8-bit)
         mt *= unit;
         const float m_new = fmaxf(m, mt);
-        const bool need = m != -INFINITY && m_new > m + kRescaleThreshold;
+        const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
         if (m == -INFINITY) m = m_new;
         if (__any_sync(kFull, need)) {
           // O holds exactly the tiles before this one once the last PV has completed
@@ -1291,11 +1286,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   tc::fence_before_sync();
   __syncthreads();
   // Never leave copies in flight: all have been waited for by the products, unless a role gave up.
-  if (!C::kConvert && threadIdx.x == 0 && sh.abort_flag)
+  if (threadIdx.x == 0 && sh.abort_flag) {
     for (int i = 0; i < NB; ++i) {
       const int n = sh.last_fill[i];
       if (n >= 0 && !bar_wait(&sh.full[i], (n / NB) & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
     }
+    for (int i = 0; i < 2; ++i)
+      if (sh.last_q[i] >= 0 && !bar_wait(&sh.q_full[i], sh.last_q[i] & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
+  }
   if (warp == 8) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
@@ -1393,6 +1391,54 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
   }
 }
 
+// ------------------------------------------------------------------ launch
+// The driver's encoder of tensor maps (looked up once).
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+cudaError_t encoder(EncodeTiled* f) {
+  static std::atomic<EncodeTiled> known{nullptr};
+  *f = known.load(std::memory_order_acquire);
+  if (*f) return cudaSuccess;
+  void* at = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !at) return cudaErrorSymbolNotFound;
+  *f = reinterpret_cast<EncodeTiled>(at);
+  known.store(*f, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// q as [token][head][dim], copied as ptile tokens x group heads x 64 dims into 128B-swizzled rows; the pool as
+// [8-token group][K, V][D * 8 elements in rows of 256], copied as a block's groups of one part.
+template <int D, Fill F>
+cudaError_t encode_maps(const ExtendParams& p, int act_dtype, CUtensorMap* q_map, CUtensorMap* kv_map) {
+  EncodeTiled f;
+  const cudaError_t e = encoder(&f);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapDataType type = act_dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.num_q_heads, (cuuint64_t)p.num_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.q_token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(kRows / p.group)};
+    if (f(q_map, type, 3, const_cast<void*>(p.q), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  if (F == kBulk) {
+    const cuuint64_t groups = (cuuint64_t)p.num_blocks * p.num_kv_heads * (p.block_size / 8);
+    const cuuint64_t dims[4] = {256, D / 32, 2, groups};
+    const cuuint64_t strides[3] = {512, (cuuint64_t)D * 16, (cuuint64_t)D * 32};
+    const cuuint32_t box[4] = {256, D / 32, 1, (cuuint32_t)(p.block_size / 8)};
+    if (f(kv_map, type, 4, const_cast<uint8_t*>(p.cache), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  return cudaSuccess;
+}
+
 template <typename T, int D, Fill F>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
   using C = Cfg<D, F>;
@@ -1400,9 +1446,12 @@ cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStr
   static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
   cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F>>(smem);
   if (e != cudaSuccess) return e;
+  CUtensorMap q_map{}, kv_map{};
+  e = encode_maps<D, F>(p, std::is_same<T, __half>::value ? PA_F16 : PA_BF16, &q_map, &kv_map);
+  if (e != cudaSuccess) return e;
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, ws, sms);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  extend_kernel<T, D, F><<<sms, C::kThreads, smem, stream>>>(p, ws);
+  extend_kernel<T, D, F><<<sms, C::kThreads, smem, stream>>>(p, ws, q_map, kv_map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   finish_kernel<T, D><<<2 * sms, 256, 0, stream>>>(p, ws);
   return cudaGetLastError();
