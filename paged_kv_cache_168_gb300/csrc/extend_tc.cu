@@ -463,6 +463,23 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 32 TMEM lanes x 32 columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 template <int N>
 __device__ __forceinline__ void set_regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -1229,39 +1246,61 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const bool part = w.part_row >= 0;
       const float scale = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const int rr = (my0 + ipos) * G + head;                        // row within the item
-      T* orow = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0 + ipos) * p.num_q_heads + w.kvh * G + head) * D;
       float* prow = ws.o + (int64_t)(w.part_row + rr) * D;
+      T* tile = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0) * p.num_q_heads + w.kvh * G) * D;
+      // Rows leave 64 bytes at a time: a store of 16 bytes a row and lane asks for 32
+      // lines, and the stores alone took 6000 clocks an item.  Lanes 4i .. 4i + 3
+      // exchange 16-byte pieces until lane 4i + k holds piece k of each of their rows.
+      const int mine = row_ok ? (ipos * p.num_q_heads + head) * D : -1;   // my row in the tile's output
+      int rows4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(kFull, mine, (lane & ~3) + k);
       float odd = 0.f;
-      for (int e = col0; e < col0 + ncol; e += 16) {
-        float o[16];
+      for (int e = col0; e < col0 + ncol; e += 32) {
+        float o[32];
         if (have0) {
-          tc::tmem_ld16(o0 + e, o);
+          tmem_ld32(o0 + e, o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0.f;
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
         if (w.alt) {
-          float b[16];
+          float b[32];
           if (have1) {
-            tc::tmem_ld16(o1 + e, b);
+            tmem_ld32(o1 + e, b);
           } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) b[k] = 0.f;
+            for (int k = 0; k < 32; ++k) b[k] = 0.f;
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = o[k] * f[0] + b[k] * f[1];
+          for (int k = 0; k < 32; ++k) o[k] = o[k] * f[0] + b[k] * f[1];
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) odd = fmaf(o[k], 0.f, odd);     // NaN once any value is not finite
-        if (row_ok && !part) {
-          uint32_t y[8];
+        for (int k = 0; k < 32; ++k) odd = fmaf(o[k], 0.f, odd);     // NaN once any value is not finite
+        if (!part) {
+          uint32_t y[4][4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = Elem<T>::pack2(o[2 * k] * scale, o[2 * k + 1] * scale);
-          *reinterpret_cast<uint4*>(orow + e) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(orow + e + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-        } else if (row_ok) {
+          for (int k = 0; k < 16; ++k) y[k >> 2][k & 3] = Elem<T>::pack2(o[2 * k] * scale, o[2 * k + 1] * scale);
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {                          // a 4 x 4 transpose in two exchanges
+            const bool up = lane & d;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!(k & d)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const uint32_t got = __shfl_xor_sync(kFull, up ? y[k][i] : y[k + d][i], d);
+                  if (up) y[k][i] = got; else y[k + d][i] = got;
+                }
+              }
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
+            if (rows4[k] >= 0)
+              *reinterpret_cast<uint4*>(tile + rows4[k] + e + (lane & 3) * 8) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+        } else if (row_ok) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
             *reinterpret_cast<float4*>(prow + e + 4 * k) = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
