@@ -70,9 +70,20 @@ class CacheDesc:
     kv_int8: bool = False
 
     def c(self) -> _Desc:
-        return _Desc(self.num_blocks, self.block_size, self.num_kv_heads, self.head_size,
-                     DTYPE_CODE[self.dtype] + (2 if self.kv_int8 else 0), self.num_layers,
-                     self.layer_stride_bytes)
+        # the C struct of the current fields, rebuilt only when one has changed
+        key = (self.num_blocks, self.block_size, self.num_kv_heads, self.head_size, self.dtype, self.num_layers,
+               self.layer_stride_bytes, self.kv_int8)
+        if key != self.__dict__.get("_key"):
+            self._c = _Desc(self.num_blocks, self.block_size, self.num_kv_heads, self.head_size,
+                            DTYPE_CODE[self.dtype] + (2 if self.kv_int8 else 0), self.num_layers,
+                            self.layer_stride_bytes)
+            self._ref = ctypes.byref(self._c)
+            self._key = key
+        return self._c
+
+    def ref(self):
+        self.c()
+        return self._ref
 
 
 def load():
@@ -305,23 +316,11 @@ def _tensors(dtype, **tensors):
             raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be {dtype}, not {t.dtype}")
 
 
-def _rows(**tensors):
-    """[tokens, heads, dims] tensors: heads and dims contiguous (the token stride is free)."""
-    for name, t in tensors.items():
-        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be [tokens, heads, dims] with heads and dims "
-                                                   f"contiguous, not {tuple(t.shape)} with strides {t.stride()}")
-
-
-def _dense(**tensors):
-    for name, t in tensors.items():
-        if t is not None and not t.is_contiguous():
-            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be contiguous")
-
-
-def _same(name, got, want):
-    if got != want:
-        raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} is {got}, expected {want}")
+def _rows(t, shape, name):
+    """A [tokens, heads, dims] tensor of that shape with heads and dims contiguous (the token stride is free)."""
+    if t.shape != shape or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+        raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be [tokens, heads, dims] = {tuple(shape)} with heads and "
+                                               f"dims contiguous, not {tuple(t.shape)} with strides {t.stride()}")
 
 
 def rope_table(max_position: int, inv_freq: torch.Tensor, device="cuda") -> torch.Tensor:
@@ -332,6 +331,21 @@ def rope_table(max_position: int, inv_freq: torch.Tensor, device="cuda") -> torc
     return torch.cat([ang.cos(), ang.sin()], 1).to(torch.float32)
 
 
+def _on_device(fn, tensor, stream, *args):
+    """fn(*args, stream) with the tensor's device current: its given stream, or that device's current one."""
+    dev = tensor.get_device()
+    if dev >= 0 and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _on_device(fn, tensor, stream, *args)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
+    else:
+        raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    status = fn(*args, raw)
+    if status:
+        _check(status)
+
+
 def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, kv_cache: torch.Tensor,
                            desc: CacheDesc, key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor,
                            positions: torch.Tensor, cos_sin: torch.Tensor, pair_axis=None, interleaved: bool = False,
@@ -339,34 +353,38 @@ def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, k
     """pa_rope_reshape_and_cache: q/q_out [N, Hq, D] (or None), key/value [N, Hkv, D], positions int32 [N] or
     [axes, N], cos_sin fp32 [max_position, rotary_dim]; pair_axis uint8 per rotary pair on the host (None: all
     on axis 0)."""
-    n, hkv = key.shape[0], desc.num_kv_heads
-    _rows(key=key, value=value)
-    _same("key's shape", tuple(key.shape), (n, hkv, desc.head_size))
-    _same("value's shape", tuple(value.shape), (n, hkv, desc.head_size))
-    _tensors(desc.dtype, key=key, value=value, q=q, q_out=q_out)
-    _tensors(torch.int64, slot_mapping=slot_mapping)
-    _tensors(torch.int32, positions=positions)
-    _tensors(torch.float32, cos_sin=cos_sin)
-    _dense(slot_mapping=slot_mapping, cos_sin=cos_sin)
+    n, dt, kv_shape = key.shape[0], desc.dtype, (key.shape[0], desc.num_kv_heads, desc.head_size)
     axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape[-1] != n or slot_mapping.numel() != n or (n > 1 and positions.stride(-1) != 1):
-        raise PagedKVError(PA_ERR_INVALID_ARG, "positions and slot_mapping must have one dense entry per token")
-    hq = 0 if q is None else q.shape[1]
+    if not (key.dtype is dt and value.dtype is dt and slot_mapping.dtype is torch.int64
+            and positions.dtype is torch.int32 and cos_sin.dtype is torch.float32
+            and (q is None or (q.dtype is dt and q_out.dtype is dt))):
+        _tensors(dt, key=key, value=value, q=q, q_out=q_out)
+        _tensors(torch.int64, slot_mapping=slot_mapping)
+        _tensors(torch.int32, positions=positions)
+        _tensors(torch.float32, cos_sin=cos_sin)
+    _rows(key, kv_shape, "key")
+    _rows(value, kv_shape, "value")
+    hq = 0
     if q is not None:
-        _rows(q=q, q_out=q_out)
-        _same("q's shape", tuple(q.shape), (n, hq, desc.head_size))
-        _same("q_out's shape", tuple(q_out.shape), (n, hq, desc.head_size))
-    pa = None
+        hq = q.shape[1]
+        _rows(q, (n, hq, desc.head_size), "q")
+        _rows(q_out, (n, hq, desc.head_size), "q_out")
+    if not (slot_mapping.is_contiguous() and cos_sin.is_contiguous()) or positions.shape[-1] != n or \
+            slot_mapping.numel() != n or (n > 1 and positions.stride(-1) != 1):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "positions and slot_mapping must have one dense entry per token, and "
+                                               "cos_sin must be contiguous")
+    pairs = None
     if pair_axis is not None:
-        pa = pair_axis if isinstance(pair_axis, np.ndarray) and pair_axis.dtype == np.uint8 and \
-            pair_axis.flags.c_contiguous else np.ascontiguousarray(np.asarray(pair_axis, dtype=np.uint8))
-        _same("pair_axis' length", pa.size, cos_sin.shape[1] // 2)
-    _check(load().pa_rope_reshape_and_cache(
-        _ptr(q_out), 0 if q is None else q_out.stride(0), _ptr(q), 0 if q is None else q.stride(0), hq,
-        _ptr(kv_cache), ctypes.byref(desc.c()), layer, _ptr(key), key.stride(0), _ptr(value), value.stride(0),
-        _ptr(slot_mapping), _ptr(positions), positions.stride(0) if axes > 1 else 0, _ptr(cos_sin), cos_sin.shape[0],
-        cos_sin.shape[1], None if pa is None else pa.ctypes.data, axes, int(interleaved), n, _ptr(dev_err),
-        _stream(stream)))
+        pairs = np.asarray(pair_axis, dtype=np.uint8).tobytes()      # (ctypes passes its address)
+        if len(pairs) != cos_sin.shape[1] // 2:
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"pair_axis has {len(pairs)} entries, not {cos_sin.shape[1] // 2}")
+    _on_device(load().pa_rope_reshape_and_cache, key, stream,
+               None if q is None else q_out.data_ptr(), 0 if q is None else q_out.stride(0),
+               None if q is None else q.data_ptr(), 0 if q is None else q.stride(0), hq, kv_cache.data_ptr(),
+               desc.ref(), layer, key.data_ptr(), key.stride(0), value.data_ptr(), value.stride(0),
+               slot_mapping.data_ptr(), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
+               cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], pairs, axes,
+               1 if interleaved else 0, n, None if dev_err is None else dev_err.data_ptr())
 
 
 def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot_mapping: torch.Tensor,
@@ -377,24 +395,30 @@ def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot
     """pa_build_tables: query_start_loc [S + 1], context_lens [S], slot_mapping int64 [max_tokens] and positions
     [max_tokens] (or None) are written, block_tables [S, W] and num_free_out [1] updated, from cached_lens [S],
     new_lens [S] and the free list free_blocks [num_blocks], num_free [1] (int32 all but slot_mapping)."""
-    S = cached_lens.shape[0]
-    _tensors(torch.int32, query_start_loc=query_start_loc, context_lens=context_lens, positions=positions,
-             block_tables=block_tables, free_blocks=free_blocks, num_free=num_free, num_free_out=num_free_out,
-             cached_lens=cached_lens, new_lens=new_lens)
-    _tensors(torch.int64, slot_mapping=slot_mapping)
-    _dense(query_start_loc=query_start_loc, context_lens=context_lens, positions=positions, free_blocks=free_blocks,
-           cached_lens=cached_lens, new_lens=new_lens, slot_mapping=slot_mapping)
-    if (query_start_loc.numel() < S + 1 or context_lens.numel() < S or new_lens.numel() != S
-            or block_tables.shape[0] < S or free_blocks.numel() < desc.num_blocks or num_free.numel() < 1
-            or num_free_out.numel() < 1
-            or (positions is not None and positions.numel() < slot_mapping.numel())
-            or (block_tables.shape[1] > 1 and block_tables.stride(1) != 1)):
-        raise PagedKVError(PA_ERR_INVALID_ARG, "an array of build_tables is too short, or table rows are not dense")
-    _check(load().pa_build_tables(
-        _ptr(query_start_loc), _ptr(context_lens), _ptr(slot_mapping), _ptr(positions), _ptr(block_tables),
-        block_tables.stride(0) if S > 1 else max(block_tables.shape[1], 1), _ptr(free_blocks), _ptr(num_free),
-        _ptr(num_free_out), ctypes.byref(desc.c()), _ptr(cached_lens), _ptr(new_lens), S, slot_mapping.numel(),
-        ring_blocks, _ptr(dev_err), _stream(stream)))
+    S, i32 = cached_lens.shape[0], torch.int32
+    if not (query_start_loc.dtype is i32 and context_lens.dtype is i32 and block_tables.dtype is i32
+            and free_blocks.dtype is i32 and num_free.dtype is i32 and num_free_out.dtype is i32
+            and cached_lens.dtype is i32 and new_lens.dtype is i32 and slot_mapping.dtype is torch.int64
+            and (positions is None or positions.dtype is i32)):
+        _tensors(i32, query_start_loc=query_start_loc, context_lens=context_lens, positions=positions,
+                 block_tables=block_tables, free_blocks=free_blocks, num_free=num_free, num_free_out=num_free_out,
+                 cached_lens=cached_lens, new_lens=new_lens)
+        _tensors(torch.int64, slot_mapping=slot_mapping)
+    T, (rows, width), (pitch, step) = slot_mapping.numel(), block_tables.shape, block_tables.stride()
+    if (query_start_loc.numel() < S + 1 or context_lens.numel() < S or new_lens.numel() != S or rows < S
+            or free_blocks.numel() < desc.num_blocks or num_free.numel() < 1 or num_free_out.numel() < 1
+            or (positions is not None and not (positions.numel() >= T and positions.is_contiguous()))
+            or (width > 1 and step != 1)
+            or not (query_start_loc.is_contiguous() and context_lens.is_contiguous() and free_blocks.is_contiguous()
+                    and cached_lens.is_contiguous() and new_lens.is_contiguous() and slot_mapping.is_contiguous())):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "an array of build_tables is too short or not contiguous, or table "
+                                               "rows are not dense")
+    _on_device(load().pa_build_tables, slot_mapping, stream,
+               query_start_loc.data_ptr(), context_lens.data_ptr(), slot_mapping.data_ptr(),
+               None if positions is None else positions.data_ptr(), block_tables.data_ptr(),
+               pitch if S > 1 else max(width, 1), free_blocks.data_ptr(), num_free.data_ptr(), num_free_out.data_ptr(),
+               desc.ref(), cached_lens.data_ptr(), new_lens.data_ptr(), S, T, ring_blocks,
+               None if dev_err is None else dev_err.data_ptr())
 
 
 def extend_workspace_bytes(desc: CacheDesc, num_seqs: int, num_tokens: int, num_q_heads: int,
@@ -408,20 +432,23 @@ def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Cac
            dev_err: torch.Tensor | None = None, stream=None) -> None:
     """pa_extend: out/q [T, Hq, D] packed by query_start_loc (int32 [S + 1]); causal over each sequence's cache
     (its last q_len positions are the queries), with an optional window and ring tables."""
-    S, T, Hq = context_lens.shape[0], q.shape[0], q.shape[1]
-    _rows(q=q)
-    _dense(out=out, context_lens=context_lens, query_start_loc=query_start_loc)
-    _tensors(desc.dtype, out=out, q=q)
-    _tensors(torch.int32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
-    _same("out's shape", tuple(out.shape), (T, Hq, desc.head_size))
-    if query_start_loc.numel() < S + 1 or block_tables.shape[0] < S or \
-            (block_tables.shape[1] > 1 and block_tables.stride(1) != 1):
-        raise PagedKVError(PA_ERR_INVALID_ARG, "query_start_loc or block_tables is too short, or rows are not dense")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().pa_extend(_ptr(out), _ptr(q), q.stride(0), _ptr(kv_cache), ctypes.byref(desc.c()), layer,
-                            _ptr(block_tables), block_tables.stride(0) if S > 1 else max(block_tables.shape[1], 1),
-                            _ptr(context_lens), _ptr(query_start_loc), S, T, Hq, max_query_len, scale, window,
-                            ring_blocks, _ptr(workspace), ws_bytes, _ptr(dev_err), _stream(stream)))
+    S, (T, Hq, D), dt, i32 = context_lens.shape[0], q.shape, desc.dtype, torch.int32
+    if not (q.dtype is dt and out.dtype is dt and block_tables.dtype is i32 and context_lens.dtype is i32
+            and query_start_loc.dtype is i32):
+        _tensors(dt, out=out, q=q)
+        _tensors(i32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
+    _rows(q, (T, Hq, desc.head_size), "q")
+    (rows, width), (pitch, step) = block_tables.shape, block_tables.stride()
+    if (out.shape != q.shape or query_start_loc.numel() < S + 1 or rows < S or (width > 1 and step != 1)
+            or not (out.is_contiguous() and context_lens.is_contiguous() and query_start_loc.is_contiguous())):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "out must be contiguous and of q's shape, query_start_loc and "
+                                               "block_tables long enough, table rows dense")
+    _on_device(load().pa_extend, q, stream, out.data_ptr(), q.data_ptr(), q.stride(0), kv_cache.data_ptr(), desc.ref(),
+               layer, block_tables.data_ptr(), pitch if S > 1 else max(width, 1), context_lens.data_ptr(),
+               query_start_loc.data_ptr(), S, T, Hq, max_query_len, scale, window, ring_blocks,
+               None if workspace is None else workspace.data_ptr(),
+               0 if workspace is None else workspace.numel() * workspace.element_size(),
+               None if dev_err is None else dev_err.data_ptr())
 
 
 def decode_window_span(max_context_len: int, block_size: int, window: int, ring_blocks: int = 0) -> int:

@@ -489,6 +489,16 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  const int n = take ? 16 : 0;             // 0: the destination is zeroed
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Tensor copies global -> shared, completing their bytes on `bar`.
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -893,7 +903,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             ++q_num1;
           }
           const int after = tok - jt * kKv;                          // tokens from this KV tile on
-          if (!kI8 && (jt * kKv < skip || after < kKv)) spin(&sh.full[vb], vp, false);   // its softmax writes V
+          if (F == kBulk && (jt * kKv < skip || after < kKv)) spin(&sh.full[vb], vp, false);   // its softmax writes V
           const uint64_t qd = qd0 + (uint64_t)((t == 0 || alt ? 0 : C::kQBytes) >> 4);
           const uint64_t kd = kd0 + (uint64_t)((kb * C::kTileBytes) >> 4);
           const bool last_q = j == n - 1 && (!alt || (t == 0 ? other < n : other <= n));
@@ -935,10 +945,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
     if constexpr (C::kConvert) {
       set_regs_dec<C::kRegsConvert>();
       const int ct = threadIdx.x - 384;                              // 0 .. 127
+      const int shift = __ffs(bs) - 1;
+      constexpr int kPer = kI8 ? 8 : D / 8;                          // 16-byte source pieces of one vector
+      constexpr int kLoads = kKv * kPer / 128;                       // of one thread, K or V
+      const int u0 = ct / kPer, piece = ct % kPer;                   // load e: piece `piece` of token u0 + e * 128 / kPer
+      const Layout L{bs, D, p.num_kv_heads};
+      const I8Layout L8{bs, p.num_kv_heads};
       int c = 0;
       bool ok = true;
-      constexpr int kPer = F == kCodes ? 8 : D / 8;                  // 16-byte source pieces of one vector
-      constexpr int kLoads = kKv * kPer / 128;                       // of one thread, K or V
       for (int i = 0; ok; ++i) {
         Work w;
         if (!next_item(i, w)) {
@@ -948,106 +962,150 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         if (w.kvh < 0) break;
         const int n = tiles_of(w);
         const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
-        const Layout L{bs, D, p.num_kv_heads};
-        const I8Layout L8{bs, p.num_kv_heads};
-        for (int j = 0; j < n && ok; ++j, ++c) {
-          const int t0 = (w.tile0 + j) * kKv;
-          // token u of the tile is read if its block holds an attended position
-          auto find = [&](int u, int& b) -> bool {
-            const int pos = t0 + u;
-            b = 0;
-            if (pos / bs < w.first / bs || pos >= w.kv_end) return false;
-            b = block_of(p, row, pos / bs);
-            if ((unsigned)b < (unsigned)p.num_blocks) return true;
-            sh.bad[i % kRing] = 1;
-            return false;
-          };
-          uint4 x[2][kLoads];
-          float sc[2] = {0.f, 0.f};
-          auto load = [&](int part) {
+        // the block of token u of KV tile j, or -1: no query attends it, or its id is bad
+        auto find = [&](int j, int u) -> int {
+          const int pos = (w.tile0 + j) * kKv + u;
+          if (pos < w.first || pos >= w.kv_end) return -1;
+          const int id = block_of(p, row, pos >> shift);
+          if ((unsigned)id < (unsigned)p.num_blocks) return id;
+          sh.bad[i % kRing] = 1;
+          return -1;
+        };
+        // a warp's loads touch 32 tokens: lane 32 / kPer * e + r keeps the block of the r-th of load e
+        constexpr int kTok = 32 / kPer;
+        static_assert(kTok * kLoads == 32, "one token a lane");
+        int mine = -1;
+        auto look_up = [&](int j) { return find(j, (ct >> 5) * kTok + lane % kTok + lane / kTok * (128 / kPer)); };
+        auto block = [&](int e) { return __shfl_sync(kFull, mine, e * kTok + lane / kPer); };
+        auto place = [&](int j, int e) { return ((w.tile0 + j) * kKv + u0 + e * (128 / kPer)) & (bs - 1); };
+        if constexpr (!kI8) {
+          // 16-byte pieces by asynchronous copies, absent tokens as zeros.  A fill is
+          // completed after the next one has been issued.
+          auto issue = [&](int j, int part) {
+            const uint32_t dst = smem_u32(buffer(2 * c + part));
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
-              const int u = (ct + e * 128) / kPer, piece = (ct + e * 128) % kPer;
-              int b;
-              const bool have = find(u, b);
-              const int t = (t0 + u) & (bs - 1);
-              x[part][e] = !have ? make_uint4(0, 0, 0, 0)
-                           : kI8 ? *reinterpret_cast<const uint4*>(p.cache + L8.code(b, w.kvh, part, t, piece * 16))
-                                 : *reinterpret_cast<const uint4*>(p.cache + 2 * L.offset(b, w.kvh, part, t, piece * 8));
+              const int id = block(e);
+              const uint8_t* src = id < 0 ? p.cache : p.cache + 2 * L.offset(id, w.kvh, part, place(j, e), piece * 8);
+              cp_async16(dst + kv_offset<D>(u0 + e * (128 / kPer), piece), src, id >= 0);
+            }
+            cp_async_commit();
+          };
+          auto complete = [&](int fill) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.full[fill % NB]);
+          };
+          int next = n > 0 ? look_up(0) : -1;
+          for (int j = 0; j < n; ++j, ++c) {
+            mine = next;
+            if (j + 1 < n) next = look_up(j + 1);
+            if (!wait_empty(2 * c)) {
+              ok = false;
+              break;
+            }
+            issue(j, 0);
+            if (j > 0) {
+              cp_async_wait<1>();
+              complete(2 * c - 1);
+            }
+            if (!wait_empty(2 * c + 1)) {
+              ok = false;
+              break;
+            }
+            issue(j, 1);
+            cp_async_wait<1>();
+            complete(2 * c);
+          }
+          cp_async_wait<0>();
+          if (ok && n > 0) complete(2 * c - 1);
+        } else {
+          // codes go through registers: a tile's are loaded while the one before is converted
+          uint4 xk[kLoads], xv[kLoads];
+          float sk = 0.f, sv = 0.f;
+          auto load = [&](int j, int part, uint4* x) {
+#pragma unroll
+            for (int e = 0; e < kLoads; ++e) {
+              const int id = block(e);
+              x[e] = id < 0 ? make_uint4(0, 0, 0, 0)
+                            : *reinterpret_cast<const uint4*>(p.cache + L8.code(id, w.kvh, part, place(j, e), piece * 16));
             }
           };
-          load(0);
-          if constexpr (kI8) {
-            load(1);                                                 // (16-bit rows: after K's have gone, registers)
-            int b;
-            if (find(ct, b)) {
-              const int t = (t0 + ct) & (bs - 1);
-              sc[0] = *reinterpret_cast<const float*>(p.cache + L8.scale(b, w.kvh, 0, t));
-              sc[1] = *reinterpret_cast<const float*>(p.cache + L8.scale(b, w.kvh, 1, t));
-            }
-          }
-          if (!wait_empty(2 * c)) {
-            ok = false;
-            break;
-          }
-          if constexpr (kI8) {
-            const int r = c % kScaleRing;
-            // zero vectors have scale 0 and zero codes: any positive scale stands for them
-            const float sv = sc[1] == 0.f ? 1.f : fmaxf(sc[1], 1.2e-38f);
-            scales.k[r][ct] = sc[0] * p.scale_log2;
-            scales.lv[r][ct] = log2f(sv);
-            scales.iv[r][ct] = 1.f / sv;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.sc_full[r]);
-          }
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            if (part == 1) {
-              if constexpr (!kI8) load(1);
-              if (!wait_empty(2 * c + 1)) {
-                ok = false;
-                break;
-              }
-            }
+          auto load_scales = [&](int j) {
+            const int id = find(j, ct), t = ((w.tile0 + j) * kKv + ct) & (bs - 1);
+            sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
+            sv = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 1, t));
+          };
+          auto write = [&](int part, const uint4* x) {
             uint8_t* dst = buffer(2 * c + part);
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
-              const int u = (ct + e * 128) / kPer, piece = (ct + e * 128) % kPer;
-              if constexpr (!kI8) {
-                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, piece)) = x[part][e];
-              } else {
-                const uint32_t in[4] = {x[part][e].x, x[part][e].y, x[part][e].z, x[part][e].w};
-                uint32_t y[8];
+              const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+              uint32_t y[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (part == 1 || !kBF16) {
-                    // fp16 1024 + (code + 128), less 1152: exact
-                    const uint32_t b = in[k] ^ 0x80808080u;
-                    const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));
-                    const uint32_t a0 = __byte_perm(b, 0x64646464u, 0x4140), a1 = __byte_perm(b, 0x64646464u, 0x4342);
-                    const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), off);
-                    const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), off);
-                    y[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
-                    y[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                  } else {
-                    // bf16 128 + (low 7 bits), less 128 (code >= 0) or 256: exact
+              for (int k = 0; k < 4; ++k) {
+                if (part == 1 || !kBF16) {
+                  // fp16 1024 + (code + 128), less 1152: exact
+                  const uint32_t b = in[k] ^ 0x80808080u;
+                  const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));
+                  const uint32_t a0 = __byte_perm(b, 0x64646464u, 0x4140), a1 = __byte_perm(b, 0x64646464u, 0x4342);
+                  const __half2 h0 = __hsub2(*reinterpret_cast<const __half2*>(&a0), off);
+                  const __half2 h1 = __hsub2(*reinterpret_cast<const __half2*>(&a1), off);
+                  y[2 * k] = *reinterpret_cast<const uint32_t*>(&h0);
+                  y[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                } else {
+                  // bf16 128 + (low 7 bits), less 128 (code >= 0) or 256: exact
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                      const uint32_t b = __byte_perm(in[k], 0, hf ? 0x4342 : 0x4140);
-                      const uint32_t a = 0x43004300u | (b & 0x007f007fu), s = 0x43004300u | (b & 0x00800080u);
-                      const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                                       *reinterpret_cast<const __nv_bfloat162*>(&s));
-                      y[2 * k + hf] = *reinterpret_cast<const uint32_t*>(&r);
-                    }
+                  for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t b = __byte_perm(in[k], 0, hf ? 0x4342 : 0x4140);
+                    const uint32_t a = 0x43004300u | (b & 0x007f007fu), s = 0x43004300u | (b & 0x00800080u);
+                    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
+                    y[2 * k + hf] = *reinterpret_cast<const uint32_t*>(&r);
                   }
                 }
-                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece)) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
               }
+              const int u = u0 + e * (128 / kPer);
+              *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.full[(2 * c + part) % NB]);
+          };
+          if (n > 0) {
+            mine = look_up(0);
+            load(0, 0, xk);
+            load(0, 1, xv);
+            load_scales(0);
+          }
+          for (int j = 0; j < n; ++j, ++c) {
+            if (j + 1 < n) mine = look_up(j + 1);
+            if (!wait_empty(2 * c)) {
+              ok = false;
+              break;
+            }
+            {
+              const int r = c % kScaleRing;
+              // zero vectors have scale 0 and zero codes: any positive scale stands for them
+              const float s = sv == 0.f ? 1.f : fmaxf(sv, 1.2e-38f);
+              scales.k[r][ct] = sk * p.scale_log2;
+              scales.lv[r][ct] = log2f(s);
+              scales.iv[r][ct] = 1.f / s;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.sc_full[r]);
+            }
+            write(0, xk);
+            if (j + 1 < n) {
+              load(j + 1, 0, xk);
+              load_scales(j + 1);
+            }
+            if (!wait_empty(2 * c + 1)) {
+              ok = false;
+              break;
+            }
+            write(1, xv);
+            if (j + 1 < n) load(j + 1, 1, xv);
           }
         }
         if (ok) done_item(i);
@@ -1075,22 +1133,23 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       tc::fence_after_sync();
     };
     for (int i = 0; ok; ++i) {
-      Work w;
-      if (!next_item(i, w)) {
+      if (!wait(&sh.item_full[i % kRing], (i / kRing) & 1)) {
         ok = false;
         break;
       }
+      const Work& w = sh.work[i % kRing];                            // (read where needed: registers are scarce here)
       if (w.kvh < 0) break;
-      const int my0 = w.alt ? 0 : t * ptile;                         // my tile's first position in the item
-      const int npos = w.alt ? w.npos : min(ptile, w.npos - my0);
-      const bool row_ok = ipos < npos;
+      const bool alt = w.alt != 0;
+      const int my0 = alt ? 0 : t * ptile;                           // my tile's first position in the item
+      const bool row_ok = ipos < (alt ? w.npos : min(ptile, w.npos - my0));
       const int pos = w.pos0 + my0 + ipos;
       const int from = attend_from(pos, p.window, w.held);
       const int n = t == 0 ? w.n[0] : w.n[1];
+      const int tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n; ++j, ++num) {
-        const int jt = w.alt ? 2 * j + t : j, c = w.c0 + jt;
-        const int t0 = (w.tile0 + jt) * kKv;
+        const int jt = alt ? 2 * j + t : j, c = c0 + jt;
+        const int t0 = (tile0 + jt) * kKv;
         if (!wait(&sh.s_full[t], num & 1)) {
           ok = false;
           break;
@@ -1099,7 +1158,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         float x[kKv];
         tmem_ld64(s_addr, x);
         tmem_ld64(s_addr + 64, x + 64);
-        const bool edge = jt < w.edge_lo || jt >= w.edge_hi;
+        const bool edge = jt < edge_lo || jt >= edge_hi;
         if constexpr (kI8) {
           if (!wait(&sh.sc_full[c % kScaleRing], (c / kScaleRing) & 1)) {
             ok = false;
@@ -1126,7 +1185,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
             }
           }
-          if constexpr (!kI8) {
+          if constexpr (F == kBulk) {
             if (ragged(w, jt)) {
               // thread = token here: V rows that hold no token of the context become
               // zero (V has landed: the issuer waited for it)
@@ -1222,7 +1281,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       int col0 = 0, ncol = D;
       bool have0 = n > 0, have1 = false;
       uint32_t o0 = o_addr, o1 = o_addr;
-      if (w.alt) {
+      if (alt) {
         sh.red[t][row][0] = m;
         sh.red[t][row][1] = l;
         meet();
@@ -1246,7 +1305,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const bool part = w.part_row >= 0;
       const float scale = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
       const int rr = (my0 + ipos) * G + head;                        // row within the item
-      float* prow = ws.o + (int64_t)(w.part_row + rr) * D;
+      const int part_row = w.part_row;
+      float* prow = ws.o + (int64_t)(part_row + rr) * D;
       T* tile = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0) * p.num_q_heads + w.kvh * G) * D;
       // Rows leave 64 bytes at a time: a store of 16 bytes a row and lane asks for 32
       // lines, and the stores alone took 6000 clocks an item.  Lanes 4i .. 4i + 3
@@ -1264,7 +1324,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
-        if (w.alt) {
+        if (alt) {
           float b[32];
           if (have1) {
             tmem_ld32(o1 + e, b);
@@ -1305,7 +1365,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
       }
       if (row_ok && part && col0 == 0)
-        *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(w.part_row + rr)) = make_float2(m, l);
+        *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(part_row + rr)) = make_float2(m, l);
       // A V that is not finite reaches rows that do not attend it (0 * NaN = NaN):
       // finish_kernel redoes the item.  (8-bit codes are finite, and a masked
       // token's weight is 0 whatever its scale.)
@@ -1314,7 +1374,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
       }
       // both halves have read both accumulators before either is overwritten
-      if (w.alt) meet(); else tc::fence_before_sync();
+      if (alt) meet(); else tc::fence_before_sync();
       if (!ok) break;
       done_item(i);
     }

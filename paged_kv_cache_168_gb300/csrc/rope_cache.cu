@@ -21,6 +21,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kDeep = 3;                             // units a thread has in flight
 
 // The two pieces (16 bytes = 8 dims each) of unit u of a head vector.
 template <bool kPairs>
@@ -67,106 +68,141 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, i
   }
 }
 
-template <typename T, int D, bool kPairs, bool kI8>
-__global__ void __launch_bounds__(kThreads) rope_cache_kernel(const __grid_constant__ RopeParams p) {
+// A round of a CTA is kTokens tokens: their cosines and sines go to shared memory,
+// then every thread takes kDeep units at a time, all their loads before any
+// arithmetic.  One token a CTA and round (two barriers for 1.5 units a thread) ran
+// at 4.4 TB/s where this one runs at the rate given in the header comment.
+template <typename T, int D, bool kPairs, bool kI8, int kTokens>
+__global__ void __launch_bounds__(kThreads, kI8 ? 3 : 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kUnits = D / 16;                     // units per head vector
-  __shared__ __align__(16) float cs[2][D];
-  __shared__ int bad_pos[2];
+  __shared__ __align__(16) float cs[kTokens][D];
+  __shared__ int64_t slots[kTokens];                 // where the token goes; -1: nowhere
+  __shared__ int skip[kTokens];                      // its position is out of range
   const int rot = p.rotary_dim, half_dims = rot / 2;
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
-  const int units = (hq + 2 * hkv) * kUnits;
+  const int hq = p.num_q_heads, hkv = p.num_kv_heads, heads = hq + 2 * hkv;
   const int64_t nslots = (int64_t)p.num_blocks * p.block_size;
+  const int shift = __ffs(p.block_size) - 1;
   const Layout L{p.block_size, D, hkv};
   const I8Layout L8{p.block_size, hkv};
-  int buf = 0;
-  for (int tok = blockIdx.x; tok < p.num_tokens; tok += gridDim.x, buf ^= 1) {
-    const int64_t slot = p.slot_mapping[tok];
-    if (threadIdx.x == 0) bad_pos[buf] = 0;
+  const int u = threadIdx.x % kUnits;                // kThreads is a multiple of kUnits
+  int a, b;
+  bool turns;
+  unit_pieces<kPairs>(u, rot, a, b, turns);
+  for (int tok0 = blockIdx.x * kTokens; tok0 < p.num_tokens; tok0 += gridDim.x * kTokens) {
+    const int count = min(kTokens, p.num_tokens - tok0);
+    __syncthreads();                                 // the round before has been used
+    if (threadIdx.x < count) {
+      const int64_t slot = p.slot_mapping[tok0 + threadIdx.x];
+      const bool bad = slot != -1 && (slot < 0 || slot >= nslots);
+      slots[threadIdx.x] = bad ? -1 : slot;
+      if (bad) report(p.dev_err, PA_DEVERR_SLOT);
+      skip[threadIdx.x] = 0;
+    }
     __syncthreads();
-    if (threadIdx.x < rot) {
-      const int pair = threadIdx.x < half_dims ? threadIdx.x : threadIdx.x - half_dims;
-      const int pos = p.positions[p.pair_axis[pair] * p.axis_stride + tok];
+    for (int i = threadIdx.x; i < count * rot; i += kThreads) {
+      const int k = i / rot, d = i - k * rot;
+      const int pos = p.positions[p.pair_axis[d < half_dims ? d : d - half_dims] * p.axis_stride + tok0 + k];
       const bool fine = pos >= 0 && pos < p.max_position;
-      cs[buf][threadIdx.x] = fine ? p.cos_sin[(int64_t)pos * rot + threadIdx.x] : 0.f;
-      if (!fine) bad_pos[buf] = 1;
+      cs[k][d] = fine ? p.cos_sin[(int64_t)pos * rot + d] : 0.f;
+      if (!fine) skip[k] = 1;
     }
     __syncthreads();
-    const bool skip = bad_pos[buf] != 0;
-    bool store = slot != -1 && !skip;
-    if (store && (slot < 0 || slot >= nslots)) {
-      store = false;
-      if (threadIdx.x == 0) report(p.dev_err, PA_DEVERR_SLOT);
+    if (threadIdx.x < count && skip[threadIdx.x]) {
+      slots[threadIdx.x] = -1;
+      report(p.dev_err, PA_DEVERR_POSITION);
     }
-    if (skip && threadIdx.x == 0) report(p.dev_err, PA_DEVERR_POSITION);
-    const int64_t block = store ? slot / p.block_size : 0;
-    const int t = store ? (int)(slot - block * p.block_size) : 0;
-    for (int i = threadIdx.x; i < units; i += kThreads) {
-      const int head = i / kUnits, u = i % kUnits;
-      const int part = head < hq ? 0 : head < hq + hkv ? 1 : 2;   // q, k, v
-      const int h = head - (part == 0 ? 0 : part == 1 ? hq : hq + hkv);
-      if (part != 0 && !store) continue;             // the same for all units of a vector
-      int a, b;
-      bool turned;
-      unit_pieces<kPairs>(u, rot, a, b, turned);
-      const T* src = part == 0   ? static_cast<const T*>(p.q) + tok * p.q_stride
-                     : part == 1 ? static_cast<const T*>(p.key) + tok * p.key_stride
-                                 : static_cast<const T*>(p.value) + tok * p.value_stride;
-      src += (int64_t)h * D;
-      uint4 va = *reinterpret_cast<const uint4*>(src + a * 8), vb = *reinterpret_cast<const uint4*>(src + b * 8);
-      turned = turned && part != 2;
-      if (kI8 && part != 0) {
-        float x[16];
-        unpack8<T>(va, x);
-        unpack8<T>(vb, x + 8);
-        if (turned) rotate<kPairs>(x, cs[buf], u, half_dims);
-        float amax = 0.f;
+    __syncthreads();
+    const int vectors = count * heads;
+    for (int v0 = threadIdx.x / kUnits; v0 < vectors; v0 += kDeep * (kThreads / kUnits)) {
+      uint4 va[kDeep], vb[kDeep];
+      int tok[kDeep], head[kDeep];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-        const unsigned lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31 & ~(kUnits - 1));
+      for (int e = 0; e < kDeep; ++e) {
+        const int v = v0 + e * (kThreads / kUnits);
+        tok[e] = v / heads;
+        head[e] = v - tok[e] * heads;
+        if (v >= vectors) tok[e] = -1;
+        else if (head[e] >= hq && slots[tok[e]] == -1) tok[e] = -1;   // K and V that are not stored
+        if (tok[e] < 0) continue;
+        const int64_t t = tok0 + tok[e];
+        const T* src = head[e] < hq ? static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)head[e] * D
+                       : head[e] < hq + hkv
+                           ? static_cast<const T*>(p.key) + t * p.key_stride + (int64_t)(head[e] - hq) * D
+                           : static_cast<const T*>(p.value) + t * p.value_stride + (int64_t)(head[e] - hq - hkv) * D;
+        va[e] = *reinterpret_cast<const uint4*>(src + a * 8);
+        vb[e] = *reinterpret_cast<const uint4*>(src + b * 8);
+      }
 #pragma unroll
-        for (int o = kUnits / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
-        uint32_t code[4] = {0, 0, 0, 0};
-        float scale = 0.f;
-        if (amax > 0.f) {
-          const float inv = __fmul_rn(127.f, __fdiv_rn(1.f, amax));
+      for (int e = 0; e < kDeep; ++e) {
+        if (tok[e] < 0) continue;                    // the same for all units of a vector
+        const int part = head[e] < hq ? 0 : head[e] < hq + hkv ? 1 : 2;      // q, k, v
+        const bool turned = turns && part != 2;
+        if (turned || (kI8 && part != 0)) {
+          float x[16];
+          unpack8<T>(va[e], x);
+          unpack8<T>(vb[e], x + 8);
+          if (turned) rotate<kPairs>(x, cs[tok[e]], u, half_dims);
+          if (kI8 && part != 0) {
+            const int h = head[e] - (part == 1 ? hq : hq + hkv);
+            const int64_t slot = slots[tok[e]], block = slot >> shift;
+            const int t = (int)(slot & (p.block_size - 1));
+            float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            code[e >> 2] |= (uint32_t)(min(127, max(-127, __float2int_rn(__fmul_rn(x[e], inv)))) & 0xff) << (8 * (e & 3));
-          scale = __fmul_rn(amax, 1.f / 127.f);
+            for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[k]));
+            const unsigned lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31 & ~(kUnits - 1));
+#pragma unroll
+            for (int o = kUnits / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+            uint32_t code[4] = {0, 0, 0, 0};
+            float scale = 0.f;
+            if (amax > 0.f) {
+              const float inv = __fmul_rn(127.f, __fdiv_rn(1.f, amax));
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                code[k >> 2] |= (uint32_t)(min(127, max(-127, __float2int_rn(__fmul_rn(x[k], inv)))) & 0xff) << (8 * (k & 3));
+              scale = __fmul_rn(amax, 1.f / 127.f);
+            }
+            *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, a * 8)) = make_uint2(code[0], code[1]);
+            *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, b * 8)) = make_uint2(code[2], code[3]);
+            if (u == 0) *reinterpret_cast<float*>(p.cache + L8.scale(block, h, part - 1, t)) = scale;
+            continue;
+          }
+          va[e] = pack8<T>(x);
+          vb[e] = pack8<T>(x + 8);
         }
-        *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, a * 8)) = make_uint2(code[0], code[1]);
-        *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, b * 8)) = make_uint2(code[2], code[3]);
-        if (u == 0) *reinterpret_cast<float*>(p.cache + L8.scale(block, h, part - 1, t)) = scale;
-        continue;
-      }
-      if (turned) {
-        float x[16];
-        unpack8<T>(va, x);
-        unpack8<T>(vb, x + 8);
-        rotate<kPairs>(x, cs[buf], u, half_dims);
-        va = pack8<T>(x);
-        vb = pack8<T>(x + 8);
-      }
-      if (part == 0) {
-        T* dst = static_cast<T*>(p.q_out) + tok * p.q_out_stride + (int64_t)h * D;
-        if (skip) va = vb = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(dst + a * 8) = va;
-        *reinterpret_cast<uint4*>(dst + b * 8) = vb;
-      } else {
-        *reinterpret_cast<uint4*>(p.cache + L.offset(block, h, part - 1, t, a * 8) * 2) = va;
-        *reinterpret_cast<uint4*>(p.cache + L.offset(block, h, part - 1, t, b * 8) * 2) = vb;
+        if (part == 0) {
+          T* dst = static_cast<T*>(p.q_out) + (tok0 + tok[e]) * p.q_out_stride + (int64_t)head[e] * D;
+          if (skip[tok[e]]) va[e] = vb[e] = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(dst + a * 8) = va[e];
+          *reinterpret_cast<uint4*>(dst + b * 8) = vb[e];
+        } else {
+          const int h = head[e] - (part == 1 ? hq : hq + hkv);
+          const int64_t slot = slots[tok[e]], block = slot >> shift;
+          const int t = (int)(slot & (p.block_size - 1));
+          *reinterpret_cast<uint4*>(p.cache + L.offset(block, h, part - 1, t, a * 8) * 2) = va[e];
+          *reinterpret_cast<uint4*>(p.cache + L.offset(block, h, part - 1, t, b * 8) * 2) = vb[e];
+        }
       }
     }
   }
 }
 
+template <typename T, int D, bool kI8, int kTokens>
+void launch_rounds(const RopeParams& p, cudaStream_t stream) {
+  const int rounds = (p.num_tokens + kTokens - 1) / kTokens;
+  const unsigned grid = (unsigned)(rounds < 152 * 8 ? rounds : 152 * 8);
+  if (p.interleaved)
+    rope_cache_kernel<T, D, true, kI8, kTokens><<<grid, kThreads, 0, stream>>>(p);
+  else
+    rope_cache_kernel<T, D, false, kI8, kTokens><<<grid, kThreads, 0, stream>>>(p);
+}
+
 template <typename T, int D, bool kI8>
 cudaError_t launch_pairs(const RopeParams& p, cudaStream_t stream) {
-  const unsigned grid = (unsigned)(p.num_tokens < 152 * 8 ? p.num_tokens : 152 * 8);
-  if (p.interleaved)
-    rope_cache_kernel<T, D, true, kI8><<<grid, kThreads, 0, stream>>>(p);
+  // up to one round per SM of single tokens: more CTAs at once, for latency
+  if (p.num_tokens <= 152 * 4)
+    launch_rounds<T, D, kI8, 1>(p, stream);
   else
-    rope_cache_kernel<T, D, false, kI8><<<grid, kThreads, 0, stream>>>(p);
+    launch_rounds<T, D, kI8, 4>(p, stream);
   return cudaGetLastError();
 }
 
