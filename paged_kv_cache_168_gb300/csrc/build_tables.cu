@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;       // the largest portable cluster
+constexpr int kRun = 4;           // consecutive tokens of a thread
 constexpr int kOneCta = 2048;     // tokens one CTA serves alone
 
 __device__ __forceinline__ void cluster_sync() {
@@ -39,7 +40,7 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t v, int lane) {
   return v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesParams p) {
+__global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesParams p, bool wide) {
   extern __shared__ int32_t dyn[];
   const int S = p.num_seqs, bs = p.block_size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int shift = __ffs(bs) - 1;                    // block sizes are powers of two
@@ -111,39 +112,59 @@ __global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesP
     }
   }
 
-  // ---- tokens
+  // ---- tokens, four in a row a thread: one search, four independent lookups
   const int n_tok = ok ? (int)total : 0;
-  for (int i = blockIdx.x * kThreads + tid; i < p.max_tokens; i += gridDim.x * kThreads) {
-    int64_t slot = -1;
-    int pos = 0;
-    if (i < n_tok) {
-      int lo = 0, hi = S;                             // the last request with starts <= i
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] <= i) lo = mid; else hi = mid;
+  for (int64_t i0 = ((int64_t)blockIdx.x * kThreads + tid) * kRun; i0 < p.max_tokens;
+       i0 += (int64_t)gridDim.x * kThreads * kRun) {
+    int64_t slot[kRun];
+    int pos[kRun], s = 0;
+    if (i0 < n_tok) {
+      int hi = S;                                     // the last request with starts <= i0
+      while (hi - s > 1) {
+        const int mid = (s + hi) >> 1;
+        if (starts[mid] <= i0) s = mid; else hi = mid;
       }
-      const int s = lo, ctx = ctxs[s];
+    }
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const int i = (int)i0 + k;
+      slot[k] = -1;
+      pos[k] = 0;
+      if (i >= n_tok) continue;
+      while (starts[s + 1] <= i) ++s;                 // (ends: i < starts[S])
+      const int ctx = ctxs[s];
       const int cached = ctx - (starts[s + 1] - starts[s]);
-      pos = cached + (i - starts[s]);
-      const int b = pos >> shift;
+      pos[k] = cached + (i - starts[s]);
+      const int b = pos[k] >> shift;
       const int have = (int)min(((int64_t)cached + bs - 1) >> shift, cap);
       const bool kept = p.ring_blocks == 0 || b > ((ctx - 1) >> shift) - p.ring_blocks;
-      int32_t* entry = p.block_tables + (int64_t)s * p.bt_stride + (p.ring_blocks > 0 ? b % p.ring_blocks : b);
-      // begun in this step: logical block b itself, or (ring) the one whose entry b takes over
       const int e = p.ring_blocks > 0 ? b % p.ring_blocks : b;
+      int32_t* entry = p.block_tables + (int64_t)s * p.bt_stride + e;
+      // begun in this step: logical block b itself, or (ring) the one whose entry b takes over
       const bool fresh = e >= have;
       if (kept || fresh) {
         const int id = fresh ? p.free_blocks[num_free - 1 - (first[s] + e - have)] : *entry;
-        if (fresh && b == e && (pos & (bs - 1)) == 0) *entry = id;
+        if (fresh && b == e && (pos[k] & (bs - 1)) == 0) *entry = id;
         if ((unsigned)id < (unsigned)p.num_blocks) {
-          if (kept) slot = ((int64_t)id << shift) + (pos & (bs - 1));
+          if (kept) slot[k] = ((int64_t)id << shift) + (pos[k] & (bs - 1));
         } else {
           report(p.dev_err, PA_DEVERR_BLOCK_ID);
         }
       }
     }
-    p.slot_mapping[i] = slot;
-    if (p.positions) p.positions[i] = pos;
+    if (wide && i0 + kRun <= p.max_tokens) {
+#pragma unroll
+      for (int k = 0; k < kRun; k += 2)
+        *reinterpret_cast<longlong2*>(p.slot_mapping + i0 + k) = make_longlong2(slot[k], slot[k + 1]);
+      if (p.positions) *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRun; ++k)
+        if (i0 + k < p.max_tokens) {
+          p.slot_mapping[i0 + k] = slot[k];
+          if (p.positions) p.positions[i0 + k] = pos[k];
+        }
+    }
   }
 }
 
@@ -165,7 +186,8 @@ cudaError_t launch_build_tables(const TablesParams& p, cudaStream_t stream) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p);
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.slot_mapping) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+  return cudaLaunchKernelEx(&cfg, build_tables_kernel, p, wide);
 }
 
 }  // namespace pkv

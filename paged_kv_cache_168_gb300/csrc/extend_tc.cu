@@ -139,6 +139,10 @@ Space lay_out(uint8_t* base, int num_seqs, int num_tokens, int num_kv_heads, int
   return w;
 }
 
+// Programmatic launches: let the next kernel on the stream begin / wait for the one before to be done.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ planner
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanCache = 8192;           // sequences whose first items are searched in shared memory
@@ -225,8 +229,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   __shared__ int nsplit;
   const int S = p.num_seqs, G = p.group, pair = 2 * (kRows / G), tid = threadIdx.x, hkv = p.num_kv_heads;
   if (tid == 0) errs = nsplit = 0;
+  launch_next();
   const int per = (S + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  // a thread's only sequence is read once
+  uint32_t err = 0;
+  Seq mine{};
+  if (per == 1 && s0 < s1) mine = read_seq(p, s0, err);
+  auto seq = [&](int s, uint32_t& e) { return per == 1 ? mine : read_seq(p, s, e); };
   // KV tiles of a sequence's last query tile
   auto last_range = [&](const Seq& q, int nt) {
     int t0;
@@ -234,10 +244,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     return tile_range(p, q, q.ctx - q.q_len + q0, q.q_len - q0, t0);
   };
 
-  uint32_t err = 0, none = 0;
+  uint32_t none = 0;
   int64_t work = 0;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = read_seq(p, s, err);
+    const Seq q = seq(s, err);
     if (!q.listed || q.zero) continue;
     const int nt = (q.q_len + pair - 1) / pair;
     int t0;
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   };
   int64_t rows = 0;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = read_seq(p, s, none);
+    const Seq q = seq(s, none);
     int64_t r = 0;
     if (q.listed) parts_of(q, (q.q_len + pair - 1) / pair, r);
     rows += r;
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   int64_t row = block_scan(rows, tmp, total);
   int64_t items = 0;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = read_seq(p, s, none);
+    const Seq q = seq(s, none);
     SeqPlan sp{0, 0, -1, 0};
     if (q.listed) {
       const int nt = (q.q_len + pair - 1) / pair;
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   int64_t n_items;
   int64_t item = block_scan(items, tmp, n_items);
   for (int s = s0; s < s1; ++s) {
-    const Seq q = read_seq(p, s, none);
+    const Seq q = seq(s, none);
     const int base = (int)min(item, (int64_t)ws.max_items);
     ws.seqs[s].base = base;
     if (s < kPlanCache) bases[s] = base;
@@ -585,6 +595,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
     tc::tmem_alloc(&sh.tmem_base, 512);
     tc::tmem_relinquish();
   }
+  launch_next();
+  launch_wait();                                                   // the planner's items
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -1443,6 +1455,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
                                                      const __grid_constant__ Space ws) {
   constexpr int kDims = D / 32;
   const int lane = threadIdx.x & 31, hkv = p.num_kv_heads, G = p.group;
+  launch_wait();
   const int64_t w0 = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5, nw = ((int64_t)gridDim.x * blockDim.x) >> 5;
   const Header hd = *ws.head;
   for (int64_t u = w0; u < (int64_t)hd.num_split * hkv * ws.tile_rows; u += nw) {
@@ -1491,6 +1504,23 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
 }
 
 // ------------------------------------------------------------------ launch
+// A launch that may begin while the kernel before it on the stream runs; it waits
+// (launch_wait) before it touches that kernel's results.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The driver's encoder of tensor maps (looked up once).
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1550,10 +1580,9 @@ cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStr
   if (e != cudaSuccess) return e;
   plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, ws, sms);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  extend_kernel<T, D, F><<<sms, C::kThreads, smem, stream>>>(p, ws, q_map, kv_map);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  finish_kernel<T, D><<<2 * sms, 256, 0, stream>>>(p, ws);
-  return cudaGetLastError();
+  e = launch_early(extend_kernel<T, D, F>, sms, C::kThreads, smem, stream, p, ws, q_map, kv_map);
+  if (e != cudaSuccess) return e;
+  return launch_early(finish_kernel<T, D>, 2 * sms, 256, 0, stream, p, ws);
 }
 
 template <typename T>
