@@ -256,7 +256,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   }
   int64_t total;
   block_scan(work, tmp, total);
-  const int64_t want = (int64_t)kPartsPerSm * sms;
+  // With K parts a SM the call takes about (work / sms) (1 + 1 / K) -- the last round
+  // is half empty -- and K times an item's own cost, about 3 KV tiles: least at
+  // K = sqrt(work / sms / 3).  (Always K = 4: 137 us where 61 now, on windows of 1000
+  // tokens; K = 1: 8 sequences of 32K to 131K tokens lose 10%.)
+  const int64_t per_sm = total * hkv / sms;
+  const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
   const int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
 
   // parts wanted and their partial rows
@@ -961,7 +966,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       constexpr int kPer = kI8 ? 8 : D / 8;                          // 16-byte source pieces of one vector
       constexpr int kLoads = kKv * kPer / 128;                       // of one thread, K or V
       const int u0 = ct / kPer, piece = ct % kPer;                   // load e: piece `piece` of token u0 + e * 128 / kPer
-      const Layout L{bs, D, p.num_kv_heads};
       const I8Layout L8{bs, p.num_kv_heads};
       int c = 0;
       bool ok = true;
@@ -998,7 +1002,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
               const int id = block(e);
-              const uint8_t* src = id < 0 ? p.cache : p.cache + 2 * L.offset(id, w.kvh, part, place(j, e), piece * 8);
+              // a block of fewer than 8 tokens is one group: K atoms, then V atoms, of bs rows each
+              const int s = place(j, e);
+              const int in_block = ((part * (D / 64) + (piece >> 3)) * bs + s) * 64 + (((piece & 7) ^ s) << 3);
+              const uint8_t* src = id < 0 ? p.cache
+                                          : p.cache + 2 * (((int64_t)id * p.num_kv_heads + w.kvh) * (2 * D * bs) + in_block);
               cp_async16(dst + kv_offset<D>(u0 + e * (128 / kPer), piece), src, id >= 0);
             }
             cp_async_commit();
