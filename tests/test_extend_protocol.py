@@ -31,8 +31,7 @@ class Model:
         fill = 4 if convert else 1
         self.nb = nb = 4 if convert else 5
         self.full, self.empty = [Bar(fill) for _ in range(nb)], [Bar(1) for _ in range(nb)]
-        self.q_full, self.q_empty, self.s_full, self.p_half, self.p_full = \
-            [[Bar(4 if i >= 3 else 1) for _ in range(2)] for i in range(5)]
+        self.q_full, self.q_empty, self.s_full, self.p_full = [[Bar(4 if i == 3 else 1) for _ in range(2)] for i in range(4)]
         self.pv_done = [[Bar(1) for _ in range(2)] for _ in range(2)]
         self.item_full = [Bar(1) for _ in range(RING)]
         self.item_empty = [Bar(14 if convert else 11) for _ in range(RING)]
@@ -171,10 +170,8 @@ class Model:
                 return
             c, first, last = owed[t]
             yield from filled("v", c)
-            yield from self.wait(self.p_half[t], num[t] & 1)
-            self.tensor.append(("pv", t, (2 * c + 1) % self.nb, c, first, 0))
             yield from self.wait(self.p_full[t], num[t] & 1)
-            self.tensor.append(("pv", t, (2 * c + 1) % self.nb, c, first, 1))
+            self.tensor.append(("pv", t, (2 * c + 1) % self.nb, c, first))
             self.tensor.append(("commit", self.pv_done[t][num[t] & 1]))
             if last:
                 self.tensor.append(("commit", self.empty[(2 * c + 1) % self.nb]))
@@ -242,14 +239,13 @@ class Model:
                     self.reading[key] -= 1
                 self.s[t] = [("s", c)] * 4
             else:
-                _, t, st, c, first, half = op
+                _, t, st, c, first = op
                 self.reading[("kv", st)] = self.reading.get(("kv", st), 0) + 1
                 yield
-                assert self.kv[st] == 2 * c + 1 and all(x in ((("h", c), ("p", c)) if half == 0 else (("p", c),)) for x in self.s[t]), op
+                assert self.kv[st] == 2 * c + 1 and all(x == ("p", c) for x in self.s[t]), op
                 self.reading[("kv", st)] -= 1
                 assert not self.reading.get(("o", t)), "accumulator overwritten while read"
-                if half:
-                    self.o[t] = [c] if first else self.o[t] + [c]
+                self.o[t] = [c] if first else self.o[t] + [c]
             self.tensor.pop(0)
             yield
 
@@ -287,10 +283,8 @@ class Model:
                     assert self.o[t][-1] == c - (2 if w["alt"] else 1)
                 for _ in range(rng.choice([0, 2, 9])):
                     yield
-                for tag, bar in (("h", self.p_half[t]), ("p", self.p_full[t])):
-                    self.s[t] = self.s[t][:me] + [(tag, c)] + self.s[t][me + 1:]
-                    bar.arrive()
-                    yield
+                self.s[t] = self.s[t][:me] + [("p", c)] + self.s[t][me + 1:]
+                self.p_full[t].arrive()
                 mine.append(c)
                 num += 1
             if w["n"][t]:
