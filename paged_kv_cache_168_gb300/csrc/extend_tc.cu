@@ -43,9 +43,9 @@
 //   warps 12-15     (caches whose chunks are not operands: 8-bit codes, blocks
 //                   of fewer than 8 tokens) fill the K and V stages in place of
 //                   the copies: codes become exact 16-bit integers, and the
-//                   scales are applied in the softmax: K's to the scores, V's
-//                   by adding log2(scale) to the exponent, so that weights stay
-//                   at most 2^8 whatever the scales are.
+//                   scales are applied in the softmax: K's to the scores, V's to
+//                   the weights, whose maximum is taken with the tile's largest V
+//                   scale, so that they stay at most 2^8 whatever the scales are.
 // Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, and the CTA drains its
 // own copies and products before releasing TMEM.
 #include <cuda.h>
@@ -387,8 +387,8 @@ struct Cfg {
   static constexpr int kThreads = kConvert ? 512 : 384;
   // registers: the softmax warpgroups hold a row's 128 scores (sums equal the launch's)
   static constexpr int kRegsSoftmax = kConvert ? 176 : 200;
-  static constexpr int kRegsRest = kConvert ? 80 : 104;
-  static constexpr int kRegsConvert = 80;
+  static constexpr int kRegsRest = kConvert ? 88 : 104;
+  static constexpr int kRegsConvert = 72;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
   // K and V tiles take turns in one ring: K of tile c is fill 2c, V fill 2c + 1, fill
@@ -418,7 +418,8 @@ struct __align__(16) Shared {
   int pad[3];
 };
 struct __align__(16) Scales {
-  float k[kScaleRing][kKv], lv[kScaleRing][kKv], iv[kScaleRing][kKv];
+  float k[kScaleRing][kKv], v[kScaleRing][kKv];    // (K's times the softmax scale, base 2)
+  float top[kScaleRing][4];                        // largest V scale of each 32 tokens
 };
 
 // Bound of every wait: about a second, far above any wait of a healthy call.
@@ -447,6 +448,11 @@ __device__ __forceinline__ void unpack2f(uint64_t v, float& a, float& b) {
 __device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
@@ -1040,10 +1046,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           cp_async_wait<0>();
           if (ok && n > 0) complete(2 * c - 1);
         } else {
-          // codes go through registers: a tile's are loaded while the one before is converted
-          uint4 xk[kLoads], xv[kLoads];
+          // codes go through registers, K and V in turn: one part's loads are in flight
+          // while the other's buffer is waited for
+          uint4 x[kLoads];
           float sk = 0.f, sv = 0.f;
-          auto load = [&](int j, int part, uint4* x) {
+          auto load = [&](int j, int part) {
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
               const int id = block(e);
@@ -1056,7 +1063,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
             sv = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 1, t));
           };
-          auto write = [&](int part, const uint4* x) {
+          auto write = [&](int part) {
             uint8_t* dst = buffer(2 * c + part);
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
@@ -1093,39 +1100,40 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.full[(2 * c + part) % NB]);
           };
+          int next = -1;
           if (n > 0) {
             mine = look_up(0);
-            load(0, 0, xk);
-            load(0, 1, xv);
+            load(0, 0);
             load_scales(0);
           }
           for (int j = 0; j < n; ++j, ++c) {
-            if (j + 1 < n) mine = look_up(j + 1);
+            if (j + 1 < n) next = look_up(j + 1);
             if (!wait_empty(2 * c)) {
               ok = false;
               break;
             }
             {
               const int r = c % kScaleRing;
-              // zero vectors have scale 0 and zero codes: any positive scale stands for them
-              const float s = sv == 0.f ? 1.f : fmaxf(sv, 1.2e-38f);
+              // the tile's largest V scale bounds its weights
+              float top = sv;
+#pragma unroll
+              for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
               scales.k[r][ct] = sk * p.scale_log2;
-              scales.lv[r][ct] = log2f(s);
-              scales.iv[r][ct] = 1.f / s;
+              scales.v[r][ct] = sv;
+              if (lane == 0) scales.top[r][ct >> 5] = top;
               __syncwarp();
               if (lane == 0) mbar_arrive(&sh.sc_full[r]);
             }
-            write(0, xk);
-            if (j + 1 < n) {
-              load(j + 1, 0, xk);
-              load_scales(j + 1);
-            }
+            write(0);
+            load(j, 1);
+            if (j + 1 < n) load_scales(j + 1);
             if (!wait_empty(2 * c + 1)) {
               ok = false;
               break;
             }
-            write(1, xv);
-            if (j + 1 < n) load(j + 1, 1, xv);
+            write(1);
+            mine = next;
+            if (j + 1 < n) load(j + 1, 0);
           }
         }
         if (ok) done_item(i);
@@ -1185,13 +1193,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             break;
           }
           const float4* sk = reinterpret_cast<const float4*>(scales.k[c % kScaleRing]);
-          const float4* lv = reinterpret_cast<const float4*>(scales.lv[c % kScaleRing]);
 #pragma unroll
           for (int e = 0; e < kKv / 4; ++e) {
-            const float4 a = sk[e], b = lv[e];
-            unpack2f(fma2f(pack2f(x[4 * e], x[4 * e + 1]), pack2f(a.x, a.y), pack2f(b.x, b.y)), x[4 * e], x[4 * e + 1]);
-            unpack2f(fma2f(pack2f(x[4 * e + 2], x[4 * e + 3]), pack2f(a.z, a.w), pack2f(b.z, b.w)), x[4 * e + 2],
-                     x[4 * e + 3]);
+            const float4 a = sk[e];
+            unpack2f(mul2f(pack2f(x[4 * e], x[4 * e + 1]), pack2f(a.x, a.y)), x[4 * e], x[4 * e + 1]);
+            unpack2f(mul2f(pack2f(x[4 * e + 2], x[4 * e + 3]), pack2f(a.z, a.w)), x[4 * e + 2], x[4 * e + 3]);
           }
         }
         if (edge) {
@@ -1230,6 +1236,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const float unit = kI8 ? 1.f : p.scale_log2;                 // x is in base-2 units already (8-bit)
         mt *= unit;
+        if constexpr (kI8) {
+          // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the scale
+          const float4 s = *reinterpret_cast<const float4*>(scales.top[c % kScaleRing]);
+          mt += log2f(fmaxf(fmaxf(fmaxf(s.x, s.y), fmaxf(s.z, s.w)), 0x1p-100f));   // (sums stay finite)
+        }
         const float m_new = fmaxf(m, mt);
         const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
         if (m == -INFINITY) m = m_new;
@@ -1261,6 +1272,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
         for (int e = 0; e < kKv / 32; ++e) {
           uint32_t y[16];
+          float4 vs;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int col = e * 32 + 2 * k;
@@ -1269,11 +1281,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             unpack2f(kI8 ? add2f(xx, nm2) : fma2f(xx, unit2, nm2), a, b);
             a = ex2_approx(a);
             b = ex2_approx(b);
-            const uint64_t ab = pack2f(a, b);
-            if constexpr (kI8)
-              sum[k & 1] = fma2f(ab, *reinterpret_cast<const uint64_t*>(&scales.iv[c % kScaleRing][col]), sum[k & 1]);
-            else
-              sum[k & 1] = add2f(ab, sum[k & 1]);
+            sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
+            if constexpr (kI8) {
+              const float4* sv = reinterpret_cast<const float4*>(scales.v[c % kScaleRing] + e * 32);
+              if (!(k & 1)) vs = sv[k >> 1];
+              unpack2f(mul2f(pack2f(a, b), k & 1 ? pack2f(vs.z, vs.w) : pack2f(vs.x, vs.y)), a, b);
+            }
             y[k] = Elem<PT>::pack2(a, b);
           }
           tc::tmem_st16u(s_addr + e * 16, y);
