@@ -1046,18 +1046,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           cp_async_wait<0>();
           if (ok && n > 0) complete(2 * c - 1);
         } else {
-          // codes go through registers, K and V in turn: one part's loads are in flight
-          // while the other's buffer is waited for
-          uint4 x[kLoads];
-          float sk = 0.f, sv = 0.f;
+          // Codes are staged in shared memory, K and V in turn: a thread copies in and
+          // converts its own 16-byte pieces, and asks for the next part's when it has
+          // read this one's (in registers they would not leave the softmax enough).
+          const uint32_t stage = smem_u32(&scales + 1) + ct * 16;
           auto load = [&](int j, int part) {
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
               const int id = block(e);
-              x[e] = id < 0 ? make_uint4(0, 0, 0, 0)
-                            : *reinterpret_cast<const uint4*>(p.cache + L8.code(id, w.kvh, part, place(j, e), piece * 16));
+              const uint8_t* src = id < 0 ? p.cache : p.cache + L8.code(id, w.kvh, part, place(j, e), piece * 16);
+              cp_async16(stage + e * 2048, src, id >= 0);
             }
+            cp_async_commit();
           };
+          float sk = 0.f, sv = 0.f;
           auto load_scales = [&](int j) {
             const int id = find(j, ct), t = ((w.tile0 + j) * kKv + ct) & (bs - 1);
             sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
@@ -1065,9 +1067,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           };
           auto write = [&](int part) {
             uint8_t* dst = buffer(2 * c + part);
-#pragma unroll
+            cp_async_wait<0>();
+#pragma unroll 2
             for (int e = 0; e < kLoads; ++e) {
-              const uint32_t in[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+              uint32_t in[4];
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(in[0]), "=r"(in[1]), "=r"(in[2]), "=r"(in[3])
+                           : "r"(stage + e * 2048)
+                           : "memory");
               uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1592,7 +1599,7 @@ cudaError_t encode_maps(const ExtendParams& p, int act_dtype, CUtensorMap* q_map
 template <typename T, int D, Fill F>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
   using C = Cfg<D, F>;
-  constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) : 0);
+  constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) + kKv * D : 0);
   static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
   cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F>>(smem);
   if (e != cudaSuccess) return e;
