@@ -73,7 +73,7 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, i
 // arithmetic.  One token a CTA and round (two barriers for 1.5 units a thread) ran
 // at 4.4 TB/s where this one runs at the rate given in the header comment.
 template <typename T, int D, bool kPairs, bool kI8, int kTokens>
-__global__ void __launch_bounds__(kThreads, kI8 ? 3 : 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kUnits = D / 16;                     // units per head vector
   __shared__ __align__(16) float cs[kTokens][D];
   __shared__ int64_t slots[kTokens];                 // where the token goes; -1: nowhere
@@ -155,14 +155,20 @@ __global__ void __launch_bounds__(kThreads, kI8 ? 3 : 4) rope_cache_kernel(const
             uint32_t code[4] = {0, 0, 0, 0};
             float scale = 0.f;
             if (amax > 0.f) {
+              // x * inv is at most 127 (1 + 2^-22) in size: added to 1.5 * 2^23 it is
+              // rounded half to even into the sum's low byte
               const float inv = __fmul_rn(127.f, __fdiv_rn(1.f, amax));
+              uint32_t r[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                code[k >> 2] |= (uint32_t)(min(127, max(-127, __float2int_rn(__fmul_rn(x[k], inv)))) & 0xff) << (8 * (k & 3));
+              for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__fadd_rn(__fmul_rn(x[k], inv), 12582912.f));
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                code[k] = __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040), __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);
               scale = __fmul_rn(amax, 1.f / 127.f);
             }
-            *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, a * 8)) = make_uint2(code[0], code[1]);
-            *reinterpret_cast<uint2*>(p.cache + L8.code(block, h, part - 1, t, b * 8)) = make_uint2(code[2], code[3]);
+            uint8_t* at = p.cache + L8.chunk(block, h) + ((part - 1) * p.block_size + t) * 128;
+            *reinterpret_cast<uint2*>(at + ((((a >> 1) ^ (t & 7)) << 4) | (a & 1) << 3)) = make_uint2(code[0], code[1]);
+            *reinterpret_cast<uint2*>(at + ((((b >> 1) ^ (t & 7)) << 4) | (b & 1) << 3)) = make_uint2(code[2], code[3]);
             if (u == 0) *reinterpret_cast<float*>(p.cache + L8.scale(block, h, part - 1, t)) = scale;
             continue;
           }
