@@ -317,10 +317,12 @@ def _tensors(dtype, **tensors):
 
 
 def _rows(t, shape, name):
-    """A [tokens, heads, dims] tensor of that shape with heads and dims contiguous (the token stride is free)."""
-    if t.shape != shape or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]):
+    """The token stride of a [tokens, heads, dims] tensor of that shape with heads and dims contiguous."""
+    st = t.stride()
+    if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
         raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be [tokens, heads, dims] = {tuple(shape)} with heads and "
-                                               f"dims contiguous, not {tuple(t.shape)} with strides {t.stride()}")
+                                               f"dims contiguous, not {tuple(t.shape)} with strides {st}")
+    return st[0]
 
 
 def rope_table(max_position: int, inv_freq: torch.Tensor, device="cuda") -> torch.Tensor:
@@ -362,13 +364,12 @@ def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, k
         _tensors(torch.int64, slot_mapping=slot_mapping)
         _tensors(torch.int32, positions=positions)
         _tensors(torch.float32, cos_sin=cos_sin)
-    _rows(key, kv_shape, "key")
-    _rows(value, kv_shape, "value")
-    hq = 0
+    key_pitch, value_pitch = _rows(key, kv_shape, "key"), _rows(value, kv_shape, "value")
+    hq = q_pitch = out_pitch = 0
     if q is not None:
         hq = q.shape[1]
-        _rows(q, (n, hq, desc.head_size), "q")
-        _rows(q_out, (n, hq, desc.head_size), "q_out")
+        q_shape = (n, hq, desc.head_size)
+        q_pitch, out_pitch = _rows(q, q_shape, "q"), _rows(q_out, q_shape, "q_out")
     if not (slot_mapping.is_contiguous() and cos_sin.is_contiguous()) or positions.shape[-1] != n or \
             slot_mapping.numel() != n or (n > 1 and positions.stride(-1) != 1):
         raise PagedKVError(PA_ERR_INVALID_ARG, "positions and slot_mapping must have one dense entry per token, and "
@@ -379,9 +380,8 @@ def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, k
         if len(pairs) != cos_sin.shape[1] // 2:
             raise PagedKVError(PA_ERR_INVALID_ARG, f"pair_axis has {len(pairs)} entries, not {cos_sin.shape[1] // 2}")
     _on_device(load().pa_rope_reshape_and_cache, key, stream,
-               None if q is None else q_out.data_ptr(), 0 if q is None else q_out.stride(0),
-               None if q is None else q.data_ptr(), 0 if q is None else q.stride(0), hq, kv_cache.data_ptr(),
-               desc.ref(), layer, key.data_ptr(), key.stride(0), value.data_ptr(), value.stride(0),
+               None if q is None else q_out.data_ptr(), out_pitch, None if q is None else q.data_ptr(), q_pitch, hq,
+               kv_cache.data_ptr(), desc.ref(), layer, key.data_ptr(), key_pitch, value.data_ptr(), value_pitch,
                slot_mapping.data_ptr(), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
                cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], pairs, axes,
                1 if interleaved else 0, n, None if dev_err is None else dev_err.data_ptr())
@@ -437,13 +437,13 @@ def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Cac
             and query_start_loc.dtype is i32):
         _tensors(dt, out=out, q=q)
         _tensors(i32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
-    _rows(q, (T, Hq, desc.head_size), "q")
+    q_pitch = _rows(q, (T, Hq, desc.head_size), "q")
     (rows, width), (pitch, step) = block_tables.shape, block_tables.stride()
     if (out.shape != q.shape or query_start_loc.numel() < S + 1 or rows < S or (width > 1 and step != 1)
             or not (out.is_contiguous() and context_lens.is_contiguous() and query_start_loc.is_contiguous())):
         raise PagedKVError(PA_ERR_INVALID_ARG, "out must be contiguous and of q's shape, query_start_loc and "
                                                "block_tables long enough, table rows dense")
-    _on_device(load().pa_extend, q, stream, out.data_ptr(), q.data_ptr(), q.stride(0), kv_cache.data_ptr(), desc.ref(),
+    _on_device(load().pa_extend, q, stream, out.data_ptr(), q.data_ptr(), q_pitch, kv_cache.data_ptr(), desc.ref(),
                layer, block_tables.data_ptr(), pitch if S > 1 else max(width, 1), context_lens.data_ptr(),
                query_start_loc.data_ptr(), S, T, Hq, max_query_len, scale, window, ring_blocks,
                None if workspace is None else workspace.data_ptr(),

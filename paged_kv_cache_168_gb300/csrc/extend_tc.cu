@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   };
 
   uint32_t none = 0;
-  int64_t work = 0;
+  int64_t work = 0, mine_tiles = 0;
   for (int s = s0; s < s1; ++s) {
     const Seq q = seq(s, err);
     if (!q.listed || q.zero) continue;
@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     int t0;
     const int n0 = tile_range(p, q, q.ctx - q.q_len, min(pair, q.q_len), t0);
     work += ((int64_t)n0 + last_range(q, nt)) * nt / 2;
+    mine_tiles += nt;
   }
   int64_t total;
   block_scan(work, tmp, total);
@@ -262,7 +263,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   // tokens; K = 1: 8 sequences of 32K to 131K tokens lose 10%.)
   const int64_t per_sm = total * hkv / sms;
   const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
-  const int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
+  int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
+  // query tiles that cover half of the SMs are not cut for less than a dozen KV tiles
+  int64_t tiles;
+  block_scan(mine_tiles, tmp, tiles);
+  if (tiles * hkv * 2 >= sms) longest = max(longest, (int64_t)12);
 
   // parts wanted and their partial rows
   auto parts_of = [&](const Seq& q, int nt, int64_t& rows) {
@@ -1001,50 +1006,55 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         auto block = [&](int e) { return __shfl_sync(kFull, mine, e * kTok + lane / kPer); };
         auto place = [&](int j, int e) { return ((w.tile0 + j) * kKv + u0 + e * (128 / kPer)) & (bs - 1); };
         if constexpr (!kI8) {
-          // 16-byte pieces by asynchronous copies, absent tokens as zeros.  A fill is
-          // completed after the next one has been issued.
-          auto issue = [&](int j, int part) {
-            const uint32_t dst = smem_u32(buffer(2 * c + part));
+          // 16-byte pieces by asynchronous copies, absent tokens as zeros; a token's K and V
+          // together (their addresses differ by a constant).  A tile is completed after
+          // the next one has been issued.
+          auto issue = [&](int j) {
+            const uint32_t k_dst = smem_u32(buffer(2 * c)), v_dst = smem_u32(buffer(2 * c + 1));
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
-              const int id = block(e);
+              const int id = block(e), s = place(j, e);
               // a block of fewer than 8 tokens is one group: K atoms, then V atoms, of bs rows each
-              const int s = place(j, e);
-              const int in_block = ((part * (D / 64) + (piece >> 3)) * bs + s) * 64 + (((piece & 7) ^ s) << 3);
-              const uint8_t* src = id < 0 ? p.cache
-                                          : p.cache + 2 * (((int64_t)id * p.num_kv_heads + w.kvh) * (2 * D * bs) + in_block);
-              cp_async16(dst + kv_offset<D>(u0 + e * (128 / kPer), piece), src, id >= 0);
+              const int in_block = ((piece >> 3) * bs + s) * 64 + (((piece & 7) ^ s) << 3);
+              const uint8_t* src = p.cache;
+              if (id >= 0) src += 2 * (((int64_t)id * p.num_kv_heads + w.kvh) * (2 * D * bs) + in_block);
+              const uint32_t at = kv_offset<D>(u0 + e * (128 / kPer), piece);
+              cp_async16(k_dst + at, src, id >= 0);
+              cp_async16(v_dst + at, id >= 0 ? src + 2 * D * bs : src, id >= 0);
             }
             cp_async_commit();
           };
-          auto complete = [&](int fill) {
+          auto complete = [&](int tile) {
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.full[fill % NB]);
+            if (lane == 0) {
+              mbar_arrive(&sh.full[2 * tile % NB]);
+              mbar_arrive(&sh.full[(2 * tile + 1) % NB]);
+            }
           };
           int next = n > 0 ? look_up(0) : -1;
           for (int j = 0; j < n; ++j, ++c) {
             mine = next;
             if (j + 1 < n) next = look_up(j + 1);
-            if (!wait_empty(2 * c)) {
+            // the tile before this one is completed now if this one's buffers are not free yet
+            bool pending = j > 0;
+            if (pending && c >= 2 && !__all_sync(kFull, mbar_test_wait(&sh.empty[(2 * c + 1) % NB], ((2 * c + 1) / NB - 1) & 1))) {
+              cp_async_wait<0>();
+              complete(c - 1);
+              pending = false;
+            }
+            if (!wait_empty(2 * c) || !wait_empty(2 * c + 1)) {
               ok = false;
               break;
             }
-            issue(j, 0);
-            if (j > 0) {
+            issue(j);
+            if (pending) {
               cp_async_wait<1>();
-              complete(2 * c - 1);
+              complete(c - 1);
             }
-            if (!wait_empty(2 * c + 1)) {
-              ok = false;
-              break;
-            }
-            issue(j, 1);
-            cp_async_wait<1>();
-            complete(2 * c);
           }
           cp_async_wait<0>();
-          if (ok && n > 0) complete(2 * c - 1);
+          if (ok && n > 0) complete(c - 1);
         } else {
           // Codes are staged in shared memory, K and V in turn: a thread copies in and
           // converts its own 16-byte pieces, and asks for the next part's when it has
