@@ -369,6 +369,7 @@ constexpr int kRing = 4;                   // items between the drawing warp and
 // and a softmax warpgroup can then be at most six tiles behind (items of one
 // tile each, all for query tile 0: their epilogues meet).
 constexpr int kScaleRing = 8;
+constexpr int kScalePitch = 36;
 
 // An item as the roles see it.
 struct Work {
@@ -390,10 +391,12 @@ struct Cfg {
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr bool kConvert = F != kBulk;
   static constexpr int kThreads = kConvert ? 512 : 384;
-  // registers: the softmax warpgroups hold a row's 128 scores (sums equal the launch's)
-  static constexpr int kRegsSoftmax = kConvert ? 176 : 200;
-  static constexpr int kRegsRest = kConvert ? 88 : 104;
-  static constexpr int kRegsConvert = 72;
+  // registers a thread, whose sum over the warpgroups is the launch's: the softmax
+  // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
+  // caches half of a tile's codes
+  static constexpr int kRegsSoftmax = F == kBulk ? 200 : F == kGather ? 176 : 160;
+  static constexpr int kRegsRest = F == kBulk ? 104 : F == kGather ? 88 : 96;
+  static constexpr int kRegsConvert = F == kGather ? 72 : 96;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
   // K and V tiles take turns in one ring: K of tile c is fill 2c, V fill 2c + 1, fill
@@ -423,7 +426,9 @@ struct __align__(16) Shared {
   int pad[3];
 };
 struct __align__(16) Scales {
-  float k[kScaleRing][kKv], v[kScaleRing][kKv];    // (K's times the softmax scale, base 2)
+  // column 8 n + 2 q + b at q * kScalePitch + 2 n + b: what a softmax thread reads is
+  // contiguous, and the four of a row read different banks
+  float k[kScaleRing][4 * kScalePitch], v[kScaleRing][4 * kScalePitch];    // (K's times the softmax scale, base 2)
   float top[kScaleRing][4];                        // largest V scale of each 32 tokens
 };
 
@@ -487,6 +492,67 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 TMEM lanes x 128 columns (16 x 256 bits, 16 times): lane l of the warp gets columns 8 n + 2 (l % 4) + {0, 1} of
+// rows l / 4 (v[4 n], v[4 n + 1]) and l / 4 + 8 (v[4 n + 2], v[4 n + 3]).
+__device__ __forceinline__ void tmem_ld16x256(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, "
+      "%51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+        "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
+        "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]),
+        "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]),
+        "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The same of 32 columns, both ways.
+__device__ __forceinline__ void tmem_ld16x256_32(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16x256_32(uint32_t taddr, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+               "%13, %14, %15, %16};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+               "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+// 16 lanes x 64 columns (16 x 128 bits, 16 times): column 4 n + l % 4 of rows l / 4 (r[2 n]) and l / 4 + 8
+// (r[2 n + 1]).
+__device__ __forceinline__ void tmem_st16x128(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+               "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+               "%31, %32};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+               "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+               "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+               "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 
 // 32 TMEM lanes x 32 columns.
@@ -1056,35 +1122,37 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           cp_async_wait<0>();
           if (ok && n > 0) complete(c - 1);
         } else {
-          // Codes are staged in shared memory, K and V in turn: a thread copies in and
-          // converts its own 16-byte pieces, and asks for the next part's when it has
-          // read this one's (in registers they would not leave the softmax enough).
+          // A thread converts the 16-byte pieces that it has loaded itself: K's are staged
+          // in shared memory by asynchronous copies, V's in registers (there is no room
+          // for both in either), each asked for as soon as the tile before is converted.
           const uint32_t stage = smem_u32(&scales + 1) + ct * 16;
-          auto load = [&](int j, int part) {
+          uint4 v[kLoads];
+          auto load = [&](int j, auto which) {
+            constexpr int part = decltype(which)::value;
 #pragma unroll
             for (int e = 0; e < kLoads; ++e) {
               const int id = block(e);
               const uint8_t* src = id < 0 ? p.cache : p.cache + L8.code(id, w.kvh, part, place(j, e), piece * 16);
-              cp_async16(stage + e * 2048, src, id >= 0);
+              if (part == 0) {
+                cp_async16(stage + e * 2048, src, id >= 0);
+              } else {
+                v[e] = id < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(src);
+              }
             }
-            cp_async_commit();
+            if (part == 0) cp_async_commit();
           };
+          constexpr std::integral_constant<int, 0> kK{};
+          constexpr std::integral_constant<int, 1> kV{};
           float sk = 0.f, sv = 0.f;
           auto load_scales = [&](int j) {
             const int id = find(j, ct), t = ((w.tile0 + j) * kKv + ct) & (bs - 1);
             sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
             sv = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 1, t));
           };
-          auto write = [&](int part) {
+          auto write = [&](auto which) {
+            constexpr int part = decltype(which)::value;
             uint8_t* dst = buffer(2 * c + part);
-            cp_async_wait<0>();
-#pragma unroll 2
-            for (int e = 0; e < kLoads; ++e) {
-              uint32_t in[4];
-              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(in[0]), "=r"(in[1]), "=r"(in[2]), "=r"(in[3])
-                           : "r"(stage + e * 2048)
-                           : "memory");
+            auto convert = [&](const uint32_t (&in)[4], int e) {
               uint32_t y[8];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -1112,6 +1180,24 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               const int u = u0 + e * (128 / kPer);
               *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece)) = make_uint4(y[0], y[1], y[2], y[3]);
               *reinterpret_cast<uint4*>(dst + kv_offset<D>(u, 2 * piece + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+            };
+            if (part == 0) {
+              cp_async_wait<0>();
+#pragma unroll 2
+              for (int e = 0; e < kLoads; ++e) {
+                uint32_t in[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(in[0]), "=r"(in[1]), "=r"(in[2]), "=r"(in[3])
+                             : "r"(stage + e * 2048)
+                             : "memory");
+                convert(in, e);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < kLoads; ++e) {
+                const uint32_t in[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+                convert(in, e);
+              }
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
@@ -1120,7 +1206,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           int next = -1;
           if (n > 0) {
             mine = look_up(0);
-            load(0, 0);
+            load(0, kK);
+            load(0, kV);
             load_scales(0);
           }
           for (int j = 0; j < n; ++j, ++c) {
@@ -1135,22 +1222,25 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               float top = sv;
 #pragma unroll
               for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-              scales.k[r][ct] = sk * p.scale_log2;
-              scales.v[r][ct] = sv;
+              const int at = (ct % 8 / 2) * kScalePitch + ct / 8 * 2 + ct % 2;
+              scales.k[r][at] = sk * p.scale_log2;
+              scales.v[r][at] = sv;
               if (lane == 0) scales.top[r][ct >> 5] = top;
               __syncwarp();
               if (lane == 0) mbar_arrive(&sh.sc_full[r]);
             }
-            write(0);
-            load(j, 1);
-            if (j + 1 < n) load_scales(j + 1);
+            write(kK);
+            mine = next;
+            if (j + 1 < n) {
+              load(j + 1, kK);
+              load_scales(j + 1);
+            }
             if (!wait_empty(2 * c + 1)) {
               ok = false;
               break;
             }
-            write(1);
-            mine = next;
-            if (j + 1 < n) load(j + 1, 0);
+            write(kV);
+            if (j + 1 < n) load(j + 1, kV);
           }
         }
         if (ok) done_item(i);
@@ -1192,6 +1282,20 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int n = t == 0 ? w.n[0] : w.n[1];
       const int tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
       float m = -INFINITY, l = 0.f;
+      // 8-bit caches: a thread has rows gr + 8 i of its warp's 32 (and a quarter of their columns)
+      float m4[4], l4[4];
+      int pos4[4];
+      uint32_t ok4 = 0;
+      if constexpr (kI8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = (warp & 3) * 32 + (lane >> 2) + 8 * k, ip = r / G;
+          pos4[k] = w.pos0 + my0 + ip;
+          if (ip < (alt ? w.npos : min(ptile, w.npos - my0))) ok4 |= 1u << k;
+          m4[k] = -INFINITY;
+          l4[k] = 0.f;
+        }
+      }
       for (int j = 0; j < n; ++j, ++num) {
         const int jt = alt ? 2 * j + t : j, c = c0 + jt;
         const int t0 = (tile0 + jt) * kKv;
@@ -1200,123 +1304,233 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           break;
         }
         tc::fence_after_sync();
-        float x[kKv];
-        tmem_ld64(s_addr, x);
-        tmem_ld64(s_addr + 64, x + 64);
         const bool edge = jt < edge_lo || jt >= edge_hi;
         if constexpr (kI8) {
-          if (!wait(&sh.sc_full[c % kScaleRing], (c / kScaleRing) & 1)) {
+          // Scales are per token, that is per column: a thread that held a whole row
+          // would read all 128 of K's and of V's, and those reads alone would keep the
+          // SM's shared memory busy for 2000 clocks a tile.  Read as 16 x 256 bits, a
+          // thread holds 32 columns (8 n + 2 q, + 1) of four rows (gr + 8 i) instead.
+          const int slot = c % kScaleRing;
+          if (!wait(&sh.sc_full[slot], (c / kScaleRing) & 1)) {
             ok = false;
             break;
           }
-          const float4* sk = reinterpret_cast<const float4*>(scales.k[c % kScaleRing]);
+          const float4 tops = *reinterpret_cast<const float4*>(scales.top[slot]);
+          // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the
+          // tile's largest one (bounded below: sums stay finite)
+          const float bias = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
+          const float4* ks = reinterpret_cast<const float4*>(&scales.k[slot][(lane & 3) * kScalePitch]);
+          const float4* vs = reinterpret_cast<const float4*>(&scales.v[slot][(lane & 3) * kScalePitch]);
+          // 16 rows each; one copy of the code (it has to stay in the instruction cache),
+          // so the rows' state changes places after each
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t half = (uint32_t)(16 * h) << 16;
+            float x[64];                                             // [n][row 2 h, 2 h + 1][2]
+            tmem_ld16x256(s_addr + half, x);
 #pragma unroll
-          for (int e = 0; e < kKv / 4; ++e) {
-            const float4 a = sk[e];
-            unpack2f(mul2f(pack2f(x[4 * e], x[4 * e + 1]), pack2f(a.x, a.y)), x[4 * e], x[4 * e + 1]);
-            unpack2f(mul2f(pack2f(x[4 * e + 2], x[4 * e + 3]), pack2f(a.z, a.w)), x[4 * e + 2], x[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) {
+              const float4 k = ks[e];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                unpack2f(mul2f(pack2f(x[8 * e + 2 * r], x[8 * e + 2 * r + 1]), pack2f(k.x, k.y)), x[8 * e + 2 * r],
+                         x[8 * e + 2 * r + 1]);
+                unpack2f(mul2f(pack2f(x[8 * e + 4 + 2 * r], x[8 * e + 5 + 2 * r]), pack2f(k.z, k.w)), x[8 * e + 4 + 2 * r],
+                         x[8 * e + 5 + 2 * r]);
+              }
+            }
+            float alpha[2];
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              if (edge) {
+                const int lo = attend_from(pos4[r], p.window, w.held) - t0, hi = ok4 >> r & 1 ? pos4[r] + 1 - t0 : 0;
+                // how many of this thread's columns lie below a limit
+                auto below = [&](int v) {
+                  const int u = min(max(v, 0), kKv);
+                  return 2 * (u >> 3) + min(max((u & 7) - 2 * (lane & 3), 0), 2);
+                };
+                const uint32_t on = (uint32_t)((1ull << below(hi)) - 1) & ~(uint32_t)((1ull << below(lo)) - 1);
+                if (__any_sync(kFull, on != kFull)) {
+#pragma unroll
+                  for (int n = 0; n < 16; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                      x[4 * n + 2 * r + k] = (on >> (2 * n + k)) & 1 ? x[4 * n + 2 * r + k] : -INFINITY;
+                }
+              }
+              float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int n = 0; n < 16; ++n) top[n & 1] = fmaxf(fmaxf(top[n & 1], x[4 * n + 2 * r]), x[4 * n + 2 * r + 1]);
+              float mt = fmaxf(top[0], top[1]);
+              mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
+              mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2)) + bias;
+              const float m_new = fmaxf(m4[r], mt);
+              const bool need = (ok4 >> r & 1) && m4[r] != -INFINITY && m_new > m4[r] + kRescaleThreshold;
+              alpha[r] = need ? exp2f(m4[r] - m_new) : 1.f;
+              if (need || m4[r] == -INFINITY) m4[r] = m_new;
+              l4[r] *= alpha[r];
+              any |= need;
+            }
+            if (__any_sync(kFull, any)) {
+              if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
+              tc::fence_after_sync();
+              for (int e = 0; ok && e < D / 32; ++e) {
+                float o[16];
+                tmem_ld16x256_32(o_addr + half + e * 32, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= alpha[(k >> 1) & 1];
+                tmem_st16x256_32(o_addr + half + e * 32, o);
+              }
+            }
+            uint32_t y[32];
+            uint64_t sum[2] = {0, 0};
+            uint64_t nm[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float v = m4[r] == -INFINITY ? 0.f : -m4[r];
+              nm[r] = pack2f(v, v);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v = vs[e];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {                          // (n = 2 e + k / 2, row k & 1)
+                float a, b;
+                unpack2f(add2f(pack2f(x[8 * e + 2 * k], x[8 * e + 2 * k + 1]), nm[k & 1]), a, b);
+                const uint64_t ab = pack2f(ex2_approx(a), ex2_approx(b));
+                sum[k & 1] = add2f(ab, sum[k & 1]);
+                unpack2f(mul2f(ab, k < 2 ? pack2f(v.x, v.y) : pack2f(v.z, v.w)), a, b);
+                y[4 * e + k] = Elem<PT>::pack2(a, b);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float a, b;
+              unpack2f(sum[r], a, b);
+              l4[r] += a + b;
+            }
+            tmem_st16x128(s_addr + half, y);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float mm = m4[r], ll = l4[r];
+              const int pp = pos4[r];
+              m4[r] = m4[r + 2];
+              l4[r] = l4[r + 2];
+              pos4[r] = pos4[r + 2];
+              m4[r + 2] = mm;
+              l4[r + 2] = ll;
+              pos4[r + 2] = pp;
+            }
+            ok4 = (ok4 >> 2 | ok4 << 2) & 15u;
           }
-        }
-        if (edge) {
-          const int lo = from - t0, hi = row_ok ? pos + 1 - t0 : 0;  // attended columns [lo, hi)
+          if (!ok) break;
+        } else {
+          float x[kKv];
+          tmem_ld64(s_addr, x);
+          tmem_ld64(s_addr + 64, x + 64);
+          if (edge) {
+            const int lo = from - t0, hi = row_ok ? pos + 1 - t0 : 0;  // attended columns [lo, hi)
+#pragma unroll
+            for (int e = 0; e < kKv / 32; ++e) {
+              const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
+              const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+              if (__any_sync(kFull, on != kFull)) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+              }
+            }
+            if constexpr (F == kBulk) {
+              if (ragged(w, jt)) {
+                // thread = token here: V rows that hold no token of the context become
+                // zero (V has landed: the issuer waited for it)
+                if (!wait(&sh.full[(2 * c + 1) % NB], ((2 * c + 1) / NB) & 1)) {
+                  ok = false;
+                  break;
+                }
+                if (t0 + row >= w.kv_end || t0 + row < w.first) {
+                  uint8_t* v = buffer(2 * c + 1);
+#pragma unroll 2
+                  for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+              }
+            }
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
+#pragma unroll
+          for (int e = 0; e < kKv; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
+          float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          mt *= p.scale_log2;
+          const float m_new = fmaxf(m, mt);
+          const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
+          if (m == -INFINITY) m = m_new;
+          if (__any_sync(kFull, need)) {
+            // O holds exactly the tiles before this one once the last PV has completed
+            if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const float alpha = need ? exp2f(m - m_new) : 1.f;
+            if (need) {
+              l *= alpha;
+              m = m_new;
+            }
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              float o[16];
+              tc::tmem_ld16(o_addr + e * 16, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= alpha;
+              tc::tmem_st16(o_addr + e * 16, o);
+            }
+          }
+          // weights 2^(x - m), the sum of the unrounded ones in fp32
+          const float nm = m == -INFINITY ? 0.f : -m;
+          const uint64_t unit2 = pack2f(p.scale_log2, p.scale_log2), nm2 = pack2f(nm, nm);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int e = 0; e < kKv / 32; ++e) {
-            const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
-            const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
-            if (__any_sync(kFull, on != kFull)) {
+            uint32_t y[16];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+            for (int k = 0; k < 16; ++k) {
+              const int col = e * 32 + 2 * k;
+              const uint64_t xx = pack2f(x[col], x[col + 1]);
+              float a, b;
+              unpack2f(fma2f(xx, unit2, nm2), a, b);
+              a = ex2_approx(a);
+              b = ex2_approx(b);
+              sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
+              y[k] = Elem<PT>::pack2(a, b);
             }
+            tc::tmem_st16u(s_addr + e * 16, y);
           }
-          if constexpr (F == kBulk) {
-            if (ragged(w, jt)) {
-              // thread = token here: V rows that hold no token of the context become
-              // zero (V has landed: the issuer waited for it)
-              if (!wait(&sh.full[(2 * c + 1) % NB], ((2 * c + 1) / NB) & 1)) {
-                ok = false;
-                break;
-              }
-              if (t0 + row >= w.kv_end || t0 + row < w.first) {
-                uint8_t* v = buffer(2 * c + 1);
-#pragma unroll 2
-                for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
-              }
-              tc::fence_proxy_async_smem();
-            }
-          }
-        }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
-#pragma unroll
-        for (int e = 0; e < kKv; e += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
-        float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const float unit = kI8 ? 1.f : p.scale_log2;                 // x is in base-2 units already (8-bit)
-        mt *= unit;
-        if constexpr (kI8) {
-          // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the scale
-          const float4 s = *reinterpret_cast<const float4*>(scales.top[c % kScaleRing]);
-          mt += log2f(fmaxf(fmaxf(fmaxf(s.x, s.y), fmaxf(s.z, s.w)), 0x1p-100f));   // (sums stay finite)
-        }
-        const float m_new = fmaxf(m, mt);
-        const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
-        if (m == -INFINITY) m = m_new;
-        if (__any_sync(kFull, need)) {
-          // O holds exactly the tiles before this one once the last PV has completed
-          if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          const float alpha = need ? exp2f(m - m_new) : 1.f;
-          if (need) {
-            l *= alpha;
-            m = m_new;
-          }
-#pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            float o[16];
-            tc::tmem_ld16(o_addr + e * 16, o);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= alpha;
-            tc::tmem_st16(o_addr + e * 16, o);
-          }
-        }
-        // weights 2^(x - m), the sum of the unrounded ones in fp32
-        const float nm = m == -INFINITY ? 0.f : -m;
-        const uint64_t unit2 = pack2f(unit, unit), nm2 = pack2f(nm, nm);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < kKv / 32; ++e) {
-          uint32_t y[16];
-          float4 vs;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int col = e * 32 + 2 * k;
-            const uint64_t xx = pack2f(x[col], x[col + 1]);
+          {
             float a, b;
-            unpack2f(kI8 ? add2f(xx, nm2) : fma2f(xx, unit2, nm2), a, b);
-            a = ex2_approx(a);
-            b = ex2_approx(b);
-            sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
-            if constexpr (kI8) {
-              const float4* sv = reinterpret_cast<const float4*>(scales.v[c % kScaleRing] + e * 32);
-              if (!(k & 1)) vs = sv[k >> 1];
-              unpack2f(mul2f(pack2f(a, b), k & 1 ? pack2f(vs.z, vs.w) : pack2f(vs.x, vs.y)), a, b);
-            }
-            y[k] = Elem<PT>::pack2(a, b);
+            unpack2f(add2f(sum[0], sum[1]), a, b);
+            l += a + b;
           }
-          tc::tmem_st16u(s_addr + e * 16, y);
-        }
-        {
-          float a, b;
-          unpack2f(add2f(sum[0], sum[1]), a, b);
-          l += a + b;
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+      if constexpr (kI8) {
+        // to one row a lane: row lane is number lane / 8 of the lanes 4 (lane % 8) ..
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          l4[k] += __shfl_xor_sync(kFull, l4[k], 1);
+          l4[k] += __shfl_xor_sync(kFull, l4[k], 2);
+          const float mk = __shfl_sync(kFull, m4[k], (lane & 7) * 4), lk = __shfl_sync(kFull, l4[k], (lane & 7) * 4);
+          if (lane >> 3 == k) {
+            m = mk;
+            l = lk;
+          }
+        }
       }
       if (ok && n > 0 && !wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
       if (!ok) break;
