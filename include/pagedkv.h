@@ -192,8 +192,9 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
  * may differ from pa_reshape_and_cache's of the same vector in its last bit).
  *   q_out, q     device [num_tokens, num_q_heads, head_size], 16-bit; token
  *                strides in elements (multiples of 8), 16-byte aligned.  q_out
- *                may be q itself (with the same stride), and may otherwise not
- *                overlap it.  num_q_heads 0: no queries, both may be NULL.
+ *                may be q itself (with the same stride; q, key and value may be
+ *                parts of one row), and may otherwise not overlap it, nor key or
+ *                value.  num_q_heads 0: no queries, both may be NULL.
  *   kv_cache, desc, layer, key, value, strides, slot_mapping: as
  *                pa_reshape_and_cache; a token with slot -1 is not stored, its
  *                query is still rotated.
@@ -384,8 +385,9 @@ size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, in
  *   workspace       device, 16-byte aligned, >= pa_extend_workspace_bytes(...);
  *                   needs no initialisation, and is free again once the call's
  *                   work on the stream is done.
- *   dev_err         optional; also PA_DEVERR_CONTEXT for q_len > ctx or (without
- *                   a ring) ctx beyond the table row (zero rows), and
+ *   dev_err         optional; also PA_DEVERR_CONTEXT for q_len > ctx, ctx beyond
+ *                   2^31 - 129 or (without a ring) beyond the table row (zero
+ *                   rows), and
  *                   PA_DEVERR_BLOCK_ID for a bad block id: every row that
  *                   attends the block is zero, and rows computed beside it may be.
  * Supported: every cache of pa_decode (16-bit with head_size 64 or 128, 8-bit

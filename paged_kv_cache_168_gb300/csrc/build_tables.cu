@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesP
     }
 #pragma unroll
     for (int k = 0; k < kRun; ++k) {
-      const int i = (int)i0 + k;
       slot[k] = -1;
       pos[k] = 0;
-      if (i >= n_tok) continue;
+      if (i0 + k >= n_tok) continue;
+      const int i = (int)i0 + k;
       while (starts[s + 1] <= i) ++s;                 // (ends: i < starts[S])
       const int ctx = ctxs[s];
       const int cached = ctx - (starts[s + 1] - starts[s]);

@@ -165,7 +165,7 @@ __device__ __forceinline__ Seq read_seq(const ExtendParams& p, int s, uint32_t& 
     if (end != q.start || q.start < 0 || end > p.num_tokens) err |= PA_DEVERR_CONTEXT;
     return q;
   }
-  if (q.q_len > p.max_query_len || q.q_len > q.ctx ||
+  if (q.q_len > p.max_query_len || q.q_len > q.ctx || q.ctx > INT32_MAX - kKv ||      // (tile ends stay in int32)
       (p.ring_blocks == 0 && (int64_t)q.ctx > (int64_t)p.bt_stride * p.block_size)) {
     q.zero = true;
     err |= PA_DEVERR_CONTEXT;
@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   block_scan(work, tmp, total);
   // With K parts a SM the call takes about (work / sms) (1 + 1 / K) -- the last round
   // is half empty -- and K times an item's own cost, about 3 KV tiles: least at
-  // K = sqrt(work / sms / 3).  (Always K = 4: 137 us where 61 now, on windows of 1000
-  // tokens; K = 1: 8 sequences of 32K to 131K tokens lose 10%.)
+  // K = sqrt(work / sms / 3).  (K = 4 whatever the work: windows of 1000 tokens took 1.5
+  // times as long.)
   const int64_t per_sm = total * hkv / sms;
   const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
   int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);

@@ -211,7 +211,8 @@ def extend(q, cache, tables, ctx, qsl, scale, window=0, ring=0, num_tokens=None)
             z = qq @ kk * scale                                        # [Hkv, G, n]
             p = np.exp(z - z.max(-1, keepdims=True))
             p /= p.sum(-1, keepdims=True)
-            o, w = p @ vv, p @ np.abs(vv)
+            with np.errstate(invalid="ignore"):                        # (infinities among the values)
+                o, w = p @ vv, p @ np.abs(vv)
             ds = D * 2.0 ** -22 * scale * (np.abs(qq) @ np.abs(kk)).max(-1, keepdims=True)
             under = 2.0 ** -25 * np.abs(vv).sum(1)[:, None] if u_p == EPS["f16"] / 2 else 0.0
             out[a + j] = o.reshape(Hq, D)

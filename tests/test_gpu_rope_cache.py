@@ -197,3 +197,46 @@ def test_binding_table_is_the_documented_one():
     t = pkv.rope_table(1000, inv).cpu().numpy()
     ang = np.arange(1000)[:, None] * inv.numpy()
     np.testing.assert_allclose(t, np.concatenate([np.cos(ang), np.sin(ang)], 1), atol=2.0 ** -24)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_parts_of_one_row_in_place(kv8):
+    """q, k and v as slices of one projection's rows, q rotated in place; a layer of a pool of three."""
+    c = Case(16, 700, 4, 2, 128, 16, "bf16", kv8, axes=2)
+    rows = torch.cat([u16_to_dev(b, "bf16").view(c.N, -1) for b in (c.q, c.k, c.v)], 1)
+    q, k, v = (x.unflatten(1, (-1, 128)) for x in rows.split([512, 256, 256], 1))
+    b = c.before
+    desc = pkv.CacheDesc(b.nb, 16, 2, 128, torch.bfloat16, num_layers=3, kv_int8=kv8)
+    one = b.pool.view(np.uint8).reshape(-1)
+    pool = torch.from_numpy(np.concatenate([one * 0, one, one * 0])).cuda()
+    pkv.rope_reshape_and_cache(q, q, pool, desc, k, v, torch.from_numpy(c.slots).cuda(), torch.from_numpy(c.pos).cuda(),
+                               torch.from_numpy(c.cos_sin).cuda(), pair_axis=c.pair_axis, layer=1)
+    want = c.expected()
+    assert np.array_equal(dev_to_u16(q), want[0])
+    assert np.array_equal(dev_to_u16(k), c.k) and np.array_equal(dev_to_u16(v), c.v)
+    got = pool.cpu().numpy().reshape(3, -1)
+    assert np.array_equal(got[1], want[1].view(np.uint8).reshape(-1)) and not got[0].any() and not got[2].any()
+
+
+def test_replays_and_another_stream():
+    c = Case(17, 90, 4, 2, 128, 16, "f16", axes=3)
+    desc = pkv.CacheDesc(c.before.nb, 16, 2, 128, torch.float16)
+    t = [u16_to_dev(b, "f16") for b in (c.q, c.k, c.v)]
+    pool = torch.from_numpy(c.before.pool.view(np.int16).copy()).cuda()
+    args = [torch.from_numpy(x).cuda() for x in (c.slots, c.pos, c.cos_sin)]
+    out = torch.zeros_like(t[0])
+    call = lambda: pkv.rope_reshape_and_cache(out, t[0], pool, desc, t[1], t[2], *args, pair_axis=c.pair_axis)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call()
+        side.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call()
+    out.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    want = c.expected()
+    assert np.array_equal(dev_to_u16(out), want[0]) and np.array_equal(pool.cpu().numpy().view(np.uint16), want[1])
