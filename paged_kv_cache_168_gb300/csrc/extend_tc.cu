@@ -364,10 +364,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
 enum Fill { kBulk, kGather, kCodes };
 
 constexpr int kRing = 4;                   // items between the drawing warp and the others
-// Tiles' scales (8-bit caches).  They have no barrier of their own for reuse: when
-// tile c's are written, tiles up to c - 2 have gone through their first product,
-// and a softmax warpgroup can then be at most six tiles behind (items of one
-// tile each, all for query tile 0: their epilogues meet).
+// Tiles' scales (8-bit caches).  They have no barriers of their own.  They are
+// written before their tile's K, and so before its scores.  When tile c's are
+// written, tiles up to c - 2 have gone through their first product, and a softmax
+// warpgroup can then be at most six tiles behind (items of one tile each, all for
+// query tile 0: their epilogues meet).
 constexpr int kScaleRing = 8;
 constexpr int kScalePitch = 36;
 
@@ -415,7 +416,6 @@ struct __align__(16) Shared {
   uint64_t pv_done[2][2];
   uint64_t item_full[kRing], item_empty[kRing];
   uint64_t xbar;                           // the two softmax warpgroups (items that share a query tile)
-  uint64_t sc_full[kScaleRing];
   uint64_t mma_drain;
   Work work[kRing];
   volatile int bad[kRing];                 // a block id out of range was met
@@ -667,7 +667,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       // 8 softmax warps, the issuing warp, the Q warp, and the V warp or 4 converter warps
       mbar_init(&sh.item_empty[i], C::kConvert ? 14 : 11);
     }
-    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sh.sc_full[i], 4);
     mbar_init(&sh.xbar, 8);
     mbar_init(&sh.mma_drain, 1);
     sh.abort_flag = 0;
@@ -1226,8 +1225,6 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               scales.k[r][at] = sk * p.scale_log2;
               scales.v[r][at] = sv;
               if (lane == 0) scales.top[r][ct >> 5] = top;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.sc_full[r]);
             }
             write(kK);
             mine = next;
@@ -1310,15 +1307,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           // would read all 128 of K's and of V's, and those reads alone would keep the
           // SM's shared memory busy for 2000 clocks a tile.  Read as 16 x 256 bits, a
           // thread holds 32 columns (8 n + 2 q, + 1) of four rows (gr + 8 i) instead.
+          // (They were written before this tile's K was, which the scores have waited for.)
           const int slot = c % kScaleRing;
-          if (!wait(&sh.sc_full[slot], (c / kScaleRing) & 1)) {
-            ok = false;
-            break;
-          }
           const float4 tops = *reinterpret_cast<const float4*>(scales.top[slot]);
-          // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the
-          // tile's largest one (bounded below: sums stay finite)
-          const float bias = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
           const float4* ks = reinterpret_cast<const float4*>(&scales.k[slot][(lane & 3) * kScalePitch]);
           const float4* vs = reinterpret_cast<const float4*>(&scales.v[slot][(lane & 3) * kScalePitch]);
           // 16 rows each; one copy of the code (it has to stay in the instruction cache),
@@ -1339,8 +1330,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                          x[8 * e + 5 + 2 * r]);
               }
             }
-            float alpha[2];
-            bool any = false;
+            // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the
+            // tile's largest one (bounded below: sums stay finite)
+            const float bias = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
+            float mt[2];
+            bool more = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               if (edge) {
@@ -1362,25 +1356,35 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int n = 0; n < 16; ++n) top[n & 1] = fmaxf(fmaxf(top[n & 1], x[4 * n + 2 * r]), x[4 * n + 2 * r + 1]);
-              float mt = fmaxf(top[0], top[1]);
-              mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 1));
-              mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, 2)) + bias;
-              const float m_new = fmaxf(m4[r], mt);
-              const bool need = (ok4 >> r & 1) && m4[r] != -INFINITY && m_new > m4[r] + kRescaleThreshold;
-              alpha[r] = need ? exp2f(m4[r] - m_new) : 1.f;
-              if (need || m4[r] == -INFINITY) m4[r] = m_new;
-              l4[r] *= alpha[r];
-              any |= need;
+              mt[r] = fmaxf(top[0], top[1]) + bias;
+              more |= m4[r] == -INFINITY || mt[r] > m4[r] + kRescaleThreshold;
             }
-            if (__any_sync(kFull, any)) {
-              if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
-              tc::fence_after_sync();
-              for (int e = 0; ok && e < D / 32; ++e) {
-                float o[16];
-                tmem_ld16x256_32(o_addr + half + e * 32, o);
+            // Shuffles are slow here (they queue with the converters' shared-memory
+            // accesses): a row's maximum is put together only where some maximum may change.
+            if (__any_sync(kFull, more)) {
+              float alpha[2];
+              bool any = false;
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha[(k >> 1) & 1];
-                tmem_st16x256_32(o_addr + half + e * 32, o);
+              for (int r = 0; r < 2; ++r) {
+                mt[r] = fmaxf(mt[r], __shfl_xor_sync(kFull, mt[r], 1));
+                mt[r] = fmaxf(mt[r], __shfl_xor_sync(kFull, mt[r], 2));
+                const float m_new = fmaxf(m4[r], mt[r]);
+                const bool need = (ok4 >> r & 1) && m4[r] != -INFINITY && m_new > m4[r] + kRescaleThreshold;
+                alpha[r] = need ? exp2f(m4[r] - m_new) : 1.f;
+                if (need || m4[r] == -INFINITY) m4[r] = m_new;
+                l4[r] *= alpha[r];
+                any |= need;
+              }
+              if (__any_sync(kFull, any)) {
+                if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
+                tc::fence_after_sync();
+                for (int e = 0; ok && e < D / 32; ++e) {
+                  float o[16];
+                  tmem_ld16x256_32(o_addr + half + e * 32, o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] *= alpha[(k >> 1) & 1];
+                  tmem_st16x256_32(o_addr + half + e * 32, o);
+                }
               }
             }
             uint32_t y[32];

@@ -35,7 +35,6 @@ class Model:
         self.pv_done = [[Bar(1) for _ in range(2)] for _ in range(2)]
         self.item_full = [Bar(1) for _ in range(RING)]
         self.item_empty = [Bar(14 if convert else 11) for _ in range(RING)]
-        self.sc_full = [Bar(4) for _ in range(SCALES)]
         self.xbar = Bar(8)
         self.work = [None] * RING
         self.kv, self.q = [None] * nb, [None] * 2
@@ -120,7 +119,6 @@ class Model:
                 n = SCALES
                 assert not self.reading.get(("sc", c % n)), "scales overwritten while read"
                 self.sc[c % n][me] = c
-                self.sc_full[c % n].arrive()
                 for part in (0, 1):
                     if part:
                         yield from self.wait_empty(2 * c + 1)
@@ -265,7 +263,6 @@ class Model:
                 assert self.s[t][me] == ("s", c)
                 if self.convert:
                     n = SCALES
-                    yield from self.wait(self.sc_full[c % n], (c // n) & 1)
                     self.reading[("sc", c % n)] = self.reading.get(("sc", c % n), 0) + 1
                     assert self.sc[c % n] == [c] * 4
                     for _ in range(rng.choice([0, 1, 30])):
