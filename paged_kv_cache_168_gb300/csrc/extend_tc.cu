@@ -69,7 +69,7 @@ constexpr int kMinPartTiles = 2;           // shortest part of a split context
 constexpr int kPartsPerSm = 4;             // parts wanted per SM where contexts are split
 
 // Flags of a query tile and kv head.
-constexpr uint32_t kBadBlock = 1, kNonFinite = 2, kTimedOut = 4;
+constexpr uint32_t kBadBlock = 1, kNonFinite = 2;
 
 // ------------------------------------------------------------------ workspace
 struct Header {
@@ -419,6 +419,7 @@ struct __align__(16) Shared {
   uint64_t mma_drain;
   Work work[kRing];
   volatile int bad[kRing];                 // a block id out of range was met
+  volatile int odd[kRing];                 // (8-bit caches) a V scale that is not finite was met
   float red[2][kRows][2];                  // the other warpgroup's (maximum, sum)
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -429,7 +430,7 @@ struct __align__(16) Scales {
   // column 8 n + 2 q + b at q * kScalePitch + 2 n + b: what a softmax thread reads is
   // contiguous, and the four of a row read different banks
   float k[kScaleRing][4 * kScalePitch], v[kScaleRing][4 * kScalePitch];    // (K's times the softmax scale, base 2)
-  float top[kScaleRing][4];                        // largest V scale of each 32 tokens
+  float top[kScaleRing][4], low[kScaleRing][4];    // largest and smallest (but 0) V scale of each 32 tokens
 };
 
 // Bound of every wait: about a second, far above any wait of a healthy call.
@@ -778,6 +779,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         if (lane == 0) {
           sh.work[slot] = w;
           sh.bad[slot] = 0;
+          sh.odd[slot] = 0;
           mbar_arrive(&sh.item_full[slot]);
         }
         __syncwarp();
@@ -1147,6 +1149,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             const int id = find(j, ct), t = ((w.tile0 + j) * kKv + ct) & (bs - 1);
             sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
             sv = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 1, t));
+            // (0 * inf would reach rows that do not attend the token)
+            if (!(fabsf(sv) < INFINITY)) {
+              sv = 0.f;
+              sh.odd[i % kRing] = 1;
+            }
           };
           auto write = [&](auto which) {
             constexpr int part = decltype(which)::value;
@@ -1217,14 +1224,16 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             }
             {
               const int r = c % kScaleRing;
-              // the tile's largest V scale bounds its weights
-              float top = sv;
-#pragma unroll
-              for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+              // the tile's largest V scale bounds its weights (floats above 0 order like integers)
+              const unsigned top = __reduce_max_sync(kFull, __float_as_uint(fmaxf(sv, 0.f)));
+              const unsigned low = __reduce_min_sync(kFull, __float_as_uint(sv > 0.f ? sv : INFINITY));
               const int at = (ct % 8 / 2) * kScalePitch + ct / 8 * 2 + ct % 2;
               scales.k[r][at] = sk * p.scale_log2;
               scales.v[r][at] = sv;
-              if (lane == 0) scales.top[r][ct >> 5] = top;
+              if (lane == 0) {
+                scales.top[r][ct >> 5] = __uint_as_float(top);
+                scales.low[r][ct >> 5] = __uint_as_float(low);
+              }
             }
             write(kK);
             mine = next;
@@ -1332,36 +1341,65 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             }
             // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the
             // tile's largest one (bounded below: sums stay finite)
-            const float bias = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
-            float mt[2];
-            bool more = false;
+            float bias[2];
+            bias[0] = bias[1] = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
+            if (__builtin_expect(edge, 0)) {
+              uint32_t on[2];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              if (edge) {
+              for (int r = 0; r < 2; ++r) {
                 const int lo = attend_from(pos4[r], p.window, w.held) - t0, hi = ok4 >> r & 1 ? pos4[r] + 1 - t0 : 0;
                 // how many of this thread's columns lie below a limit
                 auto below = [&](int v) {
                   const int u = min(max(v, 0), kKv);
                   return 2 * (u >> 3) + min(max((u & 7) - 2 * (lane & 3), 0), 2);
                 };
-                const uint32_t on = (uint32_t)((1ull << below(hi)) - 1) & ~(uint32_t)((1ull << below(lo)) - 1);
-                if (__any_sync(kFull, on != kFull)) {
+                on[r] = (uint32_t)((1ull << below(hi)) - 1) & ~(uint32_t)((1ull << below(lo)) - 1);
+              }
+              if (__any_sync(kFull, (on[0] & on[1]) != kFull)) {
 #pragma unroll
-                  for (int n = 0; n < 16; ++n)
+                for (int n = 0; n < 16; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                      x[4 * n + 2 * r + k] = (on >> (2 * n + k)) & 1 ? x[4 * n + 2 * r + k] : -INFINITY;
+                  for (int k = 0; k < 4; ++k)
+                    x[4 * n + k] = (on[k >> 1] >> (2 * n + (k & 1))) & 1 ? x[4 * n + k] : -INFINITY;
+                // Where scales differ by more than 2^4, of the tokens that the row attends:
+                // beside a masked token's large scale the others' weights would leave
+                // fp16's range.
+                const float4 lows = *reinterpret_cast<const float4*>(scales.low[slot]);
+                const float low = fminf(fminf(lows.x, lows.y), fminf(lows.z, lows.w));
+                if (fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)) > 16.f * low) {
+                  float big[2] = {0.f, 0.f};
+#pragma unroll 1
+                  for (int e = 0; e < 8; ++e) {
+                    const float4 v = vs[e];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                      const uint32_t o = on[r] >> (4 * e);
+                      big[r] = fmaxf(fmaxf(big[r], o & 1 ? v.x : 0.f), o & 2 ? v.y : 0.f);
+                      big[r] = fmaxf(fmaxf(big[r], o & 4 ? v.z : 0.f), o & 8 ? v.w : 0.f);
+                    }
+                  }
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    big[r] = fmaxf(big[r], __shfl_xor_sync(kFull, big[r], 1));
+                    big[r] = fmaxf(big[r], __shfl_xor_sync(kFull, big[r], 2));
+                    bias[r] = log2f(fmaxf(big[r], 0x1p-100f));
+                  }
                 }
               }
+            }
+            float mt[2];
+            bool more = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
               float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int n = 0; n < 16; ++n) top[n & 1] = fmaxf(fmaxf(top[n & 1], x[4 * n + 2 * r]), x[4 * n + 2 * r + 1]);
-              mt[r] = fmaxf(top[0], top[1]) + bias;
+              mt[r] = fmaxf(top[0], top[1]) + bias[r];
               more |= m4[r] == -INFINITY || mt[r] > m4[r] + kRescaleThreshold;
             }
             // Shuffles are slow here (they queue with the converters' shared-memory
             // accesses): a row's maximum is put together only where some maximum may change.
-            if (__any_sync(kFull, more)) {
+            if (__builtin_expect(__any_sync(kFull, more), 0)) {
               float alpha[2];
               bool any = false;
 #pragma unroll
@@ -1544,6 +1582,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
         report(p.dev_err, PA_DEVERR_BLOCK_ID);
       }
+      if (kI8 && lane == 0 && sh.odd[i % kRing]) {
+        atomicOr(&ws.flags[w.flag], kNonFinite);
+        atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
+      }
       // ---- results: columns [c0, c0 + nc) of my row
       float f[2] = {1.f, 1.f};
       int col0 = 0, ncol = D;
@@ -1635,8 +1677,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       if (row_ok && part && col0 == 0)
         *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(part_row + rr)) = make_float2(m, l);
       // A V that is not finite reaches rows that do not attend it (0 * NaN = NaN):
-      // finish_kernel redoes the item.  (8-bit codes are finite, and a masked
-      // token's weight is 0 whatever its scale.)
+      // finish_kernel redoes the item.  (8-bit codes are finite; scales that are not
+      // have been seen above.)
       if (!kI8 && __any_sync(kFull, row_ok && !(odd == 0.f)) && lane == 0) {
         atomicOr(&ws.flags[w.flag], kNonFinite);
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
@@ -1670,7 +1712,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 // ------------------------------------------------------------------ finish
 // Attention of one row on CUDA cores by one warp, for tiles that the tensor
 // cores cannot take: positions [from, pos], fp32 online softmax.
-template <typename T, int D>
+template <typename T, int D, bool kI8>
 __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh, int r, int lane) {
   constexpr int kDims = D / 32;
   const int bs = p.block_size, j = r / p.group, h = kvh * p.group + r % p.group;
@@ -1683,20 +1725,28 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
     o[d] = 0.f;
   }
   const Layout L{bs, D, p.num_kv_heads};
+  const I8Layout L8{bs, p.num_kv_heads};
   const int32_t* row = p.block_tables + (int64_t)it.seq * p.bt_stride;
   for (int t = from; t <= pos; ++t) {
-    const int b = block_of(p, row, t / bs);
+    const int b = block_of(p, row, t / bs), at = t & (bs - 1);
     if ((unsigned)b >= (unsigned)p.num_blocks) continue;             // its tile is flagged as bad
-    const T* cache = reinterpret_cast<const T*>(p.cache);
+    // element lane * kDims + d of the token's K (part 0) or V
+    auto element = [&](int part, int d) -> float {
+      if constexpr (kI8)
+        return (float)(int8_t)p.cache[L8.code(b, kvh, part, at, lane * kDims + d)] *
+               *reinterpret_cast<const float*>(p.cache + L8.scale(b, kvh, part, at));
+      else
+        return (float)reinterpret_cast<const T*>(p.cache)[L.offset(b, kvh, part, at, lane * kDims + d)];
+    };
     float z = 0.f;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) z = fmaf(x[d], (float)cache[L.offset(b, kvh, 0, t & (bs - 1), lane * kDims + d)], z);
+    for (int d = 0; d < kDims; ++d) z = fmaf(x[d], element(0, d), z);
 #pragma unroll
     for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(kFull, z, i);
     const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = exp2f(z - mn);
     l = l * a + e;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) o[d] = o[d] * a + e * (float)cache[L.offset(b, kvh, 1, t & (bs - 1), lane * kDims + d)];
+    for (int d = 0; d < kDims; ++d) o[d] = o[d] * a + e * element(1, d);
     m = mn;
   }
   T* out = static_cast<T*>(p.out) + ((int64_t)(it.row0 + j) * p.num_q_heads + h) * D + lane * kDims;
@@ -1706,7 +1756,7 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
 
 // Warps take rows of split query tiles: out = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, in the order of the
 // parts; then, where any flag was raised, the rows of flagged items.
-template <typename T, int D>
+template <typename T, int D, bool kI8>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ExtendParams p,
                                                      const __grid_constant__ Space ws) {
   constexpr int kDims = D / 32;
@@ -1747,13 +1797,13 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
     if (!f) continue;
     const Item& it = ws.items[item];
     for (int64_t r = w0; r < it.npos * G; r += nw) {
-      if (f & (kBadBlock | kTimedOut)) {
+      if (f & kBadBlock) {
         T* out = static_cast<T*>(p.out) +
                  ((int64_t)(it.row0 + r / G) * p.num_q_heads + h * G + r % G) * D + lane * kDims;
 #pragma unroll
         for (int d = 0; d < kDims; ++d) out[d] = Elem<T>::from_float(0.f);
       } else {
-        row_on_cuda_cores<T, D>(p, it, h, (int)r, lane);
+        row_on_cuda_cores<T, D, kI8>(p, it, h, (int)r, lane);
       }
     }
   }
@@ -1838,7 +1888,7 @@ cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStr
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_early(extend_kernel<T, D, F>, sms, C::kThreads, smem, stream, p, ws, q_map, kv_map);
   if (e != cudaSuccess) return e;
-  return launch_early(finish_kernel<T, D>, 2 * sms, 256, 0, stream, p, ws);
+  return launch_early(finish_kernel<T, D, F == kCodes>, 2 * sms, 256, 0, stream, p, ws);
 }
 
 template <typename T>

@@ -76,6 +76,14 @@ class Cache:
         return out
 
 
+    def scales(self, block, t, part):
+        """[n, Hkv] float64 scales of slots (8-bit caches)."""
+        block, t = np.asarray(block, np.int64), np.asarray(t, np.int64)
+        at = [((block * self.Hkv + h) * chunk_bytes8(self.bs) + 2 * self.bs * 128 + part * scale_bytes(self.bs) + 4 * t) // 4
+              for h in range(self.Hkv)]
+        return np.stack([self.pool.view(np.float32)[a] for a in at], 1).astype(np.float64)
+
+
 # ------------------------------------------------------------------ block tables from lengths
 OUT_OF_BLOCKS, CONTEXT, BLOCK_ID = 32, 4, 1
 
@@ -180,7 +188,11 @@ def extend(q, cache, tables, ctx, qsl, scale, window=0, ring=0, num_tokens=None)
     weights are fp16):
       output rounding         u |o|
       weights' rounding       u_p w, plus 2^-25 sum_t |v_t| for fp16 weights below its normal range
-                              (weights are taken against a running maximum, so the normaliser is at least 1)
+                              (weights are taken against a running maximum, so the normaliser is at least 1);
+                              weights of an 8-bit cache carry the token's scale s_t and are taken against
+                              x + log2 of the largest scale or at most 16 times it (masked tokens'), so the
+                              normaliser is at least 1 / (16 max s), and a stored weight meets the code
+                              v_t / s_t: 16 2^-25 max s sum_t |v_t| / s_t
       scores                  D products summed in fp32, each step off by at most 2^-22 of the sum of the
                               terms' sizes (2^-23 rounded, twice that if truncated): ds = D 2^-22 scale
                               sum |q k|; a relative change of at most 2 ds of every weight, and again of
@@ -201,6 +213,7 @@ def extend(q, cache, tables, ctx, qsl, scale, window=0, ring=0, num_tokens=None)
         blk = t // cache.bs
         ids = tables[s, blk % ring if ring else blk]
         k, v = cache.read(ids, t % cache.bs, 0), cache.read(ids, t % cache.bs, 1)
+        sv = cache.scales(ids, t % cache.bs, 1) if cache.kv8 else None
         for j in range(e - a):
             pos = c - (e - a) + j
             f = attended_from(c, pos, cache.bs, window, ring)
@@ -215,6 +228,11 @@ def extend(q, cache, tables, ctx, qsl, scale, window=0, ring=0, num_tokens=None)
                 o, w = p @ vv, p @ np.abs(vv)
             ds = D * 2.0 ** -22 * scale * (np.abs(qq) @ np.abs(kk)).max(-1, keepdims=True)
             under = 2.0 ** -25 * np.abs(vv).sum(1)[:, None] if u_p == EPS["f16"] / 2 else 0.0
+            if cache.kv8:
+                ss = sv[f - lo:pos + 1 - lo].T[:, :, None]             # [Hkv, n, 1]
+                with np.errstate(invalid="ignore"):
+                    codes = np.abs(vv) / np.where(ss > 0, ss, 1)
+                under = 2.0 ** -21 * (ss.max(1) * codes.sum(1))[:, None]
             out[a + j] = o.reshape(Hq, D)
             tol[a + j] = (u * np.abs(o) + (u_p + 4 * ds + 2.0 ** -16) * w + under + 1e-30).reshape(Hq, D)
     return out, tol

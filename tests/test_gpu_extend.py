@@ -285,6 +285,38 @@ def test_infinities_and_nan_in_masked_places(q_lens, ctx, window, bs, dtype):
     assert (got[big] == out[big]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bs", [1, 16])
+@pytest.mark.parametrize("what", [np.inf, np.nan, 1e6])
+@pytest.mark.parametrize("q_lens,ctx,window", [([40, 3], [300, 50], 0), ([90, 1], [4000, 20], 0), ([40, 200], [900, 1200], 100)])
+def test_scales_in_masked_places(q_lens, ctx, window, what, bs, dtype):
+    """8-bit caches: single tokens' scales are infinite, NaN or far above all others: queries that do not attend
+    those tokens are untouched."""
+    rng = np.random.default_rng(60 + bs + window)
+    case = Chunk(rng, q_lens, ctx, Hq=6, Hkv=2, D=128, bs=bs, dtype=dtype, kv8=True)
+    c = case.cache
+
+    def plant(s, pos, part, head):
+        block, t = int(case.tables[s, pos // bs]), pos % bs
+        at = (block * c.Hkv + head) * step_ref.chunk_bytes8(bs) + 2 * bs * 128 + part * step_ref.scale_bytes(bs) + 4 * t
+        c.pool[at:at + 4] = np.float32(what).reshape(1).view(np.uint8)
+
+    first = ctx[0] - q_lens[0]
+    plant(0, first + 21, 1, 0)                                       # V that the last queries attend
+    if np.isnan(what):
+        plant(0, first + 35, 0, 1)                                   # K
+    if window:
+        plant(0, first - window + 10, 1, 1)                          # leaves the window of the later queries
+        plant(0, first - window - 1, 1, 0)                           # attended by nobody
+    with np.errstate(invalid="ignore"):
+        out, tol = case.expected(0.09, window)
+    got = bits_to_f64(dev_to_u16(run(case, 0.09, window)), dtype)
+    fine = np.isfinite(out) & (np.abs(out) <= np.finfo(np.float16).max if dtype == "f16" else True)
+    assert np.isfinite(what) or 0.2 < fine.mean() < 1
+    assert (np.abs(got[fine] - out[fine]) <= tol[fine]).all()
+    assert not np.isfinite(got[~np.isfinite(out)]).any()
+
+
 @pytest.mark.parametrize("kv8", [False, True])
 def test_captured_call_follows_its_lengths(kv8):
     """One captured call; lengths, tables and queries change in place between replays, down to no queries at all."""
