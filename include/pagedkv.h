@@ -187,9 +187,10 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
  * results are rounded to q_out's type; k's are rounded to the cache's 16-bit
  * type; v is stored bit for bit.  An 8-bit cache stores codes and scales of k's
  * fp32 results and of v, by the scheme above with its divisions taken as
- * products: r = 127 * (1 / max|x|), codes round-half-even(x * r) clipped, scale
- * max|x| * (1 / 127), each step rounded to fp32 (one division per vector; a scale
- * may differ from pa_reshape_and_cache's of the same vector in its last bit).
+ * products: r = 127 * (1 / max|x|), at most the largest finite fp32, codes
+ * round-half-even(x * r) clipped, scale max|x| * (1 / 127), each step rounded to
+ * fp32 (one division per vector; a scale may differ from pa_reshape_and_cache's
+ * of the same vector in its last bit).
  *   q_out, q     device [num_tokens, num_q_heads, head_size], 16-bit; token
  *                strides in elements (multiples of 8), 16-byte aligned.  q_out
  *                may be q itself (with the same stride; q, key and value may be
@@ -371,7 +372,8 @@ size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, in
  * outputs accumulate in fp32; weights enter the second product as 16-bit
  * values.  Contexts are split over SMs where a step has few rows, and the parts
  * merged by log-sum-exp; results do not depend on timing.
- *   out             device [num_tokens, num_q_heads, head_size], contiguous.
+ *   out             device [num_tokens, num_q_heads, head_size], contiguous; may
+ *                   not overlap q.
  *   q               device [num_tokens, num_q_heads, head_size]; token stride
  *                   q_token_stride elements (multiple of 8); 16-byte aligned.
  *   query_start_loc device int32 [num_seqs + 1], non-decreasing from 0; rows

@@ -766,6 +766,12 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
     return fail(PA_ERR_INVALID_ARG, "block_tables, context_lens and query_start_loc must be 4-byte aligned");
   if (q_token_stride < (int64_t)num_q_heads * desc->head_size || q_token_stride % 8)
     return fail(PA_ERR_INVALID_ARG, "q_token_stride must be >= num_q_heads*head_size and a multiple of 8");
+  {
+    const uintptr_t row = (uintptr_t)num_q_heads * desc->head_size * 2, rows = (uintptr_t)num_tokens;
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), x = reinterpret_cast<uintptr_t>(q);
+    if (o < x + (rows - 1) * (uintptr_t)q_token_stride * 2 + row && x < o + rows * row)
+      return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
+  }
   if (block_table_stride <= 0) return fail(PA_ERR_INVALID_ARG, "block_table_stride %d", block_table_stride);
   if (ring_blocks < 0 || ring_blocks > block_table_stride)
     return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, block_table_stride %d]", ring_blocks,

@@ -7,10 +7,12 @@
 //
 // Bound: HBM.  A token reads q, k and v and writes q, K and V once; its cosines
 // and sines (rotary_dim floats) come from L2, once per token, into shared
-// memory, where all heads read them.  A unit is two 16-byte pieces of one head vector that hold both halves of their
-// pairs -- pieces u and u + rotary_dim / 16 when halves pair up, 2u and 2u + 1
-// when neighbours do -- so a vector is D / 16 units on neighbouring lanes and a
-// vector's amax (8-bit caches) is three shuffles.
+// memory, where all heads read them.  A unit is two 16-byte pieces of one head
+// vector that hold both halves of their pairs -- pieces u and u + rotary_dim / 16
+// when halves pair up, 2u and 2u + 1 when neighbours do -- so a vector is D / 16
+// units on neighbouring lanes and a vector's amax (8-bit caches) is three shuffles.
+#include <float.h>
+
 #include <type_traits>
 
 #include "common.cuh"
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
             if (amax > 0.f) {
               // x * inv is at most 127 (1 + 2^-22) in size: added to 1.5 * 2^23 it is
               // rounded half to even into the sum's low byte
-              const float inv = __fmul_rn(127.f, __fdiv_rn(1.f, amax));
+              const float inv = fminf(__fmul_rn(127.f, __fdiv_rn(1.f, amax)), FLT_MAX);
               uint32_t r[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__fadd_rn(__fmul_rn(x[k], inv), 12582912.f));

@@ -155,8 +155,9 @@ def quantise(x):
     reciprocals (127 * (1 / amax), amax * (1 / 127))."""
     one, n = np.float32(1), np.float32(127)
     amax = np.abs(x).max(-1, keepdims=True).astype(np.float32)
-    with np.errstate(divide="ignore", invalid="ignore"):
+    with np.errstate(divide="ignore", invalid="ignore", over="ignore"):
         inv = np.where(amax > 0, n * (one / amax), np.float32(0)).astype(np.float32)
+        inv = np.minimum(inv, np.finfo(np.float32).max)
         codes = np.clip(np.rint((x * inv).astype(np.float32)), -127, 127).astype(np.int8)
         return codes, (amax * (one / n)).astype(np.float32)
 

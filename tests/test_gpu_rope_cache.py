@@ -146,6 +146,16 @@ def test_scores_depend_on_distance_only():
     assert (np.abs(z - z[0]) <= bound).all()
 
 
+@pytest.mark.parametrize("size", [1e-37, 1e-38, 1e-40])
+def test_codes_of_vectors_near_the_smallest_numbers(size):
+    """127 / max|x| leaves fp32's range."""
+    case = Case(77, 20, 2, 2, 128, 16, "bf16", kv8=True)
+    rng = np.random.default_rng(78)
+    case.k, case.v = (to_bits(rng.uniform(-1, 1, (20, 2, 128)) * size, "bf16") for _ in range(2))
+    got, want = case.run(), case.expected()
+    assert (got[0] == want[0]).all() and (got[1] == want[1]).all()
+
+
 def test_skipped_and_bad_tokens():
     for kv8 in (False, True):
         c = Case(11, 24, 4, 2, 128, 16, "bf16", kv8, axes=3)

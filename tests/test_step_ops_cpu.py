@@ -173,6 +173,9 @@ def test_extend_refusals(lib):
         assert _extend(lib, **{name: 0}) == bad, name
     assert _extend(lib, q=FAKE + 8) == bad and _extend(lib, out=FAKE + 8) == bad
     assert _extend(lib, ctx=FAKE + 2) == bad and _extend(lib, qsl=FAKE + 1) == bad and _extend(lib, bt=FAKE + 2) == bad
+    # out over q's first or last row
+    q_bytes = 100 * 4 * 128 * 2
+    assert _extend(lib) == bad and _extend(lib, out=FAKE + q_bytes - 16) == bad and _extend(lib, q=FAKE + q_bytes, out=FAKE + 16) == bad
     # nothing to do
     assert _extend(lib, S=0) == _lib.PA_OK and _extend(lib, T=0) == _lib.PA_OK and _extend(lib, max_q=0) == _lib.PA_OK
 
