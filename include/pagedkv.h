@@ -391,7 +391,8 @@ size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, in
  *                   2^31 - 129 or (without a ring) beyond the table row (zero
  *                   rows), and
  *                   PA_DEVERR_BLOCK_ID for a bad block id: every row that
- *                   attends the block is zero, and rows computed beside it may be.
+ *                   attends the block is zero, and rows computed beside it may be;
+ *                   after PA_DEVERR_TIMEOUT no row is to be used.
  * Supported: every cache of pa_decode (16-bit with head_size 64 or 128, 8-bit
  * with 128; block_size 1 .. 32), 1 to 16 query heads per kv head. */
 pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc,

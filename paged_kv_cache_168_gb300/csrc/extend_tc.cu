@@ -46,8 +46,22 @@
 //                   scales are applied in the softmax: K's to the scores, V's to
 //                   the weights, whose maximum is taken with the tile's largest V
 //                   scale, so that they stay at most 2^8 whatever the scales are.
-// Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, and the CTA drains its
-// own copies and products before releasing TMEM.
+// Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, the call's results are
+// then not to be used, and the CTA drains its own copies and products before
+// releasing TMEM.
+//
+// What bounds it.  A pair of query tiles and one KV tile are four batches of eight
+// products, 2048 clocks at the tensor cores' rate.  Measured: 16 prompts of 2048
+// tokens, 32 + 8 heads of 128 in bf16: 588 us, 0.94 PFLOP/s; 32 chunks of 512 over 512
+// to 3584: 550 us, 1.18 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
+// around the end of an item: the chain scores - softmax - second product of a query
+// tile (TMEM has room for two), whose every hand-over costs some 300 clocks, because
+// shared memory answers slowly while products read their operands from it.  8 x 4
+// tokens over 32K to 128K: 545 us, 6.1 TB/s, bound by HBM.  8-bit caches: 32 chunks of
+// up to 700 tokens 755 us, 0.55 PFLOP/s, 6000 clocks a pair and KV tile, 3500 of them
+// softmax (two scales a score; the converters next to it slow both down; with eight
+// converter warps, whose registers come from the softmax, 884 us).  A warpgroup of its
+// own for the results took 637 us instead of 593 on the prompts.
 #include <cuda.h>
 #include <math.h>
 
@@ -65,7 +79,7 @@ constexpr int kRows = 128;                 // MMA M: rows of one query tile
 constexpr int kKv = 128;                   // tokens of a KV tile
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kRescaleThreshold = 8.f;   // base-2 units
-constexpr int kMinPartTiles = 2;           // shortest part of a split context
+constexpr int kMinPartTiles = 2;           // shortest part of a split context (1, 2 or 4: the same within 2%)
 constexpr int kPartsPerSm = 4;             // parts wanted per SM where contexts are split
 
 // Flags of a query tile and kv head.
@@ -259,12 +273,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
   block_scan(work, tmp, total);
   // With K parts a SM the call takes about (work / sms) (1 + 1 / K) -- the last round
   // is half empty -- and K times an item's own cost, about 3 KV tiles: least at
-  // K = sqrt(work / sms / 3).  (K = 4 whatever the work: windows of 1000 tokens took 1.5
-  // times as long.)
+  // K = sqrt(work / sms / 3).  32 + 8 heads, us, this rule / K = 1 / K = 4: 4 tokens over
+  // 30000: 56 / 47 / 75; 4 x 4 over 8000: 50 / 58 / 61; 2 x 512 over 8000, 8 + 1
+  // heads: 74 / 80 / 104; 8 x 4 over 32K to 128K, 64 + 8 heads: 544 / 703 / 543.
   const int64_t per_sm = total * hkv / sms;
   const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
   int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
-  // query tiles that cover half of the SMs are not cut for less than a dozen KV tiles
+  // Query tiles that cover half of the SMs are not cut for less than a dozen KV tiles (13
+  // chunks over windows of 1000 tokens: 43 us, cut 81).
   int64_t tiles;
   block_scan(mine_tiles, tmp, tiles);
   if (tiles * hkv * 2 >= sms) longest = max(longest, (int64_t)12);
@@ -402,8 +418,8 @@ struct Cfg {
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
   // K and V tiles take turns in one ring: K of tile c is fill 2c, V fill 2c + 1, fill
   // n sits in buffer n % kBufs.  Five buffers of 32 KiB beside the query tiles are
-  // all that fits (K and V in rings of two each waited ~1200 of 4500 clocks a tile
-  // for copies).
+  // all that fits (K and V in rings of two each: 1200 more clocks a tile, waiting for
+  // copies); the converting variants need the rest for scales and staged codes.
   static constexpr int kBufs = kConvert ? 4 : 5;
   static constexpr size_t kRingBytes = (size_t)kBufs * kTileBytes;
 };

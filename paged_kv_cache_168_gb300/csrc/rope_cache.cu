@@ -207,7 +207,9 @@ void launch_rounds(const RopeParams& p, cudaStream_t stream) {
 
 template <typename T, int D, bool kI8>
 cudaError_t launch_pairs(const RopeParams& p, cudaStream_t stream) {
-  // up to one round per SM of single tokens: more CTAs at once, for latency
+  // One token a CTA as long as all CTAs run at once (four an SM), for latency: 256
+  // tokens of 32 + 8 heads 3.8 us back to back in a graph against 5.9 with four a
+  // CTA, 608 4.8 against 6.0; but 2048 12.0 against 10.9, 4096 26.6 against 21.8.
   if (p.num_tokens <= 152 * 4)
     launch_rounds<T, D, kI8, 1>(p, stream);
   else
