@@ -1641,7 +1641,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       int rows4[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(kFull, mine, (lane & ~3) + k);
-      float odd = 0.f;
+      uint64_t odd[2] = {0, 0};                                      // NaN once any value is not finite
+      const uint64_t scale2 = pack2f(scale, scale);
       for (int e = col0; e < col0 + ncol; e += 32) {
         float o[32];
         if (have0) {
@@ -1662,11 +1663,15 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           for (int k = 0; k < 32; ++k) o[k] = o[k] * f[0] + b[k] * f[1];
         }
 #pragma unroll
-        for (int k = 0; k < 32; ++k) odd = fmaf(o[k], 0.f, odd);     // NaN once any value is not finite
+        for (int k = 0; k < 16; ++k) odd[k & 1] = fma2f(pack2f(o[2 * k], o[2 * k + 1]), 0, odd[k & 1]);
         if (!part) {
           uint32_t y[4][4];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) y[k >> 2][k & 3] = Elem<T>::pack2(o[2 * k] * scale, o[2 * k + 1] * scale);
+          for (int k = 0; k < 16; ++k) {
+            float a, b;
+            unpack2f(mul2f(pack2f(o[2 * k], o[2 * k + 1]), scale2), a, b);
+            y[k >> 2][k & 3] = Elem<T>::pack2(a, b);
+          }
 #pragma unroll
           for (int d = 1; d < 4; d <<= 1) {                          // a 4 x 4 transpose in two exchanges
             const bool up = lane & d;
@@ -1695,7 +1700,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       // A V that is not finite reaches rows that do not attend it (0 * NaN = NaN):
       // finish_kernel redoes the item.  (8-bit codes are finite; scales that are not
       // have been seen above.)
-      if (!kI8 && __any_sync(kFull, row_ok && !(odd == 0.f)) && lane == 0) {
+      float odd_a, odd_b;
+      unpack2f(add2f(odd[0], odd[1]), odd_a, odd_b);
+      if (!kI8 && __any_sync(kFull, row_ok && !(odd_a + odd_b == 0.f)) && lane == 0) {
         atomicOr(&ws.flags[w.flag], kNonFinite);
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
       }
