@@ -598,6 +598,17 @@ __device__ __forceinline__ void set_regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// 32 bytes; `wide`: they are 32-byte aligned (else 16).
+__device__ __forceinline__ void store32(void* at, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
   const int n = take ? 16 : 0;             // 0: the destination is zeroed
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -1634,13 +1645,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int part_row = w.part_row;
       float* prow = ws.o + (int64_t)(part_row + rr) * D;
       T* tile = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0) * p.num_q_heads + w.kvh * G) * D;
-      // Rows leave 64 bytes at a time: a store of 16 bytes a row and lane asks for 32
-      // lines, and the stores alone took 6000 clocks an item.  Lanes 4i .. 4i + 3
-      // exchange 16-byte pieces until lane 4i + k holds piece k of each of their rows.
+      // Rows leave 64 bytes at a time, a pair of lanes a row: a store of 16 bytes a row
+      // and lane asks for 32 lines, and the stores alone took 6000 clocks an item.  The
+      // lanes of a pair exchange halves, then both store of one row, then of the other.
       const int mine = row_ok ? (ipos * p.num_q_heads + head) * D : -1;   // my row in the tile's output
-      int rows4[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) rows4[k] = __shfl_sync(kFull, mine, (lane & ~3) + k);
+      const int other = __shfl_xor_sync(kFull, mine, 1);
+      const bool upper = lane & 1, wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+      const int row_a = upper ? other : mine, row_b = upper ? mine : other;
       uint64_t odd[2] = {0, 0};                                      // NaN once any value is not finite
       const uint64_t scale2 = pack2f(scale, scale);
       for (int e = col0; e < col0 + ncol; e += 32) {
@@ -1665,30 +1676,23 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
 #pragma unroll
         for (int k = 0; k < 16; ++k) odd[k & 1] = fma2f(pack2f(o[2 * k], o[2 * k + 1]), 0, odd[k & 1]);
         if (!part) {
-          uint32_t y[4][4];
+          uint32_t y[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float a, b;
             unpack2f(mul2f(pack2f(o[2 * k], o[2 * k + 1]), scale2), a, b);
-            y[k >> 2][k & 3] = Elem<T>::pack2(a, b);
+            y[k] = Elem<T>::pack2(a, b);
           }
+          uint32_t ya[8], yb[8];                                     // of the even lane's row, of the odd lane's
 #pragma unroll
-          for (int d = 1; d < 4; d <<= 1) {                          // a 4 x 4 transpose in two exchanges
-            const bool up = lane & d;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!(k & d)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t got = __shfl_xor_sync(kFull, up ? y[k][i] : y[k + d][i], d);
-                  if (up) y[k][i] = got; else y[k + d][i] = got;
-                }
-              }
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t got = __shfl_xor_sync(kFull, upper ? y[k] : y[k + 8], 1);
+            ya[k] = upper ? got : y[k];
+            yb[k] = upper ? y[k + 8] : got;
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (rows4[k] >= 0)
-              *reinterpret_cast<uint4*>(tile + rows4[k] + e + (lane & 3) * 8) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+          T* at = tile + e + (upper ? 16 : 0);
+          if (row_a >= 0) store32(at + row_a, ya, wide);
+          if (row_b >= 0) store32(at + row_b, yb, wide);
         } else if (row_ok) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)

@@ -129,6 +129,17 @@ def test_strided_queries():
     check(case, q=wide[:, :512].unflatten(1, (4, 128)))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_outputs_aligned_to_16_bytes_alone(D):
+    rng = np.random.default_rng(9)
+    case = Chunk(rng, [5, 140, 1], [50, 140, 9000], Hq=4, Hkv=2, D=D, bs=16, dtype="bf16")
+    n = case.T * 4 * D
+    room = torch.full((n + 16,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    assert room.data_ptr() % 32 == 0
+    check(case, out=room[8:8 + n].view(case.T, 4, D))
+    assert bool(torch.isnan(room[:8]).all()) and bool(torch.isnan(room[8 + n:]).all())
+
+
 @pytest.mark.parametrize("kv8", [False, True])
 def test_bad_sequences_are_zero_and_the_others_right(kv8):
     rng = np.random.default_rng(8)
