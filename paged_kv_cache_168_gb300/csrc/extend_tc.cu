@@ -52,8 +52,8 @@
 //
 // What bounds it.  A pair of query tiles and one KV tile are four batches of eight
 // products, 2048 clocks at the tensor cores' rate.  Measured: 16 prompts of 2048
-// tokens, 32 + 8 heads of 128 in bf16: 588 us, 0.94 PFLOP/s; 32 chunks of 512 over 512
-// to 3584: 550 us, 1.18 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
+// tokens, 32 + 8 heads of 128 in bf16: 570 us, 0.96 PFLOP/s; 32 chunks of 512 over 512
+// to 3584: 542 us, 1.19 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
 // around the end of an item: the chain scores - softmax - second product of a query
 // tile (TMEM has room for two), whose every hand-over costs some 300 clocks, because
 // shared memory answers slowly while products read their operands from it.  8 x 4
@@ -61,7 +61,9 @@
 // up to 700 tokens 755 us, 0.55 PFLOP/s, 6000 clocks a pair and KV tile, 3500 of them
 // softmax (two scales a score; the converters next to it slow both down; with eight
 // converter warps, whose registers come from the softmax, 884 us).  A warpgroup of its
-// own for the results took 637 us instead of 593 on the prompts.
+// own for the results took 637 us instead of 593 on the prompts; two issuing warps,
+// one a query tile, each in its own order, 628 instead of 588 (and the chunks 634
+// instead of 549: both softmaxes run at once and the tensor cores idle).
 #include <cuda.h>
 #include <math.h>
 
@@ -410,7 +412,7 @@ struct Cfg {
   static constexpr int kThreads = kConvert ? 512 : 384;
   // registers a thread, whose sum over the warpgroups is the launch's: the softmax
   // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
-  // caches half of a tile's codes
+  // caches half of a tile's codes (8 registers more or fewer for the softmax: within 2%)
   static constexpr int kRegsSoftmax = F == kBulk ? 200 : F == kGather ? 176 : 160;
   static constexpr int kRegsRest = F == kBulk ? 104 : F == kGather ? 88 : 96;
   static constexpr int kRegsConvert = F == kGather ? 72 : 96;
@@ -1647,7 +1649,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       T* tile = static_cast<T*>(p.out) + ((int64_t)(w.row0 + my0) * p.num_q_heads + w.kvh * G) * D;
       // Rows leave 64 bytes at a time, a pair of lanes a row: a store of 16 bytes a row
       // and lane asks for 32 lines, and the stores alone took 6000 clocks an item.  The
-      // lanes of a pair exchange halves, then both store of one row, then of the other.
+      // lanes of a pair exchange halves, then both store of one row, then of the other
+      // (16 prompts of 2048 tokens: 570 us; rows of four lanes 578; 32 bytes a row and
+      // lane, no exchange, 581).
       const int mine = row_ok ? (ipos * p.num_q_heads + head) * D : -1;   // my row in the tile's output
       const int other = __shfl_xor_sync(kFull, mine, 1);
       const bool upper = lane & 1, wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
