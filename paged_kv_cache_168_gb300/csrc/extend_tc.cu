@@ -53,7 +53,7 @@
 // What bounds it.  A pair of query tiles and one KV tile are four batches of eight
 // products, 2048 clocks at the tensor cores' rate.  Measured: 16 prompts of 2048
 // tokens, 32 + 8 heads of 128 in bf16: 570 us, 0.96 PFLOP/s; 32 chunks of 512 over 512
-// to 3584: 542 us, 1.19 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
+// to 3584: 546 us, 1.18 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
 // around the end of an item: the chain scores - softmax - second product of a query
 // tile (TMEM has room for two), whose every hand-over costs some 300 clocks, because
 // shared memory answers slowly while products read their operands from it.  8 x 4
