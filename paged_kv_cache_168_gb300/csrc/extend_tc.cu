@@ -71,18 +71,18 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "extend_plan.h"
 #include "kernels.h"
 #include "tc_common.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kRows = 128;                 // MMA M: rows of one query tile
-constexpr int kKv = 128;                   // tokens of a KV tile
+using plan::attend_from;
+using plan::kKv;
+using plan::kRows;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kRescaleThreshold = 8.f;   // base-2 units
-constexpr int kMinPartTiles = 2;           // shortest part of a split context (1, 2 or 4: the same within 2%)
-constexpr int kPartsPerSm = 4;             // parts wanted per SM where contexts are split
 
 // Flags of a query tile and kv head.
 constexpr uint32_t kBadBlock = 1, kNonFinite = 2;
@@ -106,22 +106,20 @@ struct __align__(16) Item {
   int32_t head_rows;                       // partial rows between kv heads
   int32_t flag;                            // the item whose flags it raises: its query tile's first
   int32_t parts;                           // of its query tile's context
-  int32_t pad[2];
-};
-
-// What the planner decides for a sequence.
-struct __align__(16) SeqPlan {
-  int32_t base, parts, part_row, pad;
+  int32_t rows;                            // partial rows of one part
+  int32_t pad;
 };
 
 struct Space {
   Header* head;
-  SeqPlan* seqs;                           // [num_seqs]
+  int32_t* seq_tile;                       // [num_seqs + 1] number of a sequence's first query tile
+  int2* tiles;                             // [max_tiles] a query tile's first item and first partial row
   Item* items;                             // [max_items]
   int32_t* splits;                         // [max_items] first items of the split query tiles
   uint32_t* flags;                         // [max_items * kv heads]
   float* o;                                // [max_rows][D]
   float* ml;                               // [max_rows][2]
+  int32_t max_tiles;
   int32_t max_items;
   int32_t tile_rows;                       // most rows an item can have
   int64_t max_rows;
@@ -132,12 +130,12 @@ size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 // The workspace of these shapes, laid out from `base`; its size in *bytes.
 Space lay_out(uint8_t* base, int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len,
               int head_size, int sms, size_t* bytes) {
-  const int pair = 2 * (kRows / group);                       // positions of two query tiles
-  const int64_t parts = (int64_t)kPartsPerSm * sms;
+  const int pair = plan::pair_positions(group);
   Space w{};
   w.tile_rows = (max_query_len < pair ? max_query_len : pair) * group;
-  w.max_items = (int32_t)((int64_t)num_tokens / pair + num_seqs + parts);
-  w.max_rows = 2 * parts * w.tile_rows;                       // see plan_kernel
+  w.max_tiles = (int32_t)plan::max_tiles(num_tokens, num_seqs, pair);
+  w.max_items = (int32_t)plan::max_items(w.max_tiles, sms);
+  w.max_rows = plan::max_rows(w.tile_rows, sms);
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -145,7 +143,8 @@ Space lay_out(uint8_t* base, int num_seqs, int num_tokens, int num_kv_heads, int
     return base + here;
   };
   w.head = reinterpret_cast<Header*>(take(sizeof(Header)));
-  w.seqs = reinterpret_cast<SeqPlan*>(take((size_t)num_seqs * sizeof(SeqPlan)));
+  w.seq_tile = reinterpret_cast<int32_t*>(take(((size_t)num_seqs + 1) * 4));
+  w.tiles = reinterpret_cast<int2*>(take((size_t)w.max_tiles * sizeof(int2)));
   w.items = reinterpret_cast<Item*>(take((size_t)w.max_items * sizeof(Item)));
   w.splits = reinterpret_cast<int32_t*>(take((size_t)w.max_items * 4));
   w.flags = reinterpret_cast<uint32_t*>(take((size_t)w.max_items * num_kv_heads * 4));
@@ -161,7 +160,7 @@ __device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wai
 
 // ------------------------------------------------------------------ planner
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCache = 8192;           // sequences whose first items are searched in shared memory
+constexpr int kPlanCache = 4096;           // sequences and query tiles whose numbers are searched in shared memory
 
 struct Seq {
   int start, q_len, ctx, held;
@@ -194,19 +193,6 @@ __device__ __forceinline__ Seq read_seq(const ExtendParams& p, int s, uint32_t& 
   return q;
 }
 
-// First position that the query at position pos attends.
-__device__ __forceinline__ int attend_from(int pos, int window, int held) {
-  const int w = window > 0 && pos - window + 1 > 0 ? pos - window + 1 : 0;
-  return max(w, held);
-}
-
-// KV tiles [tile0, tile0 + n) that the queries at pos0 .. pos0 + npos - 1 attend.
-__device__ __forceinline__ int tile_range(const ExtendParams& p, const Seq& q, int pos0, int npos, int& tile0) {
-  const int first = attend_from(pos0, p.window, q.held), last = pos0 + npos - 1;
-  tile0 = first / kKv;
-  return q.zero || first > last ? 0 : last / kKv - tile0 + 1;
-}
-
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -229,148 +215,140 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t& 
   return in - v + (warp ? before : 0);
 }
 
-// One CTA; thread t owns the sequences [t * per, (t + 1) * per) and then takes
-// items in turn.  The part length follows the whole call's work: `longest` KV
-// tiles, so that all heads' work makes kPartsPerSm parts per SM; a sequence is
-// cut into equal parts when its last (longest) query tile exceeds that.  Cut
-// tiles and parts are then at most kPartsPerSm * sms each (a cut tile has more
-// than `longest` tiles of the work), so their partial rows fit 2 * kPartsPerSm *
-// sms tiles; sequences whose rows would not (the estimate of the work is
-// rounded) stay whole.
+// A query tile: positions pos0 .. pos0 + npos - 1 of a sequence, from token row row0 on.
+struct Tile {
+  int seq, row0, pos0, npos, held;
+  int tile0, n;                            // the KV tiles that it attends
+};
+
+// One CTA.  Three passes with a scan each: over sequences (thread t owns [t * per,
+// (t + 1) * per)), which numbers their query tiles; over query tiles, whose KV
+// tiles give the call's work and with it the part length, and whose parts give the
+// items' and the partial rows' numbers; over items.  What has to be looked up
+// backwards -- a tile's sequence, an item's tile -- is searched in shared memory.
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_constant__ ExtendParams p,
                                                               const __grid_constant__ Space ws, int sms) {
   __shared__ int64_t tmp[32];
-  __shared__ int32_t bases[kPlanCache];
+  __shared__ int32_t seq_tile[kPlanCache], tile_item[kPlanCache];
   __shared__ uint32_t errs;
   __shared__ int nsplit;
-  const int S = p.num_seqs, G = p.group, pair = 2 * (kRows / G), tid = threadIdx.x, hkv = p.num_kv_heads;
+  const int S = p.num_seqs, G = p.group, pair = plan::pair_positions(G), tid = threadIdx.x, hkv = p.num_kv_heads;
   if (tid == 0) errs = nsplit = 0;
   launch_next();
+
+  // ---- sequences
   const int per = (S + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
-  // a thread's only sequence is read once
-  uint32_t err = 0;
-  Seq mine{};
-  if (per == 1 && s0 < s1) mine = read_seq(p, s0, err);
-  auto seq = [&](int s, uint32_t& e) { return per == 1 ? mine : read_seq(p, s, e); };
-  // KV tiles of a sequence's last query tile
-  auto last_range = [&](const Seq& q, int nt) {
-    int t0;
-    const int q0 = (nt - 1) * pair;
-    return tile_range(p, q, q.ctx - q.q_len + q0, q.q_len - q0, t0);
-  };
-
-  uint32_t none = 0;
-  int64_t work = 0, mine_tiles = 0;
+  uint32_t err = 0, none = 0;
+  int64_t count = 0, all;
   for (int s = s0; s < s1; ++s) {
-    const Seq q = seq(s, err);
-    if (!q.listed || q.zero) continue;
-    const int nt = (q.q_len + pair - 1) / pair;
-    int t0;
-    const int n0 = tile_range(p, q, q.ctx - q.q_len, min(pair, q.q_len), t0);
-    work += ((int64_t)n0 + last_range(q, nt)) * nt / 2;
-    mine_tiles += nt;
+    const Seq q = read_seq(p, s, err);
+    if (q.listed) count += plan::tiles_of(q.q_len, pair);
   }
-  int64_t total;
-  block_scan(work, tmp, total);
-  // With K parts a SM the call takes about (work / sms) (1 + 1 / K) -- the last round
-  // is half empty -- and K times an item's own cost, about 3 KV tiles: least at
-  // K = sqrt(work / sms / 3).  32 + 8 heads, us, this rule / K = 1 / K = 4: 4 tokens over
-  // 30000: 56 / 47 / 75; 4 x 4 over 8000: 50 / 58 / 61; 2 x 512 over 8000, 8 + 1
-  // heads: 74 / 80 / 104; 8 x 4 over 32K to 128K, 64 + 8 heads: 544 / 703 / 543.
-  const int64_t per_sm = total * hkv / sms;
-  const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
-  int64_t longest = max((int64_t)kMinPartTiles, (total * hkv + want - 1) / want);
-  // Query tiles that cover half of the SMs are not cut for less than a dozen KV tiles (13
-  // chunks over windows of 1000 tokens: 43 us, cut 81).
-  int64_t tiles;
-  block_scan(mine_tiles, tmp, tiles);
-  if (tiles * hkv * 2 >= sms) longest = max(longest, (int64_t)12);
-
-  // parts wanted and their partial rows
-  auto parts_of = [&](const Seq& q, int nt, int64_t& rows) {
-    const int64_t parts = q.zero ? 1 : max((int64_t)1, (last_range(q, nt) + longest - 1) / longest);
-    rows = parts > 1 ? parts * nt * hkv * (int64_t)(min(pair, q.q_len) * G) : 0;
-    return parts;
-  };
-  int64_t rows = 0;
+  int64_t at = block_scan(count, tmp, all);
+  if (all > ws.max_tiles) err |= PA_DEVERR_CONTEXT;           // sequences overlap: the last ones are left out
+  const int tiles = (int)min(all, (int64_t)ws.max_tiles);
   for (int s = s0; s < s1; ++s) {
-    const Seq q = seq(s, none);
-    int64_t r = 0;
-    if (q.listed) parts_of(q, (q.q_len + pair - 1) / pair, r);
-    rows += r;
-  }
-  int64_t row = block_scan(rows, tmp, total);
-  int64_t items = 0;
-  for (int s = s0; s < s1; ++s) {
-    const Seq q = seq(s, none);
-    SeqPlan sp{0, 0, -1, 0};
-    if (q.listed) {
-      const int nt = (q.q_len + pair - 1) / pair;
-      int64_t r;
-      int64_t parts = parts_of(q, nt, r);
-      if (parts > 1 && row + r > ws.max_rows) parts = 1;
-      if (parts > 1) sp.part_row = (int)row;
-      row += r;
-      sp.parts = (int)parts;
-      items += parts * nt;
+    const int base = (int)min(at, (int64_t)tiles);
+    ws.seq_tile[s] = base;
+    if (s < kPlanCache) seq_tile[s] = base;
+    if (per > 1) {
+      const Seq q = read_seq(p, s, none);
+      if (q.listed) at += plan::tiles_of(q.q_len, pair);
     }
-    ws.seqs[s] = sp;
   }
-  int64_t n_items;
-  int64_t item = block_scan(items, tmp, n_items);
-  for (int s = s0; s < s1; ++s) {
-    const Seq q = seq(s, none);
-    const int base = (int)min(item, (int64_t)ws.max_items);
-    ws.seqs[s].base = base;
-    if (s < kPlanCache) bases[s] = base;
-    if (q.listed) item += (int64_t)ws.seqs[s].parts * ((q.q_len + pair - 1) / pair);
-  }
-  if (n_items > ws.max_items) err |= PA_DEVERR_CONTEXT;       // sequences overlap: the last ones are left out
+  if (tid == 0) ws.seq_tile[S] = tiles;
   if (err) atomicOr(&errs, err);
   __syncthreads();
 
-  const int listed = (int)min(n_items, (int64_t)ws.max_items);
-  for (int i = tid; i < listed; i += kPlanThreads) {
-    int lo = 0, hi = S;                                       // the last sequence with base <= i
+  // ---- query tiles
+  auto tile = [&](int i) {
+    int lo = 0, hi = S;                                       // the last sequence whose first tile is <= i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((mid < kPlanCache ? bases[mid] : ws.seqs[mid].base) <= i) lo = mid; else hi = mid;
+      if ((mid < kPlanCache ? seq_tile[mid] : ws.seq_tile[mid]) <= i) lo = mid; else hi = mid;
     }
-    const SeqPlan sp = ws.seqs[lo];
     const Seq q = read_seq(p, lo, none);
-    const int nt = (q.q_len + pair - 1) / pair;
-    const int k = (i - sp.base) / sp.parts, part = (i - sp.base) % sp.parts;
-    const int q0 = (nt - 1 - k) * pair;                       // the longest contexts first
-    Item it;
-    it.seq = lo;
-    it.base = sp.base;
-    it.count = min(nt * sp.parts, listed - sp.base);
-    it.row0 = q.start + q0;
-    it.pos0 = q.ctx - q.q_len + q0;
-    it.npos = min(pair, q.q_len - q0);
-    int t0;
-    const int n = tile_range(p, q, it.pos0, it.npos, t0);
-    const int plen = (n + sp.parts - 1) / sp.parts;
-    it.tile0 = t0 + part * plen;
-    it.ntiles = max(0, min(plen, n - part * plen));
-    it.first = attend_from(it.pos0, p.window, q.held);
-    it.held = q.held;
-    const int tile_rows = min(pair, q.q_len) * G;
-    it.part_row = sp.part_row < 0 ? -1 : sp.part_row + (k * hkv * sp.parts + part) * tile_rows;
-    it.head_rows = sp.parts * tile_rows;
-    it.flag = sp.base + k * sp.parts;
-    it.parts = sp.parts;
-    it.pad[0] = tile_rows;
-    it.pad[1] = 0;
-    ws.items[i] = it;
-    if (sp.part_row >= 0 && part == 0) ws.splits[atomicAdd(&nsplit, 1)] = i;
+    // the longest contexts first
+    const int q0 = (plan::tiles_of(q.q_len, pair) - 1 - (i - (lo < kPlanCache ? seq_tile[lo] : ws.seq_tile[lo]))) * pair;
+    Tile t;
+    t.seq = lo;
+    t.row0 = q.start + q0;
+    t.pos0 = q.ctx - q.q_len + q0;
+    t.npos = min(pair, q.q_len - q0);
+    t.held = q.held;
+    t.n = plan::tile_range(t.pos0, t.npos, p.window, q.held, t.tile0);
+    if (q.zero) t.n = 0;
+    return t;
+  };
+  Tile mine{};                                                // tile tid: most calls have no more
+  int64_t work = 0, total;
+  for (int i = tid; i < tiles; i += kPlanThreads) {
+    const Tile t = tile(i);
+    if (i == tid) mine = t;
+    work += t.n;
   }
-  for (int i = tid; i < listed * hkv; i += kPlanThreads) ws.flags[i] = 0;
+  block_scan(work, tmp, total);
+  const int64_t longest = plan::longest_part(total, tiles, hkv, sms);
+  int64_t done = 0;                                           // items << 32 | partial rows of the tiles before
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int64_t add = 0, sum;
+    if (i < tiles) {
+      const Tile t = i0 == 0 ? mine : tile(i);
+      const int parts = plan::parts_of(t.n, longest);
+      add = (int64_t)parts << 32 | (uint32_t)(parts > 1 ? parts * t.npos * G * hkv : 0);
+    }
+    const int64_t before = done + block_scan(add, tmp, sum);
+    if (i < tiles) {
+      ws.tiles[i] = make_int2((int)(before >> 32), (int)(uint32_t)before);
+      if (i < kPlanCache) tile_item[i] = (int)(before >> 32);
+    }
+    done += sum;
+  }
+  const int items = (int)(done >> 32);
+  __syncthreads();
+
+  // ---- items
+  auto first_item = [&](int t) { return t == tiles ? items : t < kPlanCache ? tile_item[t] : ws.tiles[t].x; };
+  for (int i = tid; i < items; i += kPlanThreads) {
+    int k = i;                                                // its query tile, where none is cut
+    if (items > tiles) {
+      k = 0;
+      int hi = tiles;
+      while (hi - k > 1) {
+        const int mid = (k + hi) >> 1;
+        if (first_item(mid) <= i) k = mid; else hi = mid;
+      }
+    }
+    const Tile t = k == tid ? mine : tile(k);
+    const int first = first_item(k), part = i - first;
+    Item it;
+    it.seq = t.seq;
+    it.base = first_item(t.seq < kPlanCache ? seq_tile[t.seq] : ws.seq_tile[t.seq]);
+    it.count = first_item(t.seq + 1 < min(S, kPlanCache) ? seq_tile[t.seq + 1] : ws.seq_tile[t.seq + 1]) - it.base;
+    it.row0 = t.row0;
+    it.pos0 = t.pos0;
+    it.npos = t.npos;
+    it.parts = plan::parts_of(t.n, longest);
+    int from;
+    it.ntiles = plan::part_range(t.n, it.parts, part, from);
+    it.tile0 = t.tile0 + from;
+    it.first = attend_from(t.pos0, p.window, t.held);
+    it.held = t.held;
+    it.rows = t.npos * G;
+    it.part_row = it.parts > 1 ? ws.tiles[k].y + part * it.rows : -1;
+    it.head_rows = it.parts * it.rows;
+    it.flag = first;
+    it.pad = 0;
+    ws.items[i] = it;
+    if (it.parts > 1 && part == 0) ws.splits[atomicAdd(&nsplit, 1)] = i;
+  }
+  for (int64_t i = tid; i < (int64_t)items * hkv; i += kPlanThreads) ws.flags[i] = 0;
   __syncthreads();
   if (tid == 0) {
     ws.head->next = 0;
-    ws.head->total = listed * hkv;
+    ws.head->total = items * hkv;
     ws.head->num_split = nsplit;
     ws.head->any_flag = 0;
     if (errs) report(p.dev_err, errs);
@@ -1801,14 +1779,13 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
     const Item& it = ws.items[item];
     if (r >= it.npos * G || (hd.any_flag && ws.flags[item * hkv + h])) continue;
     const int64_t first = it.part_row + (int64_t)h * it.head_rows + r;
-    const int rows = it.pad[0];                                      // partial rows of one part
     float M = -INFINITY;
-    for (int k = lane; k < it.parts; k += 32) M = fmaxf(M, ws.ml[2 * (first + (int64_t)k * rows)]);
+    for (int k = lane; k < it.parts; k += 32) M = fmaxf(M, ws.ml[2 * (first + (int64_t)k * it.rows)]);
 #pragma unroll
     for (int i = 16; i; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, i));
     float l = 0.f, o[kDims] = {};
     for (int k = 0; k < it.parts; ++k) {
-      const int64_t at = first + (int64_t)k * rows;
+      const int64_t at = first + (int64_t)k * it.rows;
       const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
       if (ml.y == 0.f) continue;                                     // nothing attended in this part
       const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);     // (-inf with a sum: NaN scores)

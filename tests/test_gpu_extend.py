@@ -426,3 +426,21 @@ def test_very_small_and_large_value_scales():
             if block % 5 == 0:
                 scales[at:at + 16] = 0
     check(case)
+
+
+@pytest.mark.parametrize("q_lens,prefix,G", [([8192], [0], 4), ([1483], [22277], 8), ([4880], [0], 16), ([7057], [0], 8),
+                                             ([12000, 6000], [0, 40000], 16), ([21000], [0], 1)])
+def test_long_chunks_of_one_kv_head(q_lens, prefix, G):
+    """One kv head: query tiles are many, some contexts are cut, and every row is written."""
+    rng = np.random.default_rng(70 + G)
+    ctx = [q + c for q, c in zip(q_lens, prefix)]
+    case = Chunk(rng, q_lens, ctx, Hq=G, Hkv=1, D=128, bs=16, dtype="bf16")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run(case, 0.09, err=err)                                   # (into NaN)
+    assert pkv.read_device_errors(err) == 0
+    assert bool(torch.isfinite(got).all())
+    for s, q in enumerate(q_lens):
+        for j in np.unique(np.concatenate([np.arange(0, 420, 13), rng.integers(0, q, 30), [q - 1]])):
+            row = int(case.qsl[s] + j)
+            want = step_ref.extend(case.q[row:row + 1], case.cache, case.tables[s:s + 1], [prefix[s] + j + 1], [0, 1], 0.09)
+            assert_close(got[row:row + 1], want, f"sequence {s}, row {j}")
