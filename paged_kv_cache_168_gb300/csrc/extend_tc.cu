@@ -1752,7 +1752,8 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
     for (int d = 0; d < kDims; ++d) z = fmaf(x[d], element(0, d), z);
 #pragma unroll
     for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(kFull, z, i);
-    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = exp2f(z - mn);
+    // (a score of -inf has weight 0, before any finite one too: there mn is -inf as well)
+    const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = z == -INFINITY ? 0.f : exp2f(z - mn);
     l = l * a + e;
 #pragma unroll
     for (int d = 0; d < kDims; ++d) o[d] = o[d] * a + e * element(1, d);

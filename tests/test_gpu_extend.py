@@ -444,3 +444,28 @@ def test_long_chunks_of_one_kv_head(q_lens, prefix, G):
             row = int(case.qsl[s] + j)
             want = step_ref.extend(case.q[row:row + 1], case.cache, case.tables[s:s + 1], [prefix[s] + j + 1], [0, 1], 0.09)
             assert_close(got[row:row + 1], want, f"sequence {s}, row {j}")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("bs", [4, 16])
+@pytest.mark.parametrize("q_len,ctx", [(40, 300), (90, 4000)])
+def test_infinite_keys(q_len, ctx, bs, dtype):
+    """The first attended key holds an infinity: its score is -inf for queries of one sign, whose rows are the
+    attention over the other positions, and +inf for the others, whose rows the formula leaves undefined."""
+    rng = np.random.default_rng(80 + bs)
+    case = Chunk(rng, [q_len, 3], [ctx, 50], Hq=4, Hkv=2, D=128, bs=bs, dtype=dtype)
+    c = case.cache
+    at = int(case.tables[0, 0]) * c.Hkv * step_ref.chunk_elements(bs, c.D)          # position 0, kv head 0
+    c.pool[at + step_ref.offsets16(bs, c.D, [0], 0)[0][5]] = 0x7F80 if dtype == "bf16" else 0x7C00
+    got = run(case, 0.09)
+    for j in range(q_len):
+        pos = ctx - q_len + j
+        # a window of pos tokens leaves position 0 out
+        out, tol = step_ref.extend(case.q[j:j + 1], c, case.tables[:1], [pos + 1], [0, 1], 0.09, window=pos)
+        low = case.q[j, :2, 5] < 0
+        low = np.concatenate([low, [True, True]])                                   # (kv head 1 is as it was)
+        g = bits_to_f64(dev_to_u16(got[j]), dtype)
+        assert (np.abs(g - out[0])[:2][low[:2]] <= tol[0][:2][low[:2]]).all(), j
+        assert np.isnan(g[:2][~low[:2]]).all(), j
+    tail = [case.q_lens[0], case.q_lens[0] + 3]
+    assert_close(got[tail[0]:tail[1]], step_ref.extend(case.q[tail[0]:tail[1]], c, case.tables[1:], [50], [0, 3], 0.09))
