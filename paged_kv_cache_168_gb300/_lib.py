@@ -69,21 +69,33 @@ class CacheDesc:
     layer_stride_bytes: int = 0
     kv_int8: bool = False
 
-    def c(self) -> _Desc:
-        # the C struct of the current fields, rebuilt only when one has changed
+    # (fields of the struct, the struct, its reference): beside the instance's __dict__, so that copies, pickles and
+    # vars() hold the fields alone
+    __slots__ = ("__dict__", "__weakref__", "_made")
+
+    def __getstate__(self):
+        return dict(self.__dict__)
+
+    def _struct(self):
+        # rebuilt only when a field has changed
         key = (self.num_blocks, self.block_size, self.num_kv_heads, self.head_size, self.dtype, self.num_layers,
                self.layer_stride_bytes, self.kv_int8)
-        if key != self.__dict__.get("_key"):
-            self._c = _Desc(self.num_blocks, self.block_size, self.num_kv_heads, self.head_size,
-                            DTYPE_CODE[self.dtype] + (2 if self.kv_int8 else 0), self.num_layers,
-                            self.layer_stride_bytes)
-            self._ref = ctypes.byref(self._c)
-            self._key = key
-        return self._c
+        try:
+            made = self._made
+            if made[0] == key:
+                return made
+        except AttributeError:
+            pass
+        c = _Desc(self.num_blocks, self.block_size, self.num_kv_heads, self.head_size,
+                  DTYPE_CODE[self.dtype] + (2 if self.kv_int8 else 0), self.num_layers, self.layer_stride_bytes)
+        made = self._made = (key, c, ctypes.byref(c))
+        return made
+
+    def c(self) -> _Desc:
+        return self._struct()[1]
 
     def ref(self):
-        self.c()
-        return self._ref
+        return self._struct()[2]
 
 
 def load():

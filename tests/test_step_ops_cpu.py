@@ -231,3 +231,22 @@ def test_binding_refuses_wrong_tensors():
     extend(query_start_loc=i32(1))
     extend(context_lens=i32(1).long())
     extend(block_tables=i32(4, 2).t()[:1])                                 # entries two apart
+
+
+def test_a_used_descriptor_is_copied_and_pickled_like_a_new_one():
+    """A descriptor goes to worker processes; what a call keeps beside its fields does not."""
+    import copy
+    import dataclasses
+    import pickle
+    for used in (lambda d: d.c(), lambda d: d.ref(), _lib.cache_bytes):
+        d = CacheDesc(4, 16, 2, 128, torch.bfloat16, num_layers=3, kv_int8=True)
+        fields = dict(vars(d))
+        size = _lib.cache_bytes(CacheDesc(**fields))
+        used(d)
+        assert vars(d) == fields == dataclasses.asdict(d)
+        for e in (pickle.loads(pickle.dumps(d)), copy.copy(d), copy.deepcopy(d), CacheDesc(**vars(d)), dataclasses.replace(d)):
+            assert e == d and _lib.cache_bytes(e) == size
+            e.num_blocks = 8                                            # a copy's changes are its own
+            assert e.c().num_blocks == 8 and d.c().num_blocks == 4 and _lib.cache_bytes(e) == 2 * size
+        for protocol in range(pickle.HIGHEST_PROTOCOL + 1):
+            assert pickle.loads(pickle.dumps(d, protocol)) == d
