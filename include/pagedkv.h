@@ -246,8 +246,10 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
  *   query_start_loc device int32 [num_seqs + 1]; context_lens device int32
  *                   [num_seqs]; slot_mapping device int64 [max_tokens];
  *                   positions device int32 [max_tokens], may be NULL.
- * A step that cannot be built is empty: query_start_loc and context_lens 0, all
- * slots -1, all positions 0, tables unchanged, *num_free_out = *num_free, and
+ * A step that cannot be built is empty: query_start_loc and context_lens 0 (where
+ * context_lens is cached_lens, the lengths stay as they are instead, so that the
+ * step can be tried again, with more free blocks or fewer requests), all slots -1,
+ * all positions 0, tables unchanged, *num_free_out = *num_free, and
  *   PA_DEVERR_OUT_OF_BLOCKS  too few free blocks, or *num_free not in
  *                            [0, num_blocks];
  *   PA_DEVERR_CONTEXT        a negative length, a context longer than its row

@@ -103,9 +103,11 @@ __global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesP
   }
   cluster_sync();                                     // every CTA has read the lengths and the free count
   if (blockIdx.x == 0) {
+    // lengths updated in place stay as they are when the step cannot be built: it can be tried again
+    const bool keep = !ok && p.context_lens == p.cached_lens;
     for (int s = tid; s < S; s += kThreads) {
       p.query_start_loc[s] = ok ? starts[s] : 0;
-      p.context_lens[s] = ok ? ctxs[s] : 0;
+      if (!keep) p.context_lens[s] = ok ? ctxs[s] : 0;
     }
     if (tid == 0) {
       p.query_start_loc[S] = ok ? (int32_t)total : 0;

@@ -172,3 +172,34 @@ def test_captured_step_follows_its_lengths():
         for k, w in zip(("qsl", "ctx", "slots", "pos", "tables"), want):
             assert np.array_equal(bufs[k].cpu().numpy(), w), k
         assert bufs["nfo"].item() == want[5]
+
+
+@pytest.mark.parametrize("ring", [0, 4])
+def test_a_failed_update_in_place_can_be_tried_again(ring):
+    """Too few blocks, in place: lengths, tables and the free list stay as they were; with more blocks the same
+    call builds the step."""
+    s = Step(21, [30, 0, 17, 9], [20, 40, 1, 0], 8, ring)
+    S, T = 4, s.max_tokens
+    free = s.free.copy()
+    z = lambda *n, dt=torch.int32: torch.full(n, 77, dtype=dt, device="cuda")
+    qsl, slots, pos, err = z(S + 1), z(T, dt=torch.int64), z(T), z(1) * 0
+    tables, lens, new, nf = dev(s.tables), dev(s.cached), dev(s.new), dev([2])
+    desc = pkv.CacheDesc(s.nb, 8, 1, 128)
+    call = lambda: pkv.build_tables(qsl, lens, slots, pos, tables, dev(free), nf, nf, desc, lens, new, ring_blocks=ring, dev_err=err)
+    call()
+    assert pkv.read_device_errors(err) == pkv.DEVERR_OUT_OF_BLOCKS
+    assert lens.tolist() == s.cached.tolist() and nf.item() == 2
+    assert np.array_equal(tables.cpu().numpy(), s.tables)
+    assert not qsl.any() and bool((slots == -1).all()) and not pos.any()
+    nf.fill_(s.num_free)
+    call()
+    assert pkv.read_device_errors(err) == 0
+    want = step_ref.build_tables(s.tables, free, s.num_free, s.cached, s.new, s.nb, 8, ring, T)
+    for got, w in zip((qsl, lens, slots, pos, tables), want):
+        assert np.array_equal(got.cpu().numpy(), w)
+    assert nf.item() == want[5]
+    # any other reason for an empty step leaves them as well
+    lens, new = dev([30, -1, 17, 9]), dev([1, 1, 1, 1])
+    call()
+    assert pkv.read_device_errors(err) & pkv.DEVERR_CONTEXT
+    assert lens.tolist() == [30, -1, 17, 9]
