@@ -265,6 +265,17 @@ pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64
                           const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens,
                           int32_t ring_blocks, uint32_t* dev_err, void* stream);
 
+/* pa_build_tables over a view of longer rows: rows lie block_table_stride entries
+ * apart, and their first block_table_width (<= the stride) are the table.
+ * Contexts and ring_blocks are held to the width; nothing behind it is read or
+ * written.  pa_build_tables is this call with the width equal to the stride. */
+pa_status pa_build_tables_strided(int32_t* query_start_loc, int32_t* context_lens, int64_t* slot_mapping,
+                                  int32_t* positions, int32_t* block_tables, int64_t block_table_stride,
+                                  int32_t block_table_width, const int32_t* free_blocks, const int32_t* num_free,
+                                  int32_t* num_free_out, const pa_cache_desc* desc, const int32_t* cached_lens,
+                                  const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens, int32_t ring_blocks,
+                                  uint32_t* dev_err, void* stream);
+
 /* Workspace bytes pa_decode needs for these shapes (0 when no sequence can span
  * more than one partition, or desc is NULL; SIZE_MAX when the size does not fit
  * in half the address space).  partition_size 0 selects the default
@@ -402,6 +413,16 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
                     const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
                     int32_t num_tokens, int32_t num_q_heads, int32_t max_query_len, float scale, int32_t window,
                     int32_t ring_blocks, void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* pa_extend over a view of longer rows, as pa_build_tables_strided: a context
+ * longer than block_table_width blocks (without a ring) gives zero rows and
+ * PA_DEVERR_CONTEXT, and nothing behind a row's width is read. */
+pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, const void* kv_cache,
+                            const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                            int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                            const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, void* workspace,
+                            size_t workspace_bytes, uint32_t* dev_err, void* stream);
 
 /* Paged decode where groups of sequences share the first tokens of their
  * context physically: beams of one prompt, or parallel samples, whose prompt

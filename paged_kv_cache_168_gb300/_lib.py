@@ -29,8 +29,9 @@ EXPORTED = [
     "pa_cache_bytes", "pa_cache_element_offset", "pa_cache_scale_offset", "pa_reshape_and_cache", "pa_decode_workspace_bytes",
     "pa_decode_partition_size", "pa_decode", "pa_decode_window", "pa_decode_window_span", "pa_prefill",
     "pa_decode_static_workspace", "pa_decode_shared_prefix", "pa_decode_shared_prefix_partition_size",
-    "pa_decode_shared_prefix_workspace_bytes", "pa_rope_reshape_and_cache", "pa_build_tables", "pa_extend",
-    "pa_extend_workspace_bytes", "pa_copy_blocks", "pa_swap_blocks", "pa_read_device_errors",
+    "pa_decode_shared_prefix_workspace_bytes", "pa_rope_reshape_and_cache", "pa_build_tables",
+    "pa_build_tables_strided", "pa_extend", "pa_extend_strided", "pa_extend_workspace_bytes",
+    "pa_copy_blocks", "pa_swap_blocks", "pa_read_device_errors",
     "pa_status_string", "pa_last_error_message",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_can_allocate", "pa_bm_allocate", "pa_bm_append_slot", "pa_bm_fork",
     "pa_bm_free", "pa_bm_block_table", "pa_bm_swap_out", "pa_bm_swap_in", "pa_bm_num_free_blocks",
@@ -147,6 +148,11 @@ def load():
     lib.pa_extend.argtypes = [P, P, i64, P, D, i32, P, i32, P, P, i32, i32, i32, i32, ctypes.c_float, i32, i32, P, sz,
                               P, P]
     lib.pa_extend.restype = ctypes.c_int
+    lib.pa_build_tables_strided.argtypes = [P, P, P, P, P, i64, i32, P, P, P, D, P, P, i32, i32, i32, P, P]
+    lib.pa_build_tables_strided.restype = ctypes.c_int
+    lib.pa_extend_strided.argtypes = [P, P, i64, P, D, i32, P, i64, i32, P, P, i32, i32, i32, i32, ctypes.c_float, i32,
+                                      i32, P, sz, P, P]
+    lib.pa_extend_strided.restype = ctypes.c_int
     lib.pa_extend_workspace_bytes.argtypes = [D, i32, i32, i32, i32]
     lib.pa_extend_workspace_bytes.restype = sz
     lib.pa_copy_blocks.argtypes = [P, D, P, i32, P]
@@ -406,7 +412,8 @@ def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot
                  stream=None) -> None:
     """pa_build_tables: query_start_loc [S + 1], context_lens [S], slot_mapping int64 [max_tokens] and positions
     [max_tokens] (or None) are written, block_tables [S, W] and num_free_out [1] updated, from cached_lens [S],
-    new_lens [S] and the free list free_blocks [num_blocks], num_free [1] (int32 all but slot_mapping)."""
+    new_lens [S] and the free list free_blocks [num_blocks], num_free [1] (int32 all but slot_mapping).
+    Contexts are held to block_tables' width, also where it is a view of longer rows."""
     S, i32 = cached_lens.shape[0], torch.int32
     if not (query_start_loc.dtype is i32 and context_lens.dtype is i32 and block_tables.dtype is i32
             and free_blocks.dtype is i32 and num_free.dtype is i32 and num_free_out.dtype is i32
@@ -417,6 +424,8 @@ def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot
                  cached_lens=cached_lens, new_lens=new_lens)
         _tensors(torch.int64, slot_mapping=slot_mapping)
     T, (rows, width), (pitch, step) = slot_mapping.numel(), block_tables.shape, block_tables.stride()
+    if S <= 1:
+        pitch = width or 1                            # (one row's stride says nothing)
     if (query_start_loc.numel() < S + 1 or context_lens.numel() < S or new_lens.numel() != S or rows < S
             or free_blocks.numel() < desc.num_blocks or num_free.numel() < 1 or num_free_out.numel() < 1
             or (positions is not None and not (positions.numel() >= T and positions.is_contiguous()))
@@ -425,10 +434,10 @@ def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot
                     and cached_lens.is_contiguous() and new_lens.is_contiguous() and slot_mapping.is_contiguous())):
         raise PagedKVError(PA_ERR_INVALID_ARG, "an array of build_tables is too short or not contiguous, or table "
                                                "rows are not dense")
-    _on_device(load().pa_build_tables, slot_mapping, stream,
+    _on_device(load().pa_build_tables_strided, slot_mapping, stream,
                query_start_loc.data_ptr(), context_lens.data_ptr(), slot_mapping.data_ptr(),
                None if positions is None else positions.data_ptr(), block_tables.data_ptr(),
-               pitch if S > 1 else max(width, 1), free_blocks.data_ptr(), num_free.data_ptr(), num_free_out.data_ptr(),
+               pitch, min(width, pitch), free_blocks.data_ptr(), num_free.data_ptr(), num_free_out.data_ptr(),
                desc.ref(), cached_lens.data_ptr(), new_lens.data_ptr(), S, T, ring_blocks,
                None if dev_err is None else dev_err.data_ptr())
 
@@ -443,7 +452,8 @@ def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Cac
            workspace: torch.Tensor | None, window: int = 0, ring_blocks: int = 0, layer: int = 0,
            dev_err: torch.Tensor | None = None, stream=None) -> None:
     """pa_extend: out/q [T, Hq, D] packed by query_start_loc (int32 [S + 1]); causal over each sequence's cache
-    (its last q_len positions are the queries), with an optional window and ring tables."""
+    (its last q_len positions are the queries), with an optional window and ring tables.  block_tables may be a view
+    of longer rows."""
     S, (T, Hq, D), dt, i32 = context_lens.shape[0], q.shape, desc.dtype, torch.int32
     if not (q.dtype is dt and out.dtype is dt and block_tables.dtype is i32 and context_lens.dtype is i32
             and query_start_loc.dtype is i32):
@@ -451,12 +461,14 @@ def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Cac
         _tensors(i32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc)
     q_pitch = _rows(q, (T, Hq, desc.head_size), "q")
     (rows, width), (pitch, step) = block_tables.shape, block_tables.stride()
+    if S <= 1:
+        pitch = width or 1
     if (out.shape != q.shape or query_start_loc.numel() < S + 1 or rows < S or (width > 1 and step != 1)
             or not (out.is_contiguous() and context_lens.is_contiguous() and query_start_loc.is_contiguous())):
         raise PagedKVError(PA_ERR_INVALID_ARG, "out must be contiguous and of q's shape, query_start_loc and "
                                                "block_tables long enough, table rows dense")
-    _on_device(load().pa_extend, q, stream, out.data_ptr(), q.data_ptr(), q_pitch, kv_cache.data_ptr(), desc.ref(),
-               layer, block_tables.data_ptr(), pitch if S > 1 else max(width, 1), context_lens.data_ptr(),
+    _on_device(load().pa_extend_strided, q, stream, out.data_ptr(), q.data_ptr(), q_pitch, kv_cache.data_ptr(),
+               desc.ref(), layer, block_tables.data_ptr(), pitch, min(width, pitch), context_lens.data_ptr(),
                query_start_loc.data_ptr(), S, T, Hq, max_query_len, scale, window, ring_blocks,
                None if workspace is None else workspace.data_ptr(),
                0 if workspace is None else workspace.numel() * workspace.element_size(),

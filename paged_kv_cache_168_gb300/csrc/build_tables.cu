@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesP
   uint32_t err = 0;
   for (int s = s0; s < s1; ++s) {
     const int64_t c = p.cached_lens[s], n = p.new_lens[s], ctx = c + n;
-    if (c < 0 || n < 0 || ctx > INT32_MAX || (p.ring_blocks == 0 && ctx > (int64_t)p.bt_stride * bs)) {
+    if (c < 0 || n < 0 || ctx > INT32_MAX || (p.ring_blocks == 0 && ctx > (int64_t)p.bt_width * bs)) {
       err = PA_DEVERR_CONTEXT;
       continue;
     }
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) build_tables_kernel(const TablesP
       const int have = (int)min(((int64_t)cached + bs - 1) >> shift, cap);
       const bool kept = p.ring_blocks == 0 || b > ((ctx - 1) >> shift) - p.ring_blocks;
       const int e = p.ring_blocks > 0 ? b % p.ring_blocks : b;
-      int32_t* entry = p.block_tables + (int64_t)s * p.bt_stride + e;
+      int32_t* entry = p.block_tables + s * p.bt_stride + e;
       // begun in this step: logical block b itself, or (ring) the one whose entry b takes over
       const bool fresh = e >= have;
       if (kept || fresh) {

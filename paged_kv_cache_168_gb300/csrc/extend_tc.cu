@@ -181,7 +181,7 @@ __device__ __forceinline__ Seq read_seq(const ExtendParams& p, int s, uint32_t& 
     return q;
   }
   if (q.q_len > p.max_query_len || q.q_len > q.ctx || q.ctx > INT32_MAX - kKv ||      // (tile ends stay in int32)
-      (p.ring_blocks == 0 && (int64_t)q.ctx > (int64_t)p.bt_stride * p.block_size)) {
+      (p.ring_blocks == 0 && (int64_t)q.ctx > (int64_t)p.bt_width * p.block_size)) {
     q.zero = true;
     err |= PA_DEVERR_CONTEXT;
     return q;
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         if (lane == 0) w_next = atomicAdd(&ws.head->next, 1);
         const int n = tiles_of(w);
         if constexpr (!C::kConvert) {
-          const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+          const int32_t* row = p.block_tables + w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;   // blocks [fb, nblk) are read
           for (int j = 0; j < n; ++j, ++c) {
             // lane l copies the tile's block l
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           }
           if (w.kvh < 0) break;
           const int n = tiles_of(w);
-          const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+          const int32_t* row = p.block_tables + w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;
           for (int j = 0; j < n; ++j, ++c) {
             const int blk = (w.tile0 + j) * (kKv / bs) + lane;
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
         if (w.kvh < 0) break;
         const int n = tiles_of(w);
-        const int32_t* row = p.block_tables + (int64_t)w.seq * p.bt_stride;
+        const int32_t* row = p.block_tables + w.seq * p.bt_stride;
         // the block of token u of KV tile j, or -1: no query attends it, or its id is bad
         auto find = [&](int j, int u) -> int {
           const int pos = (w.tile0 + j) * kKv + u;
@@ -1735,7 +1735,7 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
   }
   const Layout L{bs, D, p.num_kv_heads};
   const I8Layout L8{bs, p.num_kv_heads};
-  const int32_t* row = p.block_tables + (int64_t)it.seq * p.bt_stride;
+  const int32_t* row = p.block_tables + it.seq * p.bt_stride;
   for (int t = from; t <= pos; ++t) {
     const int b = block_of(p, row, t / bs), at = t & (bs - 1);
     if ((unsigned)b >= (unsigned)p.num_blocks) continue;             // its tile is flagged as bad

@@ -181,7 +181,8 @@ struct TablesParams {
   int64_t* slot_mapping;
   int32_t* positions;             // may be null
   int32_t* block_tables;
-  int32_t bt_stride;
+  int64_t bt_stride;              // entries between rows
+  int32_t bt_width;               // entries of a row
   const int32_t* free_blocks;
   const int32_t* num_free;
   int32_t* num_free_out;
@@ -208,7 +209,8 @@ struct ExtendParams {
   int32_t num_q_heads;
   int32_t group;                  // query heads per kv head, 1 .. 16
   const int32_t* block_tables;
-  int32_t bt_stride;
+  int64_t bt_stride;              // entries between rows
+  int32_t bt_width;               // entries of a row
   const int32_t* context_lens;
   const int32_t* query_start_loc;
   int32_t num_seqs;

@@ -33,6 +33,13 @@ pa_status cuda_fail(cudaError_t e, const char* what) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Block-table rows `stride` entries apart, `width` entries long.
+pa_status check_rows(int64_t stride, int32_t width) {
+  if (stride <= 0 || width < 0 || width > stride)
+    return fail(PA_ERR_INVALID_ARG, "block table rows %lld entries apart, %d long", (long long)stride, width);
+  return PA_OK;
+}
+
 // Default partition sizes for the tensor-core kernels: the shortest, the longest
 // for contexts up to kLongContext tokens, the longest beyond, and the work items
 // (sequence, kv head, partition) wanted before a longer partition is taken --
@@ -399,6 +406,17 @@ pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64
                           const int32_t* num_free, int32_t* num_free_out, const pa_cache_desc* desc,
                           const int32_t* cached_lens, const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens,
                           int32_t ring_blocks, uint32_t* dev_err, void* stream) {
+  return pa_build_tables_strided(query_start_loc, context_lens, slot_mapping, positions, block_tables,
+                                 block_table_stride, block_table_stride, free_blocks, num_free, num_free_out, desc,
+                                 cached_lens, new_lens, num_seqs, max_tokens, ring_blocks, dev_err, stream);
+}
+
+pa_status pa_build_tables_strided(int32_t* query_start_loc, int32_t* context_lens, int64_t* slot_mapping,
+                                  int32_t* positions, int32_t* block_tables, int64_t block_table_stride,
+                                  int32_t block_table_width, const int32_t* free_blocks, const int32_t* num_free,
+                                  int32_t* num_free_out, const pa_cache_desc* desc, const int32_t* cached_lens,
+                                  const int32_t* new_lens, int32_t num_seqs, int32_t max_tokens, int32_t ring_blocks,
+                                  uint32_t* dev_err, void* stream) {
   pa_status st = check_desc(desc);
   if (st != PA_OK) return st;
   if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs %d < 0", num_seqs);
@@ -416,11 +434,10 @@ pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64
     if (reinterpret_cast<uintptr_t>(a) & 3) return fail(PA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(slot_mapping) & 7)
     return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned");
-  if (num_seqs > 0 && block_table_stride <= 0)
-    return fail(PA_ERR_INVALID_ARG, "block_table_stride %d", block_table_stride);
-  if (ring_blocks < 0 || (num_seqs > 0 && ring_blocks > block_table_stride))
-    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, block_table_stride %d]", ring_blocks,
-                block_table_stride);
+  if (num_seqs > 0 && check_rows(block_table_stride, block_table_width) != PA_OK) return PA_ERR_INVALID_ARG;
+  if (ring_blocks < 0 || (num_seqs > 0 && ring_blocks > block_table_width))
+    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,
+                block_table_width);
   pkv::TablesParams p{};
   p.query_start_loc = query_start_loc;
   p.context_lens = context_lens;
@@ -428,6 +445,7 @@ pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64
   p.positions = positions;
   p.block_tables = block_tables;
   p.bt_stride = block_table_stride;
+  p.bt_width = block_table_width;
   p.free_blocks = free_blocks;
   p.num_free = num_free;
   p.num_free_out = num_free_out;
@@ -741,6 +759,17 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
                     const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
                     int32_t num_tokens, int32_t num_q_heads, int32_t max_query_len, float scale, int32_t window,
                     int32_t ring_blocks, void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream) {
+  return pa_extend_strided(out, q, q_token_stride, kv_cache, desc, layer, block_tables, block_table_stride,
+                           block_table_stride, context_lens, query_start_loc, num_seqs, num_tokens, num_q_heads,
+                           max_query_len, scale, window, ring_blocks, workspace, workspace_bytes, dev_err, stream);
+}
+
+pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, const void* kv_cache,
+                            const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                            int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                            const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, void* workspace,
+                            size_t workspace_bytes, uint32_t* dev_err, void* stream) {
   pa_status st = check_desc(desc);
   if (st != PA_OK) return st;
   if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
@@ -772,10 +801,10 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
     if (o < x + (rows - 1) * (uintptr_t)q_token_stride * 2 + row && x < o + rows * row)
       return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
   }
-  if (block_table_stride <= 0) return fail(PA_ERR_INVALID_ARG, "block_table_stride %d", block_table_stride);
-  if (ring_blocks < 0 || ring_blocks > block_table_stride)
-    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, block_table_stride %d]", ring_blocks,
-                block_table_stride);
+  if (check_rows(block_table_stride, block_table_width) != PA_OK) return PA_ERR_INVALID_ARG;
+  if (ring_blocks < 0 || ring_blocks > block_table_width)
+    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,
+                block_table_width);
   const size_t need = pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
   if (workspace_bytes < need)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
@@ -794,6 +823,7 @@ pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void
   p.group = group;
   p.block_tables = block_tables;
   p.bt_stride = block_table_stride;
+  p.bt_width = block_table_width;
   p.context_lens = context_lens;
   p.query_start_loc = query_start_loc;
   p.num_seqs = num_seqs;

@@ -203,3 +203,27 @@ def test_a_failed_update_in_place_can_be_tried_again(ring):
     call()
     assert pkv.read_device_errors(err) & pkv.DEVERR_CONTEXT
     assert lens.tolist() == [30, -1, 17, 9]
+
+
+def test_tables_that_are_part_of_wider_rows():
+    """A view of the first entries of longer rows: contexts are held to its width, and what lies behind it stays."""
+    s = Step(22, [30, 0, 17], [20, 40, 1], 8, width=7)
+    S, T = 3, s.max_tokens
+    wide = dev(np.concatenate([s.tables, np.full((S, 5), 55)], 1))
+    z = lambda *n, dt=torch.int32: torch.full(n, 77, dtype=dt, device="cuda")
+    qsl, ctx, slots, pos, nfo, err = z(S + 1), z(S), z(T, dt=torch.int64), z(T), z(1), z(1) * 0
+    desc = pkv.CacheDesc(s.nb, 8, 1, 128)
+
+    def call(new, ring=0):
+        pkv.build_tables(qsl, ctx, slots, pos, wide[:, :7], dev(s.free), dev([s.num_free]), nfo, desc, dev(s.cached), dev(new), ring_blocks=ring, dev_err=err)
+    call(np.asarray([27, 40, 1]))                                    # 57 tokens: eight blocks
+    assert pkv.read_device_errors(err) == pkv.DEVERR_CONTEXT
+    assert bool((wide[:, 7:] == 55).all()) and np.array_equal(wide[:, :7].cpu().numpy(), s.tables) and not qsl.any()
+    with pytest.raises(pkv.PagedKVError):
+        call(s.new, ring=8)
+    call(s.new)
+    assert pkv.read_device_errors(err) == 0
+    want = step_ref.build_tables(s.tables, s.free, s.num_free, s.cached, s.new, s.nb, 8, 0, T)
+    for got, w in zip((qsl, ctx, slots, pos, wide[:, :7], nfo), want):
+        assert np.array_equal(got.cpu().numpy(), np.atleast_1d(w))
+    assert bool((wide[:, 7:] == 55).all())

@@ -469,3 +469,35 @@ def test_infinite_keys(q_len, ctx, bs, dtype):
         assert np.isnan(g[:2][~low[:2]]).all(), j
     tail = [case.q_lens[0], case.q_lens[0] + 3]
     assert_close(got[tail[0]:tail[1]], step_ref.extend(case.q[tail[0]:tail[1]], c, case.tables[1:], [50], [0, 3], 0.09))
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_tables_that_are_part_of_wider_rows(kv8):
+    """A view of the first entries of longer rows: its own width bounds the contexts, not the rows' pitch."""
+    rng = np.random.default_rng(90)
+    case = Chunk(rng, [10, 40, 3], [50, 160, 100], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16", kv8=kv8)
+    W = case.tables.shape[1]
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    wide = dev(np.concatenate([case.tables, np.zeros((3, 7), np.int32)], 1))         # (valid ids behind the view)
+    c = case.cache
+    desc = pkv.CacheDesc(c.nb, 16, 2, 128, torch.bfloat16, kv_int8=kv8)
+    q = u16_to_dev(case.q_bits, "bf16")
+    ws = torch.empty(pkv.extend_workspace_bytes(desc, 3, case.T, 4, 40), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(ctx, **kw):
+        out = torch.full_like(q, 7.0)
+        pkv.extend(out, q, pool_to_dev(c), desc, wide[:, :W], dev(ctx), dev(case.qsl), 40, 0.1, ws, dev_err=err, **kw)
+        return out
+    assert_close(call(case.ctx), case.expected(0.1))
+    assert pkv.read_device_errors(err) == 0
+    ctx = case.ctx.copy()
+    ctx[1] = W * 16 + 1
+    got = call(ctx)
+    assert pkv.read_device_errors(err) == pkv.DEVERR_CONTEXT
+    assert bool((got[10:50] == 0).all())
+    want, tol = case.expected(0.1)
+    assert_close(got[:10], (want[:10], tol[:10]))
+    assert_close(got[50:], (want[50:], tol[50:]))
+    with pytest.raises(pkv.PagedKVError):
+        call(case.ctx, ring_blocks=W + 1)

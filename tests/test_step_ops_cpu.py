@@ -250,3 +250,18 @@ def test_a_used_descriptor_is_copied_and_pickled_like_a_new_one():
             assert e.c().num_blocks == 8 and d.c().num_blocks == 4 and _lib.cache_bytes(e) == 2 * size
         for protocol in range(pickle.HIGHEST_PROTOCOL + 1):
             assert pickle.loads(pickle.dumps(d, protocol)) == d
+
+
+def test_rows_of_wider_tables_refusals(lib):
+    bad = _lib.PA_ERR_INVALID_ARG
+
+    def tables(stride, width, ring=0):
+        return lib.pa_build_tables_strided(V(), V(), V(), V(), V(), stride, width, V(), V(), V(), _desc(), V(), V(), 2, 8, ring, None, None)
+
+    def extend(stride, width, ring=0):
+        return lib.pa_extend_strided(V(FAKE + (1 << 24)), V(), 512, V(), _desc(), 0, V(), stride, width, V(), V(), 2, 100, 4, 100, 0.1, 0,
+                                     ring, V(), 1 << 40, None, None)
+    for f in (tables, extend):
+        assert f(8, 9) == bad and f(0, 0) == bad and f(8, -1) == bad and f(-8, -8) == bad
+        assert f(8, 5, 6) == bad                                            # a ring longer than the width
+        assert b"ring_blocks 6" in lib.pa_last_error_message()
