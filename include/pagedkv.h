@@ -77,12 +77,15 @@
  * here is per token and per kv head symmetric quantisation: each stored K or V
  * vector x gets scale = max|x| / 127 and codes round-half-even(x * (127 /
  * max|x|)) clipped to [-127, 127], both decided in IEEE fp32 (an all-zero
- * vector stores scale 0 and zero codes); the value a code stands for is
- * code * scale.  Chunk (block, kv head) holds, in bytes: K codes [block_size]
- * [128] row-major, V codes [block_size][128], K scales (fp32 [block_size]
- * padded to a multiple of 16 bytes), V scales (same).  Chunk bytes =
- * 2 * block_size * 128 + 2 * roundup16(4 * block_size); chunks are ordered by
- * (block, kv head) as above.  pa_cache_element_offset() gives code byte
+ * vector stores scale 0 and zero codes); the value a code stands for is code *
+ * scale.  max|x| leaves NaN out, and an element whose product is NaN (it is NaN
+ * itself, or the vector holds an infinity and it is infinite) has code 0; a
+ * vector with an infinity has an infinite scale.  Chunk (block, kv head) holds,
+ * in bytes: K codes [block_size] [128] row-major, V codes [block_size][128], K
+ * scales (fp32 [block_size] padded to a multiple of 16 bytes), V scales (same).
+ * Chunk bytes = 2 * block_size * 128 + 2 * roundup16(4 * block_size); chunks
+ * are ordered by (block, kv head) as above.  pa_cache_element_offset() gives
+ * code byte
  * offsets and pa_cache_scale_offset() scale byte offsets.
  */
 #ifndef PAGEDKV_H

@@ -73,7 +73,7 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, i
 // then every thread takes kDeep units at a time, all their loads before any
 // arithmetic.  32768 tokens of 32 + 8 heads in bf16, three axes: 138 us, 5.8 TB/s (one
 // token a CTA and round, two barriers for 1.5 units a thread: 185 us).  5001 tokens of
-// 32 + 32 heads into an 8-bit cache: 49 us, 4.2 TB/s; 132-byte vectors go to random
+// 32 + 32 heads into an 8-bit cache: 50 us, 4.1 TB/s; 132-byte vectors go to random
 // places there.
 template <typename T, int D, bool kPairs, bool kI8, int kTokens>
 __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
@@ -164,6 +164,15 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
               uint32_t r[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__fadd_rn(__fmul_rn(x[k], inv), 12582912.f));
+              // A product is NaN where x is, or where x is infinite (inv is 0 then): code 0.  The
+              // sums' exponent field is 150, so bit 26 is set in a NaN alone.
+              uint32_t any = 0;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) any |= r[k];
+              if (__builtin_expect(any & 0x04000000u, 0)) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) r[k] = r[k] & 0x04000000u ? 0u : r[k];
+              }
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 code[k] = __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040), __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);

@@ -250,3 +250,49 @@ def test_replays_and_another_stream():
     torch.cuda.synchronize()
     want = c.expected()
     assert np.array_equal(dev_to_u16(out), want[0]) and np.array_equal(pool.cpu().numpy().view(np.uint16), want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_codes_of_vectors_that_are_not_finite(dtype, pairs):
+    """8-bit caches: a NaN element has code 0 beside the codes of the finite ones; a vector with an infinity has codes 0
+    and an infinite scale; of NaN alone, codes and scale 0.  What is not rotated agrees with the plain cache writer."""
+    c = Case(18, 8, 2, 2, 128, 8, dtype, kv8=True, rot=16, pairs=pairs)
+    inf, nan, minf = (0x7F80, 0x7FC0, 0xFF80) if dtype == "bf16" else (0x7C00, 0x7E00, 0xFC00)
+    for x in (c.k, c.v):                                             # (dims from 16 on are not rotated)
+        x[0, 0, 20], x[1, 1, [40, 127]] = nan, nan
+        x[2, 0, 33], x[3, 1, 90], x[4, 0, [21, 60]] = inf, minf, [inf, nan]
+        x[5, 1], x[6, 0, :] = nan, minf
+        x[0, 1, 77] = nan | 0x8000
+    c.k[5, 1], c.k[6, 0] = nan, minf                                 # (and all of a rotated vector)
+    f = lambda bits: bits_to_f64(bits, dtype).astype(np.float32)
+    n = c.rot // 2
+    row = c.cos_sin[c.pos[0]]
+    with np.errstate(invalid="ignore"):
+        k = step_ref.rotate32(f(c.k), row[:, :n], row[:, n:], c.rot, pairs)
+    after = step_ref.Cache(c.before.nb, 8, 2, 128, dtype, True)
+    after.pool = c.before.pool.copy()
+    for part, x in enumerate((k, f(c.v))):
+        with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+            amax = np.fmax.reduce(np.abs(x), -1, keepdims=True)
+            amax = np.where(np.isnan(amax), 0, amax).astype(np.float32)
+            inv = np.where(amax > 0, np.float32(127) * (np.float32(1) / amax), 0).astype(np.float32)
+            y = (x * inv).astype(np.float32)
+            codes = np.where(np.isnan(y), 0, np.clip(np.rint(y), -127, 127)).astype(np.int8)
+            step_ref.store8(after, codes, (amax * (np.float32(1) / np.float32(127))).astype(np.float32), part, c.slots)
+    pool = c.run()[1]
+    assert np.array_equal(pool, after.pool)
+    # the plain writer's codes and scales of v (its scale is a division, so off by at most a step)
+    desc = pkv.CacheDesc(c.before.nb, 8, 2, 128, step_ref.torch_dtype(dtype), kv_int8=True)
+    plain = torch.from_numpy(c.before.pool.copy()).cuda()
+    pkv.reshape_and_cache(plain, desc, u16_to_dev(c.v, dtype), u16_to_dev(c.v, dtype), torch.from_numpy(c.slots).cuda())
+    a, b = after, step_ref.Cache(c.before.nb, 8, 2, 128, dtype, True)
+    b.pool = plain.cpu().numpy()
+    for i, (block, t) in enumerate(zip(c.slots // 8, c.slots % 8)):
+        for h in range(2):
+            base = (block * 2 + h) * step_ref.chunk_bytes8(8)
+            at = base + step_ref.offsets8(8, [t], 1)[0]
+            ca, cb = a.pool[at].view(np.int8).astype(int), b.pool[at].view(np.int8).astype(int)
+            assert (np.abs(ca - cb) <= 1).all() and (ca[~np.isfinite(f(c.v)[i, h])] == 0).all() and (cb[~np.isfinite(f(c.v)[i, h])] == 0).all()
+        sa, sb = a.scales([block], [t], 1), b.scales([block], [t], 1)
+        np.testing.assert_allclose(sa, sb, rtol=2.0 ** -22)
