@@ -85,8 +85,7 @@
  * scales (fp32 [block_size] padded to a multiple of 16 bytes), V scales (same).
  * Chunk bytes = 2 * block_size * 128 + 2 * roundup16(4 * block_size); chunks
  * are ordered by (block, kv head) as above.  pa_cache_element_offset() gives
- * code byte
- * offsets and pa_cache_scale_offset() scale byte offsets.
+ * code byte offsets and pa_cache_scale_offset() scale byte offsets.
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -196,9 +195,9 @@ pa_status pa_reshape_and_cache(void* kv_cache, const pa_cache_desc* desc, int32_
  * of the same vector in its last bit).
  *   q_out, q     device [num_tokens, num_q_heads, head_size], 16-bit; token
  *                strides in elements (multiples of 8), 16-byte aligned.  q_out
- *                may be q itself (with the same stride; q, key and value may be
- *                parts of one row), and may otherwise not overlap it, nor key or
- *                value.  num_q_heads 0: no queries, both may be NULL.
+ *                may be q itself (with the same stride), and may otherwise not
+ *                overlap it, nor key or value (all four may be parts of the same
+ *                rows).  num_q_heads 0: no queries, both may be NULL.
  *   kv_cache, desc, layer, key, value, strides, slot_mapping: as
  *                pa_reshape_and_cache; a token with slot -1 is not stored, its
  *                query is still rotated.

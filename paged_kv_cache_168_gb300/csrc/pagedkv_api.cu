@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "pagedkv.h"
+#include "rows.h"
 
 namespace {
 
@@ -32,6 +33,11 @@ pa_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// n tokens' rows of 16-bit elements.
+pkv::Rows token_rows(const void* p, int64_t n, int64_t stride, int64_t elements) {
+  return {reinterpret_cast<uintptr_t>(p), n, stride * 2, elements * 2};
+}
 
 // Block-table rows `stride` entries apart, `width` entries long.
 pa_status check_rows(int64_t stride, int32_t width) {
@@ -364,12 +370,14 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
       return fail(PA_ERR_INVALID_ARG, "q and q_out must be non-NULL and 16-byte aligned");
     if (q_token_stride < qrow || q_out_token_stride < qrow || q_token_stride % 8 || q_out_token_stride % 8)
       return fail(PA_ERR_INVALID_ARG, "q strides must be >= num_q_heads*head_size and multiples of 8");
-    // a row is read and written by one block, so rows may share memory only with themselves
-    const uintptr_t a = reinterpret_cast<uintptr_t>(q), b = reinterpret_cast<uintptr_t>(q_out);
-    const uintptr_t na = (uintptr_t)((num_tokens - 1) * q_token_stride + qrow) * 2;
-    const uintptr_t nb = (uintptr_t)((num_tokens - 1) * q_out_token_stride + qrow) * 2;
-    if (!(a == b && q_token_stride == q_out_token_stride) && a < b + nb && b < a + na)
+    // a row is read and written by one block, so q_out's rows may share memory only with their own
+    const pkv::Rows out = token_rows(q_out, num_tokens, q_out_token_stride, qrow);
+    if (!(q == q_out && (q_token_stride == q_out_token_stride || num_tokens == 1)) &&
+        pkv::rows_overlap(out, token_rows(q, num_tokens, q_token_stride, qrow)))
       return fail(PA_ERR_INVALID_ARG, "q_out must be q itself (with the same stride) or not overlap it");
+    if (pkv::rows_overlap(out, token_rows(key, num_tokens, key_token_stride, row)) ||
+        pkv::rows_overlap(out, token_rows(value, num_tokens, value_token_stride, row)))
+      return fail(PA_ERR_INVALID_ARG, "q_out must not overlap key or value");
   }
   pkv::RopeParams p{};
   p.q_out = q_out;
@@ -795,12 +803,9 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
     return fail(PA_ERR_INVALID_ARG, "block_tables, context_lens and query_start_loc must be 4-byte aligned");
   if (q_token_stride < (int64_t)num_q_heads * desc->head_size || q_token_stride % 8)
     return fail(PA_ERR_INVALID_ARG, "q_token_stride must be >= num_q_heads*head_size and a multiple of 8");
-  {
-    const uintptr_t row = (uintptr_t)num_q_heads * desc->head_size * 2, rows = (uintptr_t)num_tokens;
-    const uintptr_t o = reinterpret_cast<uintptr_t>(out), x = reinterpret_cast<uintptr_t>(q);
-    if (o < x + (rows - 1) * (uintptr_t)q_token_stride * 2 + row && x < o + rows * row)
-      return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
-  }
+  const int64_t row = (int64_t)num_q_heads * desc->head_size;
+  if (pkv::rows_overlap(token_rows(out, num_tokens, row, row), token_rows(q, num_tokens, q_token_stride, row)))
+    return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
   if (check_rows(block_table_stride, block_table_width) != PA_OK) return PA_ERR_INVALID_ARG;
   if (ring_blocks < 0 || ring_blocks > block_table_width)
     return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,

@@ -296,3 +296,22 @@ def test_codes_of_vectors_that_are_not_finite(dtype, pairs):
             assert (np.abs(ca - cb) <= 1).all() and (ca[~np.isfinite(f(c.v)[i, h])] == 0).all() and (cb[~np.isfinite(f(c.v)[i, h])] == 0).all()
         sa, sb = a.scales([block], [t], 1), b.scales([block], [t], 1)
         np.testing.assert_allclose(sa, sb, rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("gap", [0, 8])
+def test_output_between_the_rows_it_comes_from(gap):
+    """q_out, q, key and value as parts of the same rows, none over another."""
+    c = Case(23, 70, 4, 2, 128, 16, "bf16")
+    rows = torch.full((c.N, 3 * (512 + gap)), float("nan"), dtype=torch.bfloat16, device="cuda")
+    at = lambda i, n: rows[:, i:i + n * 128].unflatten(1, (n, 128))
+    q, q_out, k, v = at(0, 4), at(512 + gap, 4), at(2 * (512 + gap), 2), at(2 * (512 + gap) + 256, 2)
+    for x, b in ((q, c.q), (k, c.k), (v, c.v)):
+        x.copy_(u16_to_dev(b, "bf16"))
+    b = c.before
+    pool = torch.from_numpy(b.pool.view(np.int16).copy()).cuda()
+    pkv.rope_reshape_and_cache(q_out, q, pool, pkv.CacheDesc(b.nb, 16, 2, 128, torch.bfloat16), k, v, torch.from_numpy(c.slots).cuda(),
+                               torch.from_numpy(c.pos).cuda(), torch.from_numpy(c.cos_sin).cuda())
+    want = c.expected()
+    assert np.array_equal(dev_to_u16(q_out), want[0]) and np.array_equal(pool.cpu().numpy().view(np.uint16), want[1])
+    for x, bits in ((q, c.q), (k, c.k), (v, c.v)):
+        assert np.array_equal(dev_to_u16(x), bits)

@@ -265,3 +265,40 @@ def test_rows_of_wider_tables_refusals(lib):
         assert f(8, 9) == bad and f(0, 0) == bad and f(8, -1) == bad and f(-8, -8) == bad
         assert f(8, 5, 6) == bad                                            # a ring longer than the width
         assert b"ring_blocks 6" in lib.pa_last_error_message()
+
+
+def test_rows_share_memory_only_where_they_do(tmp_path):
+    """The check of overlaps against every byte of drawn rows."""
+    import os
+    import shutil
+    import subprocess
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path / "rows_check")
+    subprocess.run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-I",
+                    os.path.join(os.path.dirname(here), "paged_kv_cache_168_gb300", "csrc"), os.path.join(here, "rows_check.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+def test_outputs_over_inputs_are_refused(lib):
+    bad = _lib.PA_ERR_INVALID_ARG
+    A = FAKE
+
+    def rope(q, qo, k, v, stride, n=4):                                     # 4 + 2 + 2 heads of 128: 1024, 512, 512 bytes
+        r = lib.pa_rope_reshape_and_cache(V(A + qo), stride, V(A + q), stride, 4, V(), _desc(), 0, V(A + k), stride, V(A + v), stride, V(), V(), 0,
+                                          V(), 100, 128, None, 1, 0, n, None, None)
+        return r, lib.pa_last_error_message()
+    # rows 4096 bytes apart: q_out over value's part, over key's, over the next row's key; 2048 bytes apart and in
+    # place: over key; over half of q
+    for args in ((0, 1536, 1024, 2048, 2048), (0, 1024, 1920, 3072, 2048), (512, 3584, 256, 2048, 2048), (0, 0, 512, 1536, 1024),
+                 (0, 512, 2048, 3072, 2048)):
+        r, msg = rope(*args)
+        assert r == bad and b"overlap" in msg, (args, msg)
+
+    def extend(q, out, stride, T=3):
+        return lib.pa_extend(V(A + out), V(A + q), stride, V(), _desc(), 0, V(), 8, V(), V(), 2, T, 4, 100, 0.1, 0, 0, V(), 0, None, None)
+    small = _lib.PA_ERR_WORKSPACE_TOO_SMALL                                  # (checked after the overlap)
+    # rows of 1024 bytes: out (three of them, dense) between q's rows, or over one
+    assert extend(0, 1024, 4096) == small and extend(0, 4096 - 3 * 1024, 2048) == small
+    assert extend(0, 1040, 2048) == bad and extend(0, 1008, 4096) == bad and extend(0, 1024, 1024) == bad
+    assert extend(0, 3 * 1024, 512) == small and extend(3 * 1024, 0, 512) == small
