@@ -335,12 +335,13 @@ def _tensors(dtype, **tensors):
 
 
 def _rows(t, shape, name):
-    """The token stride of a [tokens, heads, dims] tensor of that shape with heads and dims contiguous."""
+    """The token stride of a [tokens, heads, dims] tensor of that shape with heads and dims contiguous (of a single
+    token, whose stride says nothing: the row's length)."""
     st = t.stride()
     if t.shape != shape or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
         raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be [tokens, heads, dims] = {tuple(shape)} with heads and "
                                                f"dims contiguous, not {tuple(t.shape)} with strides {st}")
-    return st[0]
+    return st[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rope_table(max_position: int, inv_freq: torch.Tensor, device="cuda") -> torch.Tensor:

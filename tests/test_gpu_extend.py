@@ -501,3 +501,12 @@ def test_tables_that_are_part_of_wider_rows(kv8):
     assert_close(got[50:], (want[50:], tol[50:]))
     with pytest.raises(pkv.PagedKVError):
         call(case.ctx, ring_blocks=W + 1)
+
+
+def test_single_tokens_of_any_stride():
+    """With one token its stride says nothing: heads by tokens, seen as tokens by heads."""
+    rng = np.random.default_rng(91)
+    case = Chunk(rng, [1], [50], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16")
+    q = u16_to_dev(case.q_bits, "bf16").transpose(0, 1).contiguous().transpose(0, 1)
+    q = q.as_strided((1, 4, 128), (128, 128, 1))
+    check(case, q=q)

@@ -315,3 +315,16 @@ def test_output_between_the_rows_it_comes_from(gap):
     assert np.array_equal(dev_to_u16(q_out), want[0]) and np.array_equal(pool.cpu().numpy().view(np.uint16), want[1])
     for x, bits in ((q, c.q), (k, c.k), (v, c.v)):
         assert np.array_equal(dev_to_u16(x), bits)
+
+
+def test_single_tokens_of_any_stride():
+    """With one token its stride says nothing: heads by tokens, seen as tokens by heads."""
+    c = Case(24, 1, 4, 2, 128, 16, "bf16")
+    one = lambda bits: u16_to_dev(bits, "bf16").as_strided((1, bits.shape[1], 128), (128, 128, 1))
+    b = c.before
+    pool = torch.from_numpy(b.pool.view(np.int16).copy()).cuda()
+    q = one(c.q)
+    pkv.rope_reshape_and_cache(q, q, pool, pkv.CacheDesc(b.nb, 16, 2, 128, torch.bfloat16), one(c.k), one(c.v), torch.from_numpy(c.slots).cuda(),
+                               torch.from_numpy(c.pos).cuda(), torch.from_numpy(c.cos_sin).cuda())
+    want = c.expected()
+    assert np.array_equal(dev_to_u16(q), want[0]) and np.array_equal(pool.cpu().numpy().view(np.uint16), want[1])
