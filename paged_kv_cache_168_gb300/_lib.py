@@ -395,7 +395,12 @@ def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, k
                                                "cos_sin must be contiguous")
     pairs = None
     if pair_axis is not None:
-        pairs = np.asarray(pair_axis, dtype=np.uint8).tobytes()      # (ctypes passes its address)
+        pairs = np.asarray(pair_axis)
+        if pairs.dtype != np.uint8:
+            if pairs.size and not (pairs.min() >= 0 and pairs.max() < axes):         # (a cast would wrap them)
+                raise PagedKVError(PA_ERR_INVALID_ARG, f"pair_axis must lie in [0, {axes})")
+            pairs = pairs.astype(np.uint8)
+        pairs = pairs.tobytes()                                      # (ctypes passes its address)
         if len(pairs) != cos_sin.shape[1] // 2:
             raise PagedKVError(PA_ERR_INVALID_ARG, f"pair_axis has {len(pairs)} entries, not {cos_sin.shape[1] // 2}")
     _on_device(load().pa_rope_reshape_and_cache, key, stream,

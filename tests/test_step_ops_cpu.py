@@ -302,3 +302,17 @@ def test_outputs_over_inputs_are_refused(lib):
     assert extend(0, 1024, 4096) == small and extend(0, 4096 - 3 * 1024, 2048) == small
     assert extend(0, 1040, 2048) == bad and extend(0, 1008, 4096) == bad and extend(0, 1024, 1024) == bad
     assert extend(0, 3 * 1024, 512) == small and extend(3 * 1024, 0, 512) == small
+
+
+@pytest.mark.parametrize("bad", [256, -1, 3, -256])
+def test_axes_that_do_not_fit_a_byte_are_refused(bad):
+    """An axis of 256 is not axis 0."""
+    d = CacheDesc(4, 16, 2, 128, torch.float16)
+    kv = torch.zeros(3, 2, 128, dtype=torch.float16)
+    axes = np.zeros(64, np.int64)
+    axes[5] = bad
+    for pair_axis in (axes, axes.tolist(), torch.from_numpy(axes)):
+        with pytest.raises(_lib.PagedKVError) as e:
+            _lib.rope_reshape_and_cache(None, None, kv, d, kv, kv, torch.zeros(3, dtype=torch.int64), torch.zeros(3, 3, dtype=torch.int32),
+                                        torch.zeros(10, 128), pair_axis=pair_axis)
+        assert e.value.status == _lib.PA_ERR_INVALID_ARG
