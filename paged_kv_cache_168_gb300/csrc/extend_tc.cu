@@ -45,7 +45,7 @@
 //                   the copies: codes become exact 16-bit integers, and the
 //                   scales are applied in the softmax: K's to the scores, V's to
 //                   the weights, whose maximum is taken with the tile's largest V
-//                   scale, so that they stay at most 2^8 whatever the scales are.
+//                   scale, so that they stay at most 2^15 whatever the scales are.
 // Every wait is bounded; a timeout sets PA_DEVERR_TIMEOUT, the call's results are
 // then not to be used, and the CTA drains its own copies and products before
 // releasing TMEM.
@@ -83,6 +83,11 @@ using plan::kKv;
 using plan::kRows;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kRescaleThreshold = 8.f;   // base-2 units
+// 8-bit caches: weights (with V's scales) and their sums are 2^kLift times as large.
+// Stored in fp16 they reach 2^15 at most, and a token that holds nearly all of a
+// row's weight keeps 11 bits of it down to a V scale 2^-21 times its tile's largest
+// one (unlifted: 2^-14, and at 2^-21 its row was off by 6%).
+constexpr float kLift = 7.f;
 
 // Flags of a query tile and kv head.
 constexpr uint32_t kBadBlock = 1, kNonFinite = 2;
@@ -1347,9 +1352,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               }
             }
             // weights carry V's scales: what is kept at most 2^8 is 2^(x - m) times the
-            // tile's largest one (bounded below: sums stay finite)
+            // tile's largest one (bounded below: sums stay finite), and 2^kLift times that
+            // is stored
             float bias[2];
-            bias[0] = bias[1] = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-100f));
+            bias[0] = bias[1] = log2f(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 0x1p-93f));
             if (__builtin_expect(edge, 0)) {
               uint32_t on[2];
 #pragma unroll
@@ -1389,7 +1395,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                   for (int r = 0; r < 2; ++r) {
                     big[r] = fmaxf(big[r], __shfl_xor_sync(kFull, big[r], 1));
                     big[r] = fmaxf(big[r], __shfl_xor_sync(kFull, big[r], 2));
-                    bias[r] = log2f(fmaxf(big[r], 0x1p-100f));
+                    bias[r] = log2f(fmaxf(big[r], 0x1p-93f));
                   }
                 }
               }
@@ -1437,7 +1443,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             uint64_t nm[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float v = m4[r] == -INFINITY ? 0.f : -m4[r];
+              const float v = m4[r] == -INFINITY ? 0.f : kLift - m4[r];
               nm[r] = pack2f(v, v);
             }
 #pragma unroll

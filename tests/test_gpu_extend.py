@@ -510,3 +510,22 @@ def test_single_tokens_of_any_stride():
     q = u16_to_dev(case.q_bits, "bf16").transpose(0, 1).contiguous().transpose(0, 1)
     q = q.as_strided((1, 4, 128), (128, 128, 1))
     check(case, q=q)
+
+
+@pytest.mark.parametrize("small", [2.0 ** -16, 2.0 ** -21])
+@pytest.mark.parametrize("q_len,ctx", [(1, 200), (40, 300), (3, 5000)])
+def test_attended_tokens_with_small_value_scales(q_len, ctx, small):
+    """8-bit caches: nearly all weight falls on a token whose V is far smaller than its neighbours'.  The row is that
+    V: off by the output's rounding (2^-8), and its weight's -- stored at 2^7 times the ratio of the scales, which is at
+    least 2^-22 here: 2^-25 / 2^-15."""
+    rng = np.random.default_rng(92)
+    case = Chunk(rng, [q_len], [ctx], Hq=2, Hkv=1, D=128, bs=16, dtype="bf16", kv8=True)
+    c, at = case.cache, 130
+    case.q_bits[:] = case.q_bits[:1, :1]                             # one query direction
+    case.q = bits_to_f64(case.q_bits, "bf16")
+    slot = np.asarray([int(case.tables[0, at // 16]) * 16 + at % 16], np.int64)
+    v = np.sign(rng.standard_normal((1, 1, 128))) * rng.uniform(0.5, 4, (1, 1, 128)) * small
+    assert c.write(case.q_bits[:1, :1], step_ref.to_bits(v, "bf16"), slot) == 0
+    got = bits_to_f64(dev_to_u16(run(case, 1.0)), "bf16")            # scores 128 +- 23 and 0 +- 12
+    want = c.read(slot // 16, slot % 16, 1)[0, 0]
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -16) * np.abs(want)).all()
