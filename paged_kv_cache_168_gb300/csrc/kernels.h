@@ -172,7 +172,7 @@ struct RopeParams {
   uint32_t* dev_err;
   uint8_t pair_axis[kMaxPairs];
 };
-cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, cudaStream_t stream);
+cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, int sms, cudaStream_t stream);
 
 // Block tables, slot mapping and positions from request lengths.
 struct TablesParams {

@@ -405,7 +405,8 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
   p.num_tokens = num_tokens;
   p.dev_err = dev_err;
   if (pair_axis) memcpy(p.pair_axis, pair_axis, rotary_dim / 2);
-  cudaError_t e = pkv::launch_rope_cache(p, act_dtype(desc), is_i8(desc), static_cast<cudaStream_t>(stream));
+  cudaError_t e = pkv::launch_rope_cache(p, act_dtype(desc), is_i8(desc), device_sm_count(),
+                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope_reshape_and_cache launch");
 }
 

@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
 }
 
 template <typename T, int D, bool kI8, int kTokens>
-void launch_rounds(const RopeParams& p, cudaStream_t stream) {
+void launch_rounds(const RopeParams& p, int sms, cudaStream_t stream) {
   const int rounds = (p.num_tokens + kTokens - 1) / kTokens;
-  const unsigned grid = (unsigned)(rounds < 152 * 8 ? rounds : 152 * 8);
+  const unsigned grid = (unsigned)(rounds < sms * 8 ? rounds : sms * 8);
   if (p.interleaved)
     rope_cache_kernel<T, D, true, kI8, kTokens><<<grid, kThreads, 0, stream>>>(p);
   else
@@ -215,27 +215,27 @@ void launch_rounds(const RopeParams& p, cudaStream_t stream) {
 }
 
 template <typename T, int D, bool kI8>
-cudaError_t launch_pairs(const RopeParams& p, cudaStream_t stream) {
+cudaError_t launch_pairs(const RopeParams& p, int sms, cudaStream_t stream) {
   // One token a CTA as long as all CTAs run at once (four an SM), for latency: 256
   // tokens of 32 + 8 heads 3.8 us back to back in a graph against 5.9 with four a
-  // CTA, 608 4.8 against 6.0; but 2048 12.0 against 10.9, 4096 26.6 against 21.8.
-  if (p.num_tokens <= 152 * 4)
-    launch_rounds<T, D, kI8, 1>(p, stream);
+  // CTA, 608 (on 152 SMs) 4.8 against 6.0; but 2048 12.0 against 10.9, 4096 26.6 against 21.8.
+  if (p.num_tokens <= sms * 4)
+    launch_rounds<T, D, kI8, 1>(p, sms, stream);
   else
-    launch_rounds<T, D, kI8, 4>(p, stream);
+    launch_rounds<T, D, kI8, 4>(p, sms, stream);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_typed(const RopeParams& p, bool i8, cudaStream_t stream) {
-  if (i8) return launch_pairs<T, 128, true>(p, stream);
-  return p.head_size == 128 ? launch_pairs<T, 128, false>(p, stream) : launch_pairs<T, 64, false>(p, stream);
+cudaError_t launch_typed(const RopeParams& p, bool i8, int sms, cudaStream_t stream) {
+  if (i8) return launch_pairs<T, 128, true>(p, sms, stream);
+  return p.head_size == 128 ? launch_pairs<T, 128, false>(p, sms, stream) : launch_pairs<T, 64, false>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, cudaStream_t stream) {
-  return act_dtype == PA_F16 ? launch_typed<__half>(p, i8, stream) : launch_typed<__nv_bfloat16>(p, i8, stream);
+cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, int sms, cudaStream_t stream) {
+  return act_dtype == PA_F16 ? launch_typed<__half>(p, i8, sms, stream) : launch_typed<__nv_bfloat16>(p, i8, sms, stream);
 }
 
 }  // namespace pkv
