@@ -12,7 +12,7 @@
 //   parts of cut tiles (n_i > longest): ceil(n_i / longest) < 2 n_i / longest, in
 //     all at most 2 want / hkv; with hkv heads of at most tile_rows rows each, the
 //     partial results are at most 2 want tile_rows rows.
-// Both hold for any lengths, so nothing is cut off and no tile is refused its cut.
+// Both hold for any lengths, so no item is ever without room.
 #pragma once
 
 #include <stdint.h>
@@ -74,9 +74,20 @@ PKV_PLAN int64_t longest_part(int64_t work, int64_t tiles, int hkv, int sms) {
   return longest;
 }
 
-// Parts of a query tile that attends n KV tiles, and part `part` of them: `from`
-// on, that many (equal but for the last; none is empty when n > 0).
-PKV_PLAN int parts_of(int n, int64_t longest) { return n > longest ? (int)((n + longest - 1) / longest) : 1; }
+// Parts of a query tile that attends n KV tiles, of a sequence whose last query
+// tile attends n_last and whose tiles have seq_rows rows together (all heads).  A
+// sequence stays whole if its tiles, were all cut like the last, would leave more
+// partial rows than there is room for: it has tiles enough to keep the SMs busy, and
+// merging costs more than it gives (prompts, us, whole / cut: 4096 tokens of 32 + 8
+// heads 160 / 252, 8192 of 8 + 2 196 / 222; but 1483 tokens over 22277, 8 + 1 heads,
+// which are below the limit: 303 / 186).
+PKV_PLAN int parts_of(int n, int n_last, int64_t seq_rows, int64_t longest, int64_t row_room) {
+  if (n <= longest || (n_last + longest - 1) / longest * seq_rows > row_room) return 1;
+  return (int)((n + longest - 1) / longest);
+}
+
+// Part `part` of n KV tiles in `parts` parts: `from` on, that many (equal but for
+// the last; none is empty when n > 0).
 PKV_PLAN int part_range(int n, int parts, int part, int& from) {
   const int len = (n + parts - 1) / parts;
   from = part * len;

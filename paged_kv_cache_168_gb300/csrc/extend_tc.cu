@@ -224,6 +224,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t& 
 struct Tile {
   int seq, row0, pos0, npos, held;
   int tile0, n;                            // the KV tiles that it attends
+  int n_last;                              // those of the sequence's last query tile
+  int64_t seq_rows;                        // rows of the sequence's query tiles, all heads
 };
 
 // One CTA.  Three passes with a scan each: over sequences (thread t owns [t * per,
@@ -284,7 +286,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     t.held = q.held;
     t.n = plan::tile_range(t.pos0, t.npos, p.window, q.held, t.tile0);
     if (q.zero) t.n = 0;
+    const int nt = plan::tiles_of(q.q_len, pair), l0 = (nt - 1) * pair;
+    int unused;
+    t.n_last = plan::tile_range(q.ctx - q.q_len + l0, q.q_len - l0, p.window, q.held, unused);
+    t.seq_rows = (int64_t)nt * min(pair, q.q_len) * G * hkv;
     return t;
+  };
+  auto parts_of = [&](const Tile& t, int64_t longest) {
+    return plan::parts_of(t.n, t.n_last, t.seq_rows, longest, ws.max_rows);
   };
   Tile mine{};                                                // tile tid: most calls have no more
   int64_t work = 0, total;
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     int64_t add = 0, sum;
     if (i < tiles) {
       const Tile t = i0 == 0 ? mine : tile(i);
-      const int parts = plan::parts_of(t.n, longest);
+      const int parts = parts_of(t, longest);
       add = (int64_t)parts << 32 | (uint32_t)(parts > 1 ? parts * t.npos * G * hkv : 0);
     }
     const int64_t before = done + block_scan(add, tmp, sum);
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
     it.row0 = t.row0;
     it.pos0 = t.pos0;
     it.npos = t.npos;
-    it.parts = plan::parts_of(t.n, longest);
+    it.parts = parts_of(t, longest);
     int from;
     it.ntiles = plan::part_range(t.n, it.parts, part, from);
     it.tile0 = t.tile0 + from;
@@ -1786,16 +1795,19 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
     const Item& it = ws.items[item];
     if (r >= it.npos * G || (hd.any_flag && ws.flags[item * hkv + h])) continue;
     const int64_t first = it.part_row + (int64_t)h * it.head_rows + r;
+    const int rows = it.rows, parts = it.parts;
     float M = -INFINITY;
-    for (int k = lane; k < it.parts; k += 32) M = fmaxf(M, ws.ml[2 * (first + (int64_t)k * it.rows)]);
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, ws.ml[2 * (first + (int64_t)k * rows)]);
 #pragma unroll
     for (int i = 16; i; i >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, i));
     float l = 0.f, o[kDims] = {};
-    for (int k = 0; k < it.parts; ++k) {
-      const int64_t at = first + (int64_t)k * it.rows;
+    // (no branch: a part's loads need not wait for those of the part before)
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const int64_t at = first + (int64_t)k * rows;
       const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
-      if (ml.y == 0.f) continue;                                     // nothing attended in this part
-      const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);     // (-inf with a sum: NaN scores)
+      // nothing attended in this part: its o is zero; -inf with a sum: NaN scores
+      const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
       l = fmaf(ml.y, f, l);
 #pragma unroll
       for (int d = 0; d < kDims; ++d) o[d] = fmaf(ws.o[at * D + lane * kDims + d], f, o[d]);

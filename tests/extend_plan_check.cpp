@@ -24,7 +24,8 @@ static void check(const std::vector<Sequence>& seqs, int group, int hkv, int sms
   int64_t num_tokens = 0, tiles = 0, work = 0;
   int max_q = 0;
   struct T {
-    int tile0, n, npos, first, last;
+    int tile0, n, npos, first, last, n_last;
+    int64_t seq_rows;
   };
   std::vector<T> list;
   for (const Sequence& s : seqs) {
@@ -37,6 +38,9 @@ static void check(const std::vector<Sequence>& seqs, int group, int hkv, int sms
       t.npos = std::min(pair, s.q_len - i * pair);
       const int pos0 = s.ctx - s.q_len + i * pair;
       t.n = tile_range(pos0, t.npos, window, held, t.tile0);
+      int unused;
+      t.n_last = tile_range(s.ctx - s.q_len + (nt - 1) * pair, s.q_len - (nt - 1) * pair, window, held, unused);
+      t.seq_rows = (int64_t)nt * std::min(pair, s.q_len) * group * hkv;
       // the same from the definition: positions attended by any query of the tile
       t.first = INT32_MAX;
       t.last = -1;
@@ -52,10 +56,13 @@ static void check(const std::vector<Sequence>& seqs, int group, int hkv, int sms
     tiles += nt;
   }
   const int64_t longest = longest_part(work, tiles, hkv, sms);
+  const int tile_rows = std::min(max_q, pair) * group;
+  const int64_t room = max_items(max_tiles((int)num_tokens, (int)seqs.size(), pair), sms), row_room = max_rows(tile_rows, sms);
   int64_t items = 0, rows = 0;
   bool covered = tiles <= max_tiles((int)num_tokens, (int)seqs.size(), pair);
   for (const T& t : list) {
-    const int parts = parts_of(t.n, longest);
+    const int parts = parts_of(t.n, t.n_last, t.seq_rows, longest, (int64_t)1 << 60), chosen = parts_of(t.n, t.n_last, t.seq_rows, longest, row_room);
+    if (chosen != parts && chosen != 1) covered = false;     // cut as its length asks, or whole
     items += parts;
     if (parts > 1) rows += (int64_t)parts * t.npos * group * hkv;
     int at = 0;
@@ -70,8 +77,6 @@ static void check(const std::vector<Sequence>& seqs, int group, int hkv, int sms
     if (at != t.n) covered = false;
     if (t.last >= 0 && (t.first / kKv < t.tile0 || t.last / kKv != t.tile0 + t.n - 1)) covered = false;
   }
-  const int tile_rows = std::min(max_q, pair) * group;
-  const int64_t room = max_items(max_tiles((int)num_tokens, (int)seqs.size(), pair), sms), row_room = max_rows(tile_rows, sms);
   most_items = std::max(most_items, 1000 * (items - tiles) / (max_items(0, sms)));
   most_rows = std::max(most_rows, 1000 * rows / row_room);
   if (items > room || rows > row_room || !covered) {
