@@ -384,9 +384,13 @@ size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, in
  * ring_blocks > 0; the ring holds what the whole step leaves in it, so it must
  * have ceil((window + q_len - 1) / bs) + 1 blocks for every window to be exact).
  * A query with nothing to attend gets a zero row.  Softmax statistics and
- * outputs accumulate in fp32; weights enter the second product as 16-bit
- * values.  Contexts are split over SMs where a step has few rows, and the parts
- * merged by log-sum-exp; results do not depend on timing.
+ * outputs accumulate in fp32; weights enter the second product rounded once to
+ * the cache's 16-bit type (pa_prefill keeps two bf16 words of each: take it where
+ * the last bit of bf16 results matters).  With an 8-bit cache they are fp16 and
+ * carry V's scales: a token that holds nearly all of a row's weight loses bits if
+ * its V scale is below 2^-21 times the largest of its 128-token tile's.  Contexts
+ * are split over SMs where a step has few rows, and the parts merged by
+ * log-sum-exp; results do not depend on timing.
  *   out             device [num_tokens, num_q_heads, head_size], contiguous; may
  *                   not overlap q.
  *   q               device [num_tokens, num_q_heads, head_size]; token stride
@@ -398,7 +402,8 @@ size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, in
  *                   [0, num_tokens), or whose start is above its end, is
  *                   skipped with PA_DEVERR_CONTEXT.
  *   max_query_len   an upper bound of every q_len (sizes the workspace); a
- *                   longer sequence gets zero rows and PA_DEVERR_CONTEXT.
+ *                   longer sequence gets zero rows and PA_DEVERR_CONTEXT (0: no
+ *                   sequence has queries, nothing is launched).
  *   workspace       device, 16-byte aligned, >= pa_extend_workspace_bytes(...);
  *                   needs no initialisation, and is free again once the call's
  *                   work on the stream is done.

@@ -16,8 +16,8 @@
 //
 // Bound: launch latency and the chain lengths -> scan -> search -> store; the
 // bytes of a step would take 0.1 us.  Back to back in a graph: 256 decoding
-// requests 5.0 us, 2048 of them 7.0, 16 prompts of 1024 tokens 5.8 (one CTA
-// instead of eight: 5.0, 7.0, 11.9).
+// requests 5.0 us, 2048 of them 7.2, 16 prompts of 1024 or 2048 tokens 5.9 (one CTA
+// instead of eight: 5.0, 7.0, and 11.9 for the prompts of 1024).
 #include "common.cuh"
 #include "kernels.h"
 

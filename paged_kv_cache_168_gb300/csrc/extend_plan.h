@@ -60,9 +60,9 @@ PKV_PLAN int64_t max_rows(int tile_rows, int sms) { return 2 * (int64_t)kPartsPe
 // tiles together.  With K parts a SM the call takes about (work / sms) (1 + 1 / K)
 // -- the last round is half empty -- and K times an item's own cost, about 3 KV
 // tiles: least at K = sqrt(work / sms / 3).  32 + 8 heads, us, this rule / K = 1 /
-// K = 4: 4 tokens over 30000: 56 / 47 / 75; 4 x 4 over 8000: 50 / 58 / 61; 2 x 512
-// over 8000, 8 + 1 heads: 74 / 80 / 104; 8 x 4 over 32K to 128K, 64 + 8 heads: 544 /
-// 703 / 543.
+// K = 4: 4 tokens over 30000: 56 / 48 / 75; 4 x 4 over 8000: 51 / 59 / 61; 2 x 512
+// over 8000, 8 + 1 heads: 84 / 83 / 104; 8 x 4 over 32K to 128K, 64 + 8 heads: 543 /
+// 736 / 543.
 PKV_PLAN int64_t longest_part(int64_t work, int64_t tiles, int hkv, int sms) {
   const int64_t per_sm = work * hkv / sms;
   const int64_t want = (int64_t)(per_sm >= 48 ? kPartsPerSm : per_sm >= 27 ? 3 : per_sm >= 12 ? 2 : 1) * sms;
@@ -80,7 +80,7 @@ PKV_PLAN int64_t longest_part(int64_t work, int64_t tiles, int hkv, int sms) {
 // partial rows than there is room for: it has tiles enough to keep the SMs busy, and
 // merging costs more than it gives (prompts, us, whole / cut: 4096 tokens of 32 + 8
 // heads 160 / 252, 8192 of 8 + 2 196 / 222; but 1483 tokens over 22277, 8 + 1 heads,
-// which are below the limit: 303 / 186).
+// which are below the limit: 303 / 182).
 PKV_PLAN int parts_of(int n, int n_last, int64_t seq_rows, int64_t longest, int64_t row_room) {
   if (n <= longest || (n_last + longest - 1) / longest * seq_rows > row_room) return 1;
   return (int)((n + longest - 1) / longest);

@@ -9,7 +9,7 @@
 //                  workspace.  An item is up to two query tiles of 128 rows (row
 //                  = position * group + head) of one sequence, over its context
 //                  or a part of it; contexts are cut only where the whole call
-//                  has too few items for the SMs.
+//                  has too few items for the SMs (extend_plan.h).
 //   extend_kernel  one persistent CTA per SM draws (item, kv head) pairs from a
 //                  counter, a sequence's heads and tiles next to each other so
 //                  that its K and V are read from L2 while they are hot.
@@ -32,11 +32,13 @@
 //                   when a tile's exceeds it by more than 8 (a factor 256), and
 //                   only then is O rescaled in TMEM.  Statistics are fp32;
 //                   weights are rounded to the cache's 16-bit type (fp16 for an
-//                   8-bit cache), the sum takes them unrounded.
+//                   8-bit cache), the sum takes them unrounded.  (One 16-bit word a
+//                   weight: a second one would double the second product.  Errors
+//                   against 64 bits are up to 1.4 times those of 32-bit arithmetic.)
 //   warp 8          issues the products, in a fixed order that alternates between
 //                   the query tiles.
-//   warp 9          draws items, publishes them in a ring, and copies K tiles
-//                   (8-token groups, one bulk copy each) into the ring of K and V.
+//   warp 9          draws items, publishes them in a ring, and copies K tiles (a
+//                   lane a block, one tensor copy each) into the ring of K and V.
 //   warp 10         copies V tiles.
 //   warp 11         copies Q rows (positions x heads of the kv head) into the
 //                   swizzled K-major operand.
@@ -53,12 +55,13 @@
 // What bounds it.  A pair of query tiles and one KV tile are four batches of eight
 // products, 2048 clocks at the tensor cores' rate.  Measured: 16 prompts of 2048
 // tokens, 32 + 8 heads of 128 in bf16: 570 us, 0.96 PFLOP/s; 32 chunks of 512 over 512
-// to 3584: 546 us, 1.18 PFLOP/s; 3200 clocks a pair and KV tile, and 5000 to 9000
+// to 3584: 546 us, 1.18 PFLOP/s (heads of 64, half of the products against the same
+// softmax a tile: 552 and 503 us); 3200 clocks a pair and KV tile, and 5000 to 9000
 // around the end of an item: the chain scores - softmax - second product of a query
 // tile (TMEM has room for two), whose every hand-over costs some 300 clocks, because
 // shared memory answers slowly while products read their operands from it.  8 x 4
 // tokens over 32K to 128K: 545 us, 6.1 TB/s, bound by HBM.  8-bit caches: 32 chunks of
-// up to 700 tokens 755 us, 0.55 PFLOP/s, 6000 clocks a pair and KV tile, 3500 of them
+// up to 700 tokens 750 us, 0.55 PFLOP/s, 6000 clocks a pair and KV tile, 3500 of them
 // softmax (two scales a score; the converters next to it slow both down; with eight
 // converter warps, whose registers come from the softmax, 884 us).  A warpgroup of its
 // own for the results took 637 us instead of 593 on the prompts; two issuing warps,
