@@ -290,18 +290,18 @@ def test_outputs_over_inputs_are_refused(lib):
         return r, lib.pa_last_error_message()
     # rows 4096 bytes apart: q_out over value's part, over key's, over the next row's key; 2048 bytes apart and in
     # place: over key; over half of q
-    for args in ((0, 1536, 1024, 2048, 2048), (0, 1024, 1920, 3072, 2048), (512, 3584, 256, 2048, 2048), (0, 0, 512, 1536, 1024),
-                 (0, 512, 2048, 3072, 2048)):
+    for args in ((0, 1536, 1024, 2048, 2048), (0, 1024, 1920, 3584, 2048), (512, 3584, 256, 2048, 2048), (0, 0, 512, 1536, 1024),
+                 (0, 512, 2048, 3584, 2048)):
         r, msg = rope(*args)
         assert r == bad and b"overlap" in msg, (args, msg)
 
-    def extend(q, out, stride, T=3):
-        return lib.pa_extend(V(A + out), V(A + q), stride, V(), _desc(), 0, V(), 8, V(), V(), 2, T, 4, 100, 0.1, 0, 0, V(), 0, None, None)
+    def extend(q, out, stride):
+        return lib.pa_extend(V(A + out), V(A + q), stride, V(), _desc(), 0, V(), 8, V(), V(), 2, 2, 4, 100, 0.1, 0, 0, V(), 0, None, None)
     small = _lib.PA_ERR_WORKSPACE_TOO_SMALL                                  # (checked after the overlap)
-    # rows of 1024 bytes: out (three of them, dense) between q's rows, or over one
-    assert extend(0, 1024, 4096) == small and extend(0, 4096 - 3 * 1024, 2048) == small
-    assert extend(0, 1040, 2048) == bad and extend(0, 1008, 4096) == bad and extend(0, 1024, 1024) == bad
-    assert extend(0, 3 * 1024, 512) == small and extend(3 * 1024, 0, 512) == small
+    # two rows of 1024 bytes: out (dense) between q's rows, over one, behind and before both
+    assert extend(0, 1024, 4096) == small and extend(0, 2048, 2048) == small
+    assert extend(0, 2064, 2048) == bad and extend(0, 1008, 4096) == bad and extend(0, 1024, 512) == bad
+    assert extend(0, 2048, 512) == small and extend(2048, 0, 512) == small
 
 
 @pytest.mark.parametrize("bad", [256, -1, 3, -256])
