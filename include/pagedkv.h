@@ -29,9 +29,13 @@
  *                         Manager and Model Runner: block table + slot_mapping).
  *   pa_rope_reshape_and_cache  rotary positions on q and k (one or several
  *                         position axes), fused with the cache write.
+ *   pa_norm_rope_reshape_and_cache  the same after a norm of each q and k vector.
  *   pa_extend             pa_prefill's attention over every cache: 8-bit
  *                         caches, windows and ring tables, small blocks, any
  *                         group up to 16, few rows over long contexts.
+ *   pa_extend_scored, pa_decode_scored  attention of chunks and of single tokens
+ *                         with capped scores, scores that fall with distance, and
+ *                         a span of positions for each query.
  *   pa_swap_blocks        whole-block moves between the GPU cache and a pinned
  *                         CPU cache ("vLLM" page, section "CacheEngine":
  *                         swap_in = CPU->GPU, swap_out = GPU->CPU; section
@@ -220,6 +224,31 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
                                     int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
                                     int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
                                     int32_t interleaved, int32_t num_tokens, uint32_t* dev_err, void* stream);
+
+/* pa_rope_reshape_and_cache after a norm of each query and key vector: layers
+ * that norm q and k head by head before they rotate them.  A head vector x of q
+ * (of key) becomes
+ *   n = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ * first, in fp32 from the 16-bit values (the mean over head_size dims, summed in
+ * fp32; bf16 vectors whose squares leave fp32 are scaled down before), and n is
+ * rotated without being rounded in between; dims from rotary_dim on are normed
+ * alone.  v is not normed.  A vector that holds infinities or NaN gives NaN in
+ * some or all of its dims.
+ *   q_weight, k_weight  device [head_size], 16-bit as q; 2-byte aligned; NULL: no
+ *                  weights (n = x / sqrt(...), whatever weight_offset is).
+ *   weight_offset  added to every weight in fp32 (1 for weights stored around 0).
+ *   eps            positive and finite.
+ * Other arguments and errors as pa_rope_reshape_and_cache. */
+pa_status pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, const void* q,
+                                         int64_t q_token_stride, int32_t num_q_heads, void* kv_cache,
+                                         const pa_cache_desc* desc, int32_t layer, const void* key,
+                                         int64_t key_token_stride, const void* value, int64_t value_token_stride,
+                                         const int64_t* slot_mapping, const int32_t* positions,
+                                         int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
+                                         int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
+                                         int32_t interleaved, const void* q_weight, const void* k_weight,
+                                         float weight_offset, float eps, int32_t num_tokens, uint32_t* dev_err,
+                                         void* stream);
 
 /* Block tables, slot mapping and positions of one step, built on the GPU from
  * the requests' lengths: the KV manager's and model runner's bookkeeping
@@ -430,6 +459,54 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
                             const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                             int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, void* workspace,
                             size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* Attention whose scores are shaped before the softmax, for models that cap
+ * their scores, lower them with distance, or mask by document or prefix.  For a
+ * query at position p and an attended position t
+ *   s = scale * q . K_t
+ *   s = softcap * tanh(s / softcap)          (softcap > 0)
+ *   s = s - slopes[h] * |p - t|              (slopes given; after the cap)
+ * and query token i (row i of q) attends the positions
+ *   from  max(first_pos[i], 0, p - window + 1, what a ring still holds)
+ *   to    min(last_pos[i], ctx - 1)  (p itself where last_pos is NULL)
+ * (the window only with window > 0).  A document mask is first_pos = the start of
+ * the document; a prefix that sees itself whole is last_pos = max(p, its last
+ * position).  A query whose span is empty gets a zero row.
+ *   softcap     0 (none) or in [1e-4, 1e6]; a capped score is off by at most 2^-20
+ *               of it, as the sums are in fp32.
+ *   slopes      device fp32 [num_q_heads], finite, any sign; NULL: none.
+ *   first_pos, last_pos  device int32 [num_tokens]; NULL: 0 and p.  Any values:
+ *               they are clamped to the positions that exist.  Positions behind p
+ *               have to be in the cache (the whole chunk is).
+ * Other arguments, errors and supported shapes as pa_extend_strided; with the
+ * workspace of pa_extend_scored_workspace_bytes. */
+pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, const void* kv_cache,
+                           const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                           int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                           const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                           int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, float softcap,
+                           const float* slopes, const int32_t* first_pos, const int32_t* last_pos, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* Workspace bytes of pa_extend_scored, as pa_extend_workspace_bytes. */
+size_t pa_extend_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                        int32_t num_q_heads, int32_t max_query_len);
+
+/* pa_extend_scored for one query token per sequence, its newest (p = ctx - 1):
+ * what pa_decode_window is to pa_extend.  q and out hold a row a sequence,
+ * first_pos an entry a sequence.  ctx <= 0 gives a zero row; a context longer than
+ * max_context_len or than its table row gives one and PA_DEVERR_CONTEXT.  Every
+ * cache, and 1 to 16 query heads per kv head. */
+pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const void* kv_cache,
+                           const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                           int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                           int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale, int32_t window,
+                           int32_t ring_blocks, float softcap, const float* slopes, const int32_t* first_pos,
+                           void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream);
+
+/* Workspace bytes of pa_decode_scored (0: nothing to do, or shapes it refuses). */
+size_t pa_decode_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t max_context_len);
 
 /* Paged decode where groups of sequences share the first tokens of their
  * context physically: beams of one prompt, or parallel samples, whose prompt

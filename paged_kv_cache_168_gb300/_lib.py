@@ -29,8 +29,10 @@ EXPORTED = [
     "pa_cache_bytes", "pa_cache_element_offset", "pa_cache_scale_offset", "pa_reshape_and_cache", "pa_decode_workspace_bytes",
     "pa_decode_partition_size", "pa_decode", "pa_decode_window", "pa_decode_window_span", "pa_prefill",
     "pa_decode_static_workspace", "pa_decode_shared_prefix", "pa_decode_shared_prefix_partition_size",
-    "pa_decode_shared_prefix_workspace_bytes", "pa_rope_reshape_and_cache", "pa_build_tables",
+    "pa_decode_shared_prefix_workspace_bytes", "pa_rope_reshape_and_cache", "pa_norm_rope_reshape_and_cache",
+    "pa_build_tables",
     "pa_build_tables_strided", "pa_extend", "pa_extend_strided", "pa_extend_workspace_bytes",
+    "pa_extend_scored", "pa_extend_scored_workspace_bytes", "pa_decode_scored", "pa_decode_scored_workspace_bytes",
     "pa_copy_blocks", "pa_swap_blocks", "pa_read_device_errors",
     "pa_status_string", "pa_last_error_message",
     "pa_bm_create", "pa_bm_destroy", "pa_bm_can_allocate", "pa_bm_allocate", "pa_bm_append_slot", "pa_bm_fork",
@@ -143,6 +145,9 @@ def load():
     lib.pa_rope_reshape_and_cache.argtypes = [P, i64, P, i64, i32, P, D, i32, P, i64, P, i64, P, P, i64, P, i32, i32,
                                               P, i32, i32, i32, P, P]
     lib.pa_rope_reshape_and_cache.restype = ctypes.c_int
+    lib.pa_norm_rope_reshape_and_cache.argtypes = [P, i64, P, i64, i32, P, D, i32, P, i64, P, i64, P, P, i64, P, i32,
+                                                   i32, P, i32, i32, P, P, ctypes.c_float, ctypes.c_float, i32, P, P]
+    lib.pa_norm_rope_reshape_and_cache.restype = ctypes.c_int
     lib.pa_build_tables.argtypes = [P, P, P, P, P, i32, P, P, P, D, P, P, i32, i32, i32, P, P]
     lib.pa_build_tables.restype = ctypes.c_int
     lib.pa_extend.argtypes = [P, P, i64, P, D, i32, P, i32, P, P, i32, i32, i32, i32, ctypes.c_float, i32, i32, P, sz,
@@ -155,6 +160,16 @@ def load():
     lib.pa_extend_strided.restype = ctypes.c_int
     lib.pa_extend_workspace_bytes.argtypes = [D, i32, i32, i32, i32]
     lib.pa_extend_workspace_bytes.restype = sz
+    lib.pa_extend_scored.argtypes = [P, P, i64, P, D, i32, P, i64, i32, P, P, i32, i32, i32, i32, ctypes.c_float, i32,
+                                     i32, ctypes.c_float, P, P, P, P, sz, P, P]
+    lib.pa_extend_scored.restype = ctypes.c_int
+    lib.pa_extend_scored_workspace_bytes.argtypes = [D, i32, i32, i32, i32]
+    lib.pa_extend_scored_workspace_bytes.restype = sz
+    lib.pa_decode_scored.argtypes = [P, P, i64, P, D, i32, P, i64, i32, P, i32, i32, i32, ctypes.c_float, i32, i32,
+                                     ctypes.c_float, P, P, P, sz, P, P]
+    lib.pa_decode_scored.restype = ctypes.c_int
+    lib.pa_decode_scored_workspace_bytes.argtypes = [D, i32, i32, i32]
+    lib.pa_decode_scored_workspace_bytes.restype = sz
     lib.pa_copy_blocks.argtypes = [P, D, P, i32, P]
     lib.pa_copy_blocks.restype = ctypes.c_int
     lib.pa_swap_blocks.argtypes = [P, D, P, D, i32, P, i32, P]
@@ -367,13 +382,8 @@ def _on_device(fn, tensor, stream, *args):
         _check(status)
 
 
-def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, kv_cache: torch.Tensor,
-                           desc: CacheDesc, key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor,
-                           positions: torch.Tensor, cos_sin: torch.Tensor, pair_axis=None, interleaved: bool = False,
-                           layer: int = 0, dev_err: torch.Tensor | None = None, stream=None) -> None:
-    """pa_rope_reshape_and_cache: q/q_out [N, Hq, D] (or None), key/value [N, Hkv, D], positions int32 [N] or
-    [axes, N], cos_sin fp32 [max_position, rotary_dim]; pair_axis uint8 per rotary pair on the host (None: all
-    on axis 0)."""
+def _rope_args(q_out, q, kv_cache, desc, key, value, slot_mapping, positions, cos_sin, pair_axis, interleaved, layer):
+    """Checked arguments of pa_rope_reshape_and_cache up to interleaved."""
     n, dt, kv_shape = key.shape[0], desc.dtype, (key.shape[0], desc.num_kv_heads, desc.head_size)
     axes = positions.shape[0] if positions.dim() == 2 else 1
     if not (key.dtype is dt and value.dtype is dt and slot_mapping.dtype is torch.int64
@@ -403,12 +413,41 @@ def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, k
         pairs = pairs.tobytes()                                      # (ctypes passes its address)
         if len(pairs) != cos_sin.shape[1] // 2:
             raise PagedKVError(PA_ERR_INVALID_ARG, f"pair_axis has {len(pairs)} entries, not {cos_sin.shape[1] // 2}")
+    return (None if q is None else q_out.data_ptr(), out_pitch, None if q is None else q.data_ptr(), q_pitch, hq,
+            kv_cache.data_ptr(), desc.ref(), layer, key.data_ptr(), key_pitch, value.data_ptr(), value_pitch,
+            slot_mapping.data_ptr(), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
+            cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], pairs, axes, 1 if interleaved else 0)
+
+
+def rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, kv_cache: torch.Tensor,
+                           desc: CacheDesc, key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor,
+                           positions: torch.Tensor, cos_sin: torch.Tensor, pair_axis=None, interleaved: bool = False,
+                           layer: int = 0, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """pa_rope_reshape_and_cache: q/q_out [N, Hq, D] (or None), key/value [N, Hkv, D], positions int32 [N] or
+    [axes, N], cos_sin fp32 [max_position, rotary_dim]; pair_axis uint8 per rotary pair on the host (None: all
+    on axis 0)."""
     _on_device(load().pa_rope_reshape_and_cache, key, stream,
-               None if q is None else q_out.data_ptr(), out_pitch, None if q is None else q.data_ptr(), q_pitch, hq,
-               kv_cache.data_ptr(), desc.ref(), layer, key.data_ptr(), key_pitch, value.data_ptr(), value_pitch,
-               slot_mapping.data_ptr(), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
-               cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], pairs, axes,
-               1 if interleaved else 0, n, None if dev_err is None else dev_err.data_ptr())
+               *_rope_args(q_out, q, kv_cache, desc, key, value, slot_mapping, positions, cos_sin, pair_axis,
+                           interleaved, layer), key.shape[0], None if dev_err is None else dev_err.data_ptr())
+
+
+def norm_rope_reshape_and_cache(q_out: torch.Tensor | None, q: torch.Tensor | None, kv_cache: torch.Tensor,
+                                desc: CacheDesc, key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Tensor,
+                                positions: torch.Tensor, cos_sin: torch.Tensor, q_weight: torch.Tensor | None,
+                                k_weight: torch.Tensor | None, eps: float, weight_offset: float = 0.0, pair_axis=None,
+                                interleaved: bool = False, layer: int = 0, dev_err: torch.Tensor | None = None,
+                                stream=None) -> None:
+    """pa_norm_rope_reshape_and_cache: rope_reshape_and_cache after x / sqrt(mean(x^2) + eps) * (weight +
+    weight_offset) of every q and key vector; q_weight, k_weight [D] of the activations' type (None: no weights)."""
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and not (w.dtype is desc.dtype and w.shape == (desc.head_size,) and w.is_contiguous()):
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must be {desc.dtype} [{desc.head_size}], contiguous, not "
+                                                   f"{w.dtype} {list(w.shape)} with strides {w.stride()}")
+    _on_device(load().pa_norm_rope_reshape_and_cache, key, stream,
+               *_rope_args(q_out, q, kv_cache, desc, key, value, slot_mapping, positions, cos_sin, pair_axis,
+                           interleaved, layer), None if q_weight is None else q_weight.data_ptr(),
+               None if k_weight is None else k_weight.data_ptr(), weight_offset, eps, key.shape[0],
+               None if dev_err is None else dev_err.data_ptr())
 
 
 def build_tables(query_start_loc: torch.Tensor, context_lens: torch.Tensor, slot_mapping: torch.Tensor,
@@ -479,6 +518,80 @@ def extend(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: Cac
                None if workspace is None else workspace.data_ptr(),
                0 if workspace is None else workspace.numel() * workspace.element_size(),
                None if dev_err is None else dev_err.data_ptr())
+
+
+def extend_scored_workspace_bytes(desc: CacheDesc, num_seqs: int, num_tokens: int, num_q_heads: int,
+                                  max_query_len: int) -> int:
+    return load().pa_extend_scored_workspace_bytes(ctypes.byref(desc.c()), num_seqs, num_tokens, num_q_heads,
+                                                   max_query_len)
+
+
+def decode_scored_workspace_bytes(desc: CacheDesc, num_seqs: int, num_q_heads: int, max_context_len: int) -> int:
+    return load().pa_decode_scored_workspace_bytes(ctypes.byref(desc.c()), num_seqs, num_q_heads, max_context_len)
+
+
+def _scored_args(out, q, desc, block_tables, context_lens, query_start_loc, slopes, first_pos, last_pos):
+    """Checks of extend_scored and decode_scored (query_start_loc None): the stride of q's rows, of the table's, and the
+    table's width."""
+    S, (T, Hq, _), dt, i32 = context_lens.shape[0], q.shape, desc.dtype, torch.int32
+    if not (q.dtype is dt and out.dtype is dt and block_tables.dtype is i32 and context_lens.dtype is i32
+            and (query_start_loc is None or query_start_loc.dtype is i32)
+            and (slopes is None or slopes.dtype is torch.float32)
+            and (first_pos is None or first_pos.dtype is i32) and (last_pos is None or last_pos.dtype is i32)):
+        _tensors(dt, out=out, q=q)
+        _tensors(i32, block_tables=block_tables, context_lens=context_lens, query_start_loc=query_start_loc,
+                 first_pos=first_pos, last_pos=last_pos)
+        _tensors(torch.float32, slopes=slopes)
+    q_pitch = _rows(q, (T, Hq, desc.head_size), "q")
+    (rows, width), (pitch, step) = block_tables.shape, block_tables.stride()
+    if S <= 1:
+        pitch = width or 1
+    if (out.shape != q.shape or rows < S or (width > 1 and step != 1)
+            or not (out.is_contiguous() and context_lens.is_contiguous())
+            or (T != S if query_start_loc is None else
+                not (query_start_loc.numel() >= S + 1 and query_start_loc.is_contiguous()))):
+        raise PagedKVError(PA_ERR_INVALID_ARG, "out must be contiguous and of q's shape, query_start_loc and "
+                                               "block_tables long enough, table rows dense, and where every sequence "
+                                               "has one token q must have a row for each")
+    for name, t, n in (("slopes", slopes, Hq), ("first_pos", first_pos, T), ("last_pos", last_pos, T)):
+        if t is not None and not (t.shape == (n,) and t.is_contiguous()):
+            raise PagedKVError(PA_ERR_INVALID_ARG, f"{name} must have {n} contiguous entries, not {list(t.shape)}")
+    return q_pitch, pitch, min(width, pitch)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def extend_scored(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: CacheDesc,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                  max_query_len: int, scale: float, workspace: torch.Tensor | None, softcap: float = 0.0,
+                  slopes: torch.Tensor | None = None, first_pos: torch.Tensor | None = None,
+                  last_pos: torch.Tensor | None = None, window: int = 0, ring_blocks: int = 0, layer: int = 0,
+                  dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """pa_extend_scored: extend with scores softcap * tanh(s / softcap), less slopes[h] (fp32 [Hq]) * |distance|, query
+    token i attending positions first_pos[i] .. last_pos[i] (int32 [T]; None: 0 and its own position)."""
+    q_pitch, pitch, width = _scored_args(out, q, desc, block_tables, context_lens, query_start_loc, slopes, first_pos,
+                                         last_pos)
+    _on_device(load().pa_extend_scored, q, stream, out.data_ptr(), q.data_ptr(), q_pitch, kv_cache.data_ptr(),
+               desc.ref(), layer, block_tables.data_ptr(), pitch, width, context_lens.data_ptr(),
+               query_start_loc.data_ptr(), context_lens.shape[0], q.shape[0], q.shape[1], max_query_len, scale, window,
+               ring_blocks, softcap, _at(slopes), _at(first_pos), _at(last_pos), _at(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(), _at(dev_err))
+
+
+def decode_scored(out: torch.Tensor, q: torch.Tensor, kv_cache: torch.Tensor, desc: CacheDesc,
+                  block_tables: torch.Tensor, context_lens: torch.Tensor, max_context_len: int, scale: float,
+                  workspace: torch.Tensor | None, softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                  first_pos: torch.Tensor | None = None, window: int = 0, ring_blocks: int = 0, layer: int = 0,
+                  dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """pa_decode_scored: extend_scored for one token per sequence; out/q [S, Hq, D], first_pos int32 [S]."""
+    q_pitch, pitch, width = _scored_args(out, q, desc, block_tables, context_lens, None, slopes, first_pos, None)
+    _on_device(load().pa_decode_scored, q, stream, out.data_ptr(), q.data_ptr(), q_pitch, kv_cache.data_ptr(),
+               desc.ref(), layer, block_tables.data_ptr(), pitch, width, context_lens.data_ptr(),
+               q.shape[0], q.shape[1], max_context_len, scale, window, ring_blocks, softcap, _at(slopes),
+               _at(first_pos), _at(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(), _at(dev_err))
 
 
 def decode_window_span(max_context_len: int, block_size: int, window: int, ring_blocks: int = 0) -> int:

@@ -171,8 +171,14 @@ struct RopeParams {
   int32_t num_tokens;
   uint32_t* dev_err;
   uint8_t pair_axis[kMaxPairs];
+  const void* q_weight;           // launch_norm_rope_cache alone: [head_size] act dtype, null: ones
+  const void* k_weight;
+  float weight_offset;
+  float eps;
 };
 cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, int sms, cudaStream_t stream);
+// The same after a norm of each q and k vector.
+cudaError_t launch_norm_rope_cache(const RopeParams& p, int act_dtype, bool i8, int sms, cudaStream_t stream);
 
 // Block tables, slot mapping and positions from request lengths.
 struct TablesParams {
@@ -220,12 +226,25 @@ struct ExtendParams {
   int32_t ring_blocks;
   float scale_log2;
   uint32_t* dev_err;
+  // launch_extend_scored alone (there query_start_loc may be null: one token a sequence)
+  const float* slopes;            // [Hq] or null
+  const int32_t* first_pos;       // [num_tokens] or null
+  const int32_t* last_pos;
+  int32_t max_context;            // longer contexts are refused
+  int32_t capped;                 // set_cap's
+  float cap_in, cap_log2;         // scale / cap, cap * log2(e)
+  float cap_poly[6];
 };
 // Workspace bytes, and the launches (planner, attention, finish) on a device of `sms` SMs.
 size_t extend_workspace(int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len, int head_size,
-                        int sms);
+                        int sms, bool scored);
 cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                           cudaStream_t stream);
+
+// The same with shaped scores.
+void set_cap(ExtendParams& p, float scale, float softcap);
+cudaError_t launch_extend_scored(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                                 cudaStream_t stream);
 
 // Paged decode over an 8-bit cache on CUDA cores: head_size 128, group 1/2/4/8;
 // q / out in act_dtype.  Launches the decode kernel and the merge.

@@ -1,6 +1,7 @@
 // pagedkv_api.cu -- the C ABI: argument validation on the host, then kernel
 // dispatch on the caller's stream.  No memory is allocated and no state is kept
 // between calls (the per-thread error message aside).
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -211,6 +212,183 @@ pa_status run_pairs(uint8_t* dst, int64_t dst_ls, const uint8_t* src, int64_t sr
   return PA_OK;
 }
 
+// The checks of pa_rope_reshape_and_cache's arguments, and its launch parameters (filled where there are tokens).
+pa_status rope_params(pkv::RopeParams& p, void* q_out, int64_t q_out_token_stride, const void* q,
+                      int64_t q_token_stride, int32_t num_q_heads, void* kv_cache, const pa_cache_desc* desc,
+                      int32_t layer, const void* key, int64_t key_token_stride, const void* value,
+                      int64_t value_token_stride, const int64_t* slot_mapping, const int32_t* positions,
+                      int64_t positions_axis_stride, const float* cos_sin, int32_t max_position, int32_t rotary_dim,
+                      const uint8_t* pair_axis, int32_t num_axes, int32_t interleaved, int32_t num_tokens,
+                      uint32_t* dev_err) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (num_q_heads < 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
+  if (rotary_dim < 16 || rotary_dim > desc->head_size || rotary_dim % 16)
+    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d must be a multiple of 16 in [16, head_size %d]", rotary_dim,
+                desc->head_size);
+  if (num_axes < 1 || num_axes > 4) return fail(PA_ERR_INVALID_ARG, "num_axes %d not in [1, 4]", num_axes);
+  if (max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position %d", max_position);
+  if (pair_axis)
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      if (pair_axis[i] >= num_axes)
+        return fail(PA_ERR_INVALID_ARG, "pair_axis[%d] = %d with num_axes %d", i, pair_axis[i], num_axes);
+  if (num_tokens == 0) return PA_OK;
+  if (!kv_cache || !key || !value || !slot_mapping || !positions || !cos_sin)
+    return fail(PA_ERR_INVALID_ARG, "kv_cache, key, value, slot_mapping, positions and cos_sin must be non-NULL");
+  if (!aligned16(kv_cache) || !aligned16(key) || !aligned16(value))
+    return fail(PA_ERR_INVALID_ARG, "kv_cache, key and value must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7) || (reinterpret_cast<uintptr_t>(positions) & 3) ||
+      (reinterpret_cast<uintptr_t>(cos_sin) & 3))
+    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned, positions and cos_sin 4-byte aligned");
+  if (positions_axis_stride < 0 || (num_axes > 1 && positions_axis_stride > 0 && positions_axis_stride < num_tokens))
+    return fail(PA_ERR_INVALID_ARG, "positions_axis_stride %lld must be 0 or >= num_tokens",
+                (long long)positions_axis_stride);
+  const int64_t row = (int64_t)desc->num_kv_heads * desc->head_size;
+  if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 || value_token_stride % 8)
+    return fail(PA_ERR_INVALID_ARG, "token strides must be >= num_kv_heads*head_size and multiples of 8");
+  if (num_q_heads > 0) {
+    const int64_t qrow = (int64_t)num_q_heads * desc->head_size;
+    if (!q || !q_out || !aligned16(q) || !aligned16(q_out))
+      return fail(PA_ERR_INVALID_ARG, "q and q_out must be non-NULL and 16-byte aligned");
+    if (q_token_stride < qrow || q_out_token_stride < qrow || q_token_stride % 8 || q_out_token_stride % 8)
+      return fail(PA_ERR_INVALID_ARG, "q strides must be >= num_q_heads*head_size and multiples of 8");
+    // a row is read and written by one block, so q_out's rows may share memory only with their own
+    const pkv::Rows out = token_rows(q_out, num_tokens, q_out_token_stride, qrow);
+    if (!(q == q_out && (q_token_stride == q_out_token_stride || num_tokens == 1)) &&
+        pkv::rows_overlap(out, token_rows(q, num_tokens, q_token_stride, qrow)))
+      return fail(PA_ERR_INVALID_ARG, "q_out must be q itself (with the same stride) or not overlap it");
+    if (pkv::rows_overlap(out, token_rows(key, num_tokens, key_token_stride, row)) ||
+        pkv::rows_overlap(out, token_rows(value, num_tokens, value_token_stride, row)))
+      return fail(PA_ERR_INVALID_ARG, "q_out must not overlap key or value");
+  }
+  p.q_out = q_out;
+  p.q_out_stride = q_out_token_stride;
+  p.q = q;
+  p.q_stride = q_token_stride;
+  p.num_q_heads = num_q_heads;
+  p.cache = static_cast<uint8_t*>(kv_cache) + layer * layer_stride(desc);
+  p.num_blocks = desc->num_blocks;
+  p.block_size = desc->block_size;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.head_size = desc->head_size;
+  p.key = key;
+  p.key_stride = key_token_stride;
+  p.value = value;
+  p.value_stride = value_token_stride;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.axis_stride = positions_axis_stride;
+  p.num_axes = num_axes;
+  p.cos_sin = cos_sin;
+  p.max_position = max_position;
+  p.rotary_dim = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.num_tokens = num_tokens;
+  p.dev_err = dev_err;
+  if (pair_axis) memcpy(p.pair_axis, pair_axis, rotary_dim / 2);
+  return PA_OK;
+}
+
+// Workspace of pa_extend, or (scored) of the calls with shaped scores.
+size_t extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                              int32_t max_query_len, bool scored) {
+  if (!desc || num_seqs <= 0 || num_tokens <= 0 || max_query_len <= 0 || num_q_heads <= 0) return 0;
+  if (check_desc(desc) != PA_OK || num_q_heads % desc->num_kv_heads) return 0;
+  const int group = num_q_heads / desc->num_kv_heads;
+  if (group > 16) return 0;
+  return pkv::extend_workspace(num_seqs, num_tokens, desc->num_kv_heads, group, max_query_len, desc->head_size,
+                               device_sm_count(), scored);
+}
+
+// The checks of pa_extend_strided's arguments (scored: of the calls with shaped scores; single: one token a sequence,
+// no query_start_loc), and its launch parameters; *empty: nothing to launch.
+pa_status extend_params(pkv::ExtendParams& p, bool scored, bool single, bool* empty, void* out, const void* q,
+                        int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc, int32_t layer,
+                        const int32_t* block_tables, int64_t block_table_stride, int32_t block_table_width,
+                        const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                        int32_t num_tokens, int32_t num_q_heads, int32_t max_query_len, float scale, int32_t window,
+                        int32_t ring_blocks, void* workspace, size_t workspace_bytes, uint32_t* dev_err) {
+  pa_status st = check_desc(desc);
+  if (st != PA_OK) return st;
+  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
+  if (num_seqs < 0 || num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_seqs %d not in [0, 65535]", num_seqs);
+  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
+  if (max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "max_query_len %d < 0", max_query_len);
+  if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads)
+    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d",
+                num_q_heads, desc->num_kv_heads);
+  const int group = num_q_heads / desc->num_kv_heads;
+  if (group > 16) return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d (supported: 1 to 16)", group);
+  if (desc->num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads > 65535");
+  if (window < 0) return fail(PA_ERR_INVALID_ARG, "window %d < 0", window);
+  if (!(scale > 0.f) || scale != scale) return fail(PA_ERR_INVALID_ARG, "scale must be a positive number");
+  *empty = num_seqs == 0 || num_tokens == 0 || max_query_len == 0;
+  if (*empty) return PA_OK;
+  if (!out || !q || !kv_cache || !block_tables || !context_lens || !(single || query_start_loc))
+    return fail(PA_ERR_INVALID_ARG, "out, q, kv_cache, block_tables, context_lens%s must be non-NULL",
+                single ? "" : " and query_start_loc");
+  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache))
+    return fail(PA_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(block_tables) & 3) || (reinterpret_cast<uintptr_t>(context_lens) & 3) ||
+      (reinterpret_cast<uintptr_t>(query_start_loc) & 3))
+    return fail(PA_ERR_INVALID_ARG, "block_tables, context_lens and query_start_loc must be 4-byte aligned");
+  if (q_token_stride < (int64_t)num_q_heads * desc->head_size || q_token_stride % 8)
+    return fail(PA_ERR_INVALID_ARG, "q_token_stride must be >= num_q_heads*head_size and a multiple of 8");
+  const int64_t row = (int64_t)num_q_heads * desc->head_size;
+  if (pkv::rows_overlap(token_rows(out, num_tokens, row, row), token_rows(q, num_tokens, q_token_stride, row)))
+    return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
+  if (check_rows(block_table_stride, block_table_width) != PA_OK) return PA_ERR_INVALID_ARG;
+  if (ring_blocks < 0 || ring_blocks > block_table_width)
+    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,
+                block_table_width);
+  const size_t need = extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len, scored);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+  if (need && (!workspace || !aligned16(workspace)))
+    return fail(PA_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
+
+  p.out = out;
+  p.q = q;
+  p.q_token_stride = q_token_stride;
+  p.cache = static_cast<const uint8_t*>(kv_cache) + layer * layer_stride(desc);
+  p.num_blocks = desc->num_blocks;
+  p.block_size = desc->block_size;
+  p.num_kv_heads = desc->num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.group = group;
+  p.block_tables = block_tables;
+  p.bt_stride = block_table_stride;
+  p.bt_width = block_table_width;
+  p.context_lens = context_lens;
+  p.query_start_loc = query_start_loc;
+  p.num_seqs = num_seqs;
+  p.num_tokens = num_tokens;
+  p.max_query_len = max_query_len;
+  p.window = window;
+  p.ring_blocks = ring_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.dev_err = dev_err;
+  return PA_OK;
+}
+
+// The checks of a score's shape, and its parameters.
+pa_status score_params(pkv::ExtendParams& p, float scale, float softcap, const float* slopes, const int32_t* first_pos,
+                       const int32_t* last_pos, int32_t max_context) {
+  if (!(softcap == 0.f || (softcap >= 1e-4f && softcap <= 1e6f)))
+    return fail(PA_ERR_INVALID_ARG, "softcap %g must be 0 or in [1e-4, 1e6]", (double)softcap);
+  if ((reinterpret_cast<uintptr_t>(slopes) & 3) || (reinterpret_cast<uintptr_t>(first_pos) & 3) ||
+      (reinterpret_cast<uintptr_t>(last_pos) & 3))
+    return fail(PA_ERR_INVALID_ARG, "slopes, first_pos and last_pos must be 4-byte aligned");
+  pkv::set_cap(p, scale, softcap);
+  p.slopes = slopes;
+  p.first_pos = first_pos;
+  p.last_pos = last_pos;
+  p.max_context = max_context;
+  return PA_OK;
+}
+
 }  // namespace
 
 namespace pkv {
@@ -336,78 +514,45 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
                                     int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
                                     int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
                                     int32_t interleaved, int32_t num_tokens, uint32_t* dev_err, void* stream) {
-  pa_status st = check_desc(desc);
-  if (st != PA_OK) return st;
-  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
-  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
-  if (num_q_heads < 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads %d < 0", num_q_heads);
-  if (rotary_dim < 16 || rotary_dim > desc->head_size || rotary_dim % 16)
-    return fail(PA_ERR_INVALID_ARG, "rotary_dim %d must be a multiple of 16 in [16, head_size %d]", rotary_dim,
-                desc->head_size);
-  if (num_axes < 1 || num_axes > 4) return fail(PA_ERR_INVALID_ARG, "num_axes %d not in [1, 4]", num_axes);
-  if (max_position <= 0) return fail(PA_ERR_INVALID_ARG, "max_position %d", max_position);
-  if (pair_axis)
-    for (int i = 0; i < rotary_dim / 2; ++i)
-      if (pair_axis[i] >= num_axes)
-        return fail(PA_ERR_INVALID_ARG, "pair_axis[%d] = %d with num_axes %d", i, pair_axis[i], num_axes);
-  if (num_tokens == 0) return PA_OK;
-  if (!kv_cache || !key || !value || !slot_mapping || !positions || !cos_sin)
-    return fail(PA_ERR_INVALID_ARG, "kv_cache, key, value, slot_mapping, positions and cos_sin must be non-NULL");
-  if (!aligned16(kv_cache) || !aligned16(key) || !aligned16(value))
-    return fail(PA_ERR_INVALID_ARG, "kv_cache, key and value must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(slot_mapping) & 7) || (reinterpret_cast<uintptr_t>(positions) & 3) ||
-      (reinterpret_cast<uintptr_t>(cos_sin) & 3))
-    return fail(PA_ERR_INVALID_ARG, "slot_mapping must be 8-byte aligned, positions and cos_sin 4-byte aligned");
-  if (positions_axis_stride < 0 || (num_axes > 1 && positions_axis_stride > 0 && positions_axis_stride < num_tokens))
-    return fail(PA_ERR_INVALID_ARG, "positions_axis_stride %lld must be 0 or >= num_tokens",
-                (long long)positions_axis_stride);
-  const int64_t row = (int64_t)desc->num_kv_heads * desc->head_size;
-  if (key_token_stride < row || value_token_stride < row || key_token_stride % 8 || value_token_stride % 8)
-    return fail(PA_ERR_INVALID_ARG, "token strides must be >= num_kv_heads*head_size and multiples of 8");
-  if (num_q_heads > 0) {
-    const int64_t qrow = (int64_t)num_q_heads * desc->head_size;
-    if (!q || !q_out || !aligned16(q) || !aligned16(q_out))
-      return fail(PA_ERR_INVALID_ARG, "q and q_out must be non-NULL and 16-byte aligned");
-    if (q_token_stride < qrow || q_out_token_stride < qrow || q_token_stride % 8 || q_out_token_stride % 8)
-      return fail(PA_ERR_INVALID_ARG, "q strides must be >= num_q_heads*head_size and multiples of 8");
-    // a row is read and written by one block, so q_out's rows may share memory only with their own
-    const pkv::Rows out = token_rows(q_out, num_tokens, q_out_token_stride, qrow);
-    if (!(q == q_out && (q_token_stride == q_out_token_stride || num_tokens == 1)) &&
-        pkv::rows_overlap(out, token_rows(q, num_tokens, q_token_stride, qrow)))
-      return fail(PA_ERR_INVALID_ARG, "q_out must be q itself (with the same stride) or not overlap it");
-    if (pkv::rows_overlap(out, token_rows(key, num_tokens, key_token_stride, row)) ||
-        pkv::rows_overlap(out, token_rows(value, num_tokens, value_token_stride, row)))
-      return fail(PA_ERR_INVALID_ARG, "q_out must not overlap key or value");
-  }
   pkv::RopeParams p{};
-  p.q_out = q_out;
-  p.q_out_stride = q_out_token_stride;
-  p.q = q;
-  p.q_stride = q_token_stride;
-  p.num_q_heads = num_q_heads;
-  p.cache = static_cast<uint8_t*>(kv_cache) + layer * layer_stride(desc);
-  p.num_blocks = desc->num_blocks;
-  p.block_size = desc->block_size;
-  p.num_kv_heads = desc->num_kv_heads;
-  p.head_size = desc->head_size;
-  p.key = key;
-  p.key_stride = key_token_stride;
-  p.value = value;
-  p.value_stride = value_token_stride;
-  p.slot_mapping = slot_mapping;
-  p.positions = positions;
-  p.axis_stride = positions_axis_stride;
-  p.num_axes = num_axes;
-  p.cos_sin = cos_sin;
-  p.max_position = max_position;
-  p.rotary_dim = rotary_dim;
-  p.interleaved = interleaved != 0;
-  p.num_tokens = num_tokens;
-  p.dev_err = dev_err;
-  if (pair_axis) memcpy(p.pair_axis, pair_axis, rotary_dim / 2);
+  const pa_status st = rope_params(p, q_out, q_out_token_stride, q, q_token_stride, num_q_heads, kv_cache, desc, layer,
+                                   key, key_token_stride, value, value_token_stride, slot_mapping, positions,
+                                   positions_axis_stride, cos_sin, max_position, rotary_dim, pair_axis, num_axes,
+                                   interleaved, num_tokens, dev_err);
+  if (st != PA_OK || num_tokens == 0) return st;
   cudaError_t e = pkv::launch_rope_cache(p, act_dtype(desc), is_i8(desc), device_sm_count(),
                                          static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "rope_reshape_and_cache launch");
+}
+
+pa_status pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, const void* q,
+                                         int64_t q_token_stride, int32_t num_q_heads, void* kv_cache,
+                                         const pa_cache_desc* desc, int32_t layer, const void* key,
+                                         int64_t key_token_stride, const void* value, int64_t value_token_stride,
+                                         const int64_t* slot_mapping, const int32_t* positions,
+                                         int64_t positions_axis_stride, const float* cos_sin, int32_t max_position,
+                                         int32_t rotary_dim, const uint8_t* pair_axis, int32_t num_axes,
+                                         int32_t interleaved, const void* q_weight, const void* k_weight,
+                                         float weight_offset, float eps, int32_t num_tokens, uint32_t* dev_err,
+                                         void* stream) {
+  pkv::RopeParams p{};
+  const pa_status st = rope_params(p, q_out, q_out_token_stride, q, q_token_stride, num_q_heads, kv_cache, desc, layer,
+                                   key, key_token_stride, value, value_token_stride, slot_mapping, positions,
+                                   positions_axis_stride, cos_sin, max_position, rotary_dim, pair_axis, num_axes,
+                                   interleaved, num_tokens, dev_err);
+  if (st != PA_OK) return st;
+  if (!(eps > 0.f) || !(eps < INFINITY)) return fail(PA_ERR_INVALID_ARG, "eps must be a positive finite number");
+  if (!(fabsf(weight_offset) < INFINITY)) return fail(PA_ERR_INVALID_ARG, "weight_offset must be finite");
+  if ((reinterpret_cast<uintptr_t>(q_weight) & 1) || (reinterpret_cast<uintptr_t>(k_weight) & 1))
+    return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight must be 2-byte aligned");
+  if (num_tokens == 0) return PA_OK;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.weight_offset = weight_offset;
+  p.eps = eps;
+  cudaError_t e = pkv::launch_norm_rope_cache(p, act_dtype(desc), is_i8(desc), device_sm_count(),
+                                              static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "norm_rope_reshape_and_cache launch");
 }
 
 pa_status pa_build_tables(int32_t* query_start_loc, int32_t* context_lens, int64_t* slot_mapping, int32_t* positions,
@@ -755,12 +900,18 @@ pa_status pa_prefill(void* out, const void* q, int64_t q_token_stride, const voi
 
 size_t pa_extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
                                  int32_t num_q_heads, int32_t max_query_len) {
-  if (!desc || num_seqs <= 0 || num_tokens <= 0 || max_query_len <= 0 || num_q_heads <= 0) return 0;
-  if (check_desc(desc) != PA_OK || num_q_heads % desc->num_kv_heads) return 0;
-  const int group = num_q_heads / desc->num_kv_heads;
-  if (group > 16) return 0;
-  return pkv::extend_workspace(num_seqs, num_tokens, desc->num_kv_heads, group, max_query_len, desc->head_size,
-                               device_sm_count());
+  return extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len, false);
+}
+
+size_t pa_extend_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens,
+                                        int32_t num_q_heads, int32_t max_query_len) {
+  return extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len, true);
+}
+
+size_t pa_decode_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t max_context_len) {
+  if (max_context_len <= 0) return 0;
+  return extend_workspace_bytes(desc, num_seqs, num_seqs, num_q_heads, 1, true);
 }
 
 pa_status pa_extend(void* out, const void* q, int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc,
@@ -779,69 +930,57 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
                             const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                             int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, void* workspace,
                             size_t workspace_bytes, uint32_t* dev_err, void* stream) {
-  pa_status st = check_desc(desc);
-  if (st != PA_OK) return st;
-  if (layer < 0 || layer >= desc->num_layers) return fail(PA_ERR_INVALID_ARG, "layer %d", layer);
-  if (num_seqs < 0 || num_seqs > 65535) return fail(PA_ERR_INVALID_ARG, "num_seqs %d not in [0, 65535]", num_seqs);
-  if (num_tokens < 0) return fail(PA_ERR_INVALID_ARG, "num_tokens %d < 0", num_tokens);
-  if (max_query_len < 0) return fail(PA_ERR_INVALID_ARG, "max_query_len %d < 0", max_query_len);
-  if (num_q_heads <= 0 || num_q_heads % desc->num_kv_heads)
-    return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d",
-                num_q_heads, desc->num_kv_heads);
-  const int group = num_q_heads / desc->num_kv_heads;
-  if (group > 16) return fail(PA_ERR_UNSUPPORTED, "query heads per kv head %d (supported: 1 to 16)", group);
-  if (desc->num_kv_heads > 65535) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads > 65535");
-  if (window < 0) return fail(PA_ERR_INVALID_ARG, "window %d < 0", window);
-  if (!(scale > 0.f) || scale != scale) return fail(PA_ERR_INVALID_ARG, "scale must be a positive number");
-  if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
-  if (!out || !q || !kv_cache || !block_tables || !context_lens || !query_start_loc)
-    return fail(PA_ERR_INVALID_ARG,
-                "out, q, kv_cache, block_tables, context_lens and query_start_loc must be non-NULL");
-  if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache))
-    return fail(PA_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(block_tables) & 3) || (reinterpret_cast<uintptr_t>(context_lens) & 3) ||
-      (reinterpret_cast<uintptr_t>(query_start_loc) & 3))
-    return fail(PA_ERR_INVALID_ARG, "block_tables, context_lens and query_start_loc must be 4-byte aligned");
-  if (q_token_stride < (int64_t)num_q_heads * desc->head_size || q_token_stride % 8)
-    return fail(PA_ERR_INVALID_ARG, "q_token_stride must be >= num_q_heads*head_size and a multiple of 8");
-  const int64_t row = (int64_t)num_q_heads * desc->head_size;
-  if (pkv::rows_overlap(token_rows(out, num_tokens, row, row), token_rows(q, num_tokens, q_token_stride, row)))
-    return fail(PA_ERR_INVALID_ARG, "out must not overlap q");
-  if (check_rows(block_table_stride, block_table_width) != PA_OK) return PA_ERR_INVALID_ARG;
-  if (ring_blocks < 0 || ring_blocks > block_table_width)
-    return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,
-                block_table_width);
-  const size_t need = pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
-  if (workspace_bytes < need)
-    return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
-  if (need && (!workspace || !aligned16(workspace)))
-    return fail(PA_ERR_INVALID_ARG, "workspace must be non-NULL and 16-byte aligned");
-
   pkv::ExtendParams p{};
-  p.out = out;
-  p.q = q;
-  p.q_token_stride = q_token_stride;
-  p.cache = static_cast<const uint8_t*>(kv_cache) + layer * layer_stride(desc);
-  p.num_blocks = desc->num_blocks;
-  p.block_size = desc->block_size;
-  p.num_kv_heads = desc->num_kv_heads;
-  p.num_q_heads = num_q_heads;
-  p.group = group;
-  p.block_tables = block_tables;
-  p.bt_stride = block_table_stride;
-  p.bt_width = block_table_width;
-  p.context_lens = context_lens;
-  p.query_start_loc = query_start_loc;
-  p.num_seqs = num_seqs;
-  p.num_tokens = num_tokens;
-  p.max_query_len = max_query_len;
-  p.window = window;
-  p.ring_blocks = ring_blocks;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.dev_err = dev_err;
+  bool empty = false;
+  const pa_status st = extend_params(p, false, false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
+                                     block_tables, block_table_stride, block_table_width, context_lens,
+                                     query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
+                                     ring_blocks, workspace, workspace_bytes, dev_err);
+  if (st != PA_OK || empty) return st;
   cudaError_t e = pkv::launch_extend(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size, is_i8(desc),
                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "extend launch");
+}
+
+pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, const void* kv_cache,
+                           const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                           int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                           const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                           int32_t max_query_len, float scale, int32_t window, int32_t ring_blocks, float softcap,
+                           const float* slopes, const int32_t* first_pos, const int32_t* last_pos, void* workspace,
+                           size_t workspace_bytes, uint32_t* dev_err, void* stream) {
+  pkv::ExtendParams p{};
+  bool empty = false;
+  pa_status st = score_params(p, scale, softcap, slopes, first_pos, last_pos, INT32_MAX);
+  if (st != PA_OK) return st;
+  st = extend_params(p, true, false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
+                     block_tables, block_table_stride, block_table_width, context_lens,
+                     query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
+                     ring_blocks, workspace, workspace_bytes, dev_err);
+  if (st != PA_OK || empty) return st;
+  cudaError_t e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size,
+                                            is_i8(desc), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "extend_scored launch");
+}
+
+pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const void* kv_cache,
+                           const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
+                           int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,
+                           int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale, int32_t window,
+                           int32_t ring_blocks, float softcap, const float* slopes, const int32_t* first_pos,
+                           void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream) {
+  if (num_seqs != 0 && max_context_len <= 0) return fail(PA_ERR_INVALID_ARG, "max_context_len %d", max_context_len);
+  pkv::ExtendParams p{};
+  bool empty = false;
+  pa_status st = score_params(p, scale, softcap, slopes, first_pos, nullptr, max_context_len);
+  if (st != PA_OK) return st;
+  st = extend_params(p, true, true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
+                     block_table_stride, block_table_width, context_lens, nullptr, num_seqs, num_seqs, num_q_heads, 1,
+                     scale, window, ring_blocks, workspace, workspace_bytes, dev_err);
+  if (st != PA_OK || empty) return st;
+  cudaError_t e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size,
+                                            is_i8(desc), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode_scored launch");
 }
 
 pa_status pa_copy_blocks(void* kv_cache, const pa_cache_desc* desc, const int64_t* pairs, int32_t num_pairs,
