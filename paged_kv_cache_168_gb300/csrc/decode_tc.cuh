@@ -68,6 +68,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "scores.cuh"
 #include "tc_common.cuh"
 
 namespace pkv {
@@ -192,6 +193,7 @@ struct TileMeta {
   int seq0, ncol, pbase;         // column n: sequence seq0 + n / G, head kvh * G + n % G (ncol real columns);
                                  // the workspace partition of partition `part` is pbase + part
   int head, item;                // tiles of the item before this one; the item's index in this CTA
+  int far;                       // shaped scores: positions from the tile's first token to the query's own
   int bad;                       // 16-bit caches: a block id of the item so far was out of range (block 0 read
                                  // instead); the item's last tile has the item's verdict
 };
@@ -200,6 +202,7 @@ struct TileMeta {
 struct ItemRec {
   int s, kvh, part, n_parts, t_first, t0, t1, jb;   // table row, kv head, partition; its token range
   int seq0, ncol, pbase, qslot, item;               // columns, Q slot, item index (-1: no more work)
+  int ctx;                                          // shaped scores: the sequence's context
   int ids[32];                                      // its first 32 block ids
 };
 
@@ -325,13 +328,13 @@ struct ItemTables {
 // ceil(rem / 128) tiles (its "class", 1 .. P / 128: a remainder of P - 1 tokens
 // has P / 128 tiles).  A sequence with no (or an invalid) context is one
 // remainder item of class 1 that writes zeros.
-__device__ __forceinline__ void work_of(const DecodeParams& p, int ctx, int& full, int& cls) {
-  if (ctx <= 0 || ctx_invalid(p, ctx)) {
+__device__ __forceinline__ void work_of(const DecodeParams& p, int s, int ctx, int& full, int& cls) {
+  if (ctx <= 0 || ctx_invalid(p, ctx) || (p.first_pos && attended_first(p, s, ctx) >= ctx)) {
     full = 0;
     cls = 1;
     return;
   }
-  const int len = ctx - attended_from(p, ctx);
+  const int len = ctx - attended_from(p, s, ctx);
   full = len / p.partition_size;
   const int rem = len - full * p.partition_size;
   cls = min((rem + kTile - 1) / kTile, kClasses - 1);
@@ -354,9 +357,12 @@ __device__ void warp_zero_rows(const DecodeParams& p, int s, int kvh, int lane) 
 // SP (shared prefix): items are virtual sequences -- each sequence's own tail
 // after its group's shared prefix, and one prefix per group chunk whose
 // columns are the query heads of up to 16 / G member sequences (kN columns).
-template <typename T, int G, int NS, bool I8, int NRH, bool SP>
+// kScored: scores are shaped (scores.cuh) as the softmax warps read them, and a
+// sequence may attend from a position of its own on.
+template <typename T, int G, int NS, bool I8, int NRH, bool SP, bool kScored>
 __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kernel(const __grid_constant__ DecodeParams p) {
   static_assert(!(SP && I8), "shared-prefix decode is for 16-bit caches");
+  static_assert(!(SP && kScored), "shared-prefix decode has plain scores");
   // columns of an item: the G query heads of one sequence, or (shared prefix)
   // up to kN heads of several sequences
   constexpr int CN = SP ? kN : G;
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         work_of_len(c - sp_eff[i], p.partition_size, full, cls);
       }
     } else {
-      work_of(p, p.context_lens[i], full, cls);
+      work_of(p, i, p.context_lens[i], full, cls);
     }
     pre[i + 1] = full;
     rcls[i] = (uint8_t)cls;
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       const int s = R.s, kvh = R.kvh, part = R.part, n_parts = R.n_parts, t_first = R.t_first;
       const int t0 = R.t0, t1 = R.t1, jb = R.jb;
       const int seq0 = R.seq0, ncol = R.ncol, pbase = R.pbase, qslot = R.qslot;
-      const int id_lane = R.ids[lane];
+      const int id_lane = R.ids[lane], R_ctx = kScored ? R.ctx : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.rec_empty[rs]);
       const int32_t* row = p.block_tables + (int64_t)s * p.bt_stride;   // entry table_index(j) holds block j
@@ -628,6 +634,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           m.qinv = 1.f;
           m.seq0 = seq0; m.ncol = ncol; m.pbase = pbase;
           m.head = k; m.item = item_seq; m.bad = item_bad ? 1 : 0;
+          m.far = kScored ? R_ctx - 1 - (t0 + k * kTile) : 0;
           sh.meta[slot] = m;
           mbar_arrive_expect_tx(&sh.full[slot], (uint32_t)(nb * chunk_bytes));
         }
@@ -727,7 +734,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
     auto item_of_round = [&](int k) {
       return k * (int)gridDim.x + ((k & 1) ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
     };
-    const bool windowed = p.window > 0 || p.ring_blocks > 0;
+    const bool windowed = p.window > 0 || p.ring_blocks > 0 || (kScored && p.first_pos);
     constexpr int kQChunks = (CN * 16 + 31) / 32;
     // What an item is (virtual sequence, kv head, partition, table row, columns,
     // context and first block) is worked out 32 rounds at a time, lane l for
@@ -771,7 +778,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           d.t0 = SP ? sp_eff[d.v] : 0;
           d.pbase = SP ? sp_npre[d.v] : 0;
         }
-        d.fb = windowed ? (attended_from(p, d.ctx) + d.part * P) / bs
+        d.fb = windowed ? (attended_from(p, d.v, d.ctx) + d.part * P) / bs
                         : d.t0 / bs + d.part * (P / bs);   // P is a multiple of 128, bs divides it
       }
       return d;
@@ -812,7 +819,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
                     (int64_t)(d.kvh * G + n % G) * kD + (lane & 1) * 64);
       if (lane == 0) {
         const int ti = windowed ? table_index(d.fb, p.ring_blocks) : d.fb;
-        if (ti >= 0 && ti < p.bt_stride) prefetch_l2(p.block_tables + (int64_t)d.row * p.bt_stride + ti);
+        if (ti >= 0 && ti < p.bt_width) prefetch_l2(p.block_tables + (int64_t)d.row * p.bt_stride + ti);
       }
     };
     struct Item {
@@ -826,7 +833,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         // the partition's later block ids, checked when the item starts: into L2
         // now, a whole item ahead, so that check waits for L2, not HBM (lane i
         // covers ids 32 (i + 1) .. 32 (i + 1) + 31; P / bs <= 1024)
-        const int row_end = min(p.bt_stride, d.fb + P / bs);
+        const int row_end = min(p.bt_width, d.fb + P / bs);
         const int t = d.fb + 32 * (lane + 1);
         if (t < row_end) {
           const int32_t* rp = p.block_tables + (int64_t)d.row * p.bt_stride;
@@ -835,7 +842,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         }
       }
       r.id_lane =
-          (lane < P / bs && ti < p.bt_stride && ti >= 0) ? p.block_tables[(int64_t)d.row * p.bt_stride + ti] : 0;
+          (lane < P / bs && ti < p.bt_width && ti >= 0) ? p.block_tables[(int64_t)d.row * p.bt_stride + ti] : 0;
       // query rows: column n is head kvh * G + n % G of sequence seq0 + n / G
 #pragma unroll
       for (int k = 0; k < kQChunks; ++k) {
@@ -870,7 +877,13 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         warp_zero_rows<T, G>(p, s, kvh, lane);
         continue;
       }
-      const int t_first = SP ? cd.t0 : window_start(ctx, bs, p.window, p.ring_blocks);
+      const int t_first = SP        ? cd.t0
+                          : kScored ? attended_first(p, s, ctx)
+                                    : window_start(ctx, bs, p.window, p.ring_blocks);
+      if (kScored && t_first >= ctx) {                                 // nothing is attended
+        warp_zero_rows<T, G>(p, s, kvh, lane);
+        continue;
+      }
       const int t_base = (t_first / bs) * bs;
       const int n_parts = (ctx - t_base + P - 1) / P;
       const int t0 = t_base + part * P, t1 = min(ctx, t0 + P);
@@ -984,6 +997,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         m.qinv = qinv;
         m.seq0 = cd.seq0; m.ncol = cd.ncol; m.pbase = cd.pbase;
         m.head = k; m.item = item_seq; m.bad = 0;
+        m.far = ctx - 1 - (t0 + k * kTile);
         // the tile's block ids, lane i holding blocks i + 32 c of the tile: the
         // item's first 32 come from the prefetched id_lane, the rest are loaded
         // here, all in flight together
@@ -1023,6 +1037,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           R.s = s; R.kvh = kvh; R.part = part; R.n_parts = n_parts; R.t_first = t_first;
           R.t0 = t0; R.t1 = t1; R.jb = jb;
           R.seq0 = cd.seq0; R.ncol = cd.ncol; R.pbase = cd.pbase; R.qslot = qslot; R.item = item_seq;
+          if (kScored) R.ctx = ctx;
         }
         R.ids[lane] = id_lane;
         __syncwarp();
@@ -1380,18 +1395,42 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       const bool rv = row >= mt.lo && row < mt.valid;
       // 8-bit: K_t = sk_t * codes and V_t = sv_t * codes; sk_t scales this row's
       // scores and sv_t its P^T row (the normaliser keeps the unscaled p)
-      const float kscale = I8 ? sh.sk[slot][row] * (p.scale_log2 * mt.qinv) : p.scale_log2;
+      const float unit = kScored && p.shape.capped ? p.shape.cap_in : p.scale_log2;
+      const float kscale = I8 ? sh.sk[slot][row] * (unit * mt.qinv) : unit;
       const float vscale = I8 ? sh.sv[slot][row] : 1.f;
       // scores; does any exceed the running maximum by more than kLazyMax?  (On
       // the group's first tile of an item m = -inf, so every valid row does.)
       float x[CN];
       bool up = false;
       {
+        if constexpr (kScored) {
+          if (p.shape.capped) {
+            bool large = false;
+#pragma unroll
+            for (int n = 0; n < CN; ++n) {
+              sv[n] *= kscale;
+              large |= fabsf(sv[n]) > 1.f;
+            }
+            if (__builtin_expect(__any_sync(kFull, rv && large), 0)) {
+#pragma unroll
+              for (int n = 0; n < CN; ++n) sv[n] = score::any_cap(p.shape, sv[n]);
+            } else {
+#pragma unroll
+              for (int n = 0; n < CN; ++n) sv[n] = score::near_cap(p.shape, sv[n]);
+            }
+          }
+          if (p.shape.slopes) {
+            const float dist = (float)(mt.far - row) * score::kLog2e, f = p.shape.capped ? 1.f : kscale;
+#pragma unroll
+            for (int n = 0; n < CN; ++n) sv[n] = fmaf(-p.shape.slopes[mt.kvh * G + n], dist, sv[n] * f);
+          }
+        }
+        const float last_scale = kScored && (p.shape.capped || p.shape.slopes) ? 1.f : kscale;
         float mv[CN];
         load_m(mv);
 #pragma unroll
         for (int n = 0; n < CN; ++n) {
-          x[n] = rv ? sv[n] * kscale : -INFINITY;
+          x[n] = rv ? sv[n] * last_scale : -INFINITY;
           up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);   // 8-bit: the V scales ride on P, keep p <= 1
         }
       }
@@ -1903,26 +1942,26 @@ __host__ __device__ inline size_t decode_tc_smem(int NS, bool I8, int NRH, bool 
          ItemTables(S, SP).end;
 }
 
-template <typename T, int G, int NS, bool I8, int NRH, bool SP = false>
+template <typename T, int G, int NS, bool I8, int NRH, bool SP = false, bool kScored = false>
 cudaError_t launch_typed(const DecodeParams& p, int num_sms, cudaStream_t stream) {
   const size_t smem = decode_tc_smem(NS, I8, NRH, SP, p.num_seqs);
-  auto kern = decode_tc_kernel<T, G, NS, I8, NRH, SP>;
-  cudaError_t e = set_smem_attribute_once<decode_tc_kernel<T, G, NS, I8, NRH, SP>>(smem);
+  auto kern = decode_tc_kernel<T, G, NS, I8, NRH, SP, kScored>;
+  cudaError_t e = set_smem_attribute_once<decode_tc_kernel<T, G, NS, I8, NRH, SP, kScored>>(smem);
   if (e != cudaSuccess) return e;
   kern<<<num_sms, threads_of(I8, SP ? kN : G), smem, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int NS, bool I8, int NRH>
+template <typename T, int NS, bool I8, int NRH, bool kScored = false>
 cudaError_t launch_group(const DecodeParams& p, int group, int num_sms, cudaStream_t stream) {
   switch (group) {
-    case 1: return launch_typed<T, 1, NS, I8, NRH>(p, num_sms, stream);
-    case 2: return launch_typed<T, 2, NS, I8, NRH>(p, num_sms, stream);
-    case 4: return launch_typed<T, 4, NS, I8, NRH>(p, num_sms, stream);
-    case 8: return launch_typed<T, 8, NS, I8, NRH>(p, num_sms, stream);
+    case 1: return launch_typed<T, 1, NS, I8, NRH, false, kScored>(p, num_sms, stream);
+    case 2: return launch_typed<T, 2, NS, I8, NRH, false, kScored>(p, num_sms, stream);
+    case 4: return launch_typed<T, 4, NS, I8, NRH, false, kScored>(p, num_sms, stream);
+    case 8: return launch_typed<T, 8, NS, I8, NRH, false, kScored>(p, num_sms, stream);
     case 16:
       if constexpr (I8) return cudaErrorInvalidValue;   // 8-bit caches serve groups up to 8
-      else return launch_typed<T, 16, NS, false, 1>(p, num_sms, stream);
+      else return launch_typed<T, 16, NS, false, 1, false, kScored>(p, num_sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

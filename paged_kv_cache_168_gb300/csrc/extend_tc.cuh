@@ -95,6 +95,7 @@
 #include "common.cuh"
 #include "extend_plan.h"
 #include "kernels.h"
+#include "scores.cuh"
 #include "tc_common.cuh"
 
 namespace pkv {
@@ -105,7 +106,6 @@ using plan::kKv;
 using plan::kRows;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kRescaleThreshold = 8.f;   // base-2 units
-constexpr float kLog2e = 1.4426950408889634f;
 // 8-bit caches: weights (with V's scales) and their sums are 2^kLift times as large.
 // Stored in fp16 they reach 2^15 at most, and a token that holds nearly all of a
 // row's weight keeps 11 bits of it down to a V scale 2^-21 times its tile's largest
@@ -479,7 +479,7 @@ struct Work {
   int part_row, flag;
 };
 
-template <int D, Fill F>
+template <int D, Fill F, bool kScored>
 struct Cfg {
   static constexpr int kTileBytes = kKv * D * 2;              // K (or V) of one KV tile
   static constexpr int kGroupBytes = 8 * D * 2;               // 8 tokens of it
@@ -489,8 +489,8 @@ struct Cfg {
   // registers a thread, whose sum over the warpgroups is the launch's: the softmax
   // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
   // caches half of a tile's codes (8 registers more or fewer for the softmax: within 2%)
-  static constexpr int kRegsSoftmax = F == kBulk ? 200 : F == kGather ? 176 : 160;
-  static constexpr int kRegsRest = F == kBulk ? 104 : F == kGather ? 88 : 96;
+  static constexpr int kRegsSoftmax = F == kBulk ? (kScored ? 216 : 200) : F == kGather ? (kScored ? 184 : 176) : 160;
+  static constexpr int kRegsRest = F == kBulk ? (kScored ? 72 : 104) : F == kGather ? (kScored ? 72 : 88) : 96;
   static constexpr int kRegsConvert = F == kGather ? 72 : 96;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
@@ -566,27 +566,20 @@ __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
   return r;
 }
 
-// c tanh(y) in base-2 units for two |y| <= 1: y P(y^2), P fitted to tanh(y) / y on [0, 1] (by weighted least squares
-// until the relative error is level: 5.9e-7), times c log2(e).
-__device__ __forceinline__ uint64_t capped2(const ExtendParams& p, uint64_t y) {
+// tanh(y) / y times c for two y: |y| <= 1/2 (kTerms 4: a polynomial of degree 3 in y^2, relative error 5.4e-7) or <= 1.
+template <int kTerms>
+__device__ __forceinline__ uint64_t cap_quotient2(const ScoreShape& w, uint64_t y) {
+  const float* c = kTerms == 4 ? w.half : w.poly;
   const uint64_t s = mul2f(y, y);
-  uint64_t v = pack2f(p.cap_poly[5], p.cap_poly[5]);
+  uint64_t v = pack2f(c[kTerms - 1], c[kTerms - 1]);
 #pragma unroll
-  for (int k = 4; k >= 0; --k) v = fma2f(v, s, pack2f(p.cap_poly[k], p.cap_poly[k]));
-  return mul2f(y, v);
+  for (int k = kTerms - 2; k >= 0; --k) v = fma2f(v, s, pack2f(c[k], c[k]));
+  return v;
 }
-// The base-2 score of any y (s / c where scores are capped, else s log2(e)), dist positions behind the reference.
-__device__ __forceinline__ float shaped_score(const ExtendParams& p, float y, float slope2, int dist) {
-  float v = y;
-  if (p.capped) {
-    const float s = y * y;
-    v = p.cap_poly[5];
-#pragma unroll
-    for (int k = 4; k >= 0; --k) v = fmaf(v, s, p.cap_poly[k]);
-    v *= y;
-    if (fabsf(y) > 1.f) v = p.cap_log2 * (1.f - __fdividef(2.f, 1.f + ex2_approx(fminf(y * (2.f * kLog2e), 64.f))));
-  }
-  return p.slopes ? v - slope2 * fabsf((float)dist) : v;
+// The base-2 score of any y (s / c where scores are capped, else s log2(e)), dist positions from the reference.
+__device__ __forceinline__ float shaped_score(const ScoreShape& w, float y, float slope2, int dist) {
+  const float v = w.capped ? score::any_cap(w, y) : y;
+  return w.slopes ? v - slope2 * fabsf((float)dist) : v;
 }
 
 // 32 TMEM lanes x 64 columns; the wait is part of the statement.
@@ -754,11 +747,11 @@ __device__ __forceinline__ int block_of(const ExtendParams& p, const int32_t* ro
 }
 
 template <typename T, int D, Fill F, bool kScored>
-__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
+__global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
                                                                        const __grid_constant__ Space ws,
                                                                        const __grid_constant__ CUtensorMap q_map,
                                                                        const __grid_constant__ CUtensorMap kv_map) {
-  using C = Cfg<D, F>;
+  using C = Cfg<D, F, kScored>;
   constexpr bool kI8 = F == kCodes;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   using PT = typename std::conditional<kI8, __half, T>::type;      // type of the weights and of V's operand
@@ -1363,7 +1356,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               const unsigned top = __reduce_max_sync(kFull, __float_as_uint(fmaxf(sv, 0.f)));
               const unsigned low = __reduce_min_sync(kFull, __float_as_uint(sv > 0.f ? sv : INFINITY));
               const int at = (ct % 8 / 2) * kScalePitch + ct / 8 * 2 + ct % 2;
-              scales.k[r][at] = sk * (kScored && p.capped ? p.cap_in : p.scale_log2);
+              scales.k[r][at] = sk * (kScored && p.shape.capped ? p.shape.cap_in : p.scale_log2);
               scales.v[r][at] = sv;
               if (lane == 0) {
                 scales.top[r][ct >> 5] = __uint_as_float(top);
@@ -1420,11 +1413,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const bool row_ok = ipos < (alt ? w.npos : min(ptile, w.npos - my0));
       const int pos = w.pos0 + my0 + ipos;
       const int token = w.row0 + (row_ok ? my0 + ipos : 0);
-      const int from = span_from<kScored>(p, pos, w.held, token);
-      const int to = span_to<kScored>(p, pos, w.kv_end, token);
-      // distances count from the nearest position that is attended: the same for a whole row
-      const int ref = min(pos, to);
-      const float slope2 = kScored && p.slopes ? p.slopes[w.kvh * G + head] * kLog2e : 0.f;
+      const int from = kScored ? 0 : attend_from(pos, p.window, w.held);
+      const float slope2 = kScored && p.shape.slopes ? p.shape.slopes[w.kvh * G + head] * score::kLog2e : 0.f;
       const int n = t == 0 ? w.n[0] : w.n[1];
       const int tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
       float m = -INFINITY, l = 0.f;
@@ -1481,26 +1471,26 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             }
             if constexpr (kScored) {
               // (the K scales made x base-2 scores, or quotients by the cap)
-              if (p.capped || p.slopes) {
+              if (p.shape.capped || p.shape.slopes) {
                 bool exact = false;
-                float sl[2] = {0.f, 0.f};
-                int at[2];                                           // my first column less the row's reference position
+                float sl[2] = {0.f, 0.f}, big[2] = {0.f, 0.f};
+                int at[2];                                           // first column less the row's reference position
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                   const bool is_row = ok4 >> r & 1;
-                  const int tok = w.row0 + (is_row ? pos4[r] - w.pos0 : 0);
                   const int rr = (warp & 3) * 32 + (lane >> 2) + 8 * (2 * h + r);
-                  if (p.slopes) sl[r] = p.slopes[w.kvh * G + rr % G] * kLog2e;
+                  if (p.shape.slopes) sl[r] = p.shape.slopes[w.kvh * G + rr % G] * score::kLog2e;
+                  const int tok = w.row0 + (is_row ? pos4[r] - w.pos0 : 0);
                   const int nearest = min(pos4[r], span_to<kScored>(p, pos4[r], w.kv_end, tok));
-                  at[r] = t0 + 2 * (lane & 3) - nearest;
-                  exact |= p.slopes && p.last_pos && is_row && t0 + kKv - 1 > nearest;
-                  if (p.capped) {
-                    float big = 0.f;
+                  at[r] = t0 - nearest;
+                  exact |= p.shape.slopes && p.last_pos && is_row && t0 + kKv - 1 > nearest;
+                  if (p.shape.capped) {
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) big = fmaxf(fmaxf(big, fabsf(x[4 * n + 2 * r])), fabsf(x[4 * n + 2 * r + 1]));
-                    exact |= is_row && big > 1.f;
+                    for (int n = 0; n < 16; ++n) big[r] = fmaxf(fmaxf(big[r], fabsf(x[4 * n + 2 * r])), fabsf(x[4 * n + 2 * r + 1]));
+                    if (!is_row) big[r] = 0.f;
                   }
                 }
+                exact |= fmaxf(big[0], big[1]) > 1.f;
                 if (__builtin_expect(__any_sync(kFull, exact), 0)) {
 #pragma unroll
                   for (int e = 0; e < 4; ++e) tmem_st16x256_32(s_addr + half + 32 * e, x + 16 * e);
@@ -1511,27 +1501,54 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                     tmem_ld16x256_32(s_addr + half + 32 * e, v);
 #pragma unroll
                     for (int k = 0; k < 16; ++k)
-                      v[k] = shaped_score(p, v[k], sl[k >> 1 & 1], at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + (k & 1));
+                      v[k] = shaped_score(p.shape, v[k], sl[k >> 1 & 1], at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + 2 * (lane & 3) + (k & 1));
                     tmem_st16x256_32(s_addr + half + 32 * e, v);
                   }
                   tc::tmem_wait_st();
                   tmem_ld16x256(s_addr + half, x);
                 } else {
-                  if (p.capped) {
+                  // in place; a slope's part in full where every 32 columns' first one is, and within those:
+                  // both products small or exact, no sum of many steps
+                  uint64_t in[2][4];
 #pragma unroll
-                    for (int e = 0; e < 64; e += 2) unpack2f(capped2(p, pack2f(x[e], x[e + 1])), x[e], x[e + 1]);
-                  }
-                  if (p.slopes) {
+                  for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                      const float base = sl[r] * (float)at[r];
-                      const uint64_t sl2 = pack2f(sl[r], sl[r]), base2 = pack2f(base, base);
+                    for (int k = 0; k < 4; ++k) {
+                      const float col = (float)(8 * k + 2 * (lane & 3));
+                      in[r][k] = pack2f(sl[r] * col, sl[r] * (col + 1.f));
+                    }
+                  if (p.shape.capped) {
+                    if (!__any_sync(kFull, fmaxf(big[0], big[1]) > 0.5f)) {
 #pragma unroll
-                      for (int n = 0; n < 16; ++n) {
-                        const int e = 4 * n + 2 * r;
-                        unpack2f(add2f(pack2f(x[e], x[e + 1]), fma2f(pack2f(8.f * n, 8.f * n + 1.f), sl2, base2)), x[e], x[e + 1]);
+                      for (int e = 0; e < 64; e += 2) {
+                        const uint64_t y = pack2f(x[e], x[e + 1]);
+                        unpack2f(fma2f(y, cap_quotient2<4>(p.shape, y), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
+                      }
+                    } else {
+#pragma unroll
+                      for (int e = 0; e < 64; e += 2) {
+                        const uint64_t y = pack2f(x[e], x[e + 1]);
+                        unpack2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
                       }
                     }
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2)
+                      unpack2f(add2f(pack2f(x[e], x[e + 1]), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
+                  }
+                  if (p.shape.slopes) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                      for (int c = 0; c < 4; ++c) {
+                        const float off = sl[r] * (float)(at[r] + 32 * c);
+                        const uint64_t off2 = pack2f(off, off);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                          const int e = 16 * c + 4 * k + 2 * r;
+                          unpack2f(add2f(pack2f(x[e], x[e + 1]), off2), x[e], x[e + 1]);
+                        }
+                      }
                   }
                 }
               }
@@ -1672,16 +1689,29 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           tmem_ld64(s_addr, x);
           tmem_ld64(s_addr + 64, x + 64);
           float unit = p.scale_log2;                                 // what makes x base-2 scores
+          // shaped scores: x unit + ahead(column / 16) is the base-2 score, or (fly) x is still q.k, to be capped in the
+          // loop that takes the powers, which leaves the units of these products idle
+          float so = 0.f, base = 0.f, most = 0.f;
+          bool fly = false, tight = false;
           if constexpr (kScored) {
-            if (p.capped || p.slopes) {
-              bool exact = p.slopes && p.last_pos && row_ok && t0 + kKv - 1 > ref;
-              if (p.capped) {
-                float big[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool capped = p.shape.capped, sloped = p.shape.slopes;
+            if (capped || sloped) {
+              int ref = pos;                                         // distances count from the nearest attended position
+              if (sloped && p.last_pos) ref = min(pos, span_to<kScored>(p, pos, w.kv_end, token));
+              bool exact = sloped && p.last_pos && row_ok && t0 + kKv - 1 > ref;
+              if (capped) {
+                float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
 #pragma unroll
-                for (int e = 0; e < kKv; e += 8)
+                for (int e = 0; e < kKv; e += 4)
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) big[k] = fmaxf(fmaxf(big[k], fabsf(x[e + k])), fabsf(x[e + 4 + k]));
-                exact |= row_ok && fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * p.cap_in > 1.f;
+                  for (int k = 0; k < 2; ++k) {
+                    hi[k] = fmaxf(fmaxf(hi[k], x[e + k]), x[e + 2 + k]);
+                    lo[k] = fminf(fminf(lo[k], x[e + k]), x[e + 2 + k]);
+                  }
+                most = fmaxf(hi[0], hi[1]) * p.shape.cap_in;
+                const float size = row_ok ? fmaxf(fabsf(most), fabsf(fminf(lo[0], lo[1]) * p.shape.cap_in)) : 0.f;
+                exact |= size > 1.f;
+                tight = !__any_sync(kFull, size > 0.5f);
               }
               if (__builtin_expect(__any_sync(kFull, exact), 0)) {
 #pragma unroll 1
@@ -1690,33 +1720,45 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                   tc::tmem_ld16(s_addr + e, v);
 #pragma unroll
                   for (int k = 0; k < 16; ++k)
-                    v[k] = shaped_score(p, p.capped ? v[k] * p.cap_in : v[k] * p.scale_log2, slope2, t0 + e + k - ref);
+                    v[k] = shaped_score(p.shape, v[k] * (capped ? p.shape.cap_in : p.scale_log2), slope2, t0 + e + k - ref);
                   tc::tmem_st16(s_addr + e, v);
                 }
                 tc::tmem_wait_st();
                 tmem_ld64(s_addr, x);
                 tmem_ld64(s_addr + 64, x + 64);
+                unit = 1.f;
+              } else if (capped && !sloped && !edge) {
+                fly = true;
               } else {
-                if (p.capped) {
-                  const uint64_t in2 = pack2f(p.cap_in, p.cap_in);
+                if (sloped) {
+                  so = slope2;
+                  base = slope2 * (float)(t0 - ref);
+                }
+                uint64_t in[8];                                      // the slope's part within 16 columns
+#pragma unroll
+                for (int k = 0; k < 8; ++k) in[k] = pack2f(so * (2.f * k), so * (2.f * k + 1.f));
+                if (capped) {
+                  const uint64_t in2 = pack2f(p.shape.cap_in, p.shape.cap_in);
+#pragma unroll
+                  for (int e = 0; e < kKv; e += 2) {
+                    const uint64_t y = mul2f(pack2f(x[e], x[e + 1]), in2);
+                    unpack2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[e / 2 % 8]), x[e], x[e + 1]);
+                  }
+                } else {
+                  const uint64_t u2 = pack2f(unit, unit);
 #pragma unroll
                   for (int e = 0; e < kKv; e += 2)
-                    unpack2f(capped2(p, mul2f(pack2f(x[e], x[e + 1]), in2)), x[e], x[e + 1]);
+                    unpack2f(fma2f(pack2f(x[e], x[e + 1]), u2, in[e / 2 % 8]), x[e], x[e + 1]);
                 }
-                if (p.slopes) {
-                  const float base = slope2 * (float)(t0 - ref), u = p.capped ? 1.f : p.scale_log2;
-                  const uint64_t slope22 = pack2f(slope2, slope2), base2 = pack2f(base, base), u2 = pack2f(u, u);
-#pragma unroll
-                  for (int e = 0; e < kKv; e += 2)
-                    unpack2f(fma2f(pack2f(x[e], x[e + 1]), u2, fma2f(pack2f((float)e, (float)(e + 1)), slope22, base2)),
-                             x[e], x[e + 1]);
-                }
+                unit = 1.f;
               }
-              unit = 1.f;
             }
           }
+          auto ahead = [&](int c) { return kScored ? fmaf(so, 16.f * c, base) : 0.f; };
           if (edge) {
-            const int lo = from - t0, hi = row_ok ? to + 1 - t0 : 0;   // attended columns [lo, hi)
+            // attended columns [lo, hi)
+            const int lo = (kScored ? span_from<kScored>(p, pos, w.held, token) : from) - t0;
+            const int hi = row_ok ? span_to<kScored>(p, pos, w.kv_end, token) + 1 - t0 : 0;
 #pragma unroll
             for (int e = 0; e < kKv / 32; ++e) {
               const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
@@ -1743,13 +1785,29 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               }
             }
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
+          float mt;
+          if constexpr (!kScored) {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
 #pragma unroll
-          for (int e = 0; e < kKv; e += 8)
+            for (int e = 0; e < kKv; e += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
-          float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          mt *= unit;
+              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
+            mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+          } else if (fly) {
+            mt = score::any_cap(p.shape, most);                      // (the cap keeps the order)
+          } else {
+            float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kKv / 16; ++c) {
+              float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) top[k] = fmaxf(fmaxf(top[k], x[16 * c + e + k]), x[16 * c + e + 2 + k]);
+              best[c & 1] = fmaxf(best[c & 1], fmaf(fmaxf(top[0], top[1]), unit, ahead(c)));
+            }
+            mt = fmaxf(best[0], best[1]);
+          }
           const float m_new = fmaxf(m, mt);
           const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
           if (m == -INFINITY) m = m_new;
@@ -1776,23 +1834,45 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           }
           // weights 2^(x - m), the sum of the unrounded ones in fp32
           const float nm = m == -INFINITY ? 0.f : -m;
-          const uint64_t unit2 = pack2f(unit, unit), nm2 = pack2f(nm, nm);
           uint64_t sum[2] = {0, 0};
+          // to_power(pair, column): what two powers are of
+          auto weigh = [&](auto to_power) {
 #pragma unroll
-          for (int e = 0; e < kKv / 32; ++e) {
-            uint32_t y[16];
+            for (int e = 0; e < kKv / 32; ++e) {
+              uint32_t y[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int col = e * 32 + 2 * k;
-              const uint64_t xx = pack2f(x[col], x[col + 1]);
-              float a, b;
-              unpack2f(fma2f(xx, unit2, nm2), a, b);
-              a = ex2_approx(a);
-              b = ex2_approx(b);
-              sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
-              y[k] = Elem<PT>::pack2(a, b);
+              for (int k = 0; k < 16; ++k) {
+                const int col = e * 32 + 2 * k;
+                float a, b;
+                unpack2f(to_power(pack2f(x[col], x[col + 1]), col), a, b);
+                a = ex2_approx(a);
+                b = ex2_approx(b);
+                sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
+                y[k] = Elem<PT>::pack2(a, b);
+              }
+              tc::tmem_st16u(s_addr + e * 16, y);
             }
-            tc::tmem_st16u(s_addr + e * 16, y);
+          };
+          const uint64_t unit2 = pack2f(unit, unit), nm2 = pack2f(nm, nm);
+          if constexpr (!kScored) {
+            weigh([&](uint64_t xx, int) { return fma2f(xx, unit2, nm2); });
+          } else if (!fly) {
+            weigh([&](uint64_t xx, int col) {
+              const float v = nm + ahead(col / 16);
+              return fma2f(xx, unit2, pack2f(v, v));
+            });
+          } else {
+            const uint64_t in2 = pack2f(p.shape.cap_in, p.shape.cap_in);
+            if (tight)
+              weigh([&](uint64_t xx, int) {
+                const uint64_t y = mul2f(xx, in2);
+                return fma2f(y, cap_quotient2<4>(p.shape, y), nm2);
+              });
+            else
+              weigh([&](uint64_t xx, int) {
+                const uint64_t y = mul2f(xx, in2);
+                return fma2f(y, cap_quotient2<6>(p.shape, y), nm2);
+              });
           }
           {
             float a, b;
@@ -1964,8 +2044,8 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
   const int bs = p.block_size, j = r / p.group, h = kvh * p.group + r % p.group;
   const int pos = it.pos0 + j, from = span_from<kScored>(p, pos, it.held, it.row0 + j);
   const int to = span_to<kScored>(p, pos, p.context_lens[it.seq], it.row0 + j), ref = min(pos, to);
-  const float unit = kScored && p.capped ? p.cap_in : p.scale_log2;
-  const float slope2 = kScored && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+  const float unit = kScored && p.shape.capped ? p.shape.cap_in : p.scale_log2;
+  const float slope2 = kScored && p.shape.slopes ? p.shape.slopes[h] * score::kLog2e : 0.f;
   const T* q = static_cast<const T*>(p.q) + (int64_t)(it.row0 + j) * p.q_token_stride + (int64_t)h * D + lane * kDims;
   float x[kDims], o[kDims], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -1992,7 +2072,7 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
     for (int d = 0; d < kDims; ++d) z = fmaf(x[d], element(0, d), z);
 #pragma unroll
     for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(kFull, z, i);
-    if constexpr (kScored) z = shaped_score(p, z, slope2, t - ref);
+    if constexpr (kScored) z = shaped_score(p.shape, z, slope2, t - ref);
     // (a score of -inf has weight 0, before any finite one too: there mn is -inf as well)
     const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = z == -INFINITY ? 0.f : exp2f(z - mn);
     l = l * a + e;
@@ -2131,7 +2211,7 @@ cudaError_t encode_maps(const ExtendParams& p, int act_dtype, CUtensorMap* q_map
 
 template <typename T, int D, Fill F, bool kScored>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
-  using C = Cfg<D, F>;
+  using C = Cfg<D, F, kScored>;
   constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) + kKv * D : 0);
   static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
   cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F, kScored>>(smem);

@@ -14,6 +14,17 @@ struct PairList {
   int64_t dst[kMaxPairsPerLaunch];
 };
 
+// How scores are shaped (scores.cuh); plain calls leave it empty.
+struct ScoreShape {
+  const float* slopes = nullptr;  // [Hq], or null
+  int32_t capped = 0;
+  float cap_in = 0.f;             // scale / cap
+  float cap_log2 = 0.f;           // cap * log2(e)
+  float poly[6] = {};             // of tanh(y) / y in y^2 up to |y| = 1, times cap_log2
+  float half[4] = {};             // the same up to 1/2
+};
+ScoreShape score_shape(float scale, float softcap, const float* slopes);
+
 struct DecodeParams {
   void* out;                  // [S, Hq, D] q dtype
   const void* q;              // [S, Hq, D] with sequence stride q_seq_stride
@@ -23,7 +34,8 @@ struct DecodeParams {
   int32_t block_size;
   int32_t num_kv_heads;
   const int32_t* block_tables;
-  int32_t bt_stride;
+  int64_t bt_stride;          // entries between rows
+  int32_t bt_width;           // entries of a row
   const int32_t* context_lens;
   int32_t num_seqs;
   int32_t num_q_heads;
@@ -45,6 +57,9 @@ struct DecodeParams {
   int32_t num_groups;
   int32_t* ws_seq;            // workspace [3][num_seqs]: partitions in all, effective prefix,
                               // first member of the sequence's prefix item (for the merge)
+  // launch_decode_scored alone
+  ScoreShape shape;
+  const int32_t* first_pos;   // [S] or null: nothing before it is attended
 };
 
 // First position a decode attends for context length ctx: inside the window
@@ -66,12 +81,20 @@ __host__ __device__ inline int table_index(int j, int ring) { return ring > 0 ? 
 // Whether a context length can be served: linear rows must hold it; every
 // context must be within max_context_len.
 __host__ __device__ inline bool context_ok(const DecodeParams& p, int ctx) {
-  return (p.ring_blocks > 0 || (int64_t)ctx <= (int64_t)p.bt_stride * p.block_size) && ctx <= p.max_context_len;
+  return (p.ring_blocks > 0 || (int64_t)ctx <= (int64_t)p.bt_width * p.block_size) && ctx <= p.max_context_len;
 }
 
-// Partitions of a sequence: windows start at the block holding window_start.
-__host__ __device__ inline int attended_from(const DecodeParams& p, int ctx) {
-  return (window_start(ctx, p.block_size, p.window, p.ring_blocks) / p.block_size) * p.block_size;
+// First position that sequence s attends (its context's end: none).
+__device__ inline int attended_first(const DecodeParams& p, int s, int ctx) {
+  const int t = window_start(ctx, p.block_size, p.window, p.ring_blocks);
+  if (!p.first_pos) return t;
+  const int f = p.first_pos[s], end = ctx > 0 ? ctx : 0;
+  return f > t ? (f < end ? f : end) : t;
+}
+
+// Partitions of a sequence: they start at the block holding attended_first.
+__device__ inline int attended_from(const DecodeParams& p, int s, int ctx) {
+  return (attended_first(p, s, ctx) / p.block_size) * p.block_size;
 }
 
 cudaError_t launch_reshape_and_cache(uint8_t* layer_base, int32_t num_blocks, int32_t block_size,
@@ -104,6 +127,8 @@ cudaError_t launch_merge(const DecodeParams& p, int dtype, int head_size, cudaSt
 // at most kTcMaxSeqs sequences.  Launches the decode kernel and the merge.
 constexpr int kTcMaxSeqs = 8192;
 cudaError_t launch_decode_tc(const DecodeParams& p, int dtype, int group, int num_sms, cudaStream_t stream);
+// The same with shaped scores and starts of each sequence (16-bit caches; 8-bit ones below).
+cudaError_t launch_decode_tc_scored(const DecodeParams& p, int dtype, int group, int num_sms, cudaStream_t stream);
 
 // Causal prefill / extend over a 16-bit cache (tcgen05): head_size 64 or 128,
 // block_size >= 8, group 1, 2, 4, 8 or 16.
@@ -132,6 +157,7 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int dtype, int head_size, 
 // group 1, 2, 4 or 8, at most kTcI8MaxSeqs sequences.  Launches decode and merge.
 constexpr int kTcI8MaxSeqs = 1024;
 cudaError_t launch_decode_tc_i8(const DecodeParams& p, int act_dtype, int group, int num_sms, cudaStream_t stream);
+cudaError_t launch_decode_tc_i8_scored(const DecodeParams& p, int act_dtype, int group, int num_sms, cudaStream_t stream);
 
 // Paged decode with shared prefixes on the tensor cores (16-bit cache, head_size
 // 128, block_size >= 8, group 1, 2, 4 or 8, at most kTcSpMaxSeqs sequences): a
@@ -227,13 +253,10 @@ struct ExtendParams {
   float scale_log2;
   uint32_t* dev_err;
   // launch_extend_scored alone (there query_start_loc may be null: one token a sequence)
-  const float* slopes;            // [Hq] or null
+  ScoreShape shape;
   const int32_t* first_pos;       // [num_tokens] or null
   const int32_t* last_pos;
   int32_t max_context;            // longer contexts are refused
-  int32_t capped;                 // set_cap's
-  float cap_in, cap_log2;         // scale / cap, cap * log2(e)
-  float cap_poly[6];
 };
 // Workspace bytes, and the launches (planner, attention, finish) on a device of `sms` SMs.
 size_t extend_workspace(int num_seqs, int num_tokens, int num_kv_heads, int group, int max_query_len, int head_size,
@@ -242,7 +265,6 @@ cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int a
                           cudaStream_t stream);
 
 // The same with shaped scores.
-void set_cap(ExtendParams& p, float scale, float softcap);
 cudaError_t launch_extend_scored(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                                  cudaStream_t stream);
 

@@ -291,6 +291,14 @@ pa_status rope_params(pkv::RopeParams& p, void* q_out, int64_t q_out_token_strid
   return PA_OK;
 }
 
+// Whether pa_decode_scored runs on the decode kernel, which streams the cache at its full rate; the others (heads of 64,
+// blocks of fewer than 8 tokens in 16-bit caches, groups that are no power of two) are chunks of one token.
+bool decode_scored_on_decode_kernel(const pa_cache_desc* d, int32_t num_seqs, int32_t num_q_heads) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_q_heads % d->num_kv_heads || !tc_by_default(d, num_seqs)) return false;
+  const int group = num_q_heads / d->num_kv_heads;
+  return group == 1 || group == 2 || group == 4 || group == 8 || (group == 16 && !is_i8(d));
+}
+
 // Workspace of pa_extend, or (scored) of the calls with shaped scores.
 size_t extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                               int32_t max_query_len, bool scored) {
@@ -302,9 +310,9 @@ size_t extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32
                                device_sm_count(), scored);
 }
 
-// The checks of pa_extend_strided's arguments (scored: of the calls with shaped scores; single: one token a sequence,
+// The checks of pa_extend_strided's arguments (need: the workspace bytes of these shapes; single: one token a sequence,
 // no query_start_loc), and its launch parameters; *empty: nothing to launch.
-pa_status extend_params(pkv::ExtendParams& p, bool scored, bool single, bool* empty, void* out, const void* q,
+pa_status extend_params(pkv::ExtendParams& p, size_t need, bool single, bool* empty, void* out, const void* q,
                         int64_t q_token_stride, const void* kv_cache, const pa_cache_desc* desc, int32_t layer,
                         const int32_t* block_tables, int64_t block_table_stride, int32_t block_table_width,
                         const int32_t* context_lens, const int32_t* query_start_loc, int32_t num_seqs,
@@ -343,7 +351,6 @@ pa_status extend_params(pkv::ExtendParams& p, bool scored, bool single, bool* em
   if (ring_blocks < 0 || ring_blocks > block_table_width)
     return fail(PA_ERR_INVALID_ARG, "ring_blocks %d not in [0, %d entries of a table row]", ring_blocks,
                 block_table_width);
-  const size_t need = extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len, scored);
   if (workspace_bytes < need)
     return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
   if (need && (!workspace || !aligned16(workspace)))
@@ -381,8 +388,7 @@ pa_status score_params(pkv::ExtendParams& p, float scale, float softcap, const f
   if ((reinterpret_cast<uintptr_t>(slopes) & 3) || (reinterpret_cast<uintptr_t>(first_pos) & 3) ||
       (reinterpret_cast<uintptr_t>(last_pos) & 3))
     return fail(PA_ERR_INVALID_ARG, "slopes, first_pos and last_pos must be 4-byte aligned");
-  pkv::set_cap(p, scale, softcap);
-  p.slopes = slopes;
+  p.shape = pkv::score_shape(scale, softcap, slopes);
   p.first_pos = first_pos;
   p.last_pos = last_pos;
   p.max_context = max_context;
@@ -679,6 +685,7 @@ pa_status pa_decode_window(void* out, const void* q, int64_t q_seq_stride, const
   p.num_kv_heads = desc->num_kv_heads;
   p.block_tables = block_tables;
   p.bt_stride = block_table_stride;
+  p.bt_width = block_table_stride;
   p.context_lens = context_lens;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
@@ -805,6 +812,7 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, int64_t q_seq_stride
   p.num_kv_heads = desc->num_kv_heads;
   p.block_tables = block_tables;
   p.bt_stride = block_table_stride;
+  p.bt_width = block_table_stride;
   p.context_lens = context_lens;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
@@ -910,7 +918,9 @@ size_t pa_extend_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_s
 
 size_t pa_decode_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
                                         int32_t max_context_len) {
-  if (max_context_len <= 0) return 0;
+  if (max_context_len <= 0 || !desc || check_desc(desc) != PA_OK) return 0;
+  if (decode_scored_on_decode_kernel(desc, num_seqs, num_q_heads))
+    return pa_decode_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len, 0);
   return extend_workspace_bytes(desc, num_seqs, num_seqs, num_q_heads, 1, true);
 }
 
@@ -932,7 +942,7 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
                             size_t workspace_bytes, uint32_t* dev_err, void* stream) {
   pkv::ExtendParams p{};
   bool empty = false;
-  const pa_status st = extend_params(p, false, false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
+  const pa_status st = extend_params(p, pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len), false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
                                      block_tables, block_table_stride, block_table_width, context_lens,
                                      query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
                                      ring_blocks, workspace, workspace_bytes, dev_err);
@@ -953,7 +963,7 @@ pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, con
   bool empty = false;
   pa_status st = score_params(p, scale, softcap, slopes, first_pos, last_pos, INT32_MAX);
   if (st != PA_OK) return st;
-  st = extend_params(p, true, false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
+  st = extend_params(p, pa_extend_scored_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len), false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
                      block_tables, block_table_stride, block_table_width, context_lens,
                      query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
                      ring_blocks, workspace, workspace_bytes, dev_err);
@@ -974,12 +984,55 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
   bool empty = false;
   pa_status st = score_params(p, scale, softcap, slopes, first_pos, nullptr, max_context_len);
   if (st != PA_OK) return st;
-  st = extend_params(p, true, true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
+  st = extend_params(p, pa_decode_scored_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len), true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
                      block_table_stride, block_table_width, context_lens, nullptr, num_seqs, num_seqs, num_q_heads, 1,
                      scale, window, ring_blocks, workspace, workspace_bytes, dev_err);
   if (st != PA_OK || empty) return st;
-  cudaError_t e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size,
-                                            is_i8(desc), static_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (decode_scored_on_decode_kernel(desc, num_seqs, num_q_heads)) {
+    pkv::DecodeParams d{};
+    d.out = out;
+    d.q = q;
+    d.q_seq_stride = q_seq_stride;
+    d.cache = p.cache;
+    d.num_blocks = desc->num_blocks;
+    d.block_size = desc->block_size;
+    d.num_kv_heads = desc->num_kv_heads;
+    d.block_tables = block_tables;
+    d.bt_stride = block_table_stride;
+    d.bt_width = block_table_width;
+    d.context_lens = context_lens;
+    d.num_seqs = num_seqs;
+    d.num_q_heads = num_q_heads;
+    d.max_context_len = max_context_len;
+    // the partitions that a windowed span wants, unless there would be more of them than the workspace of
+    // max_context_len holds (its own partition size always fits)
+    const int32_t span = pa_decode_window_span(max_context_len, desc->block_size, window, ring_blocks);
+    const int32_t most_P = pa_decode_partition_size(desc, num_seqs, max_context_len, 0);
+    const int32_t most = (max_context_len - 1) / most_P + 1;
+    int32_t P = pa_decode_partition_size(desc, num_seqs, span, 0);
+    while (P < most_P && (span - 1) / P + 1 > most) P *= 2;
+    d.partition_size = P;
+    d.max_parts = (span - 1) / P + 1;
+    d.scale_log2 = p.scale_log2;
+    if (d.max_parts > 1) {
+      d.ws_o = static_cast<float*>(workspace);
+      d.ws_ml = d.ws_o + (int64_t)num_seqs * num_q_heads * d.max_parts * desc->head_size;
+    }
+    d.dev_err = dev_err;
+    d.window = window;
+    d.ring_blocks = ring_blocks;
+    d.shape = p.shape;
+    d.first_pos = first_pos;
+    const int group = num_q_heads / desc->num_kv_heads;
+    e = is_i8(desc) ? pkv::launch_decode_tc_i8_scored(d, act_dtype(desc), group, device_sm_count(),
+                                                      static_cast<cudaStream_t>(stream))
+                    : pkv::launch_decode_tc_scored(d, act_dtype(desc), group, device_sm_count(),
+                                                   static_cast<cudaStream_t>(stream));
+  } else {
+    e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size, is_i8(desc),
+                                  static_cast<cudaStream_t>(stream));
+  }
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "decode_scored launch");
 }
 

@@ -1,0 +1,38 @@
+// scores.cuh -- what happens to a score between q.k and the softmax where it is
+// capped or falls with distance: the same arithmetic in every kernel.
+//
+// With y = scale q.k / c, a cap c makes c tanh(y) of it.  Up to |y| = 1 that is y
+// P(y^2) with a polynomial P of degree 5, fitted to tanh(y) / y by weighted least
+// squares until its relative error is level (5.9e-7); beyond, c (1 - 2 / (1 +
+// e^(2y))), whose absolute error of a few 2^-24 c is as small beside a result of
+// at least 0.76 c.  Everything is in base-2 units (times log2 e) and fp32.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+
+namespace pkv {
+namespace score {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// c tanh(y) for |y| <= 1.
+__device__ __forceinline__ float near_cap(const ScoreShape& w, float y) {
+  const float s = y * y;
+  float v = w.poly[5];
+#pragma unroll
+  for (int k = 4; k >= 0; --k) v = fmaf(v, s, w.poly[k]);
+  return v * y;
+}
+
+// c tanh(y) for any y (NaN stays NaN, infinities become -c and c).
+__device__ __forceinline__ float any_cap(const ScoreShape& w, float y) {
+  const float v = near_cap(w, y);
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(y * (2.f * kLog2e), 64.f)));
+  return fabsf(y) > 1.f ? w.cap_log2 * (1.f - __fdividef(2.f, 1.f + e)) : v;
+}
+
+}  // namespace score
+}  // namespace pkv

@@ -112,7 +112,7 @@ def _extend(lib, desc=None, S=2, T=100, Hq=4, max_q=100, q=FAKE, out=FAKE + (1 <
                                 V(slopes), V(first), V(last), V(ws), ws_bytes, None, None)
 
 
-def _decode(lib, desc=None, S=2, Hq=4, max_ctx=100, q=FAKE, out=FAKE + (1 << 24), scale=0.1, window=0, ring=0, stride=8, width=8, cap=0.0, slopes=FAKE,
+def _decode(lib, desc=None, S=2, Hq=4, max_ctx=9000, q=FAKE, out=FAKE + (1 << 24), scale=0.1, window=0, ring=0, stride=8, width=8, cap=0.0, slopes=FAKE,
             first=FAKE, ws=FAKE, ws_bytes=1 << 40, ctx=FAKE):
     return lib.pa_decode_scored(V(out), V(q), Hq * 128, V(), desc or _desc(), 0, V(), stride, width, V(ctx), S, Hq, max_ctx, scale, window, ring, cap, V(slopes),
                                 V(first), V(ws), ws_bytes, None, None)
@@ -145,7 +145,9 @@ def test_scored_refusals_of_their_own(lib):
 def test_workspaces(lib):
     d = CacheDesc(16, 16, 2, 128, torch.bfloat16)
     assert _lib.extend_scored_workspace_bytes(d, 4, 100, 8, 50) >= _lib.extend_workspace_bytes(d, 4, 100, 8, 50) > 0
-    assert _lib.decode_scored_workspace_bytes(d, 4, 8, 100) == _lib.extend_scored_workspace_bytes(d, 4, 4, 8, 1)
+    assert _lib.decode_scored_workspace_bytes(d, 4, 8, 9000) == _lib.decode_workspace_bytes(d, 4, 8, 9000) > 0      # the decode kernel
+    odd = CacheDesc(16, 16, 2, 128, torch.bfloat16)
+    assert _lib.decode_scored_workspace_bytes(odd, 4, 6, 9000) == _lib.extend_scored_workspace_bytes(odd, 4, 4, 6, 1) > 0
     for args in ((0, 8, 100), (4, 0, 100), (4, 8, 0), (4, 9, 100), (4, 34, 100)):
         assert _lib.decode_scored_workspace_bytes(d, *args) == 0
     assert _lib.extend_scored_workspace_bytes(d, 4, 100, 8, 0) == 0
