@@ -8,22 +8,33 @@ ScoreShape score_shape(float scale, float softcap, const float* slopes) {
   // tanh(y) / y in powers of y^2 on [0, 1]
   const double fit[6] = {0.9999994039535522, -0.3332904279232025, 0.13281433284282684, -0.051605675369501114,
                          0.016743116080760956, -0.0030670606065541506};
-  const double half[4] = {0.999999463558197, -0.33326318860054016, 0.13190296292304993, -0.04440222680568695};    // the same on [0, 1/2]
+  const double near[5] = {0.999999463558197, -0.3332825303077698, 0.13258983194828033, -0.05005630478262901, 0.01292963232845068};    // the same on [0, 3/4]: within 5.7e-7
   const double log2e = 1.4426950408889634;
   ScoreShape w;
   w.slopes = slopes;
   w.capped = softcap > 0.f;
   if (!w.capped) return w;
   w.cap_in = (float)((double)scale / softcap);
+  w.cap_out = (float)((double)softcap / scale);
   w.cap_log2 = (float)(softcap * log2e);
   for (int i = 0; i < 6; ++i) w.poly[i] = (float)(fit[i] * softcap * log2e);
-  for (int i = 0; i < 4; ++i) w.half[i] = (float)(half[i] * softcap * log2e);
+  double in = w.cap_in;
+  for (int i = 0; i < 5; ++i, in *= (double)w.cap_in * w.cap_in) {
+    w.three_quarters[i] = (float)(near[i] * softcap * log2e);
+    w.folded[i] = (float)(near[i] * softcap * log2e * in);
+  }
+  // cap_in^9 beside a cap of at least 2^-14, and squares of up to 2^36: normal numbers all
+  w.folds = w.cap_in >= 0x1p-12f && w.cap_in <= 0x1p10f;
   return w;
 }
 
 cudaError_t launch_extend_scored(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                                  cudaStream_t stream) {
-  return launch<true>(p, workspace, sms, act_dtype, head_size, i8, stream);
+  const bool capped = p.shape.capped, sloped = p.shape.slopes != nullptr;
+  if (!capped && !sloped) return launch_extend_spans(p, workspace, sms, act_dtype, head_size, i8, stream);
+  if (!capped) return launch_extend_slopes(p, workspace, sms, act_dtype, head_size, i8, stream);
+  if (!sloped && p.shape.folds) return launch_extend_cap(p, workspace, sms, act_dtype, head_size, i8, stream);
+  return launch<kAny>(p, workspace, sms, act_dtype, head_size, i8, stream);
 }
 
 }  // namespace pkv

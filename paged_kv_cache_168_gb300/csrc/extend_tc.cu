@@ -12,7 +12,7 @@ size_t extend_workspace(int num_seqs, int num_tokens, int num_kv_heads, int grou
 
 cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                           cudaStream_t stream) {
-  return launch<false>(p, workspace, sms, act_dtype, head_size, i8, stream);
+  return launch<kNone>(p, workspace, sms, act_dtype, head_size, i8, stream);
 }
 
 }  // namespace pkv

@@ -454,6 +454,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
 }
 
 // ------------------------------------------------------------------ the attention kernel
+// What scores become, in kernels of their own: with conditions inside, a tile's code outgrows the instruction cache,
+// and a warp alone with it waits 2 to 5 clocks for each instruction.
+enum Shape {
+  kNone,                                   // pa_extend
+  kSpans,                                  // spans of each query alone
+  kCap,                                    // a cap that folds (scores.cuh)
+  kSlope,                                  // slopes alone
+  kAny                                     // both, or a cap that does not fold
+};
+
 // How the K and V stages are filled.
 enum Fill { kBulk, kGather, kCodes };
 
@@ -479,7 +489,7 @@ struct Work {
   int part_row, flag;
 };
 
-template <int D, Fill F, bool kScored>
+template <int D, Fill F>
 struct Cfg {
   static constexpr int kTileBytes = kKv * D * 2;              // K (or V) of one KV tile
   static constexpr int kGroupBytes = 8 * D * 2;               // 8 tokens of it
@@ -489,8 +499,8 @@ struct Cfg {
   // registers a thread, whose sum over the warpgroups is the launch's: the softmax
   // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
   // caches half of a tile's codes (8 registers more or fewer for the softmax: within 2%)
-  static constexpr int kRegsSoftmax = F == kBulk ? (kScored ? 216 : 200) : F == kGather ? (kScored ? 184 : 176) : 160;
-  static constexpr int kRegsRest = F == kBulk ? (kScored ? 72 : 104) : F == kGather ? (kScored ? 72 : 88) : 96;
+  static constexpr int kRegsSoftmax = F == kBulk ? 200 : F == kGather ? 176 : 160;
+  static constexpr int kRegsRest = F == kBulk ? 104 : F == kGather ? 88 : 96;
   static constexpr int kRegsConvert = F == kGather ? 72 : 96;
   static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
@@ -566,10 +576,10 @@ __device__ __forceinline__ uint64_t add2f(uint64_t a, uint64_t b) {
   return r;
 }
 
-// tanh(y) / y times c for two y: |y| <= 1/2 (kTerms 4: a polynomial of degree 3 in y^2, relative error 5.4e-7) or <= 1.
+// tanh(y) / y times c for two y: |y| <= 3/4 (kTerms 5) or <= 1 (kTerms 6).
 template <int kTerms>
 __device__ __forceinline__ uint64_t cap_quotient2(const ScoreShape& w, uint64_t y) {
-  const float* c = kTerms == 4 ? w.half : w.poly;
+  const float* c = kTerms == 5 ? w.three_quarters : w.poly;
   const uint64_t s = mul2f(y, y);
   uint64_t v = pack2f(c[kTerms - 1], c[kTerms - 1]);
 #pragma unroll
@@ -666,6 +676,13 @@ __device__ __forceinline__ void tmem_st16x128(uint32_t taddr, const uint32_t* r)
                : "memory");
 }
 
+// The same of 16 columns (32 weights).
+__device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 32 TMEM lanes x 32 columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -746,13 +763,13 @@ __device__ __forceinline__ int block_of(const ExtendParams& p, const int32_t* ro
   return row[p.ring_blocks > 0 ? blk % p.ring_blocks : blk];
 }
 
-template <typename T, int D, Fill F, bool kScored>
-__global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
+template <typename T, int D, Fill F, int kShape>
+__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
                                                                        const __grid_constant__ Space ws,
                                                                        const __grid_constant__ CUtensorMap q_map,
                                                                        const __grid_constant__ CUtensorMap kv_map) {
-  using C = Cfg<D, F, kScored>;
-  constexpr bool kI8 = F == kCodes;
+  using C = Cfg<D, F>;
+  constexpr bool kI8 = F == kCodes, kScored = kShape != kNone;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   using PT = typename std::conditional<kI8, __half, T>::type;      // type of the weights and of V's operand
   // (no static shared memory: the operands start 1024-byte aligned without padding)
@@ -1417,7 +1434,10 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
       const float slope2 = kScored && p.shape.slopes ? p.shape.slopes[w.kvh * G + head] * score::kLog2e : 0.f;
       const int n = t == 0 ? w.n[0] : w.n[1];
       const int tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
-      float m = -INFINITY, l = 0.f;
+      // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 96 in base 2 they are taken
+      // against 0, without a maximum (2^96 times 2^20 tokens and 2^-96 are far inside that range).  Slopes leave it.
+      const bool fixed = kShape == kCap && !kI8 && kBF16 && p.shape.cap_log2 <= 96.f;
+      float m = fixed ? 0.f : -INFINITY, l = 0.f;
       // 8-bit caches: a thread has rows gr + 8 i of its warp's 32 (and a quarter of their columns)
       float m4[4], l4[4];
       int pos4[4];
@@ -1469,86 +1489,69 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
                          x[8 * e + 5 + 2 * r]);
               }
             }
-            if constexpr (kScored) {
-              // (the K scales made x base-2 scores, or quotients by the cap)
-              if (p.shape.capped || p.shape.slopes) {
-                bool exact = false;
-                float sl[2] = {0.f, 0.f}, big[2] = {0.f, 0.f};
-                int at[2];                                           // first column less the row's reference position
+            if constexpr (kShape != kNone && kShape != kSpans) {
+              // (K's scales made x base-2 scores, or quotients by the cap)
+              bool exact = false;
+              float sl[2] = {0.f, 0.f};
+              int at[2] = {0, 0};                                    // my first column less the row's reference position
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const bool is_row = ok4 >> r & 1;
+                if constexpr (kShape != kCap) {
+                  const int rr = (warp & 3) * 32 + (lane >> 2) + 8 * (2 * h + r);
+                  int nearest = pos4[r];
+                  if (p.last_pos) {
+                    nearest = min(nearest, span_to<true>(p, pos4[r], w.kv_end, w.row0 + (is_row ? pos4[r] - w.pos0 : 0)));
+                    exact |= is_row && t0 + kKv - 1 > nearest;
+                  }
+                  if (p.shape.slopes) sl[r] = p.shape.slopes[w.kvh * G + rr % G] * score::kLog2e;
+                  at[r] = t0 + 2 * (lane & 3) - nearest;
+                }
+                if constexpr (kShape != kSlope) {
+                  float big[2] = {0.f, 0.f};
+#pragma unroll
+                  for (int n = 0; n < 16; ++n) big[n & 1] = fmaxf(fmaxf(big[n & 1], fabsf(x[4 * n + 2 * r])), fabsf(x[4 * n + 2 * r + 1]));
+                  exact |= is_row && fmaxf(big[0], big[1]) > (kShape == kCap ? 0.75f : 1.f);
+                }
+              }
+              if (__builtin_expect(__any_sync(kFull, exact), 0)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) tmem_st16x256_32(s_addr + half + 32 * e, x + 16 * e);
+                tc::tmem_wait_st();
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                  float v[16];
+                  tmem_ld16x256_32(s_addr + half + 32 * e, v);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    v[k] = shaped_score(p.shape, v[k], sl[k >> 1 & 1], at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + (k & 1));
+                  tmem_st16x256_32(s_addr + half + 32 * e, v);
+                }
+                tc::tmem_wait_st();
+                tmem_ld16x256(s_addr + half, x);
+              } else {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const bool is_row = ok4 >> r & 1;
-                  const int rr = (warp & 3) * 32 + (lane >> 2) + 8 * (2 * h + r);
-                  if (p.shape.slopes) sl[r] = p.shape.slopes[w.kvh * G + rr % G] * score::kLog2e;
-                  const int tok = w.row0 + (is_row ? pos4[r] - w.pos0 : 0);
-                  const int nearest = min(pos4[r], span_to<kScored>(p, pos4[r], w.kv_end, tok));
-                  at[r] = t0 - nearest;
-                  exact |= p.shape.slopes && p.last_pos && is_row && t0 + kKv - 1 > nearest;
-                  if (p.shape.capped) {
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) big[r] = fmaxf(fmaxf(big[r], fabsf(x[4 * n + 2 * r])), fabsf(x[4 * n + 2 * r + 1]));
-                    if (!is_row) big[r] = 0.f;
-                  }
-                }
-                exact |= fmaxf(big[0], big[1]) > 1.f;
-                if (__builtin_expect(__any_sync(kFull, exact), 0)) {
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) tmem_st16x256_32(s_addr + half + 32 * e, x + 16 * e);
-                  tc::tmem_wait_st();
-#pragma unroll 1
-                  for (int e = 0; e < 4; ++e) {
-                    float v[16];
-                    tmem_ld16x256_32(s_addr + half + 32 * e, v);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                      v[k] = shaped_score(p.shape, v[k], sl[k >> 1 & 1], at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + 2 * (lane & 3) + (k & 1));
-                    tmem_st16x256_32(s_addr + half + 32 * e, v);
-                  }
-                  tc::tmem_wait_st();
-                  tmem_ld16x256(s_addr + half, x);
-                } else {
-                  // in place; a slope's part in full where every 32 columns' first one is, and within those:
-                  // both products small or exact, no sum of many steps
-                  uint64_t in[2][4];
-#pragma unroll
-                  for (int r = 0; r < 2; ++r)
+                  // a slope's part: that of 32 columns' first one, and that within those (no sum of many steps)
+                  uint64_t in[4], off[4];
+                  if constexpr (kShape != kCap) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                      const float col = (float)(8 * k + 2 * (lane & 3));
-                      in[r][k] = pack2f(sl[r] * col, sl[r] * (col + 1.f));
+                      const float v = sl[r] * (float)(at[r] + 32 * k);
+                      in[k] = pack2f(sl[r] * (8.f * k), sl[r] * (8.f * k + 1.f));
+                      off[k] = pack2f(v, v);
                     }
-                  if (p.shape.capped) {
-                    if (!__any_sync(kFull, fmaxf(big[0], big[1]) > 0.5f)) {
-#pragma unroll
-                      for (int e = 0; e < 64; e += 2) {
-                        const uint64_t y = pack2f(x[e], x[e + 1]);
-                        unpack2f(fma2f(y, cap_quotient2<4>(p.shape, y), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
-                      }
-                    } else {
-#pragma unroll
-                      for (int e = 0; e < 64; e += 2) {
-                        const uint64_t y = pack2f(x[e], x[e + 1]);
-                        unpack2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
-                      }
-                    }
-                  } else {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 2)
-                      unpack2f(add2f(pack2f(x[e], x[e + 1]), in[e >> 1 & 1][e >> 2 & 3]), x[e], x[e + 1]);
                   }
-                  if (p.shape.slopes) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                      for (int c = 0; c < 4; ++c) {
-                        const float off = sl[r] * (float)(at[r] + 32 * c);
-                        const uint64_t off2 = pack2f(off, off);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                          const int e = 16 * c + 4 * k + 2 * r;
-                          unpack2f(add2f(pack2f(x[e], x[e + 1]), off2), x[e], x[e + 1]);
-                        }
-                      }
+                  for (int n = 0; n < 16; ++n) {
+                    const int e = 4 * n + 2 * r;
+                    const uint64_t y = pack2f(x[e], x[e + 1]);
+                    if constexpr (kShape == kCap)
+                      unpack2f(mul2f(y, cap_quotient2<5>(p.shape, y)), x[e], x[e + 1]);
+                    else if constexpr (kShape == kSlope)
+                      unpack2f(add2f(add2f(y, in[n & 3]), off[n >> 2]), x[e], x[e + 1]);
+                    else
+                      unpack2f(add2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[n & 3]), off[n >> 2]), x[e], x[e + 1]);
                   }
                 }
               }
@@ -1688,73 +1691,67 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
           float x[kKv];
           tmem_ld64(s_addr, x);
           tmem_ld64(s_addr + 64, x + 64);
-          float unit = p.scale_log2;                                 // what makes x base-2 scores
-          // shaped scores: x unit + ahead(column / 16) is the base-2 score, or (fly) x is still q.k, to be capped in the
-          // loop that takes the powers, which leaves the units of these products idle
-          float so = 0.f, base = 0.f, most = 0.f;
-          bool fly = false, tight = false;
-          if constexpr (kScored) {
-            const bool capped = p.shape.capped, sloped = p.shape.slopes;
-            if (capped || sloped) {
-              int ref = pos;                                         // distances count from the nearest attended position
-              if (sloped && p.last_pos) ref = min(pos, span_to<kScored>(p, pos, w.kv_end, token));
-              bool exact = sloped && p.last_pos && row_ok && t0 + kKv - 1 > ref;
-              if (capped) {
-                float hi[2] = {-INFINITY, -INFINITY}, lo[2] = {INFINITY, INFINITY};
+          // Shaped scores: x unit + ahead(column / 16) is the base-2 score; under a cap x stays q.k (fly) and is capped in
+          // the loop that takes the powers.
+          float unit = p.scale_log2, so = 0.f, base = 0.f, most = 0.f;
+          bool fly = kShape == kCap;
+          if constexpr (kShape != kNone && kShape != kSpans) {
+            int ref = pos;                                           // distances count from the nearest attended position
+            bool exact = false;
+            if (kShape != kCap && p.last_pos) {
+              ref = min(pos, span_to<true>(p, pos, w.kv_end, token));
+              exact = row_ok && t0 + kKv - 1 > ref;
+            }
+            if constexpr (kShape != kSlope) {
+              float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < kKv; e += 4)
+              for (int e = 0; e < kKv; e += 8)
 #pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    hi[k] = fmaxf(fmaxf(hi[k], x[e + k]), x[e + 2 + k]);
-                    lo[k] = fminf(fminf(lo[k], x[e + k]), x[e + 2 + k]);
-                  }
-                most = fmaxf(hi[0], hi[1]) * p.shape.cap_in;
-                const float size = row_ok ? fmaxf(fabsf(most), fabsf(fminf(lo[0], lo[1]) * p.shape.cap_in)) : 0.f;
-                exact |= size > 1.f;
-                tight = !__any_sync(kFull, size > 0.5f);
-              }
-              if (__builtin_expect(__any_sync(kFull, exact), 0)) {
+                for (int k = 0; k < 4; ++k) big[k] = fmaxf(fmaxf(big[k], fabsf(x[e + k])), fabsf(x[e + 4 + k]));
+              exact |= row_ok && fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * p.shape.cap_in > (kShape == kCap ? 0.75f : 1.f);
+            }
+            if (__builtin_expect(__any_sync(kFull, exact), 0)) {
+              // any form, 16 columns at a time through TMEM
 #pragma unroll 1
-                for (int e = 0; e < kKv; e += 16) {
-                  float v[16];
-                  tc::tmem_ld16(s_addr + e, v);
+              for (int e = 0; e < kKv; e += 16) {
+                float v[16];
+                tc::tmem_ld16(s_addr + e, v);
 #pragma unroll
-                  for (int k = 0; k < 16; ++k)
-                    v[k] = shaped_score(p.shape, v[k] * (capped ? p.shape.cap_in : p.scale_log2), slope2, t0 + e + k - ref);
-                  tc::tmem_st16(s_addr + e, v);
-                }
-                tc::tmem_wait_st();
-                tmem_ld64(s_addr, x);
-                tmem_ld64(s_addr + 64, x + 64);
-                unit = 1.f;
-              } else if (capped && !sloped && !edge) {
-                fly = true;
-              } else {
-                if (sloped) {
-                  so = slope2;
-                  base = slope2 * (float)(t0 - ref);
-                }
-                uint64_t in[8];                                      // the slope's part within 16 columns
-#pragma unroll
-                for (int k = 0; k < 8; ++k) in[k] = pack2f(so * (2.f * k), so * (2.f * k + 1.f));
-                if (capped) {
-                  const uint64_t in2 = pack2f(p.shape.cap_in, p.shape.cap_in);
-#pragma unroll
-                  for (int e = 0; e < kKv; e += 2) {
-                    const uint64_t y = mul2f(pack2f(x[e], x[e + 1]), in2);
-                    unpack2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[e / 2 % 8]), x[e], x[e + 1]);
-                  }
-                } else {
-                  const uint64_t u2 = pack2f(unit, unit);
-#pragma unroll
-                  for (int e = 0; e < kKv; e += 2)
-                    unpack2f(fma2f(pack2f(x[e], x[e + 1]), u2, in[e / 2 % 8]), x[e], x[e + 1]);
-                }
-                unit = 1.f;
+                for (int k = 0; k < 16; ++k)
+                  v[k] = shaped_score(p.shape, v[k] * (p.shape.capped ? p.shape.cap_in : p.scale_log2), slope2, t0 + e + k - ref);
+                tc::tmem_st16(s_addr + e, v);
               }
+              tc::tmem_wait_st();
+              tmem_ld64(s_addr, x);
+              tmem_ld64(s_addr + 64, x + 64);
+              unit = 1.f;
+              fly = false;
+            } else if constexpr (kShape != kCap) {
+              if (p.shape.slopes) {
+                so = slope2;
+                base = slope2 * (float)(t0 - ref);
+              }
+              uint64_t in[8];                                        // the slope's part within 16 columns
+#pragma unroll
+              for (int k = 0; k < 8; ++k) in[k] = pack2f(so * (2.f * k), so * (2.f * k + 1.f));
+              const float u = kShape == kSlope ? p.scale_log2 : p.shape.cap_in;
+              const uint64_t u2 = pack2f(u, u);
+#pragma unroll
+              for (int e = 0; e < kKv; e += 2) {
+                if constexpr (kShape == kSlope) {
+                  unpack2f(fma2f(pack2f(x[e], x[e + 1]), u2, in[e / 2 % 8]), x[e], x[e + 1]);
+                } else {
+                  const uint64_t y = mul2f(pack2f(x[e], x[e + 1]), u2);
+                  unpack2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[e / 2 % 8]), x[e], x[e + 1]);
+                }
+              }
+              unit = 1.f;
             }
           }
-          auto ahead = [&](int c) { return kScored ? fmaf(so, 16.f * c, base) : 0.f; };
+          auto ahead = [&](int k) { return kShape == kSlope || kShape == kAny ? fmaf(so, 16.f * k, base) : 0.f; };
+          // what a masked place holds: under a cap, in the powers' loop, what the polynomial takes to far below 0
+          float none = -INFINITY;
+          if (kShape == kCap && fixed && fly) none = -64.f * p.shape.cap_out;
           if (edge) {
             // attended columns [lo, hi)
             const int lo = (kScored ? span_from<kScored>(p, pos, w.held, token) : from) - t0;
@@ -1765,7 +1762,7 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
               const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
               if (__any_sync(kFull, on != kFull)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
+                for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : none;
               }
             }
             if constexpr (F == kBulk) {
@@ -1785,51 +1782,59 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
               }
             }
           }
-          float mt;
-          if constexpr (!kScored) {
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
+          if (!fixed) {
+            float mt;
+            if constexpr (kShape == kSlope || kShape == kAny) {
+              float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < kKv; e += 8)
+              for (int k = 0; k < kKv / 16; ++k) {
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
-            mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
-          } else if (fly) {
-            mt = score::any_cap(p.shape, most);                      // (the cap keeps the order)
-          } else {
-            float best[2] = {-INFINITY, -INFINITY};
+                for (int e = 0; e < 16; e += 4)
 #pragma unroll
-            for (int c = 0; c < kKv / 16; ++c) {
-              float top[2] = {-INFINITY, -INFINITY};
+                  for (int i = 0; i < 2; ++i) top[i] = fmaxf(fmaxf(top[i], x[16 * k + e + i]), x[16 * k + e + 2 + i]);
+                best[k & 1] = fmaxf(best[k & 1], fmaxf(top[0], top[1]) + ahead(k));
+              }
+              mt = fmaxf(best[0], best[1]);
+            } else {
+              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
+              for (int e = 0; e < kKv; e += 8)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) top[k] = fmaxf(fmaxf(top[k], x[16 * c + e + k]), x[16 * c + e + 2 + k]);
-              best[c & 1] = fmaxf(best[c & 1], fmaf(fmaxf(top[0], top[1]), unit, ahead(c)));
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
+              mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+              if (kShape == kCap && fly)
+                mt = mt == -INFINITY ? mt : score::any_cap(p.shape, mt * p.shape.cap_in);      // (the cap keeps the order)
+              else
+                mt *= unit;
             }
-            mt = fmaxf(best[0], best[1]);
-          }
-          const float m_new = fmaxf(m, mt);
-          const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
-          if (m == -INFINITY) m = m_new;
-          if (__any_sync(kFull, need)) {
-            // O holds exactly the tiles before this one once the last PV has completed
-            if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
-            const float alpha = need ? exp2f(m - m_new) : 1.f;
-            if (need) {
-              l *= alpha;
-              m = m_new;
-            }
+            const float m_new = fmaxf(m, mt);
+            const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
+            if (m == -INFINITY) m = m_new;
+            if (__any_sync(kFull, need)) {
+              // O holds exactly the tiles before this one once the last PV has completed
+              if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
+                ok = false;
+                break;
+              }
+              tc::fence_after_sync();
+              const float alpha = need ? exp2f(m - m_new) : 1.f;
+              if (need) {
+                l *= alpha;
+                m = m_new;
+              }
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              float o[16];
-              tc::tmem_ld16(o_addr + e * 16, o);
+              for (int e = 0; e < D / 16; ++e) {
+                float o[16];
+                tc::tmem_ld16(o_addr + e * 16, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= alpha;
-              tc::tmem_st16(o_addr + e * 16, o);
+                for (int k = 0; k < 16; ++k) o[k] *= alpha;
+                tc::tmem_st16(o_addr + e * 16, o);
+              }
+            }
+            if (kShape == kCap && fly && edge) {
+#pragma unroll
+              for (int e = 0; e < kKv; ++e) x[e] = x[e] == -INFINITY ? -64.f * p.shape.cap_out : x[e];
             }
           }
           // weights 2^(x - m), the sum of the unrounded ones in fp32
@@ -1854,25 +1859,22 @@ __global__ void __launch_bounds__(Cfg<D, F, kScored>::kThreads, 1) extend_kernel
             }
           };
           const uint64_t unit2 = pack2f(unit, unit), nm2 = pack2f(nm, nm);
-          if constexpr (!kScored) {
-            weigh([&](uint64_t xx, int) { return fma2f(xx, unit2, nm2); });
-          } else if (!fly) {
+          if (kShape == kCap && fly) {
+            weigh([&](uint64_t xx, int) {
+              const float* f = p.shape.folded;
+              const uint64_t z = mul2f(xx, xx);
+              uint64_t v = pack2f(f[4], f[4]);
+#pragma unroll
+              for (int k = 3; k >= 0; --k) v = fma2f(v, z, pack2f(f[k], f[k]));
+              return fma2f(xx, v, nm2);
+            });
+          } else if (kShape == kSlope || kShape == kAny) {
             weigh([&](uint64_t xx, int col) {
               const float v = nm + ahead(col / 16);
-              return fma2f(xx, unit2, pack2f(v, v));
+              return add2f(xx, pack2f(v, v));
             });
           } else {
-            const uint64_t in2 = pack2f(p.shape.cap_in, p.shape.cap_in);
-            if (tight)
-              weigh([&](uint64_t xx, int) {
-                const uint64_t y = mul2f(xx, in2);
-                return fma2f(y, cap_quotient2<4>(p.shape, y), nm2);
-              });
-            else
-              weigh([&](uint64_t xx, int) {
-                const uint64_t y = mul2f(xx, in2);
-                return fma2f(y, cap_quotient2<6>(p.shape, y), nm2);
-              });
+            weigh([&](uint64_t xx, int) { return fma2f(xx, unit2, nm2); });
           }
           {
             float a, b;
@@ -2209,42 +2211,43 @@ cudaError_t encode_maps(const ExtendParams& p, int act_dtype, CUtensorMap* q_map
   return cudaSuccess;
 }
 
-template <typename T, int D, Fill F, bool kScored>
+template <typename T, int D, Fill F, int kShape>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
-  using C = Cfg<D, F, kScored>;
+  using C = Cfg<D, F>;
+  constexpr bool kScored = kShape != kNone;
   constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) + kKv * D : 0);
   static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
-  cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F, kScored>>(smem);
+  cudaError_t e = set_smem_attribute_once<extend_kernel<T, D, F, kShape>>(smem);
   if (e != cudaSuccess) return e;
   CUtensorMap q_map{}, kv_map{};
   e = encode_maps<D, F, kScored>(p, std::is_same<T, __half>::value ? PA_F16 : PA_BF16, &q_map, &kv_map);
   if (e != cudaSuccess) return e;
   plan_kernel<kScored><<<1, kPlanThreads, 0, stream>>>(p, ws, sms);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_early(extend_kernel<T, D, F, kScored>, sms, C::kThreads, smem, stream, p, ws, q_map, kv_map);
+  e = launch_early(extend_kernel<T, D, F, kShape>, sms, C::kThreads, smem, stream, p, ws, q_map, kv_map);
   if (e != cudaSuccess) return e;
   return launch_early(finish_kernel<T, D, F == kCodes, kScored>, 2 * sms, 256, 0, stream, p, ws);
 }
 
-template <bool kScored, typename T>
+template <int kShape, typename T>
 cudaError_t launch_typed(const ExtendParams& p, const Space& ws, int sms, int head_size, bool i8, cudaStream_t stream) {
-  if (i8) return launch_fill<T, 128, kCodes, kScored>(p, ws, sms, stream);
+  if (i8) return launch_fill<T, 128, kCodes, kShape>(p, ws, sms, stream);
   const bool bulk = p.block_size >= 8;                               // whole 8-token groups
   if (head_size == 128)
-    return bulk ? launch_fill<T, 128, kBulk, kScored>(p, ws, sms, stream)
-                : launch_fill<T, 128, kGather, kScored>(p, ws, sms, stream);
-  return bulk ? launch_fill<T, 64, kBulk, kScored>(p, ws, sms, stream)
-              : launch_fill<T, 64, kGather, kScored>(p, ws, sms, stream);
+    return bulk ? launch_fill<T, 128, kBulk, kShape>(p, ws, sms, stream)
+                : launch_fill<T, 128, kGather, kShape>(p, ws, sms, stream);
+  return bulk ? launch_fill<T, 64, kBulk, kShape>(p, ws, sms, stream)
+              : launch_fill<T, 64, kGather, kShape>(p, ws, sms, stream);
 }
 
-template <bool kScored>
+template <int kShape>
 cudaError_t launch(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                    cudaStream_t stream) {
   size_t bytes;
   const Space ws = lay_out(static_cast<uint8_t*>(workspace), p.num_seqs, p.num_tokens, p.num_kv_heads, p.group,
-                           p.max_query_len, head_size, sms, kScored, &bytes);
-  return act_dtype == PA_F16 ? launch_typed<kScored, __half>(p, ws, sms, head_size, i8, stream)
-                             : launch_typed<kScored, __nv_bfloat16>(p, ws, sms, head_size, i8, stream);
+                           p.max_query_len, head_size, sms, kShape != kNone, &bytes);
+  return act_dtype == PA_F16 ? launch_typed<kShape, __half>(p, ws, sms, head_size, i8, stream)
+                             : launch_typed<kShape, __nv_bfloat16>(p, ws, sms, head_size, i8, stream);
 }
 
 }  // namespace

@@ -19,9 +19,12 @@ struct ScoreShape {
   const float* slopes = nullptr;  // [Hq], or null
   int32_t capped = 0;
   float cap_in = 0.f;             // scale / cap
+  float cap_out = 0.f;            // cap / scale
   float cap_log2 = 0.f;           // cap * log2(e)
   float poly[6] = {};             // of tanh(y) / y in y^2 up to |y| = 1, times cap_log2
-  float half[4] = {};             // the same up to 1/2
+  float three_quarters[5] = {};   // the same up to 3/4
+  float folded[5] = {};           // that of q.k itself (cap_in^(2 k + 1) in it), where fp32 holds it
+  int32_t folds = 0;
 };
 ScoreShape score_shape(float scale, float softcap, const float* slopes);
 
@@ -266,6 +269,13 @@ cudaError_t launch_extend(const ExtendParams& p, void* workspace, int sms, int a
 
 // The same with shaped scores.
 cudaError_t launch_extend_scored(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                                 cudaStream_t stream);
+// (its kernels, by what scores become)
+cudaError_t launch_extend_spans(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                                cudaStream_t stream);
+cudaError_t launch_extend_cap(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
+                              cudaStream_t stream);
+cudaError_t launch_extend_slopes(const ExtendParams& p, void* workspace, int sms, int act_dtype, int head_size, bool i8,
                                  cudaStream_t stream);
 
 // Paged decode over an 8-bit cache on CUDA cores: head_size 128, group 1/2/4/8;
