@@ -460,8 +460,8 @@ enum Shape {
   kNone,                                   // pa_extend
   kSpans,                                  // spans of each query alone
   kCap,                                    // a cap that folds (scores.cuh)
-  kSlope,                                  // slopes alone
-  kAny                                     // both, or a cap that does not fold
+  kSlope,                                  // slopes alone, no position behind the query's own
+  kAny                                     // both, slopes with such positions, or a cap that does not fold
 };
 
 // How the K and V stages are filled.
@@ -489,21 +489,27 @@ struct Work {
   int part_row, flag;
 };
 
-template <int D, Fill F>
+template <typename T, int D, Fill F, int kShape>
 struct Cfg {
+  static constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   static constexpr int kTileBytes = kKv * D * 2;              // K (or V) of one KV tile
   static constexpr int kGroupBytes = 8 * D * 2;               // 8 tokens of it
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr bool kConvert = F != kBulk;
-  static constexpr int kThreads = kConvert ? 512 : 384;
+  // Shaped scores take more instructions: where registers allow (no converters), two threads a row, 64 columns each.
+  // A softmax warp is alone with its tile on its quarter of the SM otherwise, and waits for every result and every
+  // instruction fetch by itself.
+  static constexpr int kHalves = kShape == kCap && kBf16 && !kConvert ? 2 : 1;
+  static constexpr int kSoft = 8 * kHalves;                   // softmax warps; the other roles' follow
+  static constexpr int kThreads = 32 * (kSoft + 4 + (kConvert ? 4 : 0));
   // registers a thread, whose sum over the warpgroups is the launch's: the softmax
   // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
   // caches half of a tile's codes (8 registers more or fewer for the softmax: within 2%)
-  static constexpr int kRegsSoftmax = F == kBulk ? 200 : F == kGather ? 176 : 160;
-  static constexpr int kRegsRest = F == kBulk ? 104 : F == kGather ? 88 : 96;
+  static constexpr int kRegsSoftmax = kHalves == 2 ? 104 : F == kBulk ? 200 : F == kGather ? 176 : 160;
+  static constexpr int kRegsRest = kHalves == 2 ? 64 : F == kBulk ? 104 : F == kGather ? 88 : 96;
   static constexpr int kRegsConvert = F == kGather ? 72 : 96;
-  static_assert((kThreads == 512 ? 128 * 4 : 168 * 3) ==
-                2 * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
+  static_assert((kThreads == 640 ? 96 * 5 : kThreads == 512 ? 128 * 4 : 168 * 3) ==
+                2 * kHalves * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
   // K and V tiles take turns in one ring: K of tile c is fill 2c, V fill 2c + 1, fill
   // n sits in buffer n % kBufs.  Five buffers of 32 KiB beside the query tiles are
   // all that fits (K and V in rings of two each: 1200 more clocks a tile, waiting for
@@ -519,12 +525,13 @@ struct __align__(16) Shared {
   // PV of tile number n of query tile t completes pv_done[t][n & 1]: a waiter is never two phases behind
   uint64_t pv_done[2][2];
   uint64_t item_full[kRing], item_empty[kRing];
-  uint64_t xbar;                           // the two softmax warpgroups (items that share a query tile)
+  uint64_t xbar;                           // all softmax warps (items that share a query tile)
+  uint64_t rows[2][4];                     // the two warps of a query tile's 32 rows (64 columns each)
   uint64_t mma_drain;
   Work work[kRing];
   volatile int bad[kRing];                 // a block id out of range was met
   volatile int odd[kRing];                 // (8-bit caches) a V scale that is not finite was met
-  float red[2][kRows][2];                  // the other warpgroup's (maximum, sum)
+  float red[2][kRows][2];                  // of each query tile: (maximum, sum), or its halves' sums
   uint32_t tmem_base;
   volatile int abort_flag;
   int last_fill[5], last_q[2];             // the last copies into each buffer, -1: none
@@ -683,6 +690,16 @@ __device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t*
                : "memory");
 }
 
+// One column.
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+  return __uint_as_float(r);
+}
+
 // 32 TMEM lanes x 32 columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -764,11 +781,11 @@ __device__ __forceinline__ int block_of(const ExtendParams& p, const int32_t* ro
 }
 
 template <typename T, int D, Fill F, int kShape>
-__global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
+__global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kernel(const __grid_constant__ ExtendParams p,
                                                                        const __grid_constant__ Space ws,
                                                                        const __grid_constant__ CUtensorMap q_map,
                                                                        const __grid_constant__ CUtensorMap kv_map) {
-  using C = Cfg<D, F>;
+  using C = Cfg<T, D, F, kShape>;
   constexpr bool kI8 = F == kCodes, kScored = kShape != kNone;
   constexpr bool kBF16 = std::is_same<T, __nv_bfloat16>::value;
   using PT = typename std::conditional<kI8, __half, T>::type;      // type of the weights and of V's operand
@@ -777,7 +794,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   uint8_t* ring = qbuf + 2 * C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(ring + C::kRingBytes);
   Scales& scales = *reinterpret_cast<Scales*>(&sh + 1);            // 8-bit caches alone
-  constexpr int NB = C::kBufs;
+  // Scores that fall with distance are largest where the queries are: with the last KV tile first the running maximum is
+  // found at once, from left to right it would rise, and the results be rescaled, with every tile.
+  constexpr bool kBackwards = kShape == kSlope || kShape == kAny;
+  constexpr int NB = C::kBufs, kH = C::kHalves, kSoft = C::kSoft, kCols = kKv / kH;
   if (smem_u32(qbuf) & 1023u) {                                    // never, as laid out
     if (threadIdx.x == 0) report(p.dev_err, PA_DEVERR_TIMEOUT);
     return;
@@ -791,7 +811,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_empty[i], 1);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 4 * kH);
       mbar_init(&sh.pv_done[i][0], 1);
       mbar_init(&sh.pv_done[i][1], 1);
     }
@@ -803,15 +823,16 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
     sh.last_q[0] = sh.last_q[1] = -1;
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sh.item_full[i], 1);
-      // 8 softmax warps, the issuing warp, the Q warp, and the V warp or 4 converter warps
-      mbar_init(&sh.item_empty[i], C::kConvert ? 14 : 11);
+      // the softmax warps, the issuing warp, the Q warp, and the V warp or 4 converter warps
+      mbar_init(&sh.item_empty[i], kSoft + (C::kConvert ? 6 : 3));
     }
-    mbar_init(&sh.xbar, 8);
+    mbar_init(&sh.xbar, kSoft);
+    for (int i = 0; i < 8; ++i) mbar_init(&sh.rows[i >> 2][i & 3], 2);
     mbar_init(&sh.mma_drain, 1);
     sh.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kSoft) {
     tc::tmem_alloc(&sh.tmem_base, 512);
     tc::tmem_relinquish();
   }
@@ -860,10 +881,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   };
   // KV tiles of an item
   auto tiles_of = [](const Work& w) { return w.alt ? w.n[0] + w.n[1] : max(w.n[0], w.n[1]); };
+  // the number in its item of the j-th KV tile of n that is worked on
+  auto nth = [](int j, int n) { return kBackwards ? n - 1 - j : j; };
 
-  if (warp >= 8 && warp < 12) {
+  if (warp >= kSoft && warp < kSoft + 4) {
     set_regs_dec<C::kRegsRest>();
-    if (warp == 9) {
+    if (warp == kSoft + 1) {
       // ================================================================= items, and K copies
       int32_t w_next = 0;
       int total = ws.head->total;
@@ -895,7 +918,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             w.n[1] = it.ntiles / 2;
           } else {
             // tile 0's last position may need one KV tile less
-            w.n[0] = max(0, min(it.ntiles, (it.pos0 + ptile - 1) / kKv + 1 - it.tile0));
+            w.n[0] = kBackwards ? it.ntiles : max(0, min(it.ntiles, (it.pos0 + ptile - 1) / kKv + 1 - it.tile0));
             w.n[1] = it.ntiles;
           }
           int last_first = attend_from(w.kv_end - 1, p.window, it.held), first_last = it.pos0;
@@ -936,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;   // blocks [fb, nblk) are read
           for (int j = 0; j < n; ++j, ++c) {
             // lane l copies the tile's block l
-            const int blk = (w.tile0 + j) * (kKv / bs) + lane;
+            const int blk = (w.tile0 + nth(j, n)) * (kKv / bs) + lane;
             const bool take = lane < kKv / bs && blk >= fb && blk < nblk;
             int id = take ? block_of(p, row, blk) : 0;
             if (take && (unsigned)id >= (unsigned)p.num_blocks) {
@@ -956,7 +979,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       }
       if (!ok && lane == 0) give_up();
       __syncwarp();
-    } else if (warp == 10) {
+    } else if (warp == kSoft + 2) {
       // ================================================================= V copies
       if constexpr (!C::kConvert) {
         int c = 0;
@@ -972,7 +995,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           const int32_t* row = p.block_tables + w.seq * p.bt_stride;
           const int fb = w.first / bs, nblk = (w.kv_end + bs - 1) / bs;
           for (int j = 0; j < n; ++j, ++c) {
-            const int blk = (w.tile0 + j) * (kKv / bs) + lane;
+            const int blk = (w.tile0 + nth(j, n)) * (kKv / bs) + lane;
             const bool take = lane < kKv / bs && blk >= fb && blk < nblk;
             int id = take ? block_of(p, row, blk) : 0;
             if ((unsigned)id >= (unsigned)p.num_blocks) id = 0;      // reported by the K copies
@@ -987,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         if (!ok && lane == 0) give_up();
         __syncwarp();
       }
-    } else if (warp == 11) {
+    } else if (warp == kSoft + 3) {
       // ================================================================= Q rows
       bool ok = true;
       for (int i = 0; ok; ++i) {
@@ -1067,6 +1090,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       Owed owed0, owed1;
       Fills fill;
       bool k_there = false;
+      // where the weights of 16 tokens are: each half of the columns has its own over the scores it has read
+      auto p_column = [](int k) { return kH == 2 ? (k >> 2) * 64 + (k & 3) * 8 : k * 8; };
       auto pv = [&](auto which, Owed& x) {
         constexpr int t = decltype(which)::value;
         if (x.buf < 0) return;
@@ -1081,11 +1106,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           if (x.steps == kKv / 16) {
 #pragma unroll
             for (int k = 1; k < kKv / 16; ++k)
-              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8, vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
+              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + p_column(k), vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
                              id_pv, 1u);
           } else {
             for (int k = 1; k < x.steps; ++k)
-              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + k * 8, vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
+              tc::mma_f16_ta(tmem + 256 + t * 128, tmem + t * kKv + p_column(k), vd + (uint64_t)((k * 2 * C::kGroupBytes) >> 4),
                              id_pv, 1u);
           }
           tc::commit(&sh.pv_done[t][x.num & 1]);
@@ -1131,7 +1156,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           constexpr int t = decltype(which)::value;
           pv(which, x);
           if (j >= n) return;
-          const int jt = alt ? 2 * j + t : j;                        // KV tile of the item
+          const int jt = nth(alt ? 2 * j + t : j, alt ? n0 + n1 : rounds);   // KV tile of the item
           // the last of the (one or two) query tiles that use this K and V
           const bool both = !alt && j < other, last_k = !both || t == 1;
           const int kb = fill.kb, vb = fill.vb();
@@ -1180,11 +1205,11 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       if (!__all_sync(kFull, bar_wait(&sh.mma_drain, 0)) && lane == 0) report(p.dev_err, PA_DEVERR_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp >= 12) {
+  } else if (warp >= kSoft + 4) {
     // =================================================================== converters (warps 12-15)
     if constexpr (C::kConvert) {
       set_regs_dec<C::kRegsConvert>();
-      const int ct = threadIdx.x - 384;                              // 0 .. 127
+      const int ct = threadIdx.x - 32 * (kSoft + 4);                              // 0 .. 127
       const int shift = __ffs(bs) - 1;
       constexpr int kPer = kI8 ? 8 : D / 8;                          // 16-byte source pieces of one vector
       constexpr int kLoads = kKv * kPer / 128;                       // of one thread, K or V
@@ -1203,7 +1228,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         const int32_t* row = p.block_tables + w.seq * p.bt_stride;
         // the block of token u of KV tile j, or -1: no query attends it, or its id is bad
         auto find = [&](int j, int u) -> int {
-          const int pos = (w.tile0 + j) * kKv + u;
+          const int pos = (w.tile0 + nth(j, n)) * kKv + u;
           if (pos < w.first || pos >= w.kv_end) return -1;
           const int id = block_of(p, row, pos >> shift);
           if ((unsigned)id < (unsigned)p.num_blocks) return id;
@@ -1216,7 +1241,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         int mine = -1;
         auto look_up = [&](int j) { return find(j, (ct >> 5) * kTok + lane % kTok + lane / kTok * (128 / kPer)); };
         auto block = [&](int e) { return __shfl_sync(kFull, mine, e * kTok + lane / kPer); };
-        auto place = [&](int j, int e) { return ((w.tile0 + j) * kKv + u0 + e * (128 / kPer)) & (bs - 1); };
+        auto place = [&](int j, int e) { return ((w.tile0 + nth(j, n)) * kKv + u0 + e * (128 / kPer)) & (bs - 1); };
         if constexpr (!kI8) {
           // 16-byte pieces by asynchronous copies, absent tokens as zeros; a token's K and V
           // together (their addresses differ by a constant).  A tile is completed after
@@ -1291,7 +1316,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           constexpr std::integral_constant<int, 1> kV{};
           float sk = 0.f, sv = 0.f;
           auto load_scales = [&](int j) {
-            const int id = find(j, ct), t = ((w.tile0 + j) * kKv + ct) & (bs - 1);
+            const int id = find(j, ct), t = ((w.tile0 + nth(j, n)) * kKv + ct) & (bs - 1);
             sk = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 0, t));
             sv = id < 0 ? 0.f : *reinterpret_cast<const float*>(p.cache + L8.scale(id, w.kvh, 1, t));
             // (0 * inf would reach rows that do not attend the token)
@@ -1402,12 +1427,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
   } else {
     // =================================================================== softmax warpgroups (warps 0-7)
     set_regs_inc<C::kRegsSoftmax>();
-    const int t = warp >> 2;                                         // query tile
+    const int t = warp / (4 * kH);                                   // query tile
+    const int half = kH == 2 ? (warp >> 2) & 1 : 0;                  // of its columns
     const int row = threadIdx.x & 127;                               // TMEM lane
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + quarter + t * kKv, o_addr = tmem + quarter + 256 + t * 128;
+    const uint32_t s_addr = tmem + quarter + t * kKv + half * kCols, o_addr = tmem + quarter + 256 + t * 128;
     const int ipos = row / G, head = row - ipos * G;
-    int num = 0, nx = 0;                                             // KV tiles, exchanges so far
+    int num = 0, nx = 0, nr = 0;                                     // KV tiles, exchanges so far
     bool ok = true;
     // an exchange of the two warpgroups: everything before it is seen after it
     auto meet = [&]() {
@@ -1416,6 +1442,16 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       if (lane == 0) mbar_arrive(&sh.xbar);
       if (!wait(&sh.xbar, nx & 1)) ok = false;
       ++nx;
+      tc::fence_after_sync();
+    };
+    // an exchange of the two warps that share their rows
+    auto meet_rows = [&]() {
+      tc::fence_before_sync();
+      __syncwarp();
+      uint64_t* bar = &sh.rows[t][warp & 3];
+      if (lane == 0) mbar_arrive(bar);
+      if (!wait(bar, nr & 1)) ok = false;
+      ++nr;
       tc::fence_after_sync();
     };
     for (int i = 0; ok; ++i) {
@@ -1429,11 +1465,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       const int my0 = alt ? 0 : t * ptile;                           // my tile's first position in the item
       const bool row_ok = ipos < (alt ? w.npos : min(ptile, w.npos - my0));
       const int pos = w.pos0 + my0 + ipos;
-      const int token = w.row0 + (row_ok ? my0 + ipos : 0);
+      auto token = [&]() { return w.row0 + (row_ok ? pos - w.pos0 : 0); };
       const int from = kScored ? 0 : attend_from(pos, p.window, w.held);
       const float slope2 = kScored && p.shape.slopes ? p.shape.slopes[w.kvh * G + head] * score::kLog2e : 0.f;
       const int n = t == 0 ? w.n[0] : w.n[1];
-      const int tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
+      // (with two threads a row there are registers for little else: read where needed)
+      using Held = typename std::conditional<kH == 2, const int&, const int>::type;
+      Held tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
       // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 96 in base 2 they are taken
       // against 0, without a maximum (2^96 times 2^20 tokens and 2^-96 are far inside that range).  Slopes leave it.
       const bool fixed = kShape == kCap && !kI8 && kBF16 && p.shape.cap_log2 <= 96.f;
@@ -1453,8 +1491,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         }
       }
       for (int j = 0; j < n; ++j, ++num) {
-        const int jt = alt ? 2 * j + t : j, c = c0 + jt;
-        const int t0 = (tile0 + jt) * kKv;
+        const int turn = alt ? 2 * j + t : j, c = c0 + turn;
+        const int jt = kBackwards ? tiles_of(w) - 1 - turn : turn;
+        const int t0 = (tile0 + jt) * kKv + half * kCols;              // my first column's token
         if (!wait(&sh.s_full[t], num & 1)) {
           ok = false;
           break;
@@ -1500,7 +1539,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                 if constexpr (kShape != kCap) {
                   const int rr = (warp & 3) * 32 + (lane >> 2) + 8 * (2 * h + r);
                   int nearest = pos4[r];
-                  if (p.last_pos) {
+                  if (kShape == kAny && p.last_pos) {
                     nearest = min(nearest, span_to<true>(p, pos4[r], w.kv_end, w.row0 + (is_row ? pos4[r] - w.pos0 : 0)));
                     exact |= is_row && t0 + kKv - 1 > nearest;
                   }
@@ -1511,10 +1550,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                   float big[2] = {0.f, 0.f};
 #pragma unroll
                   for (int n = 0; n < 16; ++n) big[n & 1] = fmaxf(fmaxf(big[n & 1], fabsf(x[4 * n + 2 * r])), fabsf(x[4 * n + 2 * r + 1]));
-                  exact |= is_row && fmaxf(big[0], big[1]) > (kShape == kCap ? 0.75f : 1.f);
+                  exact |= is_row && p.shape.capped && fmaxf(big[0], big[1]) > (kShape == kCap ? 0.75f : 1.f);
                 }
               }
-              if (__builtin_expect(__any_sync(kFull, exact), 0)) {
+              if (kShape != kSlope && __builtin_expect(__any_sync(kFull, exact), 0)) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) tmem_st16x256_32(s_addr + half + 32 * e, x + 16 * e);
                 tc::tmem_wait_st();
@@ -1548,7 +1587,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                     const uint64_t y = pack2f(x[e], x[e + 1]);
                     if constexpr (kShape == kCap)
                       unpack2f(mul2f(y, cap_quotient2<5>(p.shape, y)), x[e], x[e + 1]);
-                    else if constexpr (kShape == kSlope)
+                    else if (kShape == kSlope || !p.shape.capped)
                       unpack2f(add2f(add2f(y, in[n & 3]), off[n >> 2]), x[e], x[e + 1]);
                     else
                       unpack2f(add2f(fma2f(y, cap_quotient2<6>(p.shape, y), in[n & 3]), off[n >> 2]), x[e], x[e + 1]);
@@ -1688,9 +1727,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           }
           if (!ok) break;
         } else {
-          float x[kKv];
+          float x[kCols];
           tmem_ld64(s_addr, x);
-          tmem_ld64(s_addr + 64, x + 64);
+          if constexpr (kH == 1) tmem_ld64(s_addr + 64, x + 64);
           // Shaped scores: x unit + ahead(column / 16) is the base-2 score; under a cap x stays q.k (fly) and is capped in
           // the loop that takes the powers.
           float unit = p.scale_log2, so = 0.f, base = 0.f, most = 0.f;
@@ -1698,22 +1737,23 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           if constexpr (kShape != kNone && kShape != kSpans) {
             int ref = pos;                                           // distances count from the nearest attended position
             bool exact = false;
-            if (kShape != kCap && p.last_pos) {
-              ref = min(pos, span_to<true>(p, pos, w.kv_end, token));
-              exact = row_ok && t0 + kKv - 1 > ref;
+            if (kShape == kAny && p.last_pos) {
+              ref = min(pos, span_to<true>(p, pos, w.kv_end, token()));
+              exact = row_ok && t0 + kCols - 1 > ref;
             }
             if constexpr (kShape != kSlope) {
               float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int e = 0; e < kKv; e += 8)
+              for (int e = 0; e < kCols; e += 8)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) big[k] = fmaxf(fmaxf(big[k], fabsf(x[e + k])), fabsf(x[e + 4 + k]));
               exact |= row_ok && fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * p.shape.cap_in > (kShape == kCap ? 0.75f : 1.f);
+              // (uncapped: cap_in is 0)
             }
-            if (__builtin_expect(__any_sync(kFull, exact), 0)) {
+            if (kShape != kSlope && __builtin_expect(__any_sync(kFull, exact), 0)) {
               // any form, 16 columns at a time through TMEM
 #pragma unroll 1
-              for (int e = 0; e < kKv; e += 16) {
+              for (int e = 0; e < kCols; e += 16) {
                 float v[16];
                 tc::tmem_ld16(s_addr + e, v);
 #pragma unroll
@@ -1723,7 +1763,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               }
               tc::tmem_wait_st();
               tmem_ld64(s_addr, x);
-              tmem_ld64(s_addr + 64, x + 64);
+              if constexpr (kH == 1) tmem_ld64(s_addr + 64, x + 64);
               unit = 1.f;
               fly = false;
             } else if constexpr (kShape != kCap) {
@@ -1734,11 +1774,12 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
               uint64_t in[8];                                        // the slope's part within 16 columns
 #pragma unroll
               for (int k = 0; k < 8; ++k) in[k] = pack2f(so * (2.f * k), so * (2.f * k + 1.f));
-              const float u = kShape == kSlope ? p.scale_log2 : p.shape.cap_in;
+              const bool straight = kShape == kSlope || !p.shape.capped;
+              const float u = straight ? p.scale_log2 : p.shape.cap_in;
               const uint64_t u2 = pack2f(u, u);
 #pragma unroll
-              for (int e = 0; e < kKv; e += 2) {
-                if constexpr (kShape == kSlope) {
+              for (int e = 0; e < kCols; e += 2) {
+                if (straight) {
                   unpack2f(fma2f(pack2f(x[e], x[e + 1]), u2, in[e / 2 % 8]), x[e], x[e + 1]);
                 } else {
                   const uint64_t y = mul2f(pack2f(x[e], x[e + 1]), u2);
@@ -1754,10 +1795,10 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           if (kShape == kCap && fixed && fly) none = -64.f * p.shape.cap_out;
           if (edge) {
             // attended columns [lo, hi)
-            const int lo = (kScored ? span_from<kScored>(p, pos, w.held, token) : from) - t0;
-            const int hi = row_ok ? span_to<kScored>(p, pos, w.kv_end, token) + 1 - t0 : 0;
+            const int lo = (kScored ? span_from<kScored>(p, pos, w.held, token()) : from) - t0;
+            const int hi = row_ok ? span_to<kScored>(p, pos, w.kv_end, token()) + 1 - t0 : 0;
 #pragma unroll
-            for (int e = 0; e < kKv / 32; ++e) {
+            for (int e = 0; e < kCols / 32; ++e) {
               const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
               const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
               if (__any_sync(kFull, on != kFull)) {
@@ -1773,7 +1814,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                   ok = false;
                   break;
                 }
-                if (t0 + row >= w.kv_end || t0 + row < w.first) {
+                const int token_row = (tile0 + jt) * kKv + row;
+                if (half == 0 && (token_row >= w.kv_end || token_row < w.first)) {
                   uint8_t* v = buffer(2 * c + 1);
 #pragma unroll 2
                   for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
@@ -1787,7 +1829,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             if constexpr (kShape == kSlope || kShape == kAny) {
               float best[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-              for (int k = 0; k < kKv / 16; ++k) {
+              for (int k = 0; k < kCols / 16; ++k) {
                 float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
@@ -1799,7 +1841,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             } else {
               float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
 #pragma unroll
-              for (int e = 0; e < kKv; e += 8)
+              for (int e = 0; e < kCols; e += 8)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
               mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
@@ -1807,6 +1849,14 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                 mt = mt == -INFINITY ? mt : score::any_cap(p.shape, mt * p.shape.cap_in);      // (the cap keeps the order)
               else
                 mt *= unit;
+            }
+            if constexpr (kH == 2) {
+              // the other half's, through TMEM: behind the weights, in a column whose score has been read
+              tmem_st1(s_addr + kCols - 1, mt);
+              tc::tmem_wait_st();
+              meet_rows();
+              if (!ok) break;
+              mt = fmaxf(mt, tmem_ld1(tmem + quarter + t * kKv + (half ^ 1) * kCols + kCols - 1));
             }
             const float m_new = fmaxf(m, mt);
             const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
@@ -1824,7 +1874,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
                 m = m_new;
               }
 #pragma unroll
-              for (int e = 0; e < D / 16; ++e) {
+              for (int e = half * (D / 16 / kH); e < (half + 1) * (D / 16 / kH); ++e) {
                 float o[16];
                 tc::tmem_ld16(o_addr + e * 16, o);
 #pragma unroll
@@ -1834,7 +1884,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
             }
             if (kShape == kCap && fly && edge) {
 #pragma unroll
-              for (int e = 0; e < kKv; ++e) x[e] = x[e] == -INFINITY ? -64.f * p.shape.cap_out : x[e];
+              for (int e = 0; e < kCols; ++e) x[e] = x[e] == -INFINITY ? -64.f * p.shape.cap_out : x[e];
             }
           }
           // weights 2^(x - m), the sum of the unrounded ones in fp32
@@ -1843,7 +1893,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
           // to_power(pair, column): what two powers are of
           auto weigh = [&](auto to_power) {
 #pragma unroll
-            for (int e = 0; e < kKv / 32; ++e) {
+            for (int e = 0; e < kCols / 32; ++e) {
               uint32_t y[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) {
@@ -1914,15 +1964,28 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
       }
       // ---- results: columns [c0, c0 + nc) of my row
       float f[2] = {1.f, 1.f};
-      int col0 = 0, ncol = D;
+      int col0 = half * (D / kH), ncol = D / kH;
       bool have0 = n > 0, have1 = false;
+      float lo = 0.f;                                                // alt: the other tile's sum
+      if constexpr (kH == 2) {
+        // the halves' sums; whoever writes here next waits until they have been read
+        auto both = [&]() { if (alt) meet(); else meet_rows(); };
+        sh.red[t][row][half] = l;
+        both();
+        if (!ok) break;
+        l = sh.red[t][row][0] + sh.red[t][row][1];
+        if (alt) lo = sh.red[t ^ 1][row][0] + sh.red[t ^ 1][row][1];
+        both();
+        if (!ok) break;
+      }
       uint32_t o0 = o_addr, o1 = o_addr;
       if (alt) {
-        sh.red[t][row][0] = m;
-        sh.red[t][row][1] = l;
+        sh.red[t][row][0] = m;                                       // (the same in both halves)
+        if (kH == 1) sh.red[t][row][1] = l;
         meet();
         if (!ok) break;
-        const float mo = sh.red[t ^ 1][row][0], lo = sh.red[t ^ 1][row][1];
+        const float mo = sh.red[t ^ 1][row][0];
+        if (kH == 1) lo = sh.red[t ^ 1][row][1];
         const float mm = fmaxf(m, mo);
         const float fm = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - mm);
         const float fo = mo == -INFINITY ? (lo == 0.f ? 0.f : 1.f) : exp2f(mo - mm);
@@ -1935,8 +1998,13 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
         have1 = w.n[1] > 0;
         o0 = tmem + quarter + 256;
         o1 = o0 + 128;
-        ncol = D / 2;
-        col0 = t * ncol;
+        if (D / 2 / kH >= 32) {                                      // (32 columns at a time)
+          ncol = D / 2 / kH;
+          col0 = (t * kH + half) * ncol;
+        } else {
+          ncol = half == 0 ? D / 2 : 0;
+          col0 = t * (D / 2) + half;
+        }
       }
       const bool part = w.part_row >= 0;
       const float scale = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -2031,7 +2099,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, 1) extend_kernel(const __
     for (int i = 0; i < 2; ++i)
       if (sh.last_q[i] >= 0 && !bar_wait(&sh.q_full[i], sh.last_q[i] & 1)) report(p.dev_err, PA_DEVERR_TIMEOUT);
   }
-  if (warp == 8) {
+  if (warp == kSoft) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -2213,7 +2281,7 @@ cudaError_t encode_maps(const ExtendParams& p, int act_dtype, CUtensorMap* q_map
 
 template <typename T, int D, Fill F, int kShape>
 cudaError_t launch_fill(const ExtendParams& p, const Space& ws, int sms, cudaStream_t stream) {
-  using C = Cfg<D, F>;
+  using C = Cfg<T, D, F, kShape>;
   constexpr bool kScored = kShape != kNone;
   constexpr size_t smem = 2 * C::kQBytes + C::kRingBytes + sizeof(Shared) + (F == kCodes ? sizeof(Scales) + kKv * D : 0);
   static_assert(smem <= 227 * 1024 && sizeof(Shared) % 16 == 0, "shared memory");
