@@ -33,7 +33,8 @@ cudaError_t launch_extend_scored(const ExtendParams& p, void* workspace, int sms
   const bool capped = p.shape.capped, sloped = p.shape.slopes != nullptr;
   if (!capped && !sloped) return launch_extend_spans(p, workspace, sms, act_dtype, head_size, i8, stream);
   if (!capped && !p.last_pos) return launch_extend_slopes(p, workspace, sms, act_dtype, head_size, i8, stream);
-  if (!sloped && p.shape.folds) return launch_extend_cap(p, workspace, sms, act_dtype, head_size, i8, stream);
+  const bool in_range = act_dtype == PA_F16 || i8 || p.shape.cap_log2 <= 96.f;
+  if (!sloped && p.shape.folds && in_range) return launch_extend_cap(p, workspace, sms, act_dtype, head_size, i8, stream);
   return launch<kAny>(p, workspace, sms, act_dtype, head_size, i8, stream);
 }
 

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
 enum Shape {
   kNone,                                   // pa_extend
   kSpans,                                  // spans of each query alone
-  kCap,                                    // a cap that folds (scores.cuh)
+  kCap,                                    // a cap that folds (scores.cuh), in bf16 one of at most 96 in base 2
   kSlope,                                  // slopes alone, no position behind the query's own
   kAny                                     // both, slopes with such positions, or a cap that does not fold
 };
@@ -496,17 +496,18 @@ struct Cfg {
   static constexpr int kGroupBytes = 8 * D * 2;               // 8 tokens of it
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr bool kConvert = F != kBulk;
-  // Shaped scores take more instructions: where registers allow (no converters), two threads a row, 64 columns each.
-  // A softmax warp is alone with its tile on its quarter of the SM otherwise, and waits for every result and every
-  // instruction fetch by itself.
+  // Where no maximum is needed (kFixed below) and registers allow, two threads share a row, 64 columns each: a softmax
+  // warp is otherwise alone with its tile on its quarter of the SM, and waits for every result and every instruction by
+  // itself.  (Capped chunks 835 -> CAPPED us.  With a maximum the halves have to meet in every tile: slopes 876 -> 987,
+  // plain scores 552 -> 632.)
   static constexpr int kHalves = kShape == kCap && kBf16 && !kConvert ? 2 : 1;
   static constexpr int kSoft = 8 * kHalves;                   // softmax warps; the other roles' follow
   static constexpr int kThreads = 32 * (kSoft + 4 + (kConvert ? 4 : 0));
   // registers a thread, whose sum over the warpgroups is the launch's: the softmax
   // warpgroups hold a row's 128 scores (8-bit caches: 64), the converters of 8-bit
   // caches half of a tile's codes (8 registers more or fewer for the softmax: within 2%)
-  static constexpr int kRegsSoftmax = kHalves == 2 ? 104 : F == kBulk ? 200 : F == kGather ? 176 : 160;
-  static constexpr int kRegsRest = kHalves == 2 ? 64 : F == kBulk ? 104 : F == kGather ? 88 : 96;
+  static constexpr int kRegsSoftmax = kHalves == 2 ? 96 : F == kBulk ? 200 : F == kGather ? 176 : 160;
+  static constexpr int kRegsRest = kHalves == 2 ? 96 : F == kBulk ? 104 : F == kGather ? 88 : 96;
   static constexpr int kRegsConvert = F == kGather ? 72 : 96;
   static_assert((kThreads == 640 ? 96 * 5 : kThreads == 512 ? 128 * 4 : 168 * 3) ==
                 2 * kHalves * kRegsSoftmax + kRegsRest + (kConvert ? kRegsConvert : 0), "register split");
@@ -690,16 +691,6 @@ __device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t*
                : "memory");
 }
 
-// One column.
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
-}
-__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
-  return __uint_as_float(r);
-}
-
 // 32 TMEM lanes x 32 columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -794,6 +785,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
   uint8_t* ring = qbuf + 2 * C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(ring + C::kRingBytes);
   Scales& scales = *reinterpret_cast<Scales*>(&sh + 1);            // 8-bit caches alone
+  // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 96 in base 2 they are taken
+  // against 0, without a maximum (2^96 times 2^20 tokens and 2^-96 are far inside that range).
+  constexpr bool kFixed = kShape == kCap && kBF16 && !kI8;
   // Scores that fall with distance are largest where the queries are: with the last KV tile first the running maximum is
   // found at once, from left to right it would rise, and the results be rescaled, with every tile.
   constexpr bool kBackwards = kShape == kSlope || kShape == kAny;
@@ -1454,6 +1448,26 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       ++nr;
       tc::fence_after_sync();
     };
+    // thread = token here: V rows of fill 2 c + 1 that hold no token of the context become zero (V has landed: the issuer
+    // waited for it); true: the wait ran out
+    auto zero_rows = [&](const Work& w, int jt, int c) -> bool {
+      if constexpr (F == kBulk) {
+        if (ragged(w, jt)) {
+          if (!wait(&sh.full[(2 * c + 1) % NB], ((2 * c + 1) / NB) & 1)) {
+            ok = false;
+            return true;
+          }
+          const int at = (w.tile0 + jt) * kKv + row;
+          if (half == 0 && (at >= w.kv_end || at < w.first)) {
+            uint8_t* v = buffer(2 * c + 1);
+#pragma unroll 2
+            for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+        }
+      }
+      return false;
+    };
     for (int i = 0; ok; ++i) {
       if (!wait(&sh.item_full[i % kRing], (i / kRing) & 1)) {
         ok = false;
@@ -1472,10 +1486,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       // (with two threads a row there are registers for little else: read where needed)
       using Held = typename std::conditional<kH == 2, const int&, const int>::type;
       Held tile0 = w.tile0, c0 = w.c0, edge_lo = w.edge_lo, edge_hi = w.edge_hi;
-      // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 96 in base 2 they are taken
-      // against 0, without a maximum (2^96 times 2^20 tokens and 2^-96 are far inside that range).  Slopes leave it.
-      const bool fixed = kShape == kCap && !kI8 && kBF16 && p.shape.cap_log2 <= 96.f;
-      float m = fixed ? 0.f : -INFINITY, l = 0.f;
+      float m = kFixed ? 0.f : -INFINITY, l = 0.f;
       // 8-bit caches: a thread has rows gr + 8 i of its warp's 32 (and a quarter of their columns)
       float m4[4], l4[4];
       int pos4[4];
@@ -1726,13 +1737,76 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
             ok4 = (ok4 >> 2 | ok4 << 2) & 15u;
           }
           if (!ok) break;
+        } else if constexpr (kFixed) {
+          // 32 columns at a time, weights against 0.  The weights wait in registers until it is known that every score was
+          // near enough for the polynomial: one vote a tile, and its other form out of the way (votes in every part, with
+          // that form between them: 742 us instead of CAPPED).
+          const int lo = edge ? span_from<true>(p, pos, w.held, token()) - t0 : 0;       // attended columns [lo, hi)
+          const int hi = edge ? (row_ok ? span_to<true>(p, pos, w.kv_end, token()) + 1 - t0 : 0) : kCols;
+          if (edge && zero_rows(w, jt, c)) break;
+          auto mask = [&](float (&x)[32], int e) {
+            const int a = min(max(lo - e * 32, 0), 32), b = min(max(hi - e * 32, 0), 32);
+            const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = (on >> k) & 1 ? x[k] : -INFINITY;
+          };
+          uint64_t sum[2] = {0, 0};
+          auto powers = [&](const float (&x)[32], uint32_t* y) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float a = ex2_approx(x[2 * k]), b = ex2_approx(x[2 * k + 1]);
+              sum[k & 1] = add2f(pack2f(a, b), sum[k & 1]);
+              y[k] = Elem<PT>::pack2(a, b);
+            }
+          };
+          uint32_t y[kCols / 2];
+          float big[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < kCols / 32; ++e) {
+            float x[32];
+            tmem_ld32(s_addr + e * 32, x);
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) big[i] = fmaxf(fmaxf(big[i], fabsf(x[k + i])), fabsf(x[k + 2 + i]));
+            const float* f = p.shape.folded;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const uint64_t xx = pack2f(x[k], x[k + 1]), z = mul2f(xx, xx);
+              uint64_t v = pack2f(f[4], f[4]);
+#pragma unroll
+              for (int i = 3; i >= 0; --i) v = fma2f(v, z, pack2f(f[i], f[i]));
+              unpack2f(mul2f(xx, v), x[k], x[k + 1]);
+            }
+            if (__builtin_expect(edge, 0)) mask(x, e);
+            powers(x, y + e * 16);
+          }
+          if (__builtin_expect(__any_sync(kFull, row_ok && fmaxf(big[0], big[1]) * p.shape.cap_in > 0.75f), 0)) {
+            sum[0] = sum[1] = 0;
+#pragma unroll 1
+            for (int e = 0; e < kCols / 32; ++e) {
+              float x[32];
+              tmem_ld32(s_addr + e * 32, x);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = score::any_cap(p.shape, x[k] * p.shape.cap_in);
+              mask(x, e);
+              powers(x, y);
+              tc::tmem_st16u(s_addr + e * 16, y);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kCols / 32; ++e) tc::tmem_st16u(s_addr + e * 16, y + e * 16);
+          }
+          float a, b;
+          unpack2f(add2f(sum[0], sum[1]), a, b);
+          l += a + b;
         } else {
           float x[kCols];
           tmem_ld64(s_addr, x);
           if constexpr (kH == 1) tmem_ld64(s_addr + 64, x + 64);
           // Shaped scores: x unit + ahead(column / 16) is the base-2 score; under a cap x stays q.k (fly) and is capped in
           // the loop that takes the powers.
-          float unit = p.scale_log2, so = 0.f, base = 0.f, most = 0.f;
+          float unit = p.scale_log2, so = 0.f, base = 0.f;
           bool fly = kShape == kCap;
           if constexpr (kShape != kNone && kShape != kSpans) {
             int ref = pos;                                           // distances count from the nearest attended position
@@ -1790,9 +1864,6 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
             }
           }
           auto ahead = [&](int k) { return kShape == kSlope || kShape == kAny ? fmaf(so, 16.f * k, base) : 0.f; };
-          // what a masked place holds: under a cap, in the powers' loop, what the polynomial takes to far below 0
-          float none = -INFINITY;
-          if (kShape == kCap && fixed && fly) none = -64.f * p.shape.cap_out;
           if (edge) {
             // attended columns [lo, hi)
             const int lo = (kScored ? span_from<kScored>(p, pos, w.held, token()) : from) - t0;
@@ -1803,89 +1874,64 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
               const uint32_t on = (uint32_t)((1ull << b) - 1) & ~(uint32_t)((1ull << a) - 1);
               if (__any_sync(kFull, on != kFull)) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : none;
+                for (int k = 0; k < 32; ++k) x[e * 32 + k] = (on >> k) & 1 ? x[e * 32 + k] : -INFINITY;
               }
             }
-            if constexpr (F == kBulk) {
-              if (ragged(w, jt)) {
-                // thread = token here: V rows that hold no token of the context become
-                // zero (V has landed: the issuer waited for it)
-                if (!wait(&sh.full[(2 * c + 1) % NB], ((2 * c + 1) / NB) & 1)) {
-                  ok = false;
-                  break;
-                }
-                const int token_row = (tile0 + jt) * kKv + row;
-                if (half == 0 && (token_row >= w.kv_end || token_row < w.first)) {
-                  uint8_t* v = buffer(2 * c + 1);
-#pragma unroll 2
-                  for (int e = 0; e < D / 8; ++e) *reinterpret_cast<uint4*>(v + kv_offset<D>(row, e)) = make_uint4(0, 0, 0, 0);
-                }
-                tc::fence_proxy_async_smem();
-              }
+            if (zero_rows(w, jt, c)) break;
+          }
+          float mt;
+          if constexpr (kShape == kSlope || kShape == kAny) {
+            float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < kCols / 16; ++k) {
+              float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) top[i] = fmaxf(fmaxf(top[i], x[16 * k + e + i]), x[16 * k + e + 2 + i]);
+              best[k & 1] = fmaxf(best[k & 1], fmaxf(top[0], top[1]) + ahead(k));
+            }
+            mt = fmaxf(best[0], best[1]);
+          } else {
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
+#pragma unroll
+            for (int e = 0; e < kCols; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
+            mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            if (kShape == kCap && fly)
+              mt = mt == -INFINITY ? mt : score::any_cap(p.shape, mt * p.shape.cap_in);      // (the cap keeps the order)
+            else
+              mt *= unit;
+          }
+          const float m_new = fmaxf(m, mt);
+          const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
+          if (m == -INFINITY) m = m_new;
+          if (__any_sync(kFull, need)) {
+            // O holds exactly the tiles before this one once the last PV has completed
+            if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const float alpha = need ? exp2f(m - m_new) : 1.f;
+            if (need) {
+              l *= alpha;
+              m = m_new;
+            }
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              float o[16];
+              tc::tmem_ld16(o_addr + e * 16, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= alpha;
+              tc::tmem_st16(o_addr + e * 16, o);
             }
           }
-          if (!fixed) {
-            float mt;
-            if constexpr (kShape == kSlope || kShape == kAny) {
-              float best[2] = {-INFINITY, -INFINITY};
+          // a masked place holds what the polynomial takes to far below 0
+          if (kShape == kCap && fly && edge) {
 #pragma unroll
-              for (int k = 0; k < kCols / 16; ++k) {
-                float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int e = 0; e < 16; e += 4)
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) top[i] = fmaxf(fmaxf(top[i], x[16 * k + e + i]), x[16 * k + e + 2 + i]);
-                best[k & 1] = fmaxf(best[k & 1], fmaxf(top[0], top[1]) + ahead(k));
-              }
-              mt = fmaxf(best[0], best[1]);
-            } else {
-              float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // four chains: latency
-#pragma unroll
-              for (int e = 0; e < kCols; e += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = fmaxf(fmaxf(top[k], x[e + k]), x[e + 4 + k]);
-              mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-              if (kShape == kCap && fly)
-                mt = mt == -INFINITY ? mt : score::any_cap(p.shape, mt * p.shape.cap_in);      // (the cap keeps the order)
-              else
-                mt *= unit;
-            }
-            if constexpr (kH == 2) {
-              // the other half's, through TMEM: behind the weights, in a column whose score has been read
-              tmem_st1(s_addr + kCols - 1, mt);
-              tc::tmem_wait_st();
-              meet_rows();
-              if (!ok) break;
-              mt = fmaxf(mt, tmem_ld1(tmem + quarter + t * kKv + (half ^ 1) * kCols + kCols - 1));
-            }
-            const float m_new = fmaxf(m, mt);
-            const bool need = row_ok && m != -INFINITY && m_new > m + kRescaleThreshold;
-            if (m == -INFINITY) m = m_new;
-            if (__any_sync(kFull, need)) {
-              // O holds exactly the tiles before this one once the last PV has completed
-              if (!wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) {
-                ok = false;
-                break;
-              }
-              tc::fence_after_sync();
-              const float alpha = need ? exp2f(m - m_new) : 1.f;
-              if (need) {
-                l *= alpha;
-                m = m_new;
-              }
-#pragma unroll
-              for (int e = half * (D / 16 / kH); e < (half + 1) * (D / 16 / kH); ++e) {
-                float o[16];
-                tc::tmem_ld16(o_addr + e * 16, o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= alpha;
-                tc::tmem_st16(o_addr + e * 16, o);
-              }
-            }
-            if (kShape == kCap && fly && edge) {
-#pragma unroll
-              for (int e = 0; e < kCols; ++e) x[e] = x[e] == -INFINITY ? -64.f * p.shape.cap_out : x[e];
-            }
+            for (int e = 0; e < kCols; ++e) x[e] = x[e] == -INFINITY ? -64.f * p.shape.cap_out : x[e];
           }
           // weights 2^(x - m), the sum of the unrounded ones in fp32
           const float nm = m == -INFINITY ? 0.f : -m;
