@@ -1403,35 +1403,45 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       float x[CN];
       bool up = false;
       {
-        if constexpr (kScored) {
-          if (p.shape.capped) {
-            bool large = false;
-#pragma unroll
-            for (int n = 0; n < CN; ++n) {
-              sv[n] *= kscale;
-              large |= fabsf(sv[n]) > 1.f;
-            }
-            if (__builtin_expect(__any_sync(kFull, rv && large), 0)) {
-#pragma unroll
-              for (int n = 0; n < CN; ++n) sv[n] = score::any_cap(p.shape, sv[n]);
-            } else {
-#pragma unroll
-              for (int n = 0; n < CN; ++n) sv[n] = score::near_cap(p.shape, sv[n]);
-            }
-          }
-          if (p.shape.slopes) {
-            const float dist = (float)(mt.far - row) * score::kLog2e, f = p.shape.capped ? 1.f : kscale;
-#pragma unroll
-            for (int n = 0; n < CN; ++n) sv[n] = fmaf(-p.shape.slopes[mt.kvh * G + n], dist, sv[n] * f);
-          }
-        }
-        const float last_scale = kScored && (p.shape.capped || p.shape.slopes) ? 1.f : kscale;
         float mv[CN];
         load_m(mv);
+        if constexpr (!kScored) {
 #pragma unroll
-        for (int n = 0; n < CN; ++n) {
-          x[n] = rv ? sv[n] * last_scale : -INFINITY;
-          up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);   // 8-bit: the V scales ride on P, keep p <= 1
+          for (int n = 0; n < CN; ++n) {
+            x[n] = rv ? sv[n] * kscale : -INFINITY;
+            up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);   // 8-bit: the V scales ride on P, keep p <= 1
+          }
+        } else {
+          const bool capped = p.shape.capped, sloped = p.shape.slopes;
+          const float dist = (float)(mt.far - row) * -score::kLog2e;
+          const float* slope = p.shape.slopes + mt.kvh * G;
+          auto finish = [&](int n, float v) {
+            x[n] = rv ? (sloped ? fmaf(slope[n], dist, v) : v) : -INFINITY;
+            up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);
+          };
+          if (!capped) {
+#pragma unroll
+            for (int n = 0; n < CN; ++n) finish(n, sv[n] * kscale);
+          } else {
+            // by the polynomial, and by the other form if some score was too near the cap for it: seen by the vote that
+            // asks for a larger maximum
+            bool far = false;
+            float big = 0.f;
+#pragma unroll
+            for (int n = 0; n < CN; n += 2) {                          // (a single column's neighbour is padding)
+              float a, b;
+              score::nearer_cap2(p.shape, kscale, sv[n], sv[n + 1], a, b);
+              big = fmaxf(fmaxf(big, fabsf(sv[n])), n + 1 < CN ? fabsf(sv[n + 1]) : 0.f);
+              finish(n, a);
+              if (n + 1 < CN) finish(n + 1, b);
+            }
+            far = rv && big > 0.75f;
+            if (__any_sync(kFull, up | far) && __any_sync(kFull, far)) {
+              up = false;
+#pragma unroll
+              for (int n = 0; n < CN; ++n) finish(n, score::any_cap(p.shape, sv[n]));
+            }
+          }
         }
       }
       const bool wup = __any_sync(kFull, up);
