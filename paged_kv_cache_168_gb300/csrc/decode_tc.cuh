@@ -1439,7 +1439,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
             if (__any_sync(kFull, up | far) && __any_sync(kFull, far)) {
               up = false;
 #pragma unroll
-              for (int n = 0; n < CN; ++n) finish(n, score::any_cap(p.shape, sv[n]));
+              for (int n = 0; n < CN; ++n) finish(n, score::any_cap_call(p.shape, sv[n]));
             }
           }
         }

@@ -28,7 +28,6 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDeep = 3;                             // units a thread has in flight
 
 // The two pieces (16 bytes = 8 dims each) of unit u of a head vector.
 template <bool kPairs>
@@ -61,11 +60,21 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                     Elem<T>::pack2(x[6], x[7]));
 }
 
-// x holds the unit's 16 values (piece a, then piece b); cs the token's cosines and sines.
+// In shared memory a unit's values lie four by four, the units' first fours together, then their second ones: what the
+// lanes of a vector read at once is contiguous and no bank is asked twice.
+__device__ __forceinline__ int shared_place(int i, int units) { return (i / 4 % 2 * units + i / 8) * 4 + i % 4; }
+
+// x holds the unit's 16 values (piece a, then piece b); cs the token's cosines, then sines (shared_place).
 template <bool kPairs>
-__device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, int half_dims) {
-  const float* c = cs + u * 8;
-  const float* s = cs + half_dims + u * 8;
+__device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, int units) {
+  float c[8], s[8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float4 v = reinterpret_cast<const float4*>(cs)[k * units + u];
+    const float4 w = reinterpret_cast<const float4*>(cs)[(k + 2) * units + u];
+    c[4 * k] = v.x, c[4 * k + 1] = v.y, c[4 * k + 2] = v.z, c[4 * k + 3] = v.w;
+    s[4 * k] = w.x, s[4 * k + 1] = w.y, s[4 * k + 2] = w.z, s[4 * k + 3] = w.w;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int a = kPairs ? 2 * i : i, b = kPairs ? 2 * i + 1 : i + 8;
@@ -75,22 +84,45 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, i
   }
 }
 
+// Two fp32 operations an instruction (instructions are what this kernel runs out of first).
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2f(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2f(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // x becomes x / sqrt(mean of the vector's squares + eps) w; the vector's D / 16 units are neighbouring lanes.
 template <int D>
-__device__ __forceinline__ void normalise(float (&x)[16], const float* weight, int a, int b, float eps) {
+__device__ __forceinline__ void normalise(float (&x)[16], const float* weight, int u, float eps) {
   constexpr int kUnits = D / 16;
   const unsigned lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31 & ~(kUnits - 1));
   auto squares = [&]() {
-    float s0 = 0.f, s1 = 0.f;
+    uint64_t s[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      s0 = fmaf(x[k], x[k], s0);
-      s1 = fmaf(x[k + 8], x[k + 8], s1);
+      const uint64_t v = pack2f(x[2 * k], x[2 * k + 1]);
+      s[k & 1] = fma2f(v, v, s[k & 1]);
     }
-    s0 += s1;
+    float a, b, c, d;
+    unpack2f(s[0], a, b);
+    unpack2f(s[1], c, d);
+    float sum = (a + b) + (c + d);
 #pragma unroll
-    for (int o = kUnits / 2; o; o >>= 1) s0 += __shfl_xor_sync(lanes, s0, o);
-    return s0;
+    for (int o = kUnits / 2; o; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+    return sum;
   };
   float ss = squares();
   // bf16 reaches 3e38, whose squares do not fit: such a vector is made smaller first,
@@ -102,19 +134,14 @@ __device__ __forceinline__ void normalise(float (&x)[16], const float* weight, i
     eps = eps * 0x1p-80f * 0x1p-80f;
   }
   const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-  const float4* wa = reinterpret_cast<const float4*>(weight + a * 8);
-  const float4* wb = reinterpret_cast<const float4*>(weight + b * 8);
+  const uint64_t r2 = pack2f(r, r);
+  // (the weights of piece a, then of piece b, each as shared_place has them)
+  const float4* w4 = reinterpret_cast<const float4*>(weight);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float4 v = wa[k], w = wb[k];
-    x[4 * k] *= r * v.x;
-    x[4 * k + 1] *= r * v.y;
-    x[4 * k + 2] *= r * v.z;
-    x[4 * k + 3] *= r * v.w;
-    x[4 * k + 8] *= r * w.x;
-    x[4 * k + 9] *= r * w.y;
-    x[4 * k + 10] *= r * w.z;
-    x[4 * k + 11] *= r * w.w;
+  for (int k = 0; k < 4; ++k) {
+    const float4 v = w4[k * kUnits + u];
+    unpack2f(mul2f(pack2f(x[4 * k], x[4 * k + 1]), mul2f(r2, pack2f(v.x, v.y))), x[4 * k], x[4 * k + 1]);
+    unpack2f(mul2f(pack2f(x[4 * k + 2], x[4 * k + 3]), mul2f(r2, pack2f(v.z, v.w))), x[4 * k + 2], x[4 * k + 3]);
   }
 }
 
@@ -130,6 +157,7 @@ __device__ __forceinline__ void normalise(float (&x)[16], const float* weight, i
 template <typename T, int D, bool kPairs, bool kI8, bool kNorm, int kTokens>
 __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kUnits = D / 16;                     // units per head vector
+  constexpr int kDeep = kNorm ? 2 : 3;               // units a thread has in flight
   __shared__ __align__(16) float cs[kTokens][D];
   __shared__ int64_t slots[kTokens];                 // where the token goes; -1: nowhere
   __shared__ int skip[kTokens];                      // its position is out of range
@@ -148,7 +176,14 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
     static_assert(kThreads >= 2 * D, "a weight a thread");
     if (threadIdx.x < 2 * D) {
       const T* w = static_cast<const T*>(threadIdx.x < D ? p.q_weight : p.k_weight);
-      weight[threadIdx.x / D][threadIdx.x % D] = w ? (float)w[threadIdx.x % D] + p.weight_offset : 1.f;
+      // value i of the unit's two pieces
+      const int at = threadIdx.x % D, unit = at / 16, i = at % 16;
+      int pa, pb;
+      bool unused;
+      unit_pieces<kPairs>(unit, rot, pa, pb, unused);
+      const int d = (i < 8 ? pa : pb) * 8 + i % 8;
+      weight[threadIdx.x / D][(i / 8) * (D / 2) + shared_place(unit * 8 + i % 8, kUnits)] =
+          w ? (float)w[d] + p.weight_offset : 1.f;
     }
   }
   for (int tok0 = blockIdx.x * kTokens; tok0 < p.num_tokens; tok0 += gridDim.x * kTokens) {
@@ -166,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
       const int k = i / rot, d = i - k * rot;
       const int pos = p.positions[p.pair_axis[d < half_dims ? d : d - half_dims] * p.axis_stride + tok0 + k];
       const bool fine = pos >= 0 && pos < p.max_position;
-      cs[k][d] = fine ? p.cos_sin[(int64_t)pos * rot + d] : 0.f;
+      cs[k][d < half_dims ? shared_place(d, rot / 16) : half_dims + shared_place(d - half_dims, rot / 16)] =
+          fine ? p.cos_sin[(int64_t)pos * rot + d] : 0.f;
       if (!fine) skip[k] = 1;
     }
     __syncthreads();
@@ -182,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < kDeep; ++e) {
         const int v = v0 + e * (kThreads / kUnits);
-        tok[e] = v / heads;
+        tok[e] = 0;                                  // v / heads, without a division (162 us instead of 170)
+#pragma unroll
+        for (int k = 1; k < kTokens; ++k) tok[e] += v >= k * heads;
         head[e] = v - tok[e] * heads;
         if (v >= vectors) tok[e] = -1;
         else if (head[e] >= hq && slots[tok[e]] == -1) tok[e] = -1;   // K and V that are not stored
@@ -204,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
           float x[16];
           unpack8<T>(va[e], x);
           unpack8<T>(vb[e], x + 8);
-          if (kNorm && part != 2) normalise<D>(x, weight[kNorm ? part : 0], a, b, p.eps);
-          if (turned) rotate<kPairs>(x, cs[tok[e]], u, half_dims);
+          if (kNorm && part != 2) normalise<D>(x, weight[kNorm ? part : 0], u, p.eps);
+          if (turned) rotate<kPairs>(x, cs[tok[e]], u, rot / 16);
           if (kI8 && part != 0) {
             const int h = head[e] - (part == 1 ? hq : hq + hkv);
             const int64_t slot = slots[tok[e]], block = slot >> shift;

@@ -52,5 +52,9 @@ __device__ __forceinline__ float any_cap(const ScoreShape& w, float y) {
   return fabsf(y) > 1.f ? w.cap_log2 * (1.f - __fdividef(2.f, 1.f + e)) : v;
 }
 
+// any_cap as a call, for where it is rarely needed: inlined it takes the place of code that is (8-bit decode of 8 columns:
+// 715 us against 691).
+static __device__ __noinline__ float any_cap_call(const ScoreShape& w, float y) { return any_cap(w, y); }
+
 }  // namespace score
 }  // namespace pkv
