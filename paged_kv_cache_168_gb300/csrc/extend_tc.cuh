@@ -1,6 +1,7 @@
 // extend_tc.cuh -- attention of a chunk of new tokens per sequence over any paged
 // cache, on the tensor cores (tcgen05 + TMEM); instantiated by extend_tc.cu (plain
-// scores) and extend_scored.cu (kScored: shaped scores, below).
+// scores), extend_spans.cu, extend_cap.cu, extend_slopes.cu and extend_scored.cu
+// (shaped scores, below).
 //
 // Sequence s owns the packed query tokens query_start_loc[s] .. [s + 1]; query j
 // of its q_len sits at position ctx - q_len + j and attends the positions from
@@ -69,21 +70,31 @@
 // one a query tile, each in its own order, 628 instead of 588 (and the chunks 634
 // instead of 549: both softmaxes run at once and the tensor cores idle).
 //
-// kScored.  A score s = scale q.k becomes c tanh(s / c) (a cap c), then less slope_h
-// |distance|, and a query attends the positions of its own span [first, last] instead
-// of all up to its own.  The softmax threads shape the scores that they have read:
-//   cap       for y = s / c of at most 1 in size, y P(y^2) with a polynomial P of
-//             degree 5 fitted to tanh(y) / y (relative error 6e-7): eight packed fp32
-//             operations for two scores, on a pipe that has room, where 2^x and 1 / x
-//             would triple the load of the special-function units, which the softmax
-//             already uses half of the time.  A warp that meets a larger |y| in a tile
-//             takes the exact form for that tile, 32 columns at a time through TMEM.
-//   distance  slope (t - p) is linear in the column up to the query's own position:
-//             a packed FMA with the columns' numbers.  Behind it (prefixes) the warp
-//             takes the exact form too.
+// Shaped scores.  A score s = scale q.k becomes c tanh(s / c) (a cap c), then less
+// slope_h |distance|, and a query attends the positions of its own span [first, last]
+// instead of all up to its own.  The softmax threads shape the scores that they have read:
+//   cap       c tanh(y) = y P(y^2) c for y = s / c of at most 3/4 (P: 5 terms, relative error
+//             5.7e-7, the division folded into them): seven packed fp32 operations for two
+//             scores, in the loop that takes the powers.  2^x and 1 / x instead would triple
+//             the load of the special-function units.  A warp that meets a larger |y| in a
+//             tile takes the exact form for that tile.
+//   distance  slope (t - p) is linear in the column up to the query's own position: a packed
+//             FMA, split into 16 columns' part and their first one's.  KV tiles are taken from
+//             the last one backwards: from left to right the maximum, and with it a rescaling
+//             of the results, would move with every tile (16 prompts of 2048 tokens: 876 us
+//             instead of 705).  Behind a query (prefixes) the warp takes the exact form.
 //   spans     the planner finds each query tile's first and last position, and which
-//             positions all of its queries attend; only KV tiles outside of those are
-//             masked.
+//             positions all of its queries attend; only KV tiles outside of those are masked.
+// What bounds it: beside what bounds the plain scores, instructions.  A softmax warp has its
+// quarter of the SM nearly to itself, and straight code beyond about 160 instructions costs it
+// 2.6 clocks an instruction, beyond about 700 in all roles 5 (measured with rows of independent
+// FMAs); packed FMAs take 2.3 clocks.  So a tile's code is what counts: each shape has kernels
+// of its own, without conditions, and rare forms stand behind what is common.  Measured (us, bf16
+// but for the slopes, the rate counts the attended pairs): 32 capped chunks of 512 over 512 to
+// 3584, 32 + 8 heads, 640 (1.0 PFLOP/s; plain scores 530); 16 prompts of 2048 with slopes, 32 + 32
+// heads in fp16, 700 (0.79; plain 592); 2 rows of 8192 tokens of packed documents with prefixes
+// 340 (0.52; most KV tiles are masked somewhere); capped chunks over an 8-bit cache in a window of
+// 1500 690 (0.37; plain 526); 8 x 4 tokens over 32K to 128K, capped, 566 (5.9 TB/s).
 #pragma once
 
 #include <cuda.h>
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
 enum Shape {
   kNone,                                   // pa_extend
   kSpans,                                  // spans of each query alone
-  kCap,                                    // a cap that folds (scores.cuh), in bf16 one of at most 96 in base 2
+  kCap,                                    // a cap that folds (scores.cuh), in bf16 one of at most 80 in base 2
   kSlope,                                  // slopes alone, no position behind the query's own
   kAny                                     // both, slopes with such positions, or a cap that does not fold
 };
@@ -498,7 +509,7 @@ struct Cfg {
   static constexpr bool kConvert = F != kBulk;
   // Where no maximum is needed (kFixed below) and registers allow, two threads share a row, 64 columns each: a softmax
   // warp is otherwise alone with its tile on its quarter of the SM, and waits for every result and every instruction by
-  // itself.  (Capped chunks 835 -> CAPPED us.  With a maximum the halves have to meet in every tile: slopes 876 -> 987,
+  // itself.  (Capped chunks 835 -> 742 us.  With a maximum the halves have to meet in every tile: slopes 876 -> 987,
   // plain scores 552 -> 632.)
   static constexpr int kHalves = kShape == kCap && kBf16 && !kConvert ? 2 : 1;
   static constexpr int kSoft = 8 * kHalves;                   // softmax warps; the other roles' follow
@@ -785,8 +796,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
   uint8_t* ring = qbuf + 2 * C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(ring + C::kRingBytes);
   Scales& scales = *reinterpret_cast<Scales*>(&sh + 1);            // 8-bit caches alone
-  // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 96 in base 2 they are taken
-  // against 0, without a maximum (2^96 times 2^20 tokens and 2^-96 are far inside that range).
+  // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 80 in base 2 they are taken
+  // against 0, without a maximum.  Sums of 2^80 over 2^31 tokens stay finite beside values up to 2^16; where all scores
+  // of a row are at -c, values down to 2^-46 are kept.
   constexpr bool kFixed = kShape == kCap && kBF16 && !kI8;
   // Scores that fall with distance are largest where the queries are: with the last KV tile first the running maximum is
   // found at once, from left to right it would rise, and the results be rescaled, with every tile.
@@ -1740,7 +1752,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
         } else if constexpr (kFixed) {
           // 32 columns at a time, weights against 0.  The weights wait in registers until it is known that every score was
           // near enough for the polynomial: one vote a tile, and its other form out of the way (votes in every part, with
-          // that form between them: 742 us instead of CAPPED).
+          // that form between them: 742 us instead of 642).
           const int lo = edge ? span_from<true>(p, pos, w.held, token()) - t0 : 0;       // attended columns [lo, hi)
           const int hi = edge ? (row_ok ? span_to<true>(p, pos, w.kv_end, token()) + 1 - t0 : 0) : kCols;
           if (edge && zero_rows(w, jt, c)) break;

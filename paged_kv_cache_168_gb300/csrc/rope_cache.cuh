@@ -153,7 +153,10 @@ __device__ __forceinline__ void normalise(float (&x)[16], const float* weight, i
 // places there.
 //
 // kNorm: q and k vectors become x / sqrt(mean(x^2) + eps) (weight + offset) first, in
-// fp32 and not rounded before the rotation; the weights wait in shared memory.
+// fp32 and not rounded before the rotation; the weights wait in shared memory.  32768
+// tokens of 32 + 8 heads: 163 us, 4.9 TB/s, the issue slots two thirds busy (squares,
+// weights and rotation of every element); three CTAs an SM with more registers 205,
+// five or six with fewer 174 to 197.
 template <typename T, int D, bool kPairs, bool kI8, bool kNorm, int kTokens>
 __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kUnits = D / 16;                     // units per head vector

@@ -162,6 +162,16 @@ def test_caps_of_every_size(cap, dtype, kv8):
 
 
 @pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale,cap", [(1e-6, 1e-4), (3e-8, 1e-4), (3e-3, 55.0), (3e-3, 56.0), (1e-4, 1e4)])
+def test_small_scales_under_caps(scale, cap, dtype, kv8):
+    """Quotients of scale and cap whose ninth power leaves fp32, and caps at both sides of those that need no maximum."""
+    rng = np.random.default_rng(30)
+    case = Scored(rng, [140, 1], [500, 300], size=20.0, Hq=4, Hkv=2, D=128, bs=16, dtype=dtype, kv8=kv8)
+    check(case, scale=scale, cap=cap)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
 def test_rows_at_both_sides_of_the_cap(kv8):
     """Query rows of one tile whose scores are tiny, and some hundreds of times the cap."""
     rng = np.random.default_rng(4)
