@@ -373,10 +373,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const __grid_cons
       for (int j = tid & 31; j < t.npos && !q.zero; j += 32) {
         const int a = span_from<kScored>(p, t.pos0 + j, t.held, t.row0 + j);
         const int b = span_to<kScored>(p, t.pos0 + j, q.ctx, t.row0 + j);
-        if (a > b) {                                          // it attends nothing: every KV tile is masked
-          first_max = INT32_MAX - kKv;
-          continue;
-        }
+        if (a > b) continue;                                  // it attends nothing; its row is zeroed in the end
         first = min(first, a);
         first_max = max(first_max, a);
         last_min = min(last_min, b);
@@ -2007,6 +2004,12 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
             l = lk;
           }
         }
+      }
+      // a row that attends nothing has not made its tiles masked ones: it was worked out like the others, and is left out
+      if (kScored && (p.first_pos || p.last_pos) &&
+          span_from<kScored>(p, pos, w.held, token()) > span_to<kScored>(p, pos, w.kv_end, token())) {
+        m = -INFINITY;
+        l = 0.f;
       }
       if (ok && n > 0 && !wait(&sh.pv_done[t][(num - 1) & 1], ((num - 1) >> 1) & 1)) ok = false;
       if (!ok) break;
