@@ -93,7 +93,7 @@
 // but for the slopes, the rate counts the attended pairs): 32 capped chunks of 512 over 512 to
 // 3584, 32 + 8 heads, 640 (1.0 PFLOP/s; plain scores 530); 16 prompts of 2048 with slopes, 32 + 32
 // heads in fp16, 700 (0.79; plain 592); 2 rows of 8192 tokens of packed documents with prefixes
-// 340 (0.52; most KV tiles are masked somewhere); capped chunks over an 8-bit cache in a window of
+// 319 (0.56; most KV tiles are masked somewhere); capped chunks over an 8-bit cache in a window of
 // 1500 690 (0.37; plain 526); 8 x 4 tokens over 32K to 128K, capped, 566 (5.9 TB/s).
 #pragma once
 

@@ -942,7 +942,8 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
                             size_t workspace_bytes, uint32_t* dev_err, void* stream) {
   pkv::ExtendParams p{};
   bool empty = false;
-  const pa_status st = extend_params(p, pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len), false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
+  const size_t need = pa_extend_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
+  const pa_status st = extend_params(p, need, false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
                                      block_tables, block_table_stride, block_table_width, context_lens,
                                      query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
                                      ring_blocks, workspace, workspace_bytes, dev_err);
@@ -963,9 +964,9 @@ pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, con
   bool empty = false;
   pa_status st = score_params(p, scale, softcap, slopes, first_pos, last_pos, INT32_MAX);
   if (st != PA_OK) return st;
-  st = extend_params(p, pa_extend_scored_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len), false, &empty, out, q, q_token_stride, kv_cache, desc, layer,
-                     block_tables, block_table_stride, block_table_width, context_lens,
-                     query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
+  const size_t need = pa_extend_scored_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
+  st = extend_params(p, need, false, &empty, out, q, q_token_stride, kv_cache, desc, layer, block_tables,
+                     block_table_stride, block_table_width, context_lens, query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
                      ring_blocks, workspace, workspace_bytes, dev_err);
   if (st != PA_OK || empty) return st;
   cudaError_t e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size,
@@ -984,7 +985,8 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
   bool empty = false;
   pa_status st = score_params(p, scale, softcap, slopes, first_pos, nullptr, max_context_len);
   if (st != PA_OK) return st;
-  st = extend_params(p, pa_decode_scored_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len), true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
+  const size_t need = pa_decode_scored_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len);
+  st = extend_params(p, need, true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
                      block_table_stride, block_table_width, context_lens, nullptr, num_seqs, num_seqs, num_q_heads, 1,
                      scale, window, ring_blocks, workspace, workspace_bytes, dev_err);
   if (st != PA_OK || empty) return st;
