@@ -966,8 +966,9 @@ pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, con
   if (st != PA_OK) return st;
   const size_t need = pa_extend_scored_workspace_bytes(desc, num_seqs, num_tokens, num_q_heads, max_query_len);
   st = extend_params(p, need, false, &empty, out, q, q_token_stride, kv_cache, desc, layer, block_tables,
-                     block_table_stride, block_table_width, context_lens, query_start_loc, num_seqs, num_tokens, num_q_heads, max_query_len, scale, window,
-                     ring_blocks, workspace, workspace_bytes, dev_err);
+                     block_table_stride, block_table_width, context_lens, query_start_loc, num_seqs,
+                     num_tokens, num_q_heads, max_query_len, scale, window, ring_blocks, workspace, workspace_bytes,
+                     dev_err);
   if (st != PA_OK || empty) return st;
   cudaError_t e = pkv::launch_extend_scored(p, workspace, device_sm_count(), act_dtype(desc), desc->head_size,
                                             is_i8(desc), static_cast<cudaStream_t>(stream));
