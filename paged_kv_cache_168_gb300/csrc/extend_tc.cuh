@@ -2084,6 +2084,11 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       const int row_a = upper ? other : mine, row_b = upper ? mine : other;
       uint64_t odd[2] = {0, 0};                                      // NaN once any value is not finite
       const uint64_t scale2 = pack2f(scale, scale);
+      // A row that attends nothing is zero, whatever the tiles that it was worked out with made of it: a K scale that is
+      // not finite, which all other rows attend, and 0 * NaN is NaN.  (Over a 16-bit cache such values are seen below,
+      // and parts are left out by their sum of 0.)
+      const bool blank = kI8 && kScored && row_ok && l == 0.f;
+      const bool blanks = kI8 && kScored && __any_sync(kFull, blank);
       for (int e = col0; e < col0 + ncol; e += 32) {
         float o[32];
         if (have0) {
@@ -2105,6 +2110,10 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) odd[k & 1] = fma2f(pack2f(o[2 * k], o[2 * k + 1]), 0, odd[k & 1]);
+        if (blanks) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = blank ? 0.f : o[k];
+        }
         if (!part) {
           uint32_t y[16];
 #pragma unroll
@@ -2243,7 +2252,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Ext
     for (int k = 0; k < parts; ++k) {
       const int64_t at = first + (int64_t)k * rows;
       const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
-      // nothing attended in this part: its o is zero; -inf with a sum: NaN scores
+      // nothing attended in this part: its o is finite and counts nothing; -inf with a sum: NaN scores
       const float f = ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
       l = fmaf(ml.y, f, l);
 #pragma unroll
