@@ -105,8 +105,9 @@ __device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
 }
 
 // x becomes x / sqrt(mean of the vector's squares + eps) w; the vector's D / 16 units are neighbouring lanes.
+// False where the vector is not finite.
 template <int D>
-__device__ __forceinline__ void normalise(float (&x)[16], const float* weight, int u, float eps) {
+__device__ __forceinline__ bool normalise(float (&x)[16], const float* weight, int u, float eps) {
   constexpr int kUnits = D / 16;
   const unsigned lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31 & ~(kUnits - 1));
   auto squares = [&]() {
@@ -143,6 +144,7 @@ __device__ __forceinline__ void normalise(float (&x)[16], const float* weight, i
     unpack2f(mul2f(pack2f(x[4 * k], x[4 * k + 1]), mul2f(r2, pack2f(v.x, v.y))), x[4 * k], x[4 * k + 1]);
     unpack2f(mul2f(pack2f(x[4 * k + 2], x[4 * k + 3]), mul2f(r2, pack2f(v.z, v.w))), x[4 * k + 2], x[4 * k + 3]);
   }
+  return r > 0.f;
 }
 
 // A round of a CTA is kTokens tokens: their cosines and sines go to shared memory,
@@ -245,7 +247,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
           float x[16];
           unpack8<T>(va[e], x);
           unpack8<T>(vb[e], x + 8);
-          if (kNorm && part != 2) normalise<D>(x, weight[kNorm ? part : 0], u, p.eps);
+          bool finite = true;
+          if (kNorm && part != 2) finite = normalise<D>(x, weight[kNorm ? part : 0], u, p.eps);
           if (turned) rotate<kPairs>(x, cs[tok[e]], u, rot / 16);
           if (kI8 && part != 0) {
             const int h = head[e] - (part == 1 ? hq : hq + hkv);
@@ -280,6 +283,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
                 code[k] = __byte_perm(__byte_perm(r[4 * k], r[4 * k + 1], 0x0040), __byte_perm(r[4 * k + 2], r[4 * k + 3], 0x0040), 0x5410);
               scale = __fmul_rn(amax, 1.f / 127.f);
             }
+            // (a norm leaves such a vector 0 and NaN, whose codes are all 0: the scale says what it is)
+            if (kNorm && !finite) scale = __int_as_float(0x7fffffff);
             uint8_t* at = p.cache + L8.chunk(block, h) + ((part - 1) * p.block_size + t) * 128;
             *reinterpret_cast<uint2*>(at + ((((a >> 1) ^ (t & 7)) << 4) | (a & 1) << 3)) = make_uint2(code[0], code[1]);
             *reinterpret_cast<uint2*>(at + ((((b >> 1) ^ (t & 7)) << 4) | (b & 1) << 3)) = make_uint2(code[2], code[3]);
