@@ -505,7 +505,10 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
                            int32_t ring_blocks, float softcap, const float* slopes, const int32_t* first_pos,
                            void* workspace, size_t workspace_bytes, uint32_t* dev_err, void* stream);
 
-/* Workspace bytes of pa_decode_scored (0: nothing to do, or shapes it refuses). */
+/* Workspace bytes of pa_decode_scored (0: nothing to do, or shapes it refuses).  For a
+ * call with a window or a ring, pa_decode_window_span(max_context_len, block_size,
+ * window, ring_blocks) may stand for max_context_len here, as for pa_decode_window;
+ * what max_context_len itself gives is enough too. */
 size_t pa_decode_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_q_heads,
                                         int32_t max_context_len);
 

@@ -527,6 +527,7 @@ def extend_scored_workspace_bytes(desc: CacheDesc, num_seqs: int, num_tokens: in
 
 
 def decode_scored_workspace_bytes(desc: CacheDesc, num_seqs: int, num_q_heads: int, max_context_len: int) -> int:
+    """Of a call with a window or a ring: with decode_window_span(...) for max_context_len."""
     return load().pa_decode_scored_workspace_bytes(ctypes.byref(desc.c()), num_seqs, num_q_heads, max_context_len)
 
 

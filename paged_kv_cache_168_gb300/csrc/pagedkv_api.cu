@@ -299,6 +299,19 @@ bool decode_scored_on_decode_kernel(const pa_cache_desc* d, int32_t num_seqs, in
   return group == 1 || group == 2 || group == 4 || group == 8 || (group == 16 && !is_i8(d));
 }
 
+// How pa_decode_scored splits contexts on the decode kernel: the partitions that a windowed span wants, unless there
+// would be more of them than a workspace for all of max_context_len holds (its own partition size always fits).
+void scored_partitions(const pa_cache_desc* d, int32_t num_seqs, int32_t max_context_len, int32_t window,
+                       int32_t ring_blocks, int32_t* size, int32_t* count) {
+  const int32_t span = pa_decode_window_span(max_context_len, d->block_size, window, ring_blocks);
+  const int32_t most_P = pa_decode_partition_size(d, num_seqs, max_context_len, 0);
+  const int32_t most = (max_context_len - 1) / most_P + 1;
+  int32_t P = pa_decode_partition_size(d, num_seqs, span, 0);
+  while (P < most_P && (span - 1) / P + 1 > most) P *= 2;
+  *size = P;
+  *count = (span - 1) / P + 1;
+}
+
 // Workspace of pa_extend, or (scored) of the calls with shaped scores.
 size_t extend_workspace_bytes(const pa_cache_desc* desc, int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                               int32_t max_query_len, bool scored) {
@@ -986,7 +999,14 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
   bool empty = false;
   pa_status st = score_params(p, scale, softcap, slopes, first_pos, nullptr, max_context_len);
   if (st != PA_OK) return st;
-  const size_t need = pa_decode_scored_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len);
+  size_t need = pa_decode_scored_workspace_bytes(desc, num_seqs, num_q_heads, max_context_len);
+  if (need && decode_scored_on_decode_kernel(desc, num_seqs, num_q_heads)) {
+    // a windowed call keeps the parts of what it attends
+    int32_t P, count;
+    scored_partitions(desc, num_seqs, max_context_len, window, ring_blocks, &P, &count);
+    need = pa_decode_workspace_bytes(desc, num_seqs, num_q_heads,
+                                     pa_decode_window_span(max_context_len, desc->block_size, window, ring_blocks), P);
+  }
   st = extend_params(p, need, true, &empty, out, q, q_seq_stride, kv_cache, desc, layer, block_tables,
                      block_table_stride, block_table_width, context_lens, nullptr, num_seqs, num_seqs, num_q_heads, 1,
                      scale, window, ring_blocks, workspace, workspace_bytes, dev_err);
@@ -1008,15 +1028,7 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
     d.num_seqs = num_seqs;
     d.num_q_heads = num_q_heads;
     d.max_context_len = max_context_len;
-    // the partitions that a windowed span wants, unless there would be more of them than the workspace of
-    // max_context_len holds (its own partition size always fits)
-    const int32_t span = pa_decode_window_span(max_context_len, desc->block_size, window, ring_blocks);
-    const int32_t most_P = pa_decode_partition_size(desc, num_seqs, max_context_len, 0);
-    const int32_t most = (max_context_len - 1) / most_P + 1;
-    int32_t P = pa_decode_partition_size(desc, num_seqs, span, 0);
-    while (P < most_P && (span - 1) / P + 1 > most) P *= 2;
-    d.partition_size = P;
-    d.max_parts = (span - 1) / P + 1;
+    scored_partitions(desc, num_seqs, max_context_len, window, ring_blocks, &d.partition_size, &d.max_parts);
     d.scale_log2 = p.scale_log2;
     if (d.max_parts > 1) {
       d.ws_o = static_cast<float*>(workspace);

@@ -1,0 +1,34 @@
+"""Refusals and workspaces of the calls with shaped scores and normed heads at the ends of their ranges.  No call here
+reaches a kernel launch."""
+import pytest
+import torch
+
+from paged_kv_cache_168_gb300 import _lib, build as build_mod
+from paged_kv_cache_168_gb300._lib import CacheDesc
+from test_scored_ops_cpu import FAKE, _decode, _desc
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return _lib.load()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("window,ring", [(0, 12), (1500, 0), (100, 12)])
+@pytest.mark.parametrize("S,Hq", [(1, 8), (256, 64), (8, 6)])
+def test_windowed_workspaces_of_single_tokens(lib, S, Hq, window, ring, kv8):
+    """What a windowed or ring call needs is what its span needs, whatever the contexts' length; the whole context's
+    workspace is enough too."""
+    d = CacheDesc(16, 16, 2, 128, torch.bfloat16, kv_int8=kv8)
+    args = lambda n, ws=FAKE: dict(desc=_desc(dtype=torch.bfloat16, kv_int8=kv8), S=S, Hq=Hq, window=window, ring=ring, stride=1 << 27, width=1 << 27,
+                                   out=FAKE + (1 << 40), ws_bytes=n, ws=ws)
+    for most in (1400, 20000, 2**31 - 1):
+        span = _lib.decode_window_span(most, 16, window, ring)
+        of_span, of_all = _lib.decode_scored_workspace_bytes(d, S, Hq, span), _lib.decode_scored_workspace_bytes(d, S, Hq, most)
+        if of_span == 0:                                             # (nothing left to refuse: the call would be made)
+            continue
+        for n in (of_span, of_all):                                  # refused for its address alone: the size is enough
+            assert _decode(lib, max_ctx=most, **args(n, FAKE + 8)) == _lib.PA_ERR_INVALID_ARG, (most, n)
+            assert b"aligned" in lib.pa_last_error_message()
+        assert _decode(lib, max_ctx=most, **args(15)) == _lib.PA_ERR_WORKSPACE_TOO_SMALL
