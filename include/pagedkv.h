@@ -351,7 +351,8 @@ int32_t pa_decode_partition_size(const pa_cache_desc* desc, int32_t num_seqs, in
  *                 ceil(ctx / block_size) are never read.
  *   context_lens  device int32 [num_seqs].
  *   max_context_len  an upper bound of context_lens (sizes the launch and the
- *                 workspace); a longer context sets PA_DEVERR_CONTEXT.
+ *                 workspace); a longer context sets PA_DEVERR_CONTEXT and gets
+ *                 a zero row, as does one beyond 2^31 - 16385.
  *   partition_size   0 (default) or a multiple of 128 in [128, 8192].
  *   workspace     device, 16-byte aligned, >= pa_decode_workspace_bytes(...);
  *                 may be NULL when that is 0.  Contents need no initialisation.
@@ -496,8 +497,9 @@ size_t pa_extend_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_s
 /* pa_extend_scored for one query token per sequence, its newest (p = ctx - 1):
  * what pa_decode_window is to pa_extend.  q and out hold a row a sequence,
  * first_pos an entry a sequence.  ctx <= 0 gives a zero row; a context longer than
- * max_context_len or than its table row gives one and PA_DEVERR_CONTEXT.  Every
- * cache, and 1 to 16 query heads per kv head. */
+ * max_context_len, than its table row or (pa_decode's shapes) than 2^31 - 16385
+ * gives one and PA_DEVERR_CONTEXT.  Every cache, and 1 to 16 query heads per kv
+ * head. */
 pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const void* kv_cache,
                            const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
                            int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,

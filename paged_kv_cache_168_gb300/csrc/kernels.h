@@ -81,6 +81,10 @@ __host__ __device__ inline int window_start(int ctx, int bs, int window, int rin
 // Table entry holding logical block j.
 __host__ __device__ inline int table_index(int j, int ring) { return ring > 0 ? j % ring : j; }
 
+// Longest context of the decode kernels (DecodeParams::max_context_len is at most that): the ends of its partitions (of
+// up to 8192 tokens), and of those that a grid has beyond the last one, stay in int32.
+constexpr int kLongestContext = INT32_MAX - 2 * 8192;
+
 // Whether a context length can be served: linear rows must hold it; every
 // context must be within max_context_len.
 __host__ __device__ inline bool context_ok(const DecodeParams& p, int ctx) {

@@ -702,9 +702,9 @@ pa_status pa_decode_window(void* out, const void* q, int64_t q_seq_stride, const
   p.context_lens = context_lens;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
-  p.max_context_len = max_context_len;
+  p.max_context_len = std::min(max_context_len, pkv::kLongestContext);
   p.partition_size = P;
-  p.max_parts = (span + P - 1) / P;
+  p.max_parts = (span - 1) / P + 1;
   p.window = window;
   p.ring_blocks = ring_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -829,9 +829,9 @@ pa_status pa_decode_shared_prefix(void* out, const void* q, int64_t q_seq_stride
   p.context_lens = context_lens;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
-  p.max_context_len = max_context_len;
+  p.max_context_len = std::min(max_context_len, pkv::kLongestContext);
   p.partition_size = P;
-  p.max_parts = (max_context_len + P - 1) / P + 1;
+  p.max_parts = (max_context_len - 1) / P + 2;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_polls = test_wait_polls();
   const int64_t rows = (int64_t)num_seqs * num_q_heads * p.max_parts;
@@ -1027,7 +1027,7 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
     d.context_lens = context_lens;
     d.num_seqs = num_seqs;
     d.num_q_heads = num_q_heads;
-    d.max_context_len = max_context_len;
+    d.max_context_len = std::min(max_context_len, pkv::kLongestContext);
     scored_partitions(desc, num_seqs, max_context_len, window, ring_blocks, &d.partition_size, &d.max_parts);
     d.scale_log2 = p.scale_log2;
     if (d.max_parts > 1) {
