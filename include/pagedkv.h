@@ -475,7 +475,12 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
  * the document; a prefix that sees itself whole is last_pos = max(p, its last
  * position).  A query whose span is empty gets a zero row.
  *   softcap     0 (none) or in [1e-4, 1e6]; a capped score is off by at most 2^-20
- *               of it, as the sums are in fp32.
+ *               of it, as the sums are in fp32.  Chunks over bf16 caches take the
+ *               weights of caps up to 55 against a score of 0: results are off by
+ *               up to 2^-86 a token, and query tiles with values too large or too
+ *               small for that (beyond 2^16 beside scores near the cap; below
+ *               2^-56, or 0, in rows whose scores are all below -28) are worked
+ *               out again on CUDA cores, which is slow.
  *   slopes      device fp32 [num_q_heads], finite, any sign; NULL: none.
  *   first_pos, last_pos  device int32 [num_tokens]; NULL: 0 and p.  Any values:
  *               they are clamped to the positions that exist.  Positions behind p

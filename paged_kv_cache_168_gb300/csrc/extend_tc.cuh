@@ -124,7 +124,7 @@ constexpr float kRescaleThreshold = 8.f;   // base-2 units
 constexpr float kLift = 7.f;
 
 // Flags of a query tile and kv head.
-constexpr uint32_t kBadBlock = 1, kNonFinite = 2;
+constexpr uint32_t kBadBlock = 1, kRedo = 2;
 
 // ------------------------------------------------------------------ workspace
 struct Header {
@@ -794,8 +794,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
   Shared& sh = *reinterpret_cast<Shared*>(ring + C::kRingBytes);
   Scales& scales = *reinterpret_cast<Scales*>(&sh + 1);            // 8-bit caches alone
   // Capped scores lie in [-c, c]: with bf16 weights, whose range is fp32's, and c up to 80 in base 2 they are taken
-  // against 0, without a maximum.  Sums of 2^80 over 2^31 tokens stay finite beside values up to 2^16; where all scores
-  // of a row are at -c, values down to 2^-46 are kept.
+  // against 0, without a maximum.  Sums of 2^80 over 2^31 tokens stay finite beside values up to 2^16; larger results are
+  // seen as infinities, and those of rows near -c whose products leave fp32 at its lower end by their size: such items are
+  // redone on CUDA cores against a maximum.  What is not seen is below 2^-126 a token beside weights of 2^-40 or more.
   constexpr bool kFixed = kShape == kCap && kBF16 && !kI8;
   // Scores that fall with distance are largest where the queries are: with the last KV tile first the running maximum is
   // found at once, from left to right it would rise, and the results be rescaled, with every tile.
@@ -2020,7 +2021,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
         report(p.dev_err, PA_DEVERR_BLOCK_ID);
       }
       if (kI8 && lane == 0 && sh.odd[i % kRing]) {
-        atomicOr(&ws.flags[w.flag], kNonFinite);
+        atomicOr(&ws.flags[w.flag], kRedo);
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
       }
       // ---- results: columns [c0, c0 + nc) of my row
@@ -2069,6 +2070,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       }
       const bool part = w.part_row >= 0;
       const float scale = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      // Weights against 0 (kFixed) whose sum is below 2^-40: products with small values may have left fp32.
+      const bool faint = kFixed && row_ok && l > 0.f && l < 0x1p-40f;
+      float least = INFINITY;                                        // of such a row's |o|
       const int rr = (my0 + ipos) * G + head;                        // row within the item
       const int part_row = w.part_row;
       float* prow = ws.o + (int64_t)(part_row + rr) * D;
@@ -2110,6 +2114,10 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) odd[k & 1] = fma2f(pack2f(o[2 * k], o[2 * k + 1]), 0, odd[k & 1]);
+        if (kFixed && faint) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) least = fminf(least, fabsf(o[k]));
+        }
         if (blanks) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = blank ? 0.f : o[k];
@@ -2142,11 +2150,13 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
         *reinterpret_cast<float2*>(ws.ml + 2 * (int64_t)(part_row + rr)) = make_float2(m, l);
       // A V that is not finite reaches rows that do not attend it (0 * NaN = NaN):
       // finish_kernel redoes the item.  (8-bit codes are finite; scales that are not
-      // have been seen above.)
+      // have been seen above.)  The same where a faint row has results so small that
+      // products of 2^-126 and less, or the lack of them, may matter.
       float odd_a, odd_b;
       unpack2f(add2f(odd[0], odd[1]), odd_a, odd_b);
-      if (!kI8 && __any_sync(kFull, row_ok && !(odd_a + odd_b == 0.f)) && lane == 0) {
-        atomicOr(&ws.flags[w.flag], kNonFinite);
+      const bool lost = faint && least < 0x1p-96f;
+      if (!kI8 && __any_sync(kFull, (row_ok && !(odd_a + odd_b == 0.f)) || lost) && lane == 0) {
+        atomicOr(&ws.flags[w.flag], kRedo);
         atomicOr(reinterpret_cast<uint32_t*>(&ws.head->any_flag), 1u);
       }
       // both halves have read both accumulators before either is overwritten

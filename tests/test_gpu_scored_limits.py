@@ -1,4 +1,6 @@
 """pa_extend_scored and pa_decode_scored at the ends of what their interface allows."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -6,7 +8,7 @@ import torch
 import paged_kv_cache_168_gb300 as pkv
 import step_ref
 from gpu_helpers import dev_to_u16, ensure_built, u16_to_dev
-from paged_helpers import bits_to_f64
+from paged_helpers import bits_to_f64, to_bits
 from scored_ref import Scored, alibi
 from test_gpu_scored import assert_close, decode, desc_of, dev, pool_to_dev, run
 
@@ -54,6 +56,66 @@ def test_empty_spans_beside_bad_key_scales(q_lens, ctx, kind, what):
     assert (np.abs(got[:, :3] - out[:, :3]) <= tol[:, :3]).all()     # the other kv head
     if np.isnan(what):
         assert np.isnan(got[~empty][:, 3:]).all()
+
+
+# ------------------------------------------------------------------ the ends of the value range under a cap
+
+def saturated(side, cap, spread, dtype="bf16", q_lens=(100, 3), ctx=(300, 200), exponents=(0, 0), share=1.0, seed=0, kv8=False):
+    """Chunks whose scores all lie near side * cap * spread (spread 1: at the cap), with values of 2^exponents."""
+    rng = np.random.default_rng(seed)
+    case = Scored(rng, list(q_lens), list(ctx), Hq=4, Hkv=2, D=128, bs=16, dtype=dtype)
+    c = case.cache
+    unit = rng.choice([-1.0, 1.0], (1, 128))
+    case.q_bits = to_bits(np.broadcast_to(side * unit, (case.T, 4, 128)) * rng.uniform(0.97, 1.0, (case.T, 4, 1)), dtype)
+    case.q = bits_to_f64(case.q_bits, dtype)
+    for s, n in enumerate(ctx):
+        t = np.arange(n)
+        for h in range(2):
+            base = (case.tables[s, t // 16] * c.Hkv + h) * step_ref.chunk_elements(16, 128)
+            c.pool[base[:, None] + step_ref.offsets16(16, 128, t % 16, 0)] = to_bits(unit * rng.uniform(0.97, 1.0, (n, 1)), dtype)
+            v = rng.standard_normal((n, 128)) * 2.0 ** rng.uniform(*exponents, (n, 1)) if exponents[0] != exponents[1] else \
+                rng.standard_normal((n, 128)) * 2.0 ** exponents[0]
+            c.pool[base[:, None] + step_ref.offsets16(16, 128, t % 16, 1)] = to_bits(v, dtype)
+    # q.k is 128 up to 6%; scale * 128 / cap = atanh(spread), or 8 (tanh is 1 - 2^-22 there) at the cap
+    y = 8.0 if spread >= 1 else math.atanh(spread)
+    return case, cap * y / 128
+
+
+@pytest.mark.parametrize("cap", [5.0, 30.0, 55.0])
+@pytest.mark.parametrize("spread", [0.5, 1.0])
+@pytest.mark.parametrize("exponent", [-40, -60, -75])
+def test_small_values_under_scores_near_the_lower_cap(exponent, spread, cap):
+    """Every score of a row is near -cap (or half of it): values far below 1 come back all the same."""
+    case, scale = saturated(-1, cap, spread, exponents=(exponent, exponent))
+    got = values(run(case, scale, cap=cap))
+    out, tol = case.shaped(scale, cap=cap)
+    big = np.abs(out).max()
+    assert 2.0 ** (exponent - 8) < big < 2.0 ** (exponent + 3)
+    # (the bound's floor of 1e-30 is far below these values)
+    bad = ~(np.abs(got - out) <= tol)
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], out[bad][:4], tol[bad][:4])
+
+
+@pytest.mark.parametrize("cap", [30.0, 55.0])
+@pytest.mark.parametrize("side", [-1, 1])
+@pytest.mark.parametrize("exponents", [(40, 40), (100, 100), (-60, 60)])
+def test_large_values_under_scores_near_a_cap(exponents, side, cap):
+    """Weights of e^cap beside values of 2^100 leave fp32; the results do not."""
+    case, scale = saturated(side, cap, 1.0, exponents=exponents)
+    assert_close(run(case, scale, cap=cap), case.shaped(scale, cap=cap))
+
+
+def test_zero_values_under_scores_near_the_lower_cap():
+    """Dims that are zero throughout stay zero, whatever the scores."""
+    case, scale = saturated(-1, 55.0, 1.0)
+    c = case.cache
+    for s, n in enumerate((300, 200)):
+        t = np.arange(n)
+        base = case.tables[s, t // 16] * c.Hkv * step_ref.chunk_elements(16, 128)
+        c.pool[base[:, None] + step_ref.offsets16(16, 128, t % 16, 1)[:, 96:]] = 0
+    got = run(case, scale, cap=55.0)
+    assert_close(got, case.shaped(scale, cap=55.0))
+    assert not values(got)[:, :2, 96:].any()
 
 
 # ------------------------------------------------------------------ rings and windows of far contexts
