@@ -481,7 +481,7 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
  *               small for that (beyond 2^16 beside scores near the cap; below
  *               2^-56, or 0, in rows whose scores are all below -28) are worked
  *               out again on CUDA cores, which is slow.
- *   slopes      device fp32 [num_q_heads], finite, any sign; NULL: none.
+ *   slopes      device fp32 [num_q_heads], at most 1e27 in size, any sign; NULL: none.
  *   first_pos, last_pos  device int32 [num_tokens]; NULL: 0 and p.  Any values:
  *               they are clamped to the positions that exist.  Positions behind p
  *               have to be in the cache (the whole chunk is).

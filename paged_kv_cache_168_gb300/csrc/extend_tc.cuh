@@ -275,6 +275,13 @@ __device__ __forceinline__ int span_to(const ExtendParams& p, int pos, int ctx, 
   return kScored && p.last_pos ? max(min(p.last_pos[row], ctx - 1), -1) : pos;
 }
 
+// Distances of a row count from a position of its own, which the softmax does not see: its nearest attended one, `near`,
+// or with a slope below 0 its farthest one (`far_from` further).  The largest bias is 0 then: beside one of 2^30, scores and
+// the maximum would be rounded by more than a power of two can hold.
+__device__ __forceinline__ int far_from(const ExtendParams& p, int near, int pos, int held, int ctx, int row) {
+  return max(near - span_from<true>(p, pos, held, row), span_to<true>(p, pos, ctx, row) - near);
+}
+
 // A query tile: positions pos0 .. pos0 + npos - 1 of a sequence, from token row row0 on.
 struct Tile {
   int seq, row0, pos0, npos, held;
@@ -602,10 +609,11 @@ __device__ __forceinline__ uint64_t cap_quotient2(const ScoreShape& w, uint64_t 
   for (int k = kTerms - 2; k >= 0; --k) v = fma2f(v, s, pack2f(c[k], c[k]));
   return v;
 }
-// The base-2 score of any y (s / c where scores are capped, else s log2(e)), dist positions from the reference.
-__device__ __forceinline__ float shaped_score(const ScoreShape& w, float y, float slope2, int dist) {
+// The base-2 score of any y (s / c where scores are capped, else s log2(e)), dist positions from the row's nearest one;
+// shift: far_from, or 0.
+__device__ __forceinline__ float shaped_score(const ScoreShape& w, float y, float slope2, int dist, int shift) {
   const float v = w.capped ? score::any_cap(w, y) : y;
-  return w.slopes ? v - slope2 * fabsf((float)dist) : v;
+  return w.slopes ? v - slope2 * (float)(abs(dist) - shift) : v;
 }
 
 // 32 TMEM lanes x 64 columns; the wait is part of the statement.
@@ -1553,19 +1561,21 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
               // (K's scales made x base-2 scores, or quotients by the cap)
               bool exact = false;
               float sl[2] = {0.f, 0.f};
-              int at[2] = {0, 0};                                    // my first column less the row's reference position
+              int at[2] = {0, 0}, shift[2] = {0, 0};                 // my first column less the row's nearest position
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const bool is_row = ok4 >> r & 1;
                 if constexpr (kShape != kCap) {
                   const int rr = (warp & 3) * 32 + (lane >> 2) + 8 * (2 * h + r);
                   int nearest = pos4[r];
+                  const int tok = w.row0 + (is_row ? pos4[r] - w.pos0 : 0);
                   if (kShape == kAny && p.last_pos) {
-                    nearest = min(nearest, span_to<true>(p, pos4[r], w.kv_end, w.row0 + (is_row ? pos4[r] - w.pos0 : 0)));
+                    nearest = min(nearest, span_to<true>(p, pos4[r], w.kv_end, tok));
                     exact |= is_row && t0 + kKv - 1 > nearest;
                   }
                   if (p.shape.slopes) sl[r] = p.shape.slopes[w.kvh * G + rr % G] * score::kLog2e;
                   at[r] = t0 + 2 * (lane & 3) - nearest;
+                  if (sl[r] < 0.f) shift[r] = far_from(p, nearest, pos4[r], w.held, w.kv_end, tok);
                 }
                 if constexpr (kShape != kSlope) {
                   float big[2] = {0.f, 0.f};
@@ -1584,7 +1594,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
                   tmem_ld16x256_32(s_addr + half + 32 * e, v);
 #pragma unroll
                   for (int k = 0; k < 16; ++k)
-                    v[k] = shaped_score(p.shape, v[k], sl[k >> 1 & 1], at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + (k & 1));
+                    v[k] = kShape == kCap ? score::any_cap(p.shape, v[k])
+                                          : shaped_score(p.shape, v[k], sl[k >> 1 & 1],
+                                                         at[k >> 1 & 1] + 32 * e + 8 * (k >> 2) + (k & 1), shift[k >> 1 & 1]);
                   tmem_st16x256_32(s_addr + half + 32 * e, v);
                 }
                 tc::tmem_wait_st();
@@ -1597,7 +1609,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
                   if constexpr (kShape != kCap) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                      const float v = sl[r] * (float)(at[r] + 32 * k);
+                      const float v = sl[r] * (float)(at[r] + shift[r] + 32 * k);
                       in[k] = pack2f(sl[r] * (8.f * k), sl[r] * (8.f * k + 1.f));
                       off[k] = pack2f(v, v);
                     }
@@ -1819,12 +1831,13 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
           float unit = p.scale_log2, so = 0.f, base = 0.f;
           bool fly = kShape == kCap;
           if constexpr (kShape != kNone && kShape != kSpans) {
-            int ref = pos;                                           // distances count from the nearest attended position
+            int ref = pos, shift = 0;                                // the nearest attended position
             bool exact = false;
             if (kShape == kAny && p.last_pos) {
               ref = min(pos, span_to<true>(p, pos, w.kv_end, token()));
               exact = row_ok && t0 + kCols - 1 > ref;
             }
+            if (kShape != kCap && slope2 < 0.f) shift = far_from(p, ref, pos, w.held, w.kv_end, token());
             if constexpr (kShape != kSlope) {
               float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1842,7 +1855,9 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
                 tc::tmem_ld16(s_addr + e, v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k)
-                  v[k] = shaped_score(p.shape, v[k] * (p.shape.capped ? p.shape.cap_in : p.scale_log2), slope2, t0 + e + k - ref);
+                  v[k] = kShape == kCap ? score::any_cap(p.shape, v[k] * p.shape.cap_in)
+                                        : shaped_score(p.shape, v[k] * (p.shape.capped ? p.shape.cap_in : p.scale_log2), slope2,
+                                                       t0 + e + k - ref, shift);
                 tc::tmem_st16(s_addr + e, v);
               }
               tc::tmem_wait_st();
@@ -1853,7 +1868,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
             } else if constexpr (kShape != kCap) {
               if (p.shape.slopes) {
                 so = slope2;
-                base = slope2 * (float)(t0 - ref);
+                base = slope2 * (float)(t0 - ref + shift);
               }
               uint64_t in[8];                                        // the slope's part within 16 columns
 #pragma unroll
@@ -2196,6 +2211,7 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
   const int to = span_to<kScored>(p, pos, p.context_lens[it.seq], it.row0 + j), ref = min(pos, to);
   const float unit = kScored && p.shape.capped ? p.shape.cap_in : p.scale_log2;
   const float slope2 = kScored && p.shape.slopes ? p.shape.slopes[h] * score::kLog2e : 0.f;
+  const int shift = kScored && slope2 < 0.f ? far_from(p, ref, pos, it.held, p.context_lens[it.seq], it.row0 + j) : 0;
   const T* q = static_cast<const T*>(p.q) + (int64_t)(it.row0 + j) * p.q_token_stride + (int64_t)h * D + lane * kDims;
   float x[kDims], o[kDims], m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -2222,7 +2238,7 @@ __device__ void row_on_cuda_cores(const ExtendParams& p, const Item& it, int kvh
     for (int d = 0; d < kDims; ++d) z = fmaf(x[d], element(0, d), z);
 #pragma unroll
     for (int i = 16; i; i >>= 1) z += __shfl_xor_sync(kFull, z, i);
-    if constexpr (kScored) z = shaped_score(p.shape, z, slope2, t - ref);
+    if constexpr (kScored) z = shaped_score(p.shape, z, slope2, t - ref, shift);
     // (a score of -inf has weight 0, before any finite one too: there mn is -inf as well)
     const float mn = fmaxf(m, z), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = z == -INFINITY ? 0.f : exp2f(z - mn);
     l = l * a + e;

@@ -118,6 +118,51 @@ def test_zero_values_under_scores_near_the_lower_cap():
     assert not values(got)[:, :2, 96:].any()
 
 
+# ------------------------------------------------------------------ slopes of any size
+
+@pytest.mark.parametrize("cap", [0.0, 9.0])
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("slopes", [[1e27, -1e27, 1e15, -1e15], [1e8, -1e8, 3e4, -3e4], [3e5, -3e5, 3e6, -2e7]])
+def test_steep_slopes(slopes, kv8, cap):
+    """A positive slope leaves the nearest attended position, a negative one the farthest, with its value: also where
+    slope times distance is far beyond what a power of two can take."""
+    rng = np.random.default_rng(1)
+    s = np.asarray(slopes, np.float32)
+    case = Scored(rng, [260, 3], [900, 5000], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16", kv8=kv8)
+    n = int(case.qsl[-1])
+    pos = np.concatenate([np.arange(c - q, c) for q, c in zip(case.q_lens, case.ctx)])
+    seq = np.repeat([0, 1], case.q_lens)
+
+    def value(p, h):
+        out = np.empty((n, 128))
+        for b in (0, 1):
+            at = p[seq == b]
+            out[seq == b] = case.cache.read(case.tables[b, at // 16], at % 16, 1)[:, h]
+        return out
+
+    def expect(got, near, far, rows=slice(None)):
+        g = values(got)
+        for h in range(4):
+            want = value(near if s[h] > 0 else far, h // 2)[rows]
+            # one weight of 1; the result's rounding (half of bf16's step of 2^-7); in an 8-bit cache that of the weight,
+            # which carries V's scale (half of fp16's step of 2^-10, or of its smallest step 2^-24 beside codes of 127
+            # times 2^8 of the tile's largest scale)
+            slack = 2.0 ** -8 + (2.0 ** -11 if kv8 else 0)
+            assert (np.abs(g[:, h] - want) <= slack * np.abs(want) + (2.0 ** -12 if kv8 else 0)).all(), h
+
+    expect(run(case, 0.1, cap=cap, slopes=s), pos, 0 * pos)
+    first = np.maximum(pos - rng.integers(0, 300, n), 0).astype(np.int32)
+    expect(run(case, 0.1, cap=cap, slopes=s, first=first), pos, first)
+    last = (first + rng.integers(0, 50, n)).astype(np.int32)
+    last = np.minimum(last, pos).astype(np.int32)
+    expect(run(case, 0.1, cap=cap, slopes=s, first=first, last=last), last, first)
+    one = Scored(rng, [1] * 2, [900, 5000], Hq=4, Hkv=2, D=128, bs=16, dtype="bf16", kv8=kv8)
+    case, n, pos, seq = one, 2, np.asarray([899, 4999]), np.asarray([0, 1])
+    f = np.asarray([100, 4000], np.int32)
+    expect(decode(one, 0.1, cap=cap, slopes=s), pos, 0 * pos)
+    expect(decode(one, 0.1, cap=cap, slopes=s, first=f), pos, f)
+
+
 # ------------------------------------------------------------------ rings and windows of far contexts
 
 def far_ring(rng, kv8, D, Hq, bs=16, ring=12):
