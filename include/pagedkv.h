@@ -230,15 +230,15 @@ pa_status pa_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, con
  * (of key) becomes
  *   n = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
  * first, in fp32 from the 16-bit values (the mean over head_size dims, summed in
- * fp32; bf16 vectors whose squares leave fp32 are scaled down before), and n is
- * rotated without being rounded in between; dims from rotary_dim on are normed
+ * fp32; vectors whose squares leave fp32 are scaled before), and n is rotated
+ * without being rounded in between; dims from rotary_dim on are normed
  * alone.  v is not normed.  A vector that holds infinities or NaN gives NaN in
  * some or all of its dims; in an 8-bit cache such a key has a NaN scale, so that
  * queries that attend it get NaN.
  *   q_weight, k_weight  device [head_size], 16-bit as q; 2-byte aligned; NULL: no
  *                  weights (n = x / sqrt(...), whatever weight_offset is).
  *   weight_offset  added to every weight in fp32 (1 for weights stored around 0).
- *   eps            positive and finite.
+ *   eps            positive, at most 1e38.
  * Other arguments and errors as pa_rope_reshape_and_cache. */
 pa_status pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride, const void* q,
                                          int64_t q_token_stride, int32_t num_q_heads, void* kv_cache,

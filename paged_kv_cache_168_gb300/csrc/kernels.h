@@ -208,6 +208,7 @@ struct RopeParams {
   const void* k_weight;
   float weight_offset;
   float eps;
+  float small_squares;            // a vector with a smaller sum of squares is scaled up first (0: none)
 };
 cudaError_t launch_rope_cache(const RopeParams& p, int act_dtype, bool i8, int sms, cudaStream_t stream);
 // The same after a norm of each q and k vector.

@@ -560,7 +560,7 @@ pa_status pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride
                                    positions_axis_stride, cos_sin, max_position, rotary_dim, pair_axis, num_axes,
                                    interleaved, num_tokens, dev_err);
   if (st != PA_OK) return st;
-  if (!(eps > 0.f) || !(eps < INFINITY)) return fail(PA_ERR_INVALID_ARG, "eps must be a positive finite number");
+  if (!(eps > 0.f) || !(eps <= 1e38f)) return fail(PA_ERR_INVALID_ARG, "eps must be positive and at most 1e38");
   if (!(fabsf(weight_offset) < INFINITY)) return fail(PA_ERR_INVALID_ARG, "weight_offset must be finite");
   if ((reinterpret_cast<uintptr_t>(q_weight) & 1) || (reinterpret_cast<uintptr_t>(k_weight) & 1))
     return fail(PA_ERR_INVALID_ARG, "q_weight and k_weight must be 2-byte aligned");
@@ -569,6 +569,7 @@ pa_status pa_norm_rope_reshape_and_cache(void* q_out, int64_t q_out_token_stride
   p.k_weight = k_weight;
   p.weight_offset = weight_offset;
   p.eps = eps;
+  p.small_squares = eps < 0x1p-100f ? 0x1p-90f : 0.f;
   cudaError_t e = pkv::launch_norm_rope_cache(p, act_dtype(desc), is_i8(desc), device_sm_count(),
                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : cuda_fail(e, "norm_rope_reshape_and_cache launch");

@@ -107,7 +107,7 @@ __device__ __forceinline__ uint64_t mul2f(uint64_t a, uint64_t b) {
 // x becomes x / sqrt(mean of the vector's squares + eps) w; the vector's D / 16 units are neighbouring lanes.
 // False where the vector is not finite.
 template <int D>
-__device__ __forceinline__ bool normalise(float (&x)[16], const float* weight, int u, float eps) {
+__device__ __forceinline__ bool normalise(float (&x)[16], const float* weight, int u, float eps, float small) {
   constexpr int kUnits = D / 16;
   const unsigned lanes = ((1u << kUnits) - 1u) << (threadIdx.x & 31 & ~(kUnits - 1));
   auto squares = [&]() {
@@ -127,12 +127,15 @@ __device__ __forceinline__ bool normalise(float (&x)[16], const float* weight, i
   };
   float ss = squares();
   // bf16 reaches 3e38, whose squares do not fit: such a vector is made smaller first,
-  // and eps with it (one that holds an infinity stays infinite, r = 0)
-  if (__builtin_expect(ss == INFINITY, 0)) {
+  // and eps with it (one that holds an infinity stays infinite, r = 0).  In the same way
+  // one whose squares are too small is made larger, unless they are nothing beside eps.
+  // (`small`: below which they are; one comparison with both ends, in the order of the bits, which takes NaN along.)
+  if (__builtin_expect(__float_as_uint(ss) - __float_as_uint(small) >= 0x7f800000u - __float_as_uint(small), 0)) {
+    const float by = ss == INFINITY ? 0x1p-80f : 0x1p80f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] *= 0x1p-80f;
+    for (int k = 0; k < 16; ++k) x[k] *= by;
     ss = squares();
-    eps = eps * 0x1p-80f * 0x1p-80f;
+    eps = eps * by * by;
   }
   const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
   const uint64_t r2 = pack2f(r, r);
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_co
           unpack8<T>(va[e], x);
           unpack8<T>(vb[e], x + 8);
           bool finite = true;
-          if (kNorm && part != 2) finite = normalise<D>(x, weight[kNorm ? part : 0], u, p.eps);
+          if (kNorm && part != 2) finite = normalise<D>(x, weight[kNorm ? part : 0], u, p.eps, p.small_squares);
           if (turned) rotate<kPairs>(x, cs[tok[e]], u, rot / 16);
           if (kI8 && part != 0) {
             const int h = head[e] - (part == 1 ? hq : hq + hkv);

@@ -50,3 +50,26 @@ def test_keys_that_are_not_finite_into_an_8_bit_cache(pairs, rot, dtype):
     ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
     pkv.decode_scored(out, q, pool, desc, tables, ctx, 16, 0.1, ws, first_pos=first)
     assert bool(torch.isnan(out[0, 1]).all()) and not bool(torch.isnan(out[0, 0]).any())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("eps", [1.4e-45, 1e-44, 1e-40, 1.2e-38, 1e-32, 1e-24, 1e20, 1e38])
+def test_vectors_beside_every_eps(eps, kv8, dtype):
+    """Squares that are too small for fp32 beside an eps that is smaller still; and an eps near fp32's end."""
+    c = Case(5, 24, 4, 2, 128, 16, dtype, kv8, eps=float(np.float32(eps)))
+    rng = np.random.default_rng(8)
+    # (sizes whose results are far above bf16's smallest numbers)
+    fits = lambda size: size / np.sqrt(max(c.eps, size * size)) > 1e-30
+    for name, h in (("q", 4), ("k", 2)):
+        x = getattr(c, name)
+        for i, size in enumerate((1e-10, 1e-15, 1e-18, 1e-20, 1e-21, 1e-22, 1e-23, 1e-25, 1e-30, 1e-35, 1e15, 1e18, 1e25, 1e38)):
+            if dtype == "bf16" and fits(size):
+                x[i] = to_bits(rng.uniform(-1, 1, (h, 128)) * size, dtype)
+        x[14] = 0
+        if dtype == "f16" or fits(9e-41):
+            x[15] = 0
+            x[15, 0, 77] = 1                                         # the smallest number there is
+    if dtype == "bf16":
+        c.w = [to_bits(rng.uniform(0.5, 2, 128), dtype) for _ in range(2)]
+    c.check()

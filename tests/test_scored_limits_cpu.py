@@ -5,13 +5,18 @@ import torch
 
 from paged_kv_cache_168_gb300 import _lib, build as build_mod
 from paged_kv_cache_168_gb300._lib import CacheDesc
-from test_scored_ops_cpu import FAKE, _decode, _desc
+from test_scored_ops_cpu import FAKE, _decode, _desc, _norm
 
 
 @pytest.fixture(scope="module")
 def lib():
     build_mod.build()
     return _lib.load()
+
+
+def test_eps_near_the_end_of_fp32(lib):
+    assert _norm(lib, eps=1.1e38) == _lib.PA_ERR_INVALID_ARG and b"eps" in lib.pa_last_error_message()
+    assert _norm(lib, eps=1e38, n=0) == _lib.PA_OK and _norm(lib, eps=1.4e-45, n=0) == _lib.PA_OK
 
 
 @pytest.mark.parametrize("kv8", [False, True])
