@@ -474,8 +474,9 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
  * (the window only with window > 0).  A document mask is first_pos = the start of
  * the document; a prefix that sees itself whole is last_pos = max(p, its last
  * position).  A query whose span is empty gets a zero row.
- *   softcap     0 (none) or in [1e-4, 1e6]; a capped score is off by at most 2^-20
- *               of it, as the sums are in fp32.  Chunks over bf16 caches take the
+ *   softcap     0 (none) or in [1e-4, 1e6], with scale / softcap a normal fp32
+ *               number; a capped score is off by at most 2^-20 of it, as the sums
+ *               are in fp32.  Chunks over bf16 caches take the
  *               weights of caps up to 55 against a score of 0: results are off by
  *               up to 2^-86 a token, and query tiles with values too large or too
  *               small for that (beyond 2^16 beside scores near the cap; below

@@ -1,6 +1,7 @@
 // pagedkv_api.cu -- the C ABI: argument validation on the host, then kernel
 // dispatch on the caller's stream.  No memory is allocated and no state is kept
 // between calls (the per-thread error message aside).
+#include <float.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -398,6 +399,9 @@ pa_status score_params(pkv::ExtendParams& p, float scale, float softcap, const f
                        const int32_t* last_pos, int32_t max_context) {
   if (!(softcap == 0.f || (softcap >= 1e-4f && softcap <= 1e6f)))
     return fail(PA_ERR_INVALID_ARG, "softcap %g must be 0 or in [1e-4, 1e6]", (double)softcap);
+  const double quotient = softcap > 0.f ? (double)scale / softcap : 1.;
+  if (scale > 0.f && !(quotient >= FLT_MIN && quotient <= FLT_MAX))
+    return fail(PA_ERR_INVALID_ARG, "scale / softcap = %g is no normal fp32 number", quotient);
   if ((reinterpret_cast<uintptr_t>(slopes) & 3) || (reinterpret_cast<uintptr_t>(first_pos) & 3) ||
       (reinterpret_cast<uintptr_t>(last_pos) & 3))
     return fail(PA_ERR_INVALID_ARG, "slopes, first_pos and last_pos must be 4-byte aligned");

@@ -118,6 +118,33 @@ def test_zero_values_under_scores_near_the_lower_cap():
     assert not values(got)[:, :2, 96:].any()
 
 
+@pytest.mark.parametrize("dtype,kv8", [("f16", False), ("bf16", False), ("bf16", True)])
+@pytest.mark.parametrize("scale", [1e30, 1e-30])
+def test_scores_far_beyond_and_far_below_a_cap(scale, dtype, kv8):
+    """Every score is the cap or its opposite; or all of them are nearly 0."""
+    rng = np.random.default_rng(4)
+    case = Scored(rng, [70, 3], [300, 500], Hq=4, Hkv=2, D=128, bs=16, dtype=dtype, kv8=kv8)
+    one = Scored(rng, [1, 1], [300, 500], Hq=4, Hkv=2, D=128, bs=16, dtype=dtype, kv8=kv8)
+    for c, got in ((case, run(case, scale, cap=2.0)), (one, decode(one, scale, cap=2.0))):
+        got, row = values(got), 0
+        for s, n in enumerate(c.q_lens):
+            t = np.arange(c.ctx[s])
+            k, v = (c.cache.read(c.tables[s, t // 16], t % 16, part) for part in (0, 1))
+            for j in range(n):
+                m = c.ctx[s] - n + j + 1
+                for h in range(4):
+                    z = 2.0 * np.sign(k[:m, h // 2] @ c.q[row, h]) if scale > 1 else np.zeros(m)
+                    w = np.exp(z - z.max())
+                    w /= w.sum()
+                    out, size = w @ v[:m, h // 2], w @ np.abs(v[:m, h // 2])
+                    # the result's rounding, the weights', and scores off by 2^-20 of 2: 4 2^-20 of every weight; in 16 bits
+                    # and fewer the weights' smallest numbers do not matter (they are at least e^-4)
+                    u = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype]
+                    tol = u * np.abs(out) + (u + 2.0 ** -16) * size + 2.0 ** -21 * np.abs(v[:m, h // 2]).sum(0)
+                    assert (np.abs(got[row, h] - out) <= tol).all()
+                row += 1
+
+
 # ------------------------------------------------------------------ slopes of any size
 
 @pytest.mark.parametrize("cap", [0.0, 9.0])

@@ -5,7 +5,7 @@ import torch
 
 from paged_kv_cache_168_gb300 import _lib, build as build_mod
 from paged_kv_cache_168_gb300._lib import CacheDesc
-from test_scored_ops_cpu import FAKE, _decode, _desc, _norm
+from test_scored_ops_cpu import FAKE, _decode, _desc, _extend, _norm
 
 
 @pytest.fixture(scope="module")
@@ -17,6 +17,19 @@ def lib():
 def test_eps_near_the_end_of_fp32(lib):
     assert _norm(lib, eps=1.1e38) == _lib.PA_ERR_INVALID_ARG and b"eps" in lib.pa_last_error_message()
     assert _norm(lib, eps=1e38, n=0) == _lib.PA_OK and _norm(lib, eps=1.4e-45, n=0) == _lib.PA_OK
+
+
+@pytest.mark.parametrize("call", [_extend, _decode])
+def test_quotients_of_scale_and_cap_that_leave_fp32(lib, call):
+    """scale / softcap is a factor of every score: it has to be a normal number."""
+    bad = _lib.PA_ERR_INVALID_ARG
+    for scale, cap in ((1e35, 1e-4), (1e-33, 1e6), (1e-38, 1.0)):
+        assert call(lib, scale=scale, cap=cap) == bad, (scale, cap)
+        assert b"softcap" in lib.pa_last_error_message()
+        assert call(lib, scale=scale, cap=0.0, S=0) == _lib.PA_OK     # (uncapped)
+    assert call(lib, scale=float("inf"), cap=1.0) == bad
+    for scale, cap in ((1e34, 1.0), (1e-30, 1e6), (1e30, 1e-4)):
+        assert call(lib, scale=scale, cap=cap, S=0) == _lib.PA_OK, (scale, cap)
 
 
 @pytest.mark.parametrize("kv8", [False, True])
