@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(D * GB) merge_partitions_kernel(const __grid_c
   } else {
     const int ctx = p.context_lens[s];
     if (ctx <= 0 || !context_ok(p, ctx)) return;
-    n = (ctx - attended_from(p, s, ctx) + p.partition_size - 1) / p.partition_size;
+    n = (ctx - attended_from<true>(p, s, ctx) + p.partition_size - 1) / p.partition_size;
     if (n <= 1) return;
   }
   const int64_t row0 = ((int64_t)s * p.num_q_heads + h) * p.max_parts;

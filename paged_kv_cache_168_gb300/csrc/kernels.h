@@ -91,17 +91,19 @@ __host__ __device__ inline bool context_ok(const DecodeParams& p, int ctx) {
   return (p.ring_blocks > 0 || (int64_t)ctx <= (int64_t)p.bt_width * p.block_size) && ctx <= p.max_context_len;
 }
 
-// First position that sequence s attends (its context's end: none).
+// First position that sequence s attends (its context's end: none); kStarts: there may be first positions of each.
+template <bool kStarts>
 __device__ inline int attended_first(const DecodeParams& p, int s, int ctx) {
   const int t = window_start(ctx, p.block_size, p.window, p.ring_blocks);
-  if (!p.first_pos) return t;
+  if (!kStarts || !p.first_pos) return t;
   const int f = p.first_pos[s], end = ctx > 0 ? ctx : 0;
   return f > t ? (f < end ? f : end) : t;
 }
 
 // Partitions of a sequence: they start at the block holding attended_first.
+template <bool kStarts>
 __device__ inline int attended_from(const DecodeParams& p, int s, int ctx) {
-  return (attended_first(p, s, ctx) / p.block_size) * p.block_size;
+  return (attended_first<kStarts>(p, s, ctx) / p.block_size) * p.block_size;
 }
 
 cudaError_t launch_reshape_and_cache(uint8_t* layer_base, int32_t num_blocks, int32_t block_size,
