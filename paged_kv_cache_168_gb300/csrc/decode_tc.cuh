@@ -328,6 +328,12 @@ struct ItemTables {
   }
 };
 
+// A sequence's row of the block tables.
+template <bool kScored>
+__device__ __forceinline__ const int32_t* table_row(const DecodeParams& p, int s) {
+  return p.block_tables + (int64_t)s * (kScored ? p.bt_pitch : p.bt_stride);
+}
+
 // Work items of one sequence: its partitions, or one item that only writes zeros.
 // A sequence's work: F full partitions (P / 128 tiles each) and, if the
 // attended length is not a multiple of P, one remainder partition of
@@ -603,7 +609,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       const int id_lane = R.ids[lane], pbase = SP ? R.pbase : 0, last_pos = kScored ? R.ctx - 1 : 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.rec_empty[rs]);
-      const int32_t* row = p.block_tables + (int64_t)s * p.bt_stride;   // entry table_index(j) holds block j
+      const int32_t* row = table_row<kScored>(p, s);   // entry table_index(j) holds block j
       const int ntiles = (t1 - t0 + kTile - 1) / kTile;
       // 16-bit: the block id of this lane's chunk of tile k.  The item's first 32
       // come from the prefetched id_lane; a later one is loaded a tile ahead, so
@@ -827,7 +833,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
                     (int64_t)(d.kvh * G + n % G) * kD + (lane & 1) * 64);
       if (lane == 0) {
         const int ti = windowed ? table_index(d.fb, p.ring_blocks) : d.fb;
-        if (ti >= 0 && ti < p.bt_width) prefetch_l2(p.block_tables + (int64_t)d.row * p.bt_stride + ti);
+        if (ti >= 0 && ti < p.bt_width) prefetch_l2(table_row<kScored>(p, d.row) + ti);
       }
     };
     struct Item {
@@ -844,13 +850,13 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         const int row_end = min(p.bt_width, d.fb + P / bs);
         const int t = d.fb + 32 * (lane + 1);
         if (t < row_end) {
-          const int32_t* rp = p.block_tables + (int64_t)d.row * p.bt_stride;
+          const int32_t* rp = table_row<kScored>(p, d.row);
           prefetch_l2(rp + t);
           prefetch_l2(rp + min(t + 31, row_end - 1));
         }
       }
       r.id_lane =
-          (lane < P / bs && ti < p.bt_width && ti >= 0) ? p.block_tables[(int64_t)d.row * p.bt_stride + ti] : 0;
+          (lane < P / bs && ti < p.bt_width && ti >= 0) ? table_row<kScored>(p, d.row)[ti] : 0;
       // query rows: column n is head kvh * G + n % G of sequence seq0 + n / G
 #pragma unroll
       for (int k = 0; k < kQChunks; ++k) {
@@ -874,7 +880,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       if (more) nxt = fetch(desc_of(round + 1));
       if (item_of_round(round + 2) < total) prefetch_item(desc_of(round + 2));
       const int s = cd.row, kvh = cd.kvh, part = cd.part, ctx = cd.ctx, id_lane = cur.id_lane;
-      const int32_t* row = p.block_tables + (int64_t)s * p.bt_stride;   // entry table_index(j) holds block j
+      const int32_t* row = table_row<kScored>(p, s);   // entry table_index(j) holds block j
       const bool is_prefix = SP && cd.v >= S;                          // valid by construction
       if (!is_prefix && ctx_invalid(p, ctx)) {
         warp_zero_rows<T, G>(p, s, kvh, lane);
@@ -1742,7 +1748,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           } else {
             tab[n] = make_float2(cf0, cf1);
             if (quarter == 0 && n < nc) {
-              const int64_t r = (hbase + (n / G) * p.num_q_heads + n % G) * p.max_parts + (SP ? mt.pbase : 0) + mt.part;
+              const int64_t r = (hbase + (n / G) * p.num_q_heads + n % G) * p.max_parts + (kScored ? 0 : mt.pbase) + mt.part;
               p.ws_ml[r * 2 + 0] = mt.bad ? 0.f : M;
               p.ws_ml[r * 2 + 1] = mt.bad ? -1.f : cL;   // an invalid partition: the merge writes zeros
             }
@@ -1767,7 +1773,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
             if (n < nc) {
               const float2 g = tab[n];
               const float O = PP ? fmaf(x0[n], g.x, x1[n] * g.y) : x0[n] * g.x;
-              const int64_t r = (hbase + (n / G) * p.num_q_heads + n % G) * p.max_parts + (SP ? mt.pbase : 0) + mt.part;
+              const int64_t r = (hbase + (n / G) * p.num_q_heads + n % G) * p.max_parts + (kScored ? 0 : mt.pbase) + mt.part;
               p.ws_o[r * kD + row] = O;
             }
           }

@@ -37,7 +37,7 @@ struct DecodeParams {
   int32_t block_size;
   int32_t num_kv_heads;
   const int32_t* block_tables;
-  int64_t bt_stride;          // entries between rows
+  int32_t bt_stride;          // entries between rows (launch_decode_scored: bt_pitch)
   int32_t bt_width;           // entries of a row
   const int32_t* context_lens;
   int32_t num_seqs;
@@ -61,6 +61,7 @@ struct DecodeParams {
   int32_t* ws_seq;            // workspace [3][num_seqs]: partitions in all, effective prefix,
                               // first member of the sequence's prefix item (for the merge)
   // launch_decode_scored alone
+  int64_t bt_pitch;           // entries between table rows
   ScoreShape shape;
   const int32_t* first_pos;   // [S] or null: nothing before it is attended
 };

@@ -1027,7 +1027,7 @@ pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const
     d.block_size = desc->block_size;
     d.num_kv_heads = desc->num_kv_heads;
     d.block_tables = block_tables;
-    d.bt_stride = block_table_stride;
+    d.bt_pitch = block_table_stride;
     d.bt_width = block_table_width;
     d.context_lens = context_lens;
     d.num_seqs = num_seqs;
