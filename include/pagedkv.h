@@ -476,16 +476,19 @@ pa_status pa_extend_strided(void* out, const void* q, int64_t q_token_stride, co
  * position).  A query whose span is empty gets a zero row.
  *   softcap     0 (none) or in [1e-4, 1e6], with scale / softcap a normal fp32
  *               number; a capped score is off by at most 2^-20 of it, as the sums
- *               are in fp32.  Chunks over bf16 caches take the
- *               weights of caps up to 55 against a score of 0: results are off by
- *               up to 2^-86 a token, and query tiles with values too large or too
- *               small for that (beyond 2^16 beside scores near the cap; below
- *               2^-56, or 0, in rows whose scores are all below -28) are worked
- *               out again on CUDA cores, which is slow.
+ *               are in fp32.  Chunks over bf16 caches take the weights of caps up
+ *               to 55 against a score of 0: results are off by up to 2^-86 a
+ *               token, and query tiles with values too large or too small for
+ *               that (beyond 2^16 beside scores near the cap; below 2^-56, or 0,
+ *               in rows whose scores are all below -28) are worked out again on
+ *               CUDA cores, which is slow.
  *   slopes      device fp32 [num_q_heads], at most 1e27 in size, any sign; NULL: none.
  *   first_pos, last_pos  device int32 [num_tokens]; NULL: 0 and p.  Any values:
  *               they are clamped to the positions that exist.  Positions behind p
  *               have to be in the cache (the whole chunk is).
+ * Biases are sums in fp32, off by up to 2^-22 of the largest slope * distance.
+ * Weights enter the second product as pa_extend's do, rounded once to 16 bits:
+ * results are up to 1.4 times as far from 64 bits as those of 32-bit arithmetic.
  * Other arguments, errors and supported shapes as pa_extend_strided; with the
  * workspace of pa_extend_scored_workspace_bytes. */
 pa_status pa_extend_scored(void* out, const void* q, int64_t q_token_stride, const void* kv_cache,
@@ -505,7 +508,9 @@ size_t pa_extend_scored_workspace_bytes(const pa_cache_desc* desc, int32_t num_s
  * first_pos an entry a sequence.  ctx <= 0 gives a zero row; a context longer than
  * max_context_len, than its table row or (pa_decode's shapes) than 2^31 - 16385
  * gives one and PA_DEVERR_CONTEXT.  Every cache, and 1 to 16 query heads per kv
- * head. */
+ * head.  Shapes that pa_decode serves with head_size 128 on tensor cores (blocks of
+ * 8 tokens or more or an 8-bit cache; groups of 1, 2, 4, 8 or, 16-bit, 16) keep
+ * pa_decode's accuracy; the others are chunks of one token. */
 pa_status pa_decode_scored(void* out, const void* q, int64_t q_seq_stride, const void* kv_cache,
                            const pa_cache_desc* desc, int32_t layer, const int32_t* block_tables,
                            int64_t block_table_stride, int32_t block_table_width, const int32_t* context_lens,

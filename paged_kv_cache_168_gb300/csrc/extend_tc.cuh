@@ -28,7 +28,9 @@
 // tile and take turns: while one's softmax runs, the other's products do.  An
 // item with at most 128 rows lets both share its one query tile instead: tile t
 // takes every other KV tile, and the two results are merged in the epilogue.
-// Roles (one warp each but for the softmax):
+// Roles (one warp each but for the softmax), numbered as they are but where two
+// threads share a row (Cfg::kHalves): there the softmax has warps 0-15, 0-7 for query
+// tile 0, four for each half of the columns, and the others follow as 16-19.
 //   warps 0-3, 4-7  softmax of query tile 0 and 1: thread = TMEM lane = row.
 //                   Base-2 online softmax; the running maximum is raised only
 //                   when a tile's exceeds it by more than 8 (a factor 256), and
@@ -74,7 +76,7 @@
 // slope_h |distance|, and a query attends the positions of its own span [first, last]
 // instead of all up to its own.  The softmax threads shape the scores that they have read:
 //   cap       c tanh(y) = y P(y^2) c for y = s / c of at most 3/4 (P: 5 terms, relative error
-//             5.7e-7, the division folded into them): seven packed fp32 operations for two
+//             6e-7, the division folded into them): seven packed fp32 operations for two
 //             scores, in the loop that takes the powers.  2^x and 1 / x instead would triple
 //             the load of the special-function units.  A warp that meets a larger |y| in a
 //             tile takes the exact form for that tile.
@@ -82,7 +84,7 @@
 //             FMA, split into 16 columns' part and their first one's.  KV tiles are taken from
 //             the last one backwards: from left to right the maximum, and with it a rescaling
 //             of the results, would move with every tile (16 prompts of 2048 tokens: 876 us
-//             instead of 705).  Behind a query (prefixes) the warp takes the exact form.
+//             instead of 705; now 676).  Behind a query (prefixes) the warp takes the exact form.
 //   spans     the planner finds each query tile's first and last position, and which
 //             positions all of its queries attend; only KV tiles outside of those are masked.
 // What bounds it: beside what bounds the plain scores, instructions.  A softmax warp has its
@@ -91,10 +93,13 @@
 // FMAs); packed FMAs take 2.3 clocks.  So a tile's code is what counts: each shape has kernels
 // of its own, without conditions, and rare forms stand behind what is common.  Measured (us, bf16
 // but for the slopes, the rate counts the attended pairs): 32 capped chunks of 512 over 512 to
-// 3584, 32 + 8 heads, 640 (1.0 PFLOP/s; plain scores 530); 16 prompts of 2048 with slopes, 32 + 32
-// heads in fp16, 700 (0.79; plain 592); 2 rows of 8192 tokens of packed documents with prefixes
-// 319 (0.56; most KV tiles are masked somewhere); capped chunks over an 8-bit cache in a window of
-// 1500 690 (0.37; plain 526); 8 x 4 tokens over 32K to 128K, capped, 566 (5.9 TB/s).
+// 3584, 32 + 8 heads, 645 (1.0 PFLOP/s; plain scores 540; in fp16, with a maximum, 1034; what takes
+// kAny: cap 56 in bf16 1166, cap and slopes 1088; blocks of 4 tokens 1016, heads of 64 612); 16
+// prompts of 2048 with slopes, 32 + 32 heads in fp16, 676 (0.81; plain 592); 2 rows of 8192 tokens of
+// packed documents with prefixes 312 (0.57; most KV tiles are masked somewhere; capped as well 362,
+// with slopes 488); capped chunks over an 8-bit cache in a window of 1500 691 (0.37; plain 526); 8 x
+// 4 tokens over 32K to 128K, capped, 566 (5.9 TB/s).  The planner's pass over spans is one CTA's: 18
+// us of these documents' (7 without spans), 114 of 2150 for 128K tokens of them.
 #pragma once
 
 #include <cuda.h>
@@ -700,13 +705,6 @@ __device__ __forceinline__ void tmem_st16x128(uint32_t taddr, const uint32_t* r)
                : "memory");
 }
 
-// The same of 16 columns (32 weights).
-__device__ __forceinline__ void tmem_st16x128_16(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 // 32 TMEM lanes x 32 columns.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -1057,7 +1055,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       if (!ok && lane == 0) give_up();
       __syncwarp();
     } else {
-      // ================================================================= warp 8: products
+      // ================================================================= products
       // The whole warp runs the schedule, so that operands stay in uniform registers;
       // one elected lane issues.  Order: items in turn, and per item, KV tile by KV
       // tile, for query tile t = 0, 1: PV_t of its tile before, then QK_t of this one.
@@ -1218,7 +1216,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
     }
     __syncwarp();
   } else if (warp >= kSoft + 4) {
-    // =================================================================== converters (warps 12-15)
+    // =================================================================== converters
     if constexpr (C::kConvert) {
       set_regs_dec<C::kRegsConvert>();
       const int ct = threadIdx.x - 32 * (kSoft + 4);                              // 0 .. 127
@@ -1437,7 +1435,7 @@ __global__ void __launch_bounds__(Cfg<T, D, F, kShape>::kThreads, 1) extend_kern
       __syncwarp();
     }
   } else {
-    // =================================================================== softmax warpgroups (warps 0-7)
+    // =================================================================== softmax warpgroups
     set_regs_inc<C::kRegsSoftmax>();
     const int t = warp / (4 * kH);                                   // query tile
     const int half = kH == 2 ? (warp >> 2) & 1 : 0;                  // of its columns

@@ -84,7 +84,7 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float* cs, int u, i
   }
 }
 
-// Two fp32 operations an instruction (instructions are what this kernel runs out of first).
+// Two fp32 operations an instruction.
 __device__ __forceinline__ uint64_t pack2f(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -159,9 +159,10 @@ __device__ __forceinline__ bool normalise(float (&x)[16], const float* weight, i
 //
 // kNorm: q and k vectors become x / sqrt(mean(x^2) + eps) (weight + offset) first, in
 // fp32 and not rounded before the rotation; the weights wait in shared memory.  32768
-// tokens of 32 + 8 heads: 163 us, 4.9 TB/s, the issue slots two thirds busy (squares,
-// weights and rotation of every element); three CTAs an SM with more registers 205,
-// five or six with fewer 174 to 197.
+// tokens of 32 + 8 heads: 165 us, 4.9 TB/s.  Nothing is full there (issue slots 58%,
+// DRAM 60%): a round's slots, positions and cosines wait for one another before its
+// first vector is loaded.  Three CTAs an SM with more registers 205, five or six with
+// fewer 174 to 197.  Into an 8-bit cache 192 us.
 template <typename T, int D, bool kPairs, bool kI8, bool kNorm, int kTokens>
 __global__ void __launch_bounds__(kThreads, 4) rope_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kUnits = D / 16;                     // units per head vector

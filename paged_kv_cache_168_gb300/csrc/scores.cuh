@@ -3,10 +3,10 @@
 //
 // With y = scale q.k / c, a cap c makes c tanh(y) of it.  Up to |y| = 1 that is y
 // P(y^2) with a polynomial P of degree 5, fitted to tanh(y) / y by weighted least
-// squares until its relative error is level (5.9e-7); beyond, c (1 - 2 / (1 +
+// squares until its relative error is level (6.1e-7); beyond, c (1 - 2 / (1 +
 // e^(2y))), whose absolute error of a few 2^-24 c is as small beside a result of
 // at least 0.76 c.  Everything is in base-2 units (times log2 e) and fp32.  Up to
-// |y| = 3/4 five terms do as well (5.7e-7): scores are rarely nearer to their cap.
+// |y| = 3/4 five terms do as well (5.9e-7): scores are rarely nearer to their cap.
 #pragma once
 
 #include <cuda_runtime.h>
