@@ -259,7 +259,7 @@ struct Shared {
   } u;
   uint64_t rec_full[2], rec_empty[2];
   // 8-bit caches: copy warp -> converter ring of raw half tiles, and the token
-  // scales of each converted stage
+  // scales of each converted stage (V's as value_log)
   // (two rings of NRH slots, one per 64-token half: slot h * NRH + k % NRH)
   uint64_t raw_full[I8 ? 2 * NRH : 1], raw_empty[I8 ? 2 * NRH : 1];
   TileMeta raw_meta[I8 ? 2 * NRH : 1];
@@ -278,8 +278,9 @@ struct Shared {
 // 1152 is taken off; bf16: the byte goes into the mantissa of 2^23 in fp32,
 // 2^23 + 128 is taken off, and the (exact) high halves are packed.
 template <typename T>
-__device__ __forceinline__ void codes_to_16bit(const uint4 w4, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {w4.x ^ 0x80808080u, w4.y ^ 0x80808080u, w4.z ^ 0x80808080u, w4.w ^ 0x80808080u};
+__device__ __forceinline__ void codes_to_16bit(const uint4 w4, uint32_t (&o)[8], uint32_t keep = 0xffffffffu) {
+  const uint32_t w[4] = {(w4.x & keep) ^ 0x80808080u, (w4.y & keep) ^ 0x80808080u, (w4.z & keep) ^ 0x80808080u,
+                         (w4.w & keep) ^ 0x80808080u};
   if constexpr (std::is_same<T, __half>::value) {
     const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));   // 1152
 #pragma unroll
@@ -299,6 +300,14 @@ __device__ __forceinline__ void codes_to_16bit(const uint4 w4, uint32_t (&o)[8])
         o[2 * k + (b >> 1)] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
       }
   }
+}
+
+// What a V scale adds to its token's scores (below): its logarithm, not below -120.  Where it is 0, and the codes are
+// taken as 0, any number that keeps the token's weight: -64.  Infinity where it is NaN: masked tokens have a weight of 0
+// then, as with any other scale, and rows that attend it are NaN.
+__device__ __forceinline__ float value_log(float scale) {
+  if (scale == 0.f) return -64.f;
+  return scale < INFINITY ? fmaxf(__log2f(scale), -120.f) : INFINITY;
 }
 
 __device__ __forceinline__ bool ctx_invalid(const DecodeParams& p, int ctx) { return !context_ok(p, ctx); }
@@ -1409,10 +1418,15 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
       if (lane == 0) mbar_arrive(&sh.s_free[sb]);
       const bool rv = row >= mt.lo && row < mt.valid;
       // 8-bit: K_t = sk_t * codes and V_t = sv_t * codes; sk_t scales this row's
-      // scores and sv_t its P^T row (the normaliser keeps the unscaled p)
+      // scores, and sv_t its weights: the maximum is that of x + log2 sv_t, so what
+      // is stored, 2^(x + log2 sv_t - m), is at most 1 and keeps its bits whatever
+      // the values' size, and the normaliser takes it divided by sv_t.  (Weights
+      // taken against the maximum of x and multiplied by sv_t lost those below
+      // 2^-25 / sv_t.  That took 485 and 246 us of plain scores, 8 x 131072 tokens in
+      // groups of 8 and 64 x 8192 in groups of 4; this 494 and 252.)
       const float unit = kScored && p.shape.capped ? p.shape.cap_in : p.scale_log2;
       const float kscale = I8 ? sh.sk[slot][row] * (unit * mt.qinv) : unit;
-      const float vscale = I8 ? sh.sv[slot][row] : 1.f;
+      const float vlog = I8 ? sh.sv[slot][row] : 0.f, vinv = I8 ? ex2_approx(-vlog) : 1.f;
       // scores; does any exceed the running maximum by more than kLazyMax?  (On
       // the group's first tile of an item m = -inf, so every valid row does.)
       float x[CN];
@@ -1423,8 +1437,8 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
         if constexpr (!kScored) {
 #pragma unroll
           for (int n = 0; n < CN; ++n) {
-            x[n] = rv ? sv[n] * kscale : -INFINITY;
-            up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);   // 8-bit: the V scales ride on P, keep p <= 1
+            x[n] = rv ? (I8 ? fmaf(sv[n], kscale, vlog) : sv[n] * kscale) : -INFINITY;
+            up |= x[n] > mv[n] + (I8 ? 0.f : kLazyMax);   // 8-bit: fp16 weights, at most 1
           }
         } else {
           const bool capped = p.shape.capped, sloped = p.shape.slopes;
@@ -1436,7 +1450,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           };
           if (!capped) {
 #pragma unroll
-            for (int n = 0; n < CN; ++n) finish(n, sv[n] * kscale);
+            for (int n = 0; n < CN; ++n) finish(n, I8 ? fmaf(sv[n], kscale, vlog) : sv[n] * kscale);
           } else {
             // by the polynomial, and by the other form if some score was too near the cap for it: seen by the vote that
             // asks for a larger maximum
@@ -1445,7 +1459,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
 #pragma unroll
             for (int n = 0; n < CN; n += 2) {                          // (a single column's neighbour is padding)
               float a, b;
-              score::nearer_cap2(p.shape, kscale, sv[n], sv[n + 1], a, b);
+              score::nearer_cap2(p.shape, kscale, vlog, sv[n], sv[n + 1], a, b);
               big = fmaxf(fmaxf(big, fabsf(sv[n])), n + 1 < CN ? fabsf(sv[n + 1]) : 0.f);
               finish(n, a);
               if (n + 1 < CN) finish(n + 1, b);
@@ -1454,7 +1468,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
             if (__any_sync(kFull, up | far) && __any_sync(kFull, far)) {
               up = false;
 #pragma unroll
-              for (int n = 0; n < CN; ++n) finish(n, score::any_cap_call(p.shape, sv[n]));
+              for (int n = 0; n < CN; ++n) finish(n, score::any_cap_call(p.shape, sv[n]) + vlog);
             }
           }
         }
@@ -1548,13 +1562,13 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
 #pragma unroll
         for (int n = 0; n < CN; ++n) {
           pr[n] = rv ? ex2_approx(x[n] - mv[n]) : 0.f;
-          lp[n] += pr[n];
+          lp[n] = I8 ? fmaf(pr[n], vinv, lp[n]) : lp[n] + pr[n];
         }
       }
       uint32_t pk[NPV / 2];   // [p_hi of heads 0..HG-1 | p_lo of heads 0..HG-1], two per word
 #pragma unroll
       for (int n2 = 0; n2 < HG; n2 += 2) {
-        const float a = (n2 < CN) ? pr[n2] * vscale : 0.f, b = (n2 + 1 < CN) ? pr[n2 + 1] * vscale : 0.f;
+        const float a = (n2 < CN) ? pr[n2] : 0.f, b = (n2 + 1 < CN) ? pr[n2 + 1] : 0.f;
         pk[n2 >> 1] = Elem<OpT>::pack2(a, b);
         const float2 r = Elem<OpT>::to_float2(pk[n2 >> 1]);
         pk[(HG + n2) >> 1] = Elem<OpT>::pack2(a - r.x, b - r.y);
@@ -1836,12 +1850,13 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           skv = *reinterpret_cast<const float*>(chunk + 2LL * bs * kD + 4 * tb);
           svv = *reinterpret_cast<const float*>(chunk + 2LL * bs * kD + sbytes + 4 * tb);
         }
-        // V -> the stage's V atoms (8-token group t / 8 at 2 KiB per group)
+        // V -> the stage's V atoms (8-token group t / 8 at 2 KiB per group); no codes where the scale is 0
+        const uint32_t keep = svv == 0.f ? 0u : 0xffffffffu;
         uint8_t* vrow = stages + slot * kStage + (t >> 3) * 2048 + (t & 7) * 128;
 #pragma unroll
         for (int j = 0; j < kPc; ++j) {
           uint32_t o[8];
-          codes_to_16bit<__half>(vin[j], o);
+          codes_to_16bit<__half>(vin[j], o, keep);
           const int pg = dh * kPc + j;                       // 16 dims: two 16-byte pieces of atom pg / 4
           uint8_t* atom = vrow + (pg >> 2) * 1024;
           const int p0 = (2 * pg) & 7;
@@ -1862,7 +1877,7 @@ __global__ void __launch_bounds__(threads_of(I8, SP ? kN : G), 1) decode_tc_kern
           tc::tmem_st32u(k_lane + slot * 64 + g * 32, kr);
         }
         if (dh == 0) sh.sk[slot][t] = skv;
-        if (dh == kSplit - 1) sh.sv[slot][t] = svv;
+        if (dh == kSplit - 1) sh.sv[slot][t] = value_log(svv);
         tc::tmem_wait_st();
       }
       if (warp == kThreads / 32 && lane == 0) sh.meta[slot] = mt;   // a real tile, or "no more work"

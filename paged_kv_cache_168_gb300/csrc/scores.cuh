@@ -27,8 +27,9 @@ __device__ __forceinline__ float near_cap(const ScoreShape& w, float y) {
   return v * y;
 }
 
-// The same for two |y| <= 3/4, a step less and two operations an instruction; a and b are multiplied by unit first.
-__device__ __forceinline__ void nearer_cap2(const ScoreShape& w, float unit, float& a, float& b, float& ca, float& cb) {
+// The same for two |y| <= 3/4, a step less and two operations an instruction; a and b are multiplied by unit first, and
+// more is added to the results.
+__device__ __forceinline__ void nearer_cap2(const ScoreShape& w, float unit, float more, float& a, float& b, float& ca, float& cb) {
   uint64_t y, u, s, v, c;
   asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
   asm("mov.b64 %0, {%1, %1};" : "=l"(u) : "f"(unit));
@@ -40,7 +41,8 @@ __device__ __forceinline__ void nearer_cap2(const ScoreShape& w, float unit, flo
     asm("mov.b64 %0, {%1, %1};" : "=l"(c) : "f"(w.three_quarters[k]));
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(s), "l"(c));
   }
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(c) : "f"(more));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(v) : "l"(y), "l"(c));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(y));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(ca), "=f"(cb) : "l"(v));
 }
